@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import numpy as np
 
@@ -30,6 +31,7 @@ HS_STATUS_TIMEOUT = 8
 HS_FLAG_NO_COPY = 1
 HS_FLAG_TEST_STALL = 2
 POLICY_LRU, POLICY_FIFO, POLICY_RANDOM = 0, 1, 2
+HS_BF16, HS_F16 = 0, 1
 
 # every symbol include/hs.h declares, with (restype, argtypes)
 _VP, _I, _SZ, _U = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_uint
@@ -48,6 +50,28 @@ class PlanResult(ctypes.Structure):
     _fields_ = [("device_bytes_per_request", _I64), ("requests_by_device", _I64), ("host_pool_rows", _I64),
                 ("host_pool_bytes", _I64), ("requests_by_host", _I64), ("requests", _I64),
                 ("miss_bytes_per_step", _F64), ("link_us_per_step", _F64)]
+
+
+class _PageShape(ctypes.Structure):
+    """hs_page_shape (include/hs.h)."""
+    _fields_ = [("tokens", _I), ("kv_heads", _I), ("head_dim", _I)]
+
+
+class _TokenRows(ctypes.Structure):
+    """hs_token_rows (include/hs.h)."""
+    _fields_ = [("k", _VP), ("v", _VP), ("k_token_stride", _I64), ("k_head_stride", _I64),
+                ("v_token_stride", _I64), ("v_head_stride", _I64)]
+
+
+class _PageAttention(ctypes.Structure):
+    """hs_page_attention (include/hs.h)."""
+    _fields_ = [("shape", _PageShape), ("dtype", _I), ("B", _I), ("S", _I), ("k", _I), ("q_heads", _I),
+                ("q_tokens", _I), ("q", _VP), ("q_batch_stride", _I64), ("q_token_stride", _I64),
+                ("q_head_stride", _I64), ("o", _VP), ("o_batch_stride", _I64), ("o_token_stride", _I64),
+                ("o_head_stride", _I64), ("lse", _VP), ("pages", _VP), ("slots", _VP), ("selections", _VP),
+                ("lengths", _VP), ("sm_scale", ctypes.c_float), ("softcap", ctypes.c_float), ("slopes", _VP),
+                ("start", _VP), ("prefix", _VP), ("status", _VP), ("wait_ns", ctypes.c_uint64)]
+
 
 SIGNATURES = {
     "hs_create": (_VP, [_I, _I, _I, _I]),
@@ -73,6 +97,12 @@ SIGNATURES = {
     "hs_set_wait_limit": (_I, [_VP, ctypes.c_uint64]),
     "hs_attend": (_I, [_VP, _VP, _VP, _I, _I, _VP, _I, ctypes.c_float, _VP, _VP, _VP, ctypes.c_size_t]),
     "hs_attend_workspace": (_I, [_VP, _I, _I, _I, ctypes.POINTER(ctypes.c_size_t)]),
+    "hs_page_bytes": (_SZ, [_VP]),
+    "hs_write_tokens": (_I, [_VP, _VP, _I, _VP, _I64, _VP, _VP, _I64, _VP]),
+    "hs_append_tokens": (_I, [_VP, _VP, _VP, _I, _VP, _I64, _VP, _VP]),
+    "hs_read_pages": (_I, [_VP, _VP, _I, _VP, _I, _I, _VP, _I, _VP, _VP, _VP]),
+    "hs_attend_pages": (_I, [_VP, _VP]),
+    "hs_status_word": (_VP, [_VP]),
     "hs_kernels_per_call": (_I, [_VP]),
     "hs_plan": (_I, [ctypes.POINTER(PlanParams), ctypes.POINTER(PlanResult)]),
     "hs_pool_create": (_VP, [_I64]),
@@ -168,6 +198,128 @@ def plan(**params) -> dict:
     return {name: getattr(out, name) for name, _ in PlanResult._fields_}
 
 
+class PageShape(NamedTuple):
+    """The shape of 4-bit pages (hs_page_shape); the page calls take any such triple."""
+    tokens: int
+    kv_heads: int
+    head_dim: int
+
+    @property
+    def bytes(self) -> int:
+        """Bytes of a page: the entry_bytes of a context that holds such pages."""
+        n = int(load_library().hs_page_bytes(ctypes.byref(_PageShape(*self))))
+        if n == 0:
+            raise ValueError(f"unsupported page shape {tuple(self)}")
+        return n
+
+
+def _page_bytes(shape) -> int:
+    return shape[0] * shape[1] * shape[2] * 9 // 8
+
+
+def _dtype_code(x) -> int:
+    import torch
+    if x.dtype is torch.bfloat16:
+        return HS_BF16
+    if x.dtype is torch.float16:
+        return HS_F16
+    raise ValueError(f"bfloat16 or float16 wanted, got {x.dtype}")
+
+
+def _on_device(device: int, **tensors) -> None:
+    """Every tensor (None: left out) is on the calling thread's current device."""
+    for name, x in tensors.items():
+        if x is not None and x.get_device() != device:
+            raise ValueError(f"{name} must be on the current CUDA device {device}, it is on {x.device}")
+
+
+def _vector(name: str, x, dtype, shape) -> None:
+    if x is not None and (x.dtype is not dtype or tuple(x.shape) != tuple(shape) or not x.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
+                         f"got {x.dtype} {tuple(x.shape)}")
+
+
+def _rows(shape, k, v):
+    """hs_token_rows of k and v [n, kv_heads, head_dim] (any token and head strides), and n."""
+    n = k.shape[0]
+    want = (n, shape[1], shape[2])
+    for name, x in (("k", k), ("v", v)):
+        if tuple(x.shape) != want or (x.stride(2) != 1 and x.numel()):
+            raise ValueError(f"{name} must have shape {want} with contiguous rows, got {tuple(x.shape)}")
+    if v.dtype is not k.dtype:
+        raise ValueError("k and v must have one dtype")
+    return _TokenRows(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), v.stride(0), v.stride(1)), n
+
+
+def _checked(rc: int, what: str) -> None:
+    if rc != HS_OK:
+        raise HsError(f"{what} failed ({rc}): {last_error()}")
+
+
+def write_tokens(shape, k, v, dest, pages, status=None, stream=None) -> None:
+    """hs_write_tokens: k, v bf16 or fp16 [n, kv_heads, head_dim] (rows contiguous) quantised
+    into uint8 pages [P, page bytes] (device, or pinned) at the token slots dest int64 [n]
+    (page * tokens + offset; negative: padding). status: a device int32 word, or None."""
+    import torch
+    rows, n = _rows(shape, k, v)
+    _vector("dest", dest, torch.int64, (n,))
+    _vector("pages", pages, torch.uint8, (pages.shape[0], _page_bytes(shape)))
+    device = torch.cuda.current_device()
+    _on_device(device, k=k, v=v, dest=dest, status=status, pages=None if pages.is_pinned() else pages)
+    _checked(load_library().hs_write_tokens(_stream(stream), ctypes.byref(_PageShape(*shape)), _dtype_code(k),
+                                            ctypes.byref(rows), n, dest.data_ptr(), pages.data_ptr(),
+                                            pages.shape[0], _addr(status)), "hs_write_tokens")
+
+
+def read_pages(shape, pages, slots, k, v, status=None, stream=None) -> None:
+    """hs_read_pages: the pages [B, S, page bytes] in slots int32 [B, n] decoded into k and v
+    [B, n * tokens, kv_heads, head_dim], bf16 or fp16 (zeros where a slot is negative)."""
+    import torch
+    B, n = slots.shape
+    _vector("slots", slots, torch.int32, (B, n))
+    _vector("pages", pages, torch.uint8, (B, pages.shape[1], _page_bytes(shape)))
+    want = (B, n * shape[0], shape[1], shape[2])
+    _vector("k", k, k.dtype, want)
+    _vector("v", v, k.dtype, want)
+    device = torch.cuda.current_device()
+    _on_device(device, slots=slots, k=k, v=v, status=status, pages=pages)
+    _checked(load_library().hs_read_pages(_stream(stream), ctypes.byref(_PageShape(*shape)), _dtype_code(k),
+                                          pages.data_ptr(), B, pages.shape[1], slots.data_ptr(), n, k.data_ptr(),
+                                          v.data_ptr(), _addr(status)), "hs_read_pages")
+
+
+def attend_pages(shape, q, pages, slots, selections, lengths, o, lse, sm_scale: float, softcap: float = 0.0,
+                 slopes=None, start=None, prefix=None, status=None, stream=None, wait_ns: int = 0) -> None:
+    """hs_attend_pages: q [B, q_tokens, q_heads, head_dim], bf16 or fp16, over the pages
+    [B, S, page bytes] in slots int32 [B, k], which are the pages numbered selections int32
+    [B, k] of sequences of lengths int32 [B] tokens; into o (as q) and lse float32 [B,
+    q_tokens, q_heads]. softcap: 0, or the cap of the scores; slopes: float32 [q_heads] of a
+    distance bias; start, prefix: int32 [B], keys before start are masked but for the first
+    prefix; status: a device int32 word."""
+    import torch
+    B, T, Hq, D = q.shape
+    k = slots.shape[1]
+    if D != shape[2] or o.shape != q.shape or o.dtype is not q.dtype or q.stride(3) != 1 or o.stride(3) != 1:
+        raise ValueError(f"q and o must be [B, q_tokens, q_heads, {shape[2]}] of one dtype with contiguous rows")
+    i32, f32 = torch.int32, torch.float32
+    _vector("pages", pages, torch.uint8, (B, pages.shape[1], _page_bytes(shape)))
+    _vector("slots", slots, i32, (B, k))
+    _vector("selections", selections, i32, (B, k))
+    _vector("lengths", lengths, i32, (B,))
+    _vector("lse", lse, f32, (B, T, Hq))
+    _vector("slopes", slopes, f32, (Hq,))
+    _vector("start", start, i32, (B,))
+    _vector("prefix", prefix, i32, (B,))
+    _on_device(torch.cuda.current_device(), q=q, o=o, lse=lse, pages=pages, slots=slots, selections=selections,
+               lengths=lengths, slopes=slopes, start=start, prefix=prefix, status=status)
+    args = _PageAttention(_PageShape(*shape), _dtype_code(q), B, pages.shape[1], k, Hq, T,
+                          q.data_ptr(), q.stride(0), q.stride(1), q.stride(2),
+                          o.data_ptr(), o.stride(0), o.stride(1), o.stride(2), lse.data_ptr(), pages.data_ptr(),
+                          slots.data_ptr(), selections.data_ptr(), lengths.data_ptr(), sm_scale, softcap,
+                          _addr(slopes), _addr(start), _addr(prefix), _addr(status), wait_ns)
+    _checked(load_library().hs_attend_pages(_stream(stream), ctypes.byref(args)), "hs_attend_pages")
+
+
 class Pool:
     """Admission bookkeeping of a shared host pool of `rows` rows (hs_pool_*)."""
 
@@ -212,6 +364,7 @@ class Context:
         self._lib = load_library()
         self.R, self.C, self.S, self.E = num_requests, context_len, slots, entry_bytes
         self.pool_rows = 0
+        self._wait_ns = 0  # the library's default
         if pool is not None:
             addr, rows, stride = pool
             self.pool_rows = rows
@@ -311,6 +464,30 @@ class Context:
         self._check(self._lib.hs_attend(self._h, _stream(stream), _addr(q), B, H, _addr(out_slots), k,
                                         float(sm_scale), _addr(o), _addr(lse), ws, nbytes), "hs_attend")
 
+    # ------------------------------------------------------------------ 4-bit pages
+    def append_tokens(self, shape, k, v, positions, requests=None, stream=None) -> None:
+        """hs_append_tokens: k, v bf16 or fp16 [n, kv_heads, head_dim] join the histories at
+        token positions int32 [n] (negative: skipped) of the requests int32 [n] (None: token i
+        of request i), in the host store and the resident slots."""
+        import torch
+        rows, n = _rows(shape, k, v)
+        _vector("positions", positions, torch.int32, (n,))
+        _vector("requests", requests, torch.int32, (n,))
+        _on_device(torch.cuda.current_device(), k=k, v=v, positions=positions, requests=requests)
+        self._check(self._lib.hs_append_tokens(self._h, _stream(stream), ctypes.byref(_PageShape(*shape)), _dtype_code(k),
+                                               ctypes.byref(rows), n, _addr(requests), positions.data_ptr()),
+                    "hs_append_tokens")
+
+    def read_pages(self, shape, out_slots, k, v, stream=None) -> None:
+        """read_pages() over this context's device buffer and status word."""
+        read_pages(shape, self.device_kv(), out_slots, k, v, status=self.status_word(), stream=stream)
+
+    def attend_pages(self, shape, q, out_slots, selections, lengths, o, lse, sm_scale: float, softcap: float = 0.0,
+                     slopes=None, start=None, prefix=None, stream=None) -> None:
+        """attend_pages() over this context's device buffer, status word and wait limit."""
+        attend_pages(shape, q, self.device_kv(), out_slots, selections, lengths, o, lse, sm_scale, softcap, slopes,
+                     start, prefix, status=self.status_word(), stream=stream, wait_ns=self._wait_ns)
+
     def reset(self, stream=None) -> None:
         self._check(self._lib.hs_reset(self._h, _stream(stream)), "hs_reset")
 
@@ -324,6 +501,7 @@ class Context:
     def set_wait_limit(self, ns: int) -> None:
         """Time limit (global-timer ns from a CTA's start) of the kernels' device waits."""
         self._check(self._lib.hs_set_wait_limit(self._h, int(ns)), "hs_set_wait_limit")
+        self._wait_ns = int(ns)
 
     def kernels_per_call(self) -> int:
         return int(self._lib.hs_kernels_per_call(self._h))
@@ -375,3 +553,6 @@ class Context:
 
     def step(self):
         return self._dev("hs_step", (self.R,), "<i4")
+
+    def status_word(self):
+        return self._dev("hs_status_word", (1,), "<i4")

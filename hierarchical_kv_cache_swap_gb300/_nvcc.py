@@ -14,8 +14,9 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OBJDIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libhs.so")
-SOURCES = ["hs_api.cu", "hs_kernels.cu", "hs_noalloc.cu", "hs_consume.cu", "hs_attend.cu", "hs_pool.cu"]
-HEADERS = [os.path.join(CSRC, "hs_internal.h"), os.path.join(ROOT, "include", "hs.h")]
+SOURCES = ["hs_api.cu", "hs_kernels.cu", "hs_noalloc.cu", "hs_consume.cu", "hs_attend.cu", "hs_pool.cu",
+           "hs_page.cu", "hs_page_attend.cu"]
+HEADERS = [os.path.join(CSRC, "hs_internal.h"), os.path.join(CSRC, "hs_page.h"), os.path.join(ROOT, "include", "hs.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-Xptxas", "-v",
               "-I", os.path.join(ROOT, "include")]

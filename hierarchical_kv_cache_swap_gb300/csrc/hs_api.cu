@@ -17,6 +17,7 @@
 
 #include "hs.h"
 #include "hs_internal.h"
+#include "hs_page.h"
 
 struct hs_ctx {
     hs::Layout L;
@@ -479,6 +480,166 @@ int hs_resolve_host(hs_ctx* h, hs_stream_t stream, const int32_t* sel_host, int 
     if ((e = cudaStreamSynchronize(s)) != cudaSuccess) return cuda_fail(e, "cudaStreamSynchronize");
     return HS_OK;
 }
+
+static bool page_shape(const hs_page_shape* shape, hs::PageShape* ps) {
+    if (!shape) return false;
+    *ps = hs::PageShape{shape->tokens, shape->kv_heads, shape->head_dim};
+    return ps->valid();
+}
+
+size_t hs_page_bytes(const hs_page_shape* shape) {
+    hs::PageShape ps;
+    return page_shape(shape, &ps) ? ps.bytes() : 0;
+}
+
+static int page_check(const hs_page_shape* shape, int dtype, hs::PageShape* ps) {
+    if (!shape) return fail(HS_ERR_INVALID, "null page shape");
+    if (!page_shape(shape, ps))
+        return fail(HS_ERR_INVALID, "unsupported page shape (%d tokens, %d heads, head_dim %d)", shape->tokens,
+                    shape->kv_heads, shape->head_dim);
+    if (dtype != HS_BF16 && dtype != HS_F16) return fail(HS_ERR_INVALID, "unknown dtype %d", dtype);
+    return HS_OK;
+}
+
+static bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+
+static int rows_check(const hs_token_rows* r, int64_t n, hs::TokenRows* out) {
+    if (!r) return fail(HS_ERR_INVALID, "null token rows");
+    if (n < 0) return fail(HS_ERR_INVALID, "n=%lld must not be negative", (long long)n);
+    if (n > 0 && (!r->k || !r->v)) return fail(HS_ERR_INVALID, "null k/v");
+    if (!aligned16(r->k) || !aligned16(r->v) ||
+        ((r->k_token_stride | r->k_head_stride | r->v_token_stride | r->v_head_stride) & 7))
+        return fail(HS_ERR_INVALID, "rows of k and v must be 16-byte aligned");
+    *out = hs::TokenRows{(const uint16_t*)r->k, (const uint16_t*)r->v, r->k_token_stride, r->k_head_stride,
+                         r->v_token_stride, r->v_head_stride};
+    return HS_OK;
+}
+
+static int sm_count(int* sms) {
+    int dev = 0;
+    cudaError_t e;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess ||
+        (e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
+        return cuda_fail(e, "device query");
+    return HS_OK;
+}
+
+int hs_write_tokens(hs_stream_t stream, const hs_page_shape* shape, int dtype, const hs_token_rows* rows, int64_t n,
+                    const int64_t* dest, uint8_t* pages, int64_t num_pages, uint32_t* status) {
+    hs::PageShape ps;
+    hs::TokenRows tr;
+    int rc = page_check(shape, dtype, &ps), sms = 0;
+    if (rc != HS_OK || (rc = rows_check(rows, n, &tr)) != HS_OK) return rc;
+    if (num_pages < 0 || num_pages > INT64_MAX / ((int64_t)ps.bytes() * 2))
+        return fail(HS_ERR_INVALID, "num_pages=%lld out of range", (long long)num_pages);
+    if (n > 0 && (!dest || (!pages && num_pages > 0))) return fail(HS_ERR_INVALID, "null dest/pages");
+    if (!aligned16(pages)) return fail(HS_ERR_INVALID, "pages must be 16-byte aligned");
+    if ((rc = sm_count(&sms)) != HS_OK) return rc;
+    cudaError_t e = hs::launch_write_tokens((cudaStream_t)stream, ps, dtype == HS_BF16, tr, n, dest, pages, num_pages, status, sms);
+    if (e != cudaSuccess) return cuda_fail(e, "write kernel launch");
+    g_err[0] = 0;
+    return HS_OK;
+}
+
+int hs_append_tokens(hs_ctx* h, hs_stream_t stream, const hs_page_shape* shape, int dtype, const hs_token_rows* rows,
+                     int64_t n, const int32_t* requests, const int32_t* positions) {
+    hs::PageShape ps;
+    hs::TokenRows tr;
+    if (!h) return fail(HS_ERR_INVALID, "null context");
+    int rc = page_check(shape, dtype, &ps), dev = -1;
+    if (rc != HS_OK || (rc = rows_check(rows, n, &tr)) != HS_OK) return rc;
+    if ((size_t)h->L.E != ps.bytes())
+        return fail(HS_ERR_INVALID, "pages of %zu bytes, but the context's entries have %d", ps.bytes(), h->L.E);
+    if (n > 0 && !positions) return fail(HS_ERR_INVALID, "null positions");
+    if (!requests && n != h->L.R)
+        return fail(HS_ERR_INVALID, "n=%lld without requests, but the context has %d", (long long)n, h->L.R);
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    if (dev != h->device)
+        return fail(HS_ERR_INVALID, "current device %d is not the context's device %d", dev, h->device);
+    e = hs::launch_append_tokens(h->L, (cudaStream_t)stream, ps, dtype == HS_BF16, tr, n, requests, positions, h->num_sms);
+    if (e != cudaSuccess) return cuda_fail(e, "append kernel launch");
+    g_err[0] = 0;
+    return HS_OK;
+}
+
+int hs_read_pages(hs_stream_t stream, const hs_page_shape* shape, int dtype, const uint8_t* pages, int B, int S,
+                  const int32_t* slots, int n, void* k, void* v, uint32_t* status) {
+    hs::PageShape ps;
+    int rc = page_check(shape, dtype, &ps), sms = 0;
+    if (rc != HS_OK) return rc;
+    if (B < 0 || S < 0 || n < 0) return fail(HS_ERR_INVALID, "B=%d, S=%d and n=%d must not be negative", B, S, n);
+    if (B > 0 && n > 0 && (!slots || !k || !v || (!pages && S > 0))) return fail(HS_ERR_INVALID, "null pages/slots/k/v");
+    if (!aligned16(pages) || !aligned16(k) || !aligned16(v))
+        return fail(HS_ERR_INVALID, "pages, k and v must be 16-byte aligned");
+    if ((rc = sm_count(&sms)) != HS_OK) return rc;
+    cudaError_t e = hs::launch_read_pages((cudaStream_t)stream, ps, dtype == HS_BF16, pages, B, S, slots, n, k, v, status, sms);
+    if (e != cudaSuccess) return cuda_fail(e, "read kernel launch");
+    g_err[0] = 0;
+    return HS_OK;
+}
+
+int hs_attend_pages(hs_stream_t stream, const hs_page_attention* a) {
+    hs::PageShape ps;
+    if (!a) return fail(HS_ERR_INVALID, "null arguments");
+    int rc = page_check(&a->shape, a->dtype, &ps), sms = 0;
+    if (rc != HS_OK) return rc;
+    if (a->B < 0 || a->S < 0 || a->k < 0) return fail(HS_ERR_INVALID, "B=%d, S=%d and k=%d must not be negative", a->B, a->S, a->k);
+    if (a->q_heads < 1 || a->q_heads % ps.heads != 0)
+        return fail(HS_ERR_INVALID, "q_heads=%d must be a positive multiple of kv_heads=%d", a->q_heads, ps.heads);
+    if (a->q_tokens < 1) return fail(HS_ERR_INVALID, "q_tokens=%d must be >= 1", a->q_tokens);
+    if ((int64_t)a->q_heads * a->q_tokens > (1 << 20)) return fail(HS_ERR_LIMIT, "q_heads * q_tokens exceeds 2^20");
+    if ((int64_t)a->S * ps.tiles() > 1 << 30 || (int64_t)a->k * ps.tiles() > 1 << 30)
+        return fail(HS_ERR_LIMIT, "S=%d or k=%d pages exceed 2^30 tiles of 16 tokens", a->S, a->k);
+    if (!(a->sm_scale > -1e30f && a->sm_scale < 1e30f)) return fail(HS_ERR_INVALID, "sm_scale must be finite, below 1e30");
+    if (!(a->softcap >= 0.f && a->softcap < 1e30f) || (a->softcap > 0.f && a->softcap < 1e-6f))
+        return fail(HS_ERR_INVALID, "softcap must be 0 or in [1e-6, 1e30)");
+    if (a->B > 0 && (!a->q || !a->o || !a->lse || !a->lengths)) return fail(HS_ERR_INVALID, "null q/o/lse/lengths");
+    if (a->B > 0 && a->k > 0 && (!a->slots || !a->selections || (!a->pages && a->S > 0)))
+        return fail(HS_ERR_INVALID, "null pages/slots/selections");
+    if (!aligned16(a->q) || !aligned16(a->o) || !aligned16(a->pages))
+        return fail(HS_ERR_INVALID, "q, o and pages must be 16-byte aligned");
+    if ((a->q_batch_stride | a->q_token_stride | a->q_head_stride | a->o_batch_stride | a->o_token_stride | a->o_head_stride) & 7)
+        return fail(HS_ERR_INVALID, "rows of q and o must be 16-byte aligned");
+    if (a->wait_ns != 0 && (a->wait_ns < hs::kMinWaitNs || a->wait_ns > hs::kMaxWaitNs))
+        return fail(HS_ERR_INVALID, "wait limit %llu ns outside [%llu, %llu]", (unsigned long long)a->wait_ns,
+                    (unsigned long long)hs::kMinWaitNs, (unsigned long long)hs::kMaxWaitNs);
+    if ((rc = sm_count(&sms)) != HS_OK) return rc;
+    hs::PageAttention p;
+    p.q = (const uint16_t*)a->q;
+    p.o = (uint16_t*)a->o;
+    p.lse = a->lse;
+    p.pages = a->pages;
+    p.slots = a->slots;
+    p.sel = a->selections;
+    p.lengths = a->lengths;
+    p.start = a->start;
+    p.prefix = a->start ? a->prefix : nullptr;
+    p.slopes = a->slopes;
+    p.status = a->status;
+    p.q_batch = a->q_batch_stride;
+    p.q_token = a->q_token_stride;
+    p.q_head = a->q_head_stride;
+    p.o_batch = a->o_batch_stride;
+    p.o_token = a->o_token_stride;
+    p.o_head = a->o_head_stride;
+    p.B = a->B;
+    p.S = a->S;
+    p.k = a->k;
+    p.H = ps.heads;
+    p.G = a->q_heads / ps.heads;
+    p.Tq = a->q_tokens;
+    p.tiles = ps.tiles();
+    p.scale = a->sm_scale;
+    p.cap = a->softcap;
+    p.wait_ns = a->wait_ns ? a->wait_ns : hs::kDefaultWaitNs;
+    cudaError_t e = hs::launch_attend_pages((cudaStream_t)stream, ps, a->dtype == HS_BF16, p, sms);
+    if (e != cudaSuccess) return cuda_fail(e, "page attention kernel launch");
+    g_err[0] = 0;
+    return HS_OK;
+}
+
+uint32_t* hs_status_word(hs_ctx* h) { return h ? h->L.status : nullptr; }
 
 uint8_t* hs_host_kv(hs_ctx* h) { return h ? h->host_kv : nullptr; }
 size_t hs_host_stride(hs_ctx* h) { return h ? h->L.host_stride : 0; }

@@ -362,6 +362,127 @@ hs_ctx* hs_create_pooled(int num_requests, int context_len, int slots, int entry
  */
 int hs_set_extents(hs_ctx* ctx, hs_stream_t stream, const int64_t* base, const int32_t* len);
 
+/*
+ * ---------------------------------------------------------------------------------
+ * 4-bit pages. A KV entry may be a page: the K and V of `tokens` consecutive tokens for
+ * all KV heads (Quest-style page selection; a position is then a page number). Stored in
+ * 4 bits, a page crosses the host link and takes a slot at 9/32 of its 16-bit size. The
+ * calls below write tokens into such pages, read pages back, and attend over the pages
+ * that a resolution left in its slots. A context that holds them has entry_bytes =
+ * hs_page_bytes(). All of them are enqueue-only and graph-capturable, allocate nothing and
+ * need no workspace; their device pointers belong to the calling thread's current device.
+ *
+ * Layout: for tile i (tokens 16 i .. 16 i + 15 of the page) and head h, the 18 * head_dim
+ * bytes at (i * kv_heads + h) * 18 * head_dim hold K codes [16][head_dim / 2], K scales
+ * [16][head_dim / 16], V codes and V scales alike. Byte c of a row of codes holds dimension
+ * 2 c in its low half and 2 c + 1 in its high half; a code is a sign bit and an E2M1
+ * magnitude (0, .5, 1, 1.5, 2, 3, 4, 6). A scale byte u belongs to 16 dimensions of one
+ * token and is the half-precision number whose bits are u << 7. Value = code * scale, which
+ * is exact in bf16 and fp16.
+ * Written from a block of 16 values x with a = max |x|: the scale s nearest to a / 6 (ties
+ * to the even byte, at most 10240), codes nearest to x / s (ties to the even code, at most
+ * 6; a value that rounds to zero gets code 0). A block with an infinity or a NaN gets scale
+ * byte 255 and reads back as NaNs; one whose largest magnitude is under 6 * 2^-18 as zeros.
+ */
+typedef struct {
+    int tokens;   /* of a page: a multiple of 16, at most 256 */
+    int kv_heads; /* 1 .. 65535 */
+    int head_dim; /* 64, 128 or 256 */
+} hs_page_shape;
+
+/* 16-bit types of K, V, q and o */
+#define HS_BF16 0
+#define HS_F16 1
+
+/* hs_page_bytes -- bytes of a page, tokens * kv_heads * head_dim * 9 / 8 (0: unsupported shape). */
+size_t hs_page_bytes(const hs_page_shape* shape);
+
+/* K and V of tokens: row (token i, head h) starts i * token_stride + h * head_stride elements
+ * into the tensor; rows are contiguous and 16-byte aligned (strides multiples of 8). */
+typedef struct {
+    const void* k;
+    const void* v;
+    int64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+} hs_token_rows;
+
+/*
+ * hs_write_tokens -- quantises n tokens into pages (device memory, or pinned memory mapped
+ * on the device; 16-byte aligned): token i into token slot dest[i] = page * tokens + offset
+ * (device int64 [n]; negative: the token is padding and is skipped). A slot >= num_pages *
+ * tokens is skipped and sets HS_STATUS_RANGE in *status (device word, or NULL). The slots of
+ * one call are distinct (two tokens sent to one slot leave a mixture). Other tokens' bytes
+ * are not touched. Returns HS_OK, HS_ERR_INVALID or HS_ERR_CUDA.
+ */
+int hs_write_tokens(hs_stream_t stream, const hs_page_shape* shape, int dtype, const hs_token_rows* rows, int64_t n,
+                    const int64_t* dest, uint8_t* pages, int64_t num_pages, uint32_t* status);
+
+/*
+ * hs_append_tokens -- hs_append for tokens of 4-bit pages: token i joins request
+ * requests[i] (device int32 [n]; NULL: request i, and n must be num_requests) at token
+ * position positions[i] (device int32 [n]; negative: skipped), which is offset position %
+ * tokens of page position / tokens. It is written into the host store and, when the page is
+ * resident, into its slot as well, so the cache stays exact; the replacement state does not
+ * change. A page >= context_len (or the request's extent), or a request >= num_requests, is
+ * skipped and sets HS_STATUS_RANGE. Distinct (request, position) pairs only. Stream ordered
+ * with the context's other calls.
+ */
+int hs_append_tokens(hs_ctx* ctx, hs_stream_t stream, const hs_page_shape* shape, int dtype, const hs_token_rows* rows,
+                     int64_t n, const int32_t* requests, const int32_t* positions);
+
+/*
+ * hs_read_pages -- decodes pages: for each request b < B and j < n the page in slot
+ * slots[b][j] (device int32 [B][n]) of pages [B][S] (16-byte aligned, e.g. hs_device_kv())
+ * becomes tokens j * tokens .. of k[b] and v[b] (device [B][n * tokens][kv_heads][head_dim],
+ * contiguous, 16-byte aligned, overwritten). A negative slot reads as zeros, one >= S too,
+ * setting HS_STATUS_RANGE in *status (or NULL).
+ */
+int hs_read_pages(hs_stream_t stream, const hs_page_shape* shape, int dtype, const uint8_t* pages, int B, int S,
+                  const int32_t* slots, int n, void* k, void* v, uint32_t* status);
+
+/*
+ * hs_attend_pages -- decode attention of every request over the pages its selections
+ * resolved to. Each KV head serves q_heads / kv_heads query heads. With p_j the token
+ * position of key j, qpos = lengths[b] - q_tokens + t that of query token t and, for head h,
+ *   s_j = sm_scale <q, K_j>;  c_j = softcap * tanh(s_j / softcap) (softcap > 0, else s_j);
+ *   x_j = c_j - slopes[h] * (qpos - p_j);
+ *   o = sum_j softmax_j(x) V_j,  lse = ln sum_j exp(x_j)
+ * over the keys of pages with slots[b][j] >= 0 and selections[b][j] >= 0 that have p_j <=
+ * qpos and, where a document mask is given, p_j >= start[b] or p_j < prefix[b]. A query that
+ * sees no key gets o = 0 and lse = -inf. Keys that no query sees are not read into the
+ * result, whatever their bytes hold; a page selected twice counts twice.
+ * Rows of q and o are contiguous and 16-byte aligned: (b, t, head) starts b * batch_stride +
+ * t * token_stride + head * head_stride elements in. The products run on the tensor cores
+ * with f32 sums; the queries enter them as halves (bf16 ones scaled by a power of two per
+ * row) and the softmax weights are rounded to half for the product with V.
+ */
+typedef struct {
+    hs_page_shape shape;
+    int dtype;               /* of q and o: HS_BF16 or HS_F16 */
+    int B, S, k;             /* requests; slots and selections of each (k may be 0) */
+    int q_heads;             /* a multiple of shape.kv_heads */
+    int q_tokens;            /* query tokens of each request, the last of its sequence (>= 1) */
+    const void* q;
+    int64_t q_batch_stride, q_token_stride, q_head_stride;
+    void* o;
+    int64_t o_batch_stride, o_token_stride, o_head_stride;
+    float* lse;              /* device [B][q_tokens][q_heads], overwritten */
+    const uint8_t* pages;    /* device [B][S] pages, 16-byte aligned (hs_device_kv()) */
+    const int32_t* slots;    /* device [B][k], as written by hs_resolve */
+    const int32_t* selections; /* device [B][k], the page numbers resolved */
+    const int32_t* lengths;  /* device [B]: tokens of the sequence, the query tokens among them */
+    float sm_scale, softcap; /* finite; softcap >= 0 (0: none) */
+    const float* slopes;     /* device [q_heads], or NULL */
+    const int32_t* start;    /* device [B], or NULL (no document mask; prefix is then ignored) */
+    const int32_t* prefix;   /* device [B], or NULL (0) */
+    uint32_t* status;        /* device word: HS_STATUS_RANGE (a slot >= S; its page is left out) and
+                                HS_STATUS_TIMEOUT are set in it; or NULL */
+    uint64_t wait_ns;        /* limit of the device waits (hs_set_wait_limit), 0: its default */
+} hs_page_attention;
+int hs_attend_pages(hs_stream_t stream, const hs_page_attention* args);
+
+/* hs_status_word -- the context's device status word, for the calls above. */
+uint32_t* hs_status_word(hs_ctx* ctx);
+
 /* Number of kernels one hs_resolve call enqueues under the current flags. */
 int hs_kernels_per_call(hs_ctx* ctx);
 
