@@ -45,6 +45,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "hs_page.h"
@@ -52,8 +53,9 @@
 namespace hs {
 namespace {
 
-constexpr int kWarps = 8, kThreads = kWarps * 32;
-constexpr int kListTiles = 1024;       // tiles listed at a time
+constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr int kMaxSplit = 8;           // CTAs that share a selection: the portable cluster size
+constexpr int kList = 64;              // a warp's list of live tiles (a ring; 32 are added at a time)
 constexpr float kRescale = 8.f;        // a row's reference maximum moves when exceeded by 2^8
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 
@@ -62,8 +64,8 @@ struct Config {
     static constexpr int kChunk = 18 * D;           // bytes of a tile of one head
     static constexpr int kRows = 8 * NT;            // query rows of a CTA
     static constexpr int kSteps = D / 16;
-    static constexpr int kCtas = NT * D <= 128 ? 2 : 1;  // CTAs an SM: registers
-    static constexpr int kStages = D == 64 ? 6 : D == 128 ? 4 : 4;
+    static constexpr int kCtas = NT * D <= 128 ? 4 : NT * D <= 256 ? 3 : 2;  // CTAs an SM: registers
+    static constexpr int kStages = D == 64 ? 6 : D == 128 ? 4 : 3;
     static constexpr int kRing = kWarps * kStages * kChunk;
     static constexpr int kPart = kWarps * kRows * D * 4;  // the warps' outputs, over the ring
     static constexpr int kSpace = kRing > kPart ? kRing : kPart;
@@ -73,16 +75,18 @@ template <int D, int NT>
 struct Smem {
     using C = Config<D, NT>;
     alignas(128) uint8_t space[C::kSpace];
-    alignas(16) uint16_t q[C::kRows][D + 8];  // the rows as halves, scaled
-    float joined[C::kRows][D];                // this CTA's output, relative to its maxima
+    uint2 qf[NT][C::kSteps][32];              // Q as the lanes take it
+    alignas(16) float joined[C::kRows][D];    // this CTA's output, relative to its maxima
+    float qscale[C::kRows], slope[C::kRows];  // of the rows: to log2 units
+    int qpos[C::kRows];
     float m[kWarps][C::kRows], l[kWarps][C::kRows];
+    float f[kMaxSplit][C::kRows];             // factors of the warps, then of the shares
     float cm[C::kRows], cl[C::kRows];         // this CTA's maxima and sums
-    float qscale[C::kRows];
+    float pm[kMaxSplit][C::kRows], pl[kMaxSplit][C::kRows];  // every share's
+    float inv[C::kRows];
+    int wref[kWarps], cref;                   // positions that biases are relative to
     uint64_t bar[kWarps][C::kStages];
-    int2 list[kListTiles];                    // unit (slot * tiles + tile), position | partial
-    int count[kListTiles / 32];
-    int kref[kWarps];
-    int ref;                                  // position that biases are relative to
+    int2 list[kWarps][kList];                 // unit (slot * tiles + tile), position | partial
 };
 
 __device__ __forceinline__ uint32_t su32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -110,7 +114,7 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-__device__ __forceinline__ uint32_t scale2(uint32_t u) { return u << 7 | u << 23; }  // (s, s) of scale byte u
+__device__ __forceinline__ uint32_t scale2(uint32_t u) { return u * 0x00800080u; }  // (s, s) of scale byte u
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) { return __byte_perm(a, b, s); }
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -178,38 +182,91 @@ __global__ void __launch_bounds__(kThreads, (Config<D, NT>::kCtas)) attend_pages
     Smem<D, NT>& sm = *reinterpret_cast<Smem<D, NT>*>(raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const uint64_t deadline = global_ns() + A.wait_ns;
-    int64_t job = blockIdx.x / nsplit;
-    const int split = (int)(blockIdx.x - job * nsplit);  // = the rank in the cluster
-    const int rt = (int)(job % row_tiles);
+    int job = blockIdx.x / nsplit;
+    const int split = blockIdx.x - job * nsplit;  // = the rank in the cluster
+    const int rt = job % row_tiles;
     job /= row_tiles;
-    const int h = (int)(job % A.H), b = (int)(job / A.H);
+    const int b = job / A.H, h = job - b * A.H;
     const int rows = A.G * A.Tq, r0 = rt * C::kRows;
 
-    if (tid < kWarps * C::kStages) {
-        asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(su32(&sm.bar[0][0] + tid)) : "memory");
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
-
-    // the request's mask: row token t sees p <= length - Tq + t and (p >= start or p < prefix)
+    // ---------------- this warp's tiles: every (nsplit * kWarps)-th of the selection. Lane i
+    // looks up the i-th of the next 32; those that hold a visible key go on the warp's list.
+    const int32_t* slots = A.slots + (size_t)b * A.k;
+    const int32_t* sel = A.sel + (size_t)b * A.k;
+    const int ntiles = A.k * A.tiles, stride = nsplit * kWarps;
+    int next = lane * stride + split * kWarps + warp;  // this lane's tile of the next group
+    int gslot = -1, gsel = -1;                          // its page, loaded a group ahead
+    auto look_up = [&]() {
+        gslot = -1;
+        if (next < ntiles) {
+            const int j = next / A.tiles;
+            gslot = __ldg(slots + j);
+            gsel = __ldg(sel + j);
+        }
+    };
+    look_up();
+    // the request's mask: query token t sees p <= length - Tq + t and (p >= start or p < prefix)
     const int length = __ldg(A.lengths + b);
     const int start = A.start ? __ldg(A.start + b) : 0;
     const int prefix = A.prefix ? __ldg(A.prefix + b) : 0;
     const int qpos0 = length - A.Tq;  // may be negative
-    const int j0 = (int)((int64_t)A.k * split / nsplit), j1 = (int)((int64_t)A.k * (split + 1) / nsplit);
-    const int32_t* slots = A.slots + (size_t)b * A.k;
-    const int32_t* sel = A.sel + (size_t)b * A.k;
-    const int ntiles = (j1 - j0) * A.tiles;  // of this CTA's share
     const uint8_t* pages = A.pages + ((size_t)b * A.S * A.tiles * A.H + h) * C::kChunk;
     const size_t unit_bytes = (size_t)A.H * C::kChunk;
 
-    // the query rows as halves
+    uint8_t* ring = sm.space + warp * (C::kStages * C::kChunk);
+    uint64_t* bar = sm.bar[warp];
+    int2* list = sm.list[warp];
+    if (lane < C::kStages) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(su32(bar + lane)) : "memory");
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    __syncwarp();
+
+    int groups = (ntiles + 32 * stride - 1) / (32 * stride);  // not yet on the list
+    uint32_t used = 0, fill = 0, tail = 0;  // listed tiles consumed, copied (or on their way), listed
+    auto append = [&]() {
+        bool live = false;
+        int2 e;
+        if (gslot >= A.S && A.status) atomicOr(A.status, 1u /* HS_STATUS_RANGE */);
+        if (gslot >= 0 && gslot < A.S && gsel >= 0) {
+            const int tile = next % A.tiles;
+            const int64_t at = (int64_t)gsel * (A.tiles * kTile) + tile * kTile;
+            if (at < length) {
+                const int pos = (int)at, end = pos + (kTile - 1);
+                const bool full = end <= qpos0 && (!A.start || pos >= start || end < prefix);
+                live = !A.start || end >= start || pos < prefix;
+                e = make_int2(gslot * A.tiles + tile, pos | (full ? 0 : 1));
+            }
+        }
+        const uint32_t which = __ballot_sync(0xffffffffu, live);
+        if (live) list[(tail + __popc(which & ((1u << lane) - 1u))) % kList] = e;
+        tail += __popc(which);
+        --groups;
+        next = ntiles - next > 32 * stride ? next + 32 * stride : ntiles;
+        look_up();
+        __syncwarp();
+    };
+    auto top_up = [&]() {  // keep every stage on its way
+        while (fill - used < C::kStages) {
+            if (fill == tail) {
+                if (groups == 0) break;
+                append();
+                continue;
+            }
+            if (lane == 0) {
+                const int st = fill % C::kStages;
+                copy_in(ring + st * C::kChunk, pages + (size_t)list[fill % kList].x * unit_bytes, C::kChunk, &bar[st]);
+            }
+            ++fill;
+        }
+    };
+    top_up();
+
+    // ---------------- the query rows as halves, in the lanes' order
     for (int r = warp; r < C::kRows; r += kWarps) {
         constexpr int N = D / 32;
-        float x[N];
         const int row = r0 + r;
-        float scale = 0.f;
+        float x[N], scale = 0.f;
         if (row < rows) {
-            const int tok = row / A.G, head = h * A.G + row % A.G;
+            const int tok = row / A.G, head = h * A.G + row - tok * A.G;
             const uint16_t* src = A.q + b * A.q_batch + tok * A.q_token + head * A.q_head + lane * N;
             uint32_t w[N / 2];
             if constexpr (N == 2) {
@@ -240,60 +297,41 @@ __global__ void __launch_bounds__(kThreads, (Config<D, NT>::kCtas)) attend_pages
                     for (int i = 0; i < N; ++i) x[i] *= inv;
                 }
             }
+            if (lane == 0) {
+                // to log2 units; with a cap, to 2 log2 e s / cap
+                sm.qscale[r] = MOD && A.cap > 0.f ? scale * (A.scale * (2.f * kLog2e / A.cap)) : scale * (A.scale * kLog2e);
+                sm.slope[r] = MOD && A.slopes ? __ldg(A.slopes + head) * kLog2e : 0.f;
+                sm.qpos[r] = qpos0 + tok;
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < N; ++i) x[i] = 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < N; ++i) sm.q[r][lane * N + i] = __half_as_ushort(__float2half_rn(x[i]));
-        // to log2 units; with a cap, to 2 log2 e s / cap
-        if (lane == 0) sm.qscale[r] = MOD && A.cap > 0.f ? scale * (A.scale * (2.f * kLog2e / A.cap)) : scale * (A.scale * kLog2e);
-    }
-    // biases are taken relative to the last position of the share, so that far shares keep
-    // their differences (the whole bias of a far key has few fraction bits left in f32)
-    if (MOD) {
-        int last = -1;
-        for (int j = j0 + tid; j < j1; j += kThreads) {
-            const int s = __ldg(slots + j), p = __ldg(sel + j);
-            if (s >= 0 && s < A.S && p >= 0) {
-                const int64_t e = ((int64_t)p + 1) * (A.tiles * kTile) - 1;
-                if (e - (A.tiles * kTile - 1) < length) last = max(last, (int)min(e, (int64_t)length - 1));
+            if (lane == 0) {
+                sm.qscale[r] = sm.slope[r] = 0.f;
+                sm.qpos[r] = qpos0;
             }
         }
-        last = __reduce_max_sync(0xffffffffu, last);
-        if (lane == 0) sm.kref[warp] = last;
+        // dimension d is taken by lane t = d / (D/4) of row r's group at step d % (D/4) / 4
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            const int d = lane * N + i, dt = d / (D / 4), step = d % (D / 4) / 4;
+            reinterpret_cast<uint32_t*>(&sm.qf[r / 8][step][(r % 8) * 4 + dt])[d % 4 / 2] = pack_half(x[i], x[i + 1]);
+        }
     }
     __syncthreads();
-    int ref = 0;
-    if (MOD) {
-        ref = sm.kref[0];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) ref = max(ref, sm.kref[w]);
-    }
 
-    // this lane's part of Q, and its rows' factors (rows 8 n + 2 t, + 1)
-    uint32_t qf[NT][C::kSteps][2];
-    float qs[NT][2], slope[NT][2];
-    int qpos[NT][2];
+    constexpr bool kKeepQ = NT == 1 && D <= 128;  // Q in registers
+    uint2 qreg[kKeepQ ? C::kSteps : 1];
+    if (kKeepQ) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-#pragma unroll
-        for (int i = 0; i < C::kSteps; ++i) {
-            const uint2 w = *reinterpret_cast<const uint2*>(&sm.q[8 * n + g][t * (D / 4) + 4 * i]);
-            qf[n][i][0] = w.x;
-            qf[n][i][1] = w.y;
-        }
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            const int row = min(r0 + 8 * n + 2 * t + c, rows - 1);
-            qs[n][c] = sm.qscale[8 * n + 2 * t + c];
-            qpos[n][c] = qpos0 + row / A.G;
-            slope[n][c] = MOD && A.slopes ? __ldg(A.slopes + h * A.G + row % A.G) * kLog2e : 0.f;
-        }
+        for (int i = 0; i < C::kSteps; ++i) qreg[kKeepQ ? i : 0] = sm.qf[0][i][lane];
     }
+    float2 qs[NT];  // rows 8 n + 2 t, + 1
+#pragma unroll
+    for (int n = 0; n < NT; ++n) qs[n] = *reinterpret_cast<const float2*>(&sm.qscale[8 * n + 2 * t]);
     const float cap2 = A.cap * kLog2e;
 
-    float acc[C::kSteps][NT][4];  // O^T: dims g D/8 + 2 i, + 1 (c = 0, 1 and 2, 3), rows 8 n + 2 t, + 1
+    float acc[C::kSteps][NT][4];  // O^T: dims g D/8 + 2 i (c = 0, 1), + 1 (2, 3); rows 8 n + 2 t, + 1
     float m[NT][2], l[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -304,110 +342,68 @@ __global__ void __launch_bounds__(kThreads, (Config<D, NT>::kCtas)) attend_pages
 #pragma unroll
             for (int c = 0; c < 4; ++c) acc[i][n][c] = 0.f;
     }
-
-    uint8_t* ring = sm.space + warp * (C::kStages * C::kChunk);
-    uint64_t* bar = sm.bar[warp];
-    uint32_t fill = 0, use = 0;  // copies issued and waited for by this warp
+    int ref = 0;  // biases are relative to this position: the last of the tiles so far
+    // The order of a tile's keys along the instruction: place r holds token order(r). A lane's
+    // four tokens of V (places 2t, 2t + 1, + 8) then lie in both halves of the 128 bytes that
+    // the shared memory banks cover, and its keys still do.
+    auto order = [](int r) { return r ^ (r >> 1 & 1); };
     bool ok = true;
 
-    for (int base = 0; base < ntiles; base += kListTiles) {
-        // the share's next live tiles, in order
-        const int here = min(kListTiles, ntiles - base);
-        int2 mine[kListTiles / kThreads];
-        uint32_t live[kListTiles / kThreads];
+    // ---------------- two tiles at a time: their chains of products are independent
+#pragma unroll 1
+    while (used != fill) {
+        const bool two = fill - used >= 2;
+        const uint8_t* tile[2];
+        int pos[2];
+        bool partial = !two;
 #pragma unroll
-        for (int i = 0; i < kListTiles / kThreads; ++i) {
-            const int x = i * kThreads + tid;
-            bool is = false;
-            if (x < here) {
-                const int j = (base + x) / A.tiles, tile = base + x - j * A.tiles;
-                const int s = __ldg(slots + j0 + j), p = __ldg(sel + j0 + j);
-                const int64_t at = (int64_t)p * (A.tiles * kTile) + tile * kTile;
-                if (s >= A.S && A.status) atomicOr(A.status, 1u /* HS_STATUS_RANGE */);
-                if (s >= 0 && s < A.S && p >= 0 && at < length) {
-                    const int pos = (int)at, end = pos + (kTile - 1);
-                    const bool in = !A.start || end >= start || pos < prefix;
-                    const bool full = end <= qpos0 && (!A.start || pos >= start || end < prefix);
-                    is = in;
-                    mine[i] = make_int2(s * A.tiles + tile, pos | (full ? 0 : 1));
-                }
-            }
-            live[i] = __ballot_sync(0xffffffffu, is);
-            if (lane == 0) sm.count[i * kWarps + warp] = __popc(live[i]);
+        for (int u = 0; u < 2; ++u) {
+            const uint32_t at = used + (two ? u : 0), st = at % C::kStages;
+            tile[u] = ring + st * C::kChunk;
+            const int word = list[at % kList].y;
+            pos[u] = word & ~15;
+            partial |= word & 1;
+            if (!__all_sync(0xffffffffu, bar_wait(&bar[st], (at / C::kStages) & 1u, deadline))) ok = false;
         }
-        __syncthreads();
-        int total;
+        if (!ok) break;
+
+        // ---------------- S^T = K Q^T
+        float s[2][NT][4];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) s[u][n][0] = s[u][n][1] = s[u][n][2] = s[u][n][3] = 0.f;
         {
-            const int c = sm.count[lane];  // 32 counts, in the tiles' order
-            int sum = c;
+            constexpr int W = D / 32;  // words of codes: D/8 bytes of the keys in places g and g + 8
+            uint32_t kw[2][2][W], ku[2][2];
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, sum, o);
-                if (lane >= o) sum += v;
-            }
-            total = __shfl_sync(0xffffffffu, sum, 31);
-#pragma unroll
-            for (int i = 0; i < kListTiles / kThreads; ++i) {
-                const int before = __shfl_sync(0xffffffffu, sum - c, i * kWarps + warp);
-                if (live[i] >> lane & 1u) sm.list[before + __popc(live[i] & ((1u << lane) - 1u))] = mine[i];
-            }
-        }
-        __syncthreads();
-
-        auto issue = [&](int x) {  // the copy of listed tile x
-            if (lane == 0) {
-                const int st = fill % C::kStages;
-                copy_in(ring + st * C::kChunk, pages + (size_t)sm.list[x].x * unit_bytes, C::kChunk, &bar[st]);
-            }
-            ++fill;
-        };
-        // after a wait that ran out the warp takes part in the barriers only
-#pragma unroll 1
-        for (int i = 0; i < C::kStages; ++i)
-            if (ok && warp + i * kWarps < total) issue(warp + i * kWarps);
-#pragma unroll 1
-        for (int x = warp; ok && x < total; x += kWarps) {
-            const int st = use % C::kStages;
-            const uint8_t* tile = ring + st * C::kChunk;
-            if (!__all_sync(0xffffffffu, bar_wait(&bar[st], (use / C::kStages) & 1u, deadline))) {
-                ok = false;
-                break;
-            }
-            ++use;
-            const int word = sm.list[x].y;
-            const int pos = word & ~15;
-            const bool partial = word & 1;
-
-            // ---------------- S^T = K Q^T
-            float s[NT][4];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-            {
-                uint32_t kw[2][D / 32];  // D/8 bytes of keys g and g + 8
-                uint32_t ku[2];          // their D/64 scale bytes
+            for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const uint8_t* src = tile + (g + 8 * c) * (D / 2) + t * (D / 8);
-                    const uint8_t* us = tile + 8 * D + (g + 8 * c) * (D / 16) + t * (D / 64);
-                    if (D == 64) {
+                    const int tok = order(g) + 8 * c;
+                    const uint8_t* src = tile[u] + tok * (D / 2) + t * (D / 8);
+                    const uint8_t* us = tile[u] + 8 * D + tok * (D / 16) + t * (D / 64);
+                    if constexpr (D == 64) {
                         const uint2 v = *reinterpret_cast<const uint2*>(src);
-                        kw[c][0] = v.x; kw[c][1] = v.y;
-                        ku[c] = *us;
+                        kw[u][c][0] = v.x; kw[u][c][1] = v.y;
+                        ku[u][c] = *us;
                     } else {
 #pragma unroll
                         for (int i = 0; i < D / 128; ++i) {
                             const uint4 v = reinterpret_cast<const uint4*>(src)[i];
-                            kw[c][4 * i] = v.x; kw[c][4 * i + 1] = v.y; kw[c][4 * i + 2] = v.z; kw[c][4 * i + 3] = v.w;
+                            kw[u][c][4 * i] = v.x; kw[u][c][4 * i + 1] = v.y; kw[u][c][4 * i + 2] = v.z; kw[u][c][4 * i + 3] = v.w;
                         }
-                        ku[c] = D == 128 ? *reinterpret_cast<const uint16_t*>(us) : *reinterpret_cast<const uint32_t*>(us);
+                        ku[u][c] = D == 128 ? *reinterpret_cast<const uint16_t*>(us) : *reinterpret_cast<const uint32_t*>(us);
                     }
                 }
 #pragma unroll
-                for (int w = 0; w < D / 32; ++w) {  // a word: 8 dims, two steps
-                    const uint32_t sc0 = scale2(ku[0] >> (8 * (w / 2)) & 0xFFu), sc1 = scale2(ku[1] >> (8 * (w / 2)) & 0xFFu);
+            for (int w = 0; w < W; ++w) {  // a word: 8 dims, two steps
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const uint32_t sc0 = scale2(ku[u][0] >> (8 * (w / 2)) & 0xFFu), sc1 = scale2(ku[u][1] >> (8 * (w / 2)) & 0xFFu);
                     uint32_t a[4], c[4];
-                    decode_word(kw[0][w], a);
-                    decode_word(kw[1][w], c);
+                    decode_word(kw[u][0][w], a);
+                    decode_word(kw[u][1][w], c);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         a[i] = mul2(a[i], sc0);
@@ -415,158 +411,190 @@ __global__ void __launch_bounds__(kThreads, (Config<D, NT>::kCtas)) attend_pages
                     }
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        mma(s[n], a[0], c[0], a[1], c[1], qf[n][2 * w][0], qf[n][2 * w][1]);
-                        mma(s[n], a[2], c[2], a[3], c[3], qf[n][2 * w + 1][0], qf[n][2 * w + 1][1]);
+                        const uint2 q0 = kKeepQ ? qreg[kKeepQ ? 2 * w : 0] : sm.qf[n][2 * w][lane];
+                        const uint2 q1 = kKeepQ ? qreg[kKeepQ ? 2 * w + 1 : 0] : sm.qf[n][2 * w + 1][lane];
+                        mma(s[u][n], a[0], c[0], a[1], c[1], q0.x, q0.y);
+                        mma(s[u][n], a[2], c[2], a[3], c[3], q1.x, q1.y);
                     }
                 }
             }
+        }
 
-            // ---------------- scores in log2 units, masked; s[n][c + 2 k]: row c, key g + 8 k
+        // ---------------- scores in log2 units, masked; s[u][n][c + 2 k]: row c, place g + 8 k
+        if (MOD) {
+            const int last = max(pos[0], pos[1]) + (kTile - 1), moved = last - ref;
+            if (A.slopes && moved > 0) {  // move the origin of the biases
+                ref = last;
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    float y = s[n][c] * qs[n][c & 1];
-                    if (MOD) {
+                    for (int c = 0; c < 2; ++c) m[n][c] -= sm.slope[8 * n + 2 * t + c] * (float)moved;
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const float2 sl = *reinterpret_cast<const float2*>(&sm.slope[8 * n + 2 * t]);
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        float y = s[u][n][c] * (c & 1 ? qs[n].y : qs[n].x);
                         if (A.cap > 0.f) y = cap2 * tanh_of(y);
-                        y -= slope[n][c & 1] * (float)(ref - (pos + g + 8 * (c >> 1)));
+                        s[u][n][c] = y - (c & 1 ? sl.y : sl.x) * (float)(ref - (pos[u] + order(g) + 8 * (c >> 1)));
                     }
-                    s[n][c] = y;
-                }
-            bool more = false;
-            if (partial) {
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) s[u][n][c] *= c & 1 ? qs[n].y : qs[n].x;
+        }
+        if (partial) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const int p = pos + g + 8 * k;
-                    const bool in = !A.start || p >= start || p < prefix;
+                    const int p = pos[u] + order(g) + 8 * k;
+                    const bool in = (u == 0 || two) && (!A.start || p >= start || p < prefix);
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int c = 0; c < 2; ++c)
-                            if (!in || p > qpos[n][c]) s[n][c + 2 * k] = -INFINITY;
+                            if (!in || p > sm.qpos[8 * n + 2 * t + c]) s[u][n][c + 2 * k] = -INFINITY;
                 }
-            }
+        }
+        bool more = false;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+                more |= !(fmaxf(fmaxf(s[0][n][c], s[0][n][c + 2]), fmaxf(s[1][n][c], s[1][n][c + 2])) <= m[n][c] + kRescale);
+        if (__any_sync(0xffffffffu, more)) {  // a row's maximum has grown: move every row's reference
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) more |= !(s[n][c] <= m[n][c & 1] + kRescale);
-            if (__any_sync(0xffffffffu, more)) {  // a row's maximum has grown: move every row's reference
+                for (int c = 0; c < 2; ++c) {
+                    float top = m[n][c];
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                    for (int u = 0; u < 2; ++u)
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        // a NaN score counts as +inf here, so that the join keeps the row's NaNs
-                        float top = fmaxf(s[n][c] == s[n][c] ? s[n][c] : INFINITY, s[n][c + 2] == s[n][c + 2] ? s[n][c + 2] : INFINITY);
-#pragma unroll
-                        for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                        const float now = fmaxf(m[n][c], top);
-                        const float f = now > -INFINITY ? ex2(m[n][c] - now) : 1.f;
-                        m[n][c] = now;
-                        l[n][c] *= f;
-#pragma unroll
-                        for (int i = 0; i < C::kSteps; ++i) {
-                            acc[i][n][c] *= f;
-                            acc[i][n][c + 2] *= f;
+                        for (int k = 0; k < 2; ++k) {  // a NaN counts as +inf, so that the joins keep the row
+                            const float y = s[u][n][c + 2 * k];
+                            top = fmaxf(top, y == y ? y : INFINITY);
                         }
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    const float f = top > -INFINITY ? ex2(m[n][c] - top) : 1.f;
+                    m[n][c] = top;
+                    l[n][c] *= f;
+#pragma unroll
+                    for (int i = 0; i < C::kSteps; ++i) {
+                        acc[i][n][c] *= f;
+                        acc[i][n][c + 2] *= f;
                     }
-            }
-            uint32_t pf[NT][2];
+                }
+        }
+        uint32_t pf[2][NT][2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
+                float w[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    // a row without a key yet has s = m = -inf
-                    const float w = partial && s[n][c] == -INFINITY ? 0.f : ex2(s[n][c] - m[n][c & 1]);
-                    l[n][c & 1] += w;
-                    s[n][c] = w;
+                    w[c] = ex2(s[u][n][c] - m[n][c & 1]);
+                    if (partial && s[u][n][c] == -INFINITY) w[c] = 0.f;  // m is -inf too in a row without a key yet
                 }
-                pf[n][0] = transpose8x8(pack_half(s[n][0], s[n][1]));
-                pf[n][1] = transpose8x8(pack_half(s[n][2], s[n][3]));
+                l[n][0] += w[0] + w[2];
+                l[n][1] += w[1] + w[3];
+                pf[u][n][0] = transpose8x8(pack_half(w[0], w[1]));
+                pf[u][n][1] = transpose8x8(pack_half(w[2], w[3]));
             }
 
-            // ---------------- O^T += V^T P
-            {
-                constexpr int W = D / 64;  // words of codes a token: D/8 dims
-                uint32_t vw[4][W], vs[4];  // tokens 2t, 2t + 1, 2t + 8, 2t + 9
+        // ---------------- O^T += V^T P
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int tok = 2 * t + (c & 1) + 8 * (c >> 1);
-                    const uint8_t* src = tile + 9 * D + tok * (D / 2) + g * (D / 16);
-                    const uint8_t* us = tile + 17 * D + tok * (D / 16);
-                    if (D == 64) {
-                        vw[c][0] = *reinterpret_cast<const uint32_t*>(src);
-                        vs[c] = us[g >> 1];
-                    } else if (D == 128) {
-                        const uint2 v = *reinterpret_cast<const uint2*>(src);
-                        vw[c][0] = v.x; vw[c][W - 1] = v.y;
-                        vs[c] = us[g];
-                    } else {
-                        const uint4 v = *reinterpret_cast<const uint4*>(src);
-                        vw[c][0] = v.x; vw[c][1] = v.y; vw[c][W - 2] = v.z; vw[c][W - 1] = v.w;
-                        vs[c] = *reinterpret_cast<const uint16_t*>(us + 2 * g);
-                    }
-                }
-                if (partial) {
-                    // a key that no row sees may hold anything: its values become zeros, since a
-                    // weight of 0 would not undo a NaN. One that only later rows see has been
-                    // written, but its NaNs must not reach the rows before it: they are taken
-                    // out of the product and set in the outputs of the rows that see them.
-                    uint32_t nans = 0;  // bit 16 (half of the dims) + token
+        for (int u = 0; u < 2; ++u) {
+            if (u == 1 && !two) break;
+            constexpr int W = D / 64;  // words of codes of a token: D/8 dims
+            uint32_t vw[4][W], vs[4];  // of the tokens in places 2t, 2t + 1, 2t + 8, 2t + 9
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const int tok = 2 * t + (c & 1) + 8 * (c >> 1), p = pos + tok;
-                        if (p >= length || (A.start && p < start && p >= prefix)) vs[c] = 0;
-                        if ((vs[c] & 0xFFu) >= 0xF8u) { vs[c] &= 0xFF00u; nans |= 1u << tok; }
-                        if (D == 256 && vs[c] >= 0xF800u) { vs[c] &= 0xFFu; nans |= 0x10000u << tok; }
-                    }
-                    if (__any_sync(0xffffffffu, nans != 0)) {
-                        nans |= __shfl_xor_sync(0xffffffffu, nans, 1);
-                        nans |= __shfl_xor_sync(0xffffffffu, nans, 2);
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int c = 0; c < 2; ++c) {
-                                const int seen = qpos[n][c] - pos;  // the row sees tokens 0 .. seen of the tile
-                                const uint32_t see = seen < 0 ? 0u : seen >= 15 ? 0xFFFFu : (2u << seen) - 1u;
-#pragma unroll
-                                for (int i = 0; i < C::kSteps; ++i)
-                                    if ((D == 256 && i >= C::kSteps / 2 ? nans >> 16 : nans) & see) acc[i][n][c] = acc[i][n][c + 2] = NAN;
-                            }
-                    }
-                }
-#pragma unroll
-                for (int w = 0; w < W; ++w) {
-                    uint32_t d[4][4];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        decode_word(vw[c][w], d[c]);
-                        const uint32_t sc = scale2(D == 256 ? vs[c] >> (8 * (w / 2)) & 0xFFu : vs[c]);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) d[c][i] = mul2(d[c][i], sc);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t a0 = prmt(d[0][i], d[1][i], 0x5410), a1 = prmt(d[0][i], d[1][i], 0x7632);
-                        const uint32_t a2 = prmt(d[2][i], d[3][i], 0x5410), a3 = prmt(d[2][i], d[3][i], 0x7632);
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) mma(acc[4 * w + i][n], a0, a1, a2, a3, pf[n][0], pf[n][1]);
-                    }
+            for (int c = 0; c < 4; ++c) {
+                const int tok = order(2 * t + (c & 1)) + 8 * (c >> 1);
+                const uint8_t* src = tile[u] + 9 * D + tok * (D / 2) + g * (D / 16);
+                const uint8_t* us = tile[u] + 17 * D + tok * (D / 16);
+                if constexpr (D == 64) {
+                    vw[c][0] = *reinterpret_cast<const uint32_t*>(src);
+                    vs[c] = us[g >> 1];
+                } else if constexpr (D == 128) {
+                    const uint2 v = *reinterpret_cast<const uint2*>(src);
+                    vw[c][0] = v.x; vw[c][1] = v.y;
+                    vs[c] = us[g];
+                } else {
+                    const uint4 v = *reinterpret_cast<const uint4*>(src);
+                    vw[c][0] = v.x; vw[c][1] = v.y; vw[c][2] = v.z; vw[c][3] = v.w;
+                    vs[c] = *reinterpret_cast<const uint16_t*>(us + 2 * g);
                 }
             }
-            __syncwarp();  // every lane has read the stage: refill it
-            if (x + C::kStages * kWarps < total) issue(x + C::kStages * kWarps);
+            if (partial) {
+                // a key that no row sees may hold anything: its values become zeros, since a
+                // weight of 0 would not undo a NaN. One that only later rows see has been
+                // written, but its NaNs must not reach the rows before it: they are taken
+                // out of the product and set in the outputs of the rows that see them.
+                uint32_t nans = 0;  // bit 16 (half of the dims) + token
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int tok = order(2 * t + (c & 1)) + 8 * (c >> 1), p = pos[u] + tok;
+                    if (p >= length || (A.start && p < start && p >= prefix)) vs[c] = 0;
+                    if ((vs[c] & 0xFFu) >= 0xF8u) { vs[c] &= 0xFF00u; nans |= 1u << tok; }
+                    if (D == 256 && vs[c] >= 0xF800u) { vs[c] &= 0xFFu; nans |= 0x10000u << tok; }
+                }
+                if (__any_sync(0xffffffffu, nans != 0)) {
+                    nans |= __shfl_xor_sync(0xffffffffu, nans, 1);
+                    nans |= __shfl_xor_sync(0xffffffffu, nans, 2);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const int seen = sm.qpos[8 * n + 2 * t + c] - pos[u];  // the row sees tokens 0 .. seen of the tile
+                            const uint32_t see = seen < 0 ? 0u : seen >= 15 ? 0xFFFFu : (2u << seen) - 1u;
+#pragma unroll
+                            for (int i = 0; i < C::kSteps; ++i)
+                                if ((D == 256 && i >= C::kSteps / 2 ? nans >> 16 : nans) & see) acc[i][n][c] = acc[i][n][c + 2] = NAN;
+                        }
+                }
+            }
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                uint32_t d[4][4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    decode_word(vw[c][w], d[c]);
+                    const uint32_t sc = scale2(D == 256 ? vs[c] >> (8 * (w / 2)) & 0xFFu : vs[c]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) d[c][i] = mul2(d[c][i], sc);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t a0 = prmt(d[0][i], d[1][i], 0x5410), a1 = prmt(d[0][i], d[1][i], 0x7632);
+                    const uint32_t a2 = prmt(d[2][i], d[3][i], 0x5410), a3 = prmt(d[2][i], d[3][i], 0x7632);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mma(acc[4 * w + i][n], a0, a1, a2, a3, pf[u][n][0], pf[u][n][1]);
+                }
+            }
         }
-        __syncthreads();  // the list is rebuilt
+        __syncwarp();  // every lane has read the stages: refill them
+        used += two ? 2 : 1;
+        top_up();
     }
-    if (!ok && A.status && lane == 0) atomicOr(A.status, 8u /* HS_STATUS_TIMEOUT */);
-    if (!ok) {  // no copy may still be landing when the CTA exits: wait for them, bounded again
+    if (!ok) {
+        if (A.status && lane == 0) atomicOr(A.status, 8u /* HS_STATUS_TIMEOUT */);
+        // no copy may still be landing when the CTA exits: wait for them, bounded again
         const uint64_t by = global_ns() + kDefaultWaitNs;
-        for (; use != fill; ++use) bar_wait(&bar[use % C::kStages], (use / C::kStages) & 1u, by);
+        for (; used != fill; ++used) bar_wait(&bar[used % C::kStages], (used / C::kStages) & 1u, by);
     }
-    __syncthreads();
 
-    // ---------------- join the warps
-    float* part = reinterpret_cast<float*>(sm.space);  // [warp][row][D]
+    // ---------------- join the warps: their outputs in the lanes' order, over the ring
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -574,77 +602,107 @@ __global__ void __launch_bounds__(kThreads, (Config<D, NT>::kCtas)) attend_pages
             float sum = l[n][c];
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            const int r = 8 * n + 2 * t + c;
             if (g == 0) {
-                sm.m[warp][r] = m[n][c];
-                sm.l[warp][r] = sum;
+                sm.m[warp][8 * n + 2 * t + c] = m[n][c];
+                sm.l[warp][8 * n + 2 * t + c] = sum;
             }
-            float* dst = part + ((size_t)warp * C::kRows + r) * D + g * (D / 8);
-#pragma unroll
-            for (int i = 0; i < C::kSteps; ++i) *reinterpret_cast<float2*>(dst + 2 * i) = make_float2(acc[i][n][c], acc[i][n][c + 2]);
         }
-    if (tid == 0) sm.ref = ref;
-    __syncthreads();
-    for (int x = tid; x < C::kRows * (D / 4); x += kThreads) {
-        const int r = x / (D / 4), d = x % (D / 4) * 4;
-        float top = -INFINITY;
+    if (lane == 0) sm.wref[warp] = ref;
+    __syncthreads();  // every warp is done with its ring
+    constexpr int kFrags = C::kSteps * NT * 32;
+    float4* part = reinterpret_cast<float4*>(sm.space);  // [warp][step][n][lane]
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm.m[w][r]);
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        float sum = 0.f;
+    for (int i = 0; i < C::kSteps; ++i)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            part[warp * kFrags + (i * NT + n) * 32 + lane] = make_float4(acc[i][n][0], acc[i][n][1], acc[i][n][2], acc[i][n][3]);
+    if (tid < C::kRows) {
+        int last = sm.wref[0];
+        if (MOD)
+            for (int w = 1; w < kWarps; ++w) last = max(last, sm.wref[w]);
+        float mw[kWarps], top = -INFINITY, sum = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            if (sm.m[w][r] == -INFINITY) continue;  // the warp saw no key of this row
-            const float f = ex2(sm.m[w][r] - top);
-            const float4 v = *reinterpret_cast<const float4*>(part + ((size_t)w * C::kRows + r) * D + d);
-            sum += f * sm.l[w][r];
-            o.x += f * v.x; o.y += f * v.y; o.z += f * v.z; o.w += f * v.w;
+            mw[w] = sm.m[w][tid];
+            if (MOD) mw[w] -= sm.slope[tid] * (float)(last - sm.wref[w]);
+            top = fmaxf(top, mw[w]);
         }
-        *reinterpret_cast<float4*>(&sm.joined[r][d]) = o;
-        if (d == 0) {
-            sm.cm[r] = top;
-            sm.cl[r] = sum;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float f = mw[w] == -INFINITY ? 0.f : ex2(mw[w] - top);  // -inf: the warp saw no key of the row
+            sm.f[w][tid] = f;
+            sum += f * sm.l[w][tid];
         }
+        sm.cm[tid] = top;
+        sm.cl[tid] = sum;
+        sm.inv[tid] = top > -INFINITY ? 1.f / sum : 0.f;
+        if (tid == 0) sm.cref = last;
+    }
+    __syncthreads();
+    for (int x = tid; x < kFrags; x += kThreads) {
+        const int ln = x % 32, n = x / 32 % NT, i = x / 32 / NT, r = 8 * n + 2 * (ln & 3), d = (ln >> 2) * (D / 8) + 2 * i;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float4 v = part[w * kFrags + x];
+            const float2 f = *reinterpret_cast<const float2*>(&sm.f[w][r]);
+            o.x += f.x * v.x; o.y += f.y * v.y; o.z += f.x * v.z; o.w += f.y * v.w;
+        }
+        *reinterpret_cast<float2*>(&sm.joined[r][d]) = make_float2(o.x, o.z);
+        *reinterpret_cast<float2*>(&sm.joined[r + 1][d]) = make_float2(o.y, o.w);
     }
     // ---------------- join the shares, each CTA a part of the rows' elements, and write
-    if (nsplit > 1) cluster_sync();
-    else __syncthreads();
-    int far = ref;
-    if (MOD && A.slopes)
-        for (int s = 0; s < nsplit; ++s) far = max(far, nsplit > 1 ? peer_int(&sm.ref, s) : ref);
+    int last = 0;
+    if (nsplit > 1) {
+        cluster_sync();
+        if (MOD) {
+            last = sm.cref;
+            for (int s = 0; s < nsplit; ++s) last = max(last, peer_int(&sm.cref, s));
+        }
+        for (int x = tid; x < nsplit * C::kRows; x += kThreads) {
+            const int s = x / C::kRows, r = x % C::kRows;
+            float ms = peer_float(&sm.cm[r], s);
+            if (MOD) ms -= sm.slope[r] * (float)(last - peer_int(&sm.cref, s));
+            sm.pm[s][r] = ms;
+            sm.pl[s][r] = peer_float(&sm.cl[r], s);
+        }
+        __syncthreads();
+        if (tid < C::kRows) {
+            float top = -INFINITY, sum = 0.f;
+            for (int s = 0; s < nsplit; ++s) top = fmaxf(top, sm.pm[s][tid]);
+            for (int s = 0; s < nsplit; ++s) {
+                const float f = sm.pm[s][tid] == -INFINITY ? 0.f : ex2(sm.pm[s][tid] - top);  // no key in the share
+                sm.f[s][tid] = f;
+                sum += f * sm.pl[s][tid];
+            }
+            sm.pm[0][tid] = top;  // this CTA's own copies: cm and cl are still read by the peers
+            sm.pl[0][tid] = sum;
+            sm.inv[tid] = top > -INFINITY ? 1.f / sum : 0.f;
+        }
+        __syncthreads();
+    } else {
+        if (MOD) last = sm.cref;
+        __syncthreads();
+    }
     const int todo = min(C::kRows, rows - r0) * (D / 4);
     for (int x = split * kThreads + tid; x < todo; x += nsplit * kThreads) {
         const int r = x / (D / 4), d = x % (D / 4) * 4, row = r0 + r;
-        const int tok = row / A.G, head = h * A.G + row % A.G;
-        const float sl = MOD && A.slopes ? __ldg(A.slopes + head) * kLog2e : 0.f;
+        const int tok = row / A.G, head = h * A.G + row - tok * A.G;
         float4 o;
-        float top, sum;
         if (nsplit == 1) {
             o = *reinterpret_cast<const float4*>(&sm.joined[r][d]);
-            top = sm.cm[r];
-            sum = sm.cl[r];
         } else {
-            top = -INFINITY;
-            for (int s = 0; s < nsplit; ++s) {
-                float ms = peer_float(&sm.cm[r], s);
-                if (MOD && sl != 0.f) ms -= sl * (float)(far - peer_int(&sm.ref, s));
-                top = fmaxf(top, ms);
-            }
             o = make_float4(0.f, 0.f, 0.f, 0.f);
-            sum = 0.f;
-            for (int s = 0; s < nsplit; ++s) {
-                float ms = peer_float(&sm.cm[r], s);
-                if (MOD && sl != 0.f) ms -= sl * (float)(far - peer_int(&sm.ref, s));
-                if (ms == -INFINITY) continue;  // the share holds no key of this row
-                const float f = ex2(ms - top);
+#pragma unroll
+            for (int s = 0; s < kMaxSplit; ++s) {
+                if (s >= nsplit) break;
                 const float4 v = peer_float4(&sm.joined[r][d], s);
-                sum += f * peer_float(&sm.cl[r], s);
+                const float f = sm.f[s][r];
                 o.x += f * v.x; o.y += f * v.y; o.z += f * v.z; o.w += f * v.w;
             }
         }
-        const float inv = top > -INFINITY ? 1.f / sum : 0.f;
+        const float inv = sm.inv[r];
         o.x *= inv; o.y *= inv; o.z *= inv; o.w *= inv;
-        uint16_t* dst = A.o + b * A.o_batch + tok * A.o_token + head * A.o_head + d;
         uint2 w;
         if (bf16) {
             const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x, o.y), hi = __floats2bfloat162_rn(o.z, o.w);
@@ -652,12 +710,13 @@ __global__ void __launch_bounds__(kThreads, (Config<D, NT>::kCtas)) attend_pages
         } else {
             w = make_uint2(pack_half(o.x, o.y), pack_half(o.z, o.w));
         }
-        *reinterpret_cast<uint2*>(dst) = w;
+        *reinterpret_cast<uint2*>(A.o + b * A.o_batch + tok * A.o_token + head * A.o_head + d) = w;
         if (d == 0) {
+            const float top = nsplit == 1 ? sm.cm[r] : sm.pm[0][r], sum = nsplit == 1 ? sm.cl[r] : sm.pl[0][r];
             float e = -INFINITY;
             if (top > -INFINITY) {
                 e = (top + lg2(sum)) * kLn2;
-                if (MOD && sl != 0.f) e -= __ldg(A.slopes + head) * (float)(qpos0 + tok - far);
+                if (MOD && A.slopes) e -= __ldg(A.slopes + head) * (float)(qpos0 + tok - last);
             }
             A.lse[((size_t)b * A.Tq + tok) * A.H * A.G + head] = e;
         }
@@ -665,12 +724,11 @@ __global__ void __launch_bounds__(kThreads, (Config<D, NT>::kCtas)) attend_pages
     if (nsplit > 1) cluster_sync();  // no CTA may exit while a peer reads its shared memory
 }
 
-// The shares of a selection: enough CTAs to fill the GPU, at most 8 (the portable cluster),
-// and no share below two tiles a warp.
-int plan_splits(int64_t jobs, int64_t tiles, int ctas) {
-    int n = 1;
-    while (n < 8 && jobs * n < ctas && tiles / (2 * n) >= 2 * kWarps) n *= 2;
-    return n;
+// The shares of a selection: as many as fill the GPU in one wave, at most 8 (the portable
+// cluster size), and no share below two tiles a warp.
+int plan_splits(int64_t jobs, int64_t tiles, int slots) {
+    const int64_t n = std::min((int64_t)slots / (jobs > 0 ? jobs : 1), tiles / (2 * kWarps));
+    return (int)(n < 1 ? 1 : n > kMaxSplit ? kMaxSplit : n);
 }
 
 template <int D, int NT, bool MOD>
