@@ -5,7 +5,8 @@ small fixed-size cache of slots on the GPU; per layer and decode step one fused
 resolution does hit detection, LRU replacement, the page-table update and the
 host-to-device fetch of the misses. All of that runs in the library's CUDA kernels
 (sm_103a) behind the C ABI of ``include/hs.h``; this module only marshals arguments
-(torch tensors or raw addresses, streams, events) to those calls. There is no
+(torch tensors or raw addresses, streams, events) to those calls, the page calls through a
+compiled part of it (``_hs_torch.so``). There is no
 fallback: if the compiled library is missing, loading fails with an error.
 """
 from __future__ import annotations
@@ -18,6 +19,7 @@ import numpy as np
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libhs.so")
+TORCH_PATH = os.path.join(_HERE, "_hs_torch.so")
 
 HS_OK = 0
 HS_ERR_INVALID = -1
@@ -103,6 +105,7 @@ SIGNATURES = {
     "hs_read_pages": (_I, [_VP, _VP, _I, _VP, _I, _I, _VP, _I, _VP, _VP, _VP]),
     "hs_attend_pages": (_I, [_VP, _VP]),
     "hs_status_word": (_VP, [_VP]),
+    "hs_device": (_I, [_VP]),
     "hs_kernels_per_call": (_I, [_VP]),
     "hs_plan": (_I, [ctypes.POINTER(PlanParams), ctypes.POINTER(PlanResult)]),
     "hs_pool_create": (_VP, [_I64]),
@@ -127,7 +130,7 @@ _lib = None
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile libhs.so in-tree with nvcc for sm_103a (see _nvcc.py)."""
+    """Compile libhs.so (nvcc, sm_103a) and the torch binding in-tree (see _nvcc.py)."""
     from . import _nvcc
     return _nvcc.build(force=force, verbose=verbose)
 
@@ -213,79 +216,38 @@ class PageShape(NamedTuple):
         return n
 
 
-def _page_bytes(shape) -> int:
-    return shape[0] * shape[1] * shape[2] * 9 // 8
+_torch_binding = None
 
 
-def _dtype_code(x) -> int:
-    import torch
-    if x.dtype is torch.bfloat16:
-        return HS_BF16
-    if x.dtype is torch.float16:
-        return HS_F16
-    raise ValueError(f"bfloat16 or float16 wanted, got {x.dtype}")
+def _native():
+    """The compiled torch binding (csrc/hs_torch.cpp); raises if it has not been built."""
+    global _torch_binding
+    if _torch_binding is None:
+        import importlib.util
 
-
-def _on_device(device: int, **tensors) -> None:
-    """Every tensor (None: left out) is on the calling thread's current device."""
-    for name, x in tensors.items():
-        if x is not None and x.get_device() != device:
-            raise ValueError(f"{name} must be on the current CUDA device {device}, it is on {x.device}")
-
-
-def _vector(name: str, x, dtype, shape) -> None:
-    if x is not None and (x.dtype is not dtype or tuple(x.shape) != tuple(shape) or not x.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
-                         f"got {x.dtype} {tuple(x.shape)}")
-
-
-def _rows(shape, k, v):
-    """hs_token_rows of k and v [n, kv_heads, head_dim] (any token and head strides), and n."""
-    n = k.shape[0]
-    want = (n, shape[1], shape[2])
-    for name, x in (("k", k), ("v", v)):
-        if tuple(x.shape) != want or (x.stride(2) != 1 and x.numel()):
-            raise ValueError(f"{name} must have shape {want} with contiguous rows, got {tuple(x.shape)}")
-    if v.dtype is not k.dtype:
-        raise ValueError("k and v must have one dtype")
-    return _TokenRows(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), v.stride(0), v.stride(1)), n
-
-
-def _checked(rc: int, what: str) -> None:
-    if rc != HS_OK:
-        raise HsError(f"{what} failed ({rc}): {last_error()}")
+        import torch  # noqa: F401  (the binding links against its libraries)
+        load_library()
+        if not os.path.exists(TORCH_PATH):
+            raise HsError(f"{TORCH_PATH} is missing: build it first (hierarchical_kv_cache_swap_gb300.build())")
+        spec = importlib.util.spec_from_file_location("_hs_torch", TORCH_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.set_error(HsError)
+        _torch_binding = module
+    return _torch_binding
 
 
 def write_tokens(shape, k, v, dest, pages, status=None, stream=None) -> None:
     """hs_write_tokens: k, v bf16 or fp16 [n, kv_heads, head_dim] (rows contiguous) quantised
     into uint8 pages [P, page bytes] (device, or pinned) at the token slots dest int64 [n]
-    (page * tokens + offset; negative: padding). status: a device int32 word, or None."""
-    import torch
-    rows, n = _rows(shape, k, v)
-    _vector("dest", dest, torch.int64, (n,))
-    _vector("pages", pages, torch.uint8, (pages.shape[0], _page_bytes(shape)))
-    device = torch.cuda.current_device()
-    _on_device(device, k=k, v=v, dest=dest, status=status, pages=None if pages.is_pinned() else pages)
-    _checked(load_library().hs_write_tokens(_stream(stream), ctypes.byref(_PageShape(*shape)), _dtype_code(k),
-                                            ctypes.byref(rows), n, dest.data_ptr(), pages.data_ptr(),
-                                            pages.shape[0], _addr(status)), "hs_write_tokens")
+    (page * tokens + offset; negative: padding). status: a device int32 word [1], or None."""
+    (_torch_binding or _native()).write_tokens(shape, k, v, dest, pages, status, stream)
 
 
 def read_pages(shape, pages, slots, k, v, status=None, stream=None) -> None:
     """hs_read_pages: the pages [B, S, page bytes] in slots int32 [B, n] decoded into k and v
     [B, n * tokens, kv_heads, head_dim], bf16 or fp16 (zeros where a slot is negative)."""
-    import torch
-    B, n = slots.shape
-    _vector("slots", slots, torch.int32, (B, n))
-    _vector("pages", pages, torch.uint8, (B, pages.shape[1], _page_bytes(shape)))
-    want = (B, n * shape[0], shape[1], shape[2])
-    _vector("k", k, k.dtype, want)
-    _vector("v", v, k.dtype, want)
-    device = torch.cuda.current_device()
-    _on_device(device, slots=slots, k=k, v=v, status=status, pages=pages)
-    _checked(load_library().hs_read_pages(_stream(stream), ctypes.byref(_PageShape(*shape)), _dtype_code(k),
-                                          pages.data_ptr(), B, pages.shape[1], slots.data_ptr(), n, k.data_ptr(),
-                                          v.data_ptr(), _addr(status)), "hs_read_pages")
+    (_torch_binding or _native()).read_pages(shape, pages, slots, k, v, status, stream)
 
 
 def attend_pages(shape, q, pages, slots, selections, lengths, o, lse, sm_scale: float, softcap: float = 0.0,
@@ -295,29 +257,9 @@ def attend_pages(shape, q, pages, slots, selections, lengths, o, lse, sm_scale: 
     [B, k] of sequences of lengths int32 [B] tokens; into o (as q) and lse float32 [B,
     q_tokens, q_heads]. softcap: 0, or the cap of the scores; slopes: float32 [q_heads] of a
     distance bias; start, prefix: int32 [B], keys before start are masked but for the first
-    prefix; status: a device int32 word."""
-    import torch
-    B, T, Hq, D = q.shape
-    k = slots.shape[1]
-    if D != shape[2] or o.shape != q.shape or o.dtype is not q.dtype or q.stride(3) != 1 or o.stride(3) != 1:
-        raise ValueError(f"q and o must be [B, q_tokens, q_heads, {shape[2]}] of one dtype with contiguous rows")
-    i32, f32 = torch.int32, torch.float32
-    _vector("pages", pages, torch.uint8, (B, pages.shape[1], _page_bytes(shape)))
-    _vector("slots", slots, i32, (B, k))
-    _vector("selections", selections, i32, (B, k))
-    _vector("lengths", lengths, i32, (B,))
-    _vector("lse", lse, f32, (B, T, Hq))
-    _vector("slopes", slopes, f32, (Hq,))
-    _vector("start", start, i32, (B,))
-    _vector("prefix", prefix, i32, (B,))
-    _on_device(torch.cuda.current_device(), q=q, o=o, lse=lse, pages=pages, slots=slots, selections=selections,
-               lengths=lengths, slopes=slopes, start=start, prefix=prefix, status=status)
-    args = _PageAttention(_PageShape(*shape), _dtype_code(q), B, pages.shape[1], k, Hq, T,
-                          q.data_ptr(), q.stride(0), q.stride(1), q.stride(2),
-                          o.data_ptr(), o.stride(0), o.stride(1), o.stride(2), lse.data_ptr(), pages.data_ptr(),
-                          slots.data_ptr(), selections.data_ptr(), lengths.data_ptr(), sm_scale, softcap,
-                          _addr(slopes), _addr(start), _addr(prefix), _addr(status), wait_ns)
-    _checked(load_library().hs_attend_pages(_stream(stream), ctypes.byref(args)), "hs_attend_pages")
+    prefix; status: a device int32 word [1]."""
+    (_torch_binding or _native()).attend_pages(shape, q, pages, slots, selections, lengths, o, lse, sm_scale, softcap,
+                                               slopes, start, prefix, status, stream, wait_ns)
 
 
 class Pool:
@@ -465,28 +407,27 @@ class Context:
                                         float(sm_scale), _addr(o), _addr(lse), ws, nbytes), "hs_attend")
 
     # ------------------------------------------------------------------ 4-bit pages
+    def _pages(self, shape):
+        """This context's device buffer as the page calls take it: (address, R, S, device)."""
+        if self.E != PageShape(*shape).bytes:
+            raise ValueError(f"pages of {PageShape(*shape).bytes} bytes, but the context's entries have {self.E}")
+        return (self._lib.hs_device_kv(self._h), self.R, self.S, self._lib.hs_device(self._h))
+
     def append_tokens(self, shape, k, v, positions, requests=None, stream=None) -> None:
         """hs_append_tokens: k, v bf16 or fp16 [n, kv_heads, head_dim] join the histories at
         token positions int32 [n] (negative: skipped) of the requests int32 [n] (None: token i
         of request i), in the host store and the resident slots."""
-        import torch
-        rows, n = _rows(shape, k, v)
-        _vector("positions", positions, torch.int32, (n,))
-        _vector("requests", requests, torch.int32, (n,))
-        _on_device(torch.cuda.current_device(), k=k, v=v, positions=positions, requests=requests)
-        self._check(self._lib.hs_append_tokens(self._h, _stream(stream), ctypes.byref(_PageShape(*shape)), _dtype_code(k),
-                                               ctypes.byref(rows), n, _addr(requests), positions.data_ptr()),
-                    "hs_append_tokens")
+        _native().append_tokens(self._h, shape, k, v, positions, requests, stream)
 
     def read_pages(self, shape, out_slots, k, v, stream=None) -> None:
         """read_pages() over this context's device buffer and status word."""
-        read_pages(shape, self.device_kv(), out_slots, k, v, status=self.status_word(), stream=stream)
+        _native().read_pages(shape, self._pages(shape), out_slots, k, v, self._lib.hs_status_word(self._h), stream)
 
     def attend_pages(self, shape, q, out_slots, selections, lengths, o, lse, sm_scale: float, softcap: float = 0.0,
                      slopes=None, start=None, prefix=None, stream=None) -> None:
         """attend_pages() over this context's device buffer, status word and wait limit."""
-        attend_pages(shape, q, self.device_kv(), out_slots, selections, lengths, o, lse, sm_scale, softcap, slopes,
-                     start, prefix, status=self.status_word(), stream=stream, wait_ns=self._wait_ns)
+        _native().attend_pages(shape, q, self._pages(shape), out_slots, selections, lengths, o, lse, sm_scale, softcap,
+                               slopes, start, prefix, self._lib.hs_status_word(self._h), stream, self._wait_ns)
 
     def reset(self, stream=None) -> None:
         self._check(self._lib.hs_reset(self._h, _stream(stream)), "hs_reset")
@@ -553,6 +494,3 @@ class Context:
 
     def step(self):
         return self._dev("hs_step", (self.R,), "<i4")
-
-    def status_word(self):
-        return self._dev("hs_status_word", (1,), "<i4")

@@ -639,6 +639,8 @@ int hs_attend_pages(hs_stream_t stream, const hs_page_attention* a) {
     return HS_OK;
 }
 
+int hs_device(hs_ctx* h) { return h ? h->device : -1; }
+
 uint32_t* hs_status_word(hs_ctx* h) { return h ? h->L.status : nullptr; }
 
 uint8_t* hs_host_kv(hs_ctx* h) { return h ? h->host_kv : nullptr; }

@@ -483,6 +483,9 @@ int hs_attend_pages(hs_stream_t stream, const hs_page_attention* args);
 /* hs_status_word -- the context's device status word, for the calls above. */
 uint32_t* hs_status_word(hs_ctx* ctx);
 
+/* hs_device -- the CUDA device the context was created on (-1: null context). */
+int hs_device(hs_ctx* ctx);
+
 /* Number of kernels one hs_resolve call enqueues under the current flags. */
 int hs_kernels_per_call(hs_ctx* ctx);
 
