@@ -9,11 +9,11 @@
 // exact in bf16 and in fp16, where it is always finite (6 * 10240 = 61440). A block that
 // holds an infinity or a NaN gets a NaN scale and reads back as NaN.
 //
-// One thread makes (or reads) one block of K and the same block of V: 2 x 32 bytes of 16-bit
-// floats against 2 x 9 bytes of page. The lanes of a warp take the D / 16 blocks of a row and
-// 512 / D consecutive tokens of one head, whose codes lie together in the page (256 bytes,
-// and 32 bytes of scales), so both sides move in whole 32-byte sectors. Both kernels are
-// bound by memory traffic: 2 + 9/16 bytes a value.
+// One thread makes (or reads) one block of K and the same block of V at a time: 2 x 32 bytes
+// of 16-bit floats against 2 x 9 bytes of page. The lanes of a warp take the D / 16 blocks of
+// a row and 512 / D consecutive tokens of one head, whose codes lie together in the page (256
+// bytes, and 32 bytes of scales), so both sides move in whole 32-byte sectors. Both kernels
+// are bound by memory traffic: 2 + 9/16 bytes a value.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -157,33 +157,43 @@ struct ToContext {
     }
 };
 
-// Warp unit: one head and 512 / D consecutive tokens. Units run over heads first.
+// A warp takes groups of 512 / D consecutive tokens of one head (blockIdx.y), kWays groups at a
+// time with all their loads in flight.
 template <int D, bool BF16, class Dest>
-__global__ void __launch_bounds__(kThreads) write_kernel(const TokenRows in, int64_t n, int heads, const Dest dest) {
-    constexpr int kBlocks = D / 16, kTok = 32 / kBlocks;
-    const int lane = threadIdx.x & 31, blk = lane % kBlocks;
-    const int64_t groups = (n + kTok - 1) / kTok, units = groups * heads;
-    for (int64_t u = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); u < units;
-         u += (int64_t)gridDim.x * (kThreads / 32)) {
-        const int64_t grp = u / heads;
-        const int h = (int)(u - grp * heads);
-        const int64_t i = grp * kTok + lane / kBlocks;
-        if (i >= n) continue;
-        uint32_t kw[8], vw[8];
-        load_block(kw, in.k + i * in.k_token + h * in.k_head + 16 * blk);
-        load_block(vw, in.v + i * in.v_token + h * in.v_head + 16 * blk);
-        const Place p = dest(i, h == 0 && blk == 0);
-        if (p.row < 0) continue;
-        const Block kb = quantise<BF16>(kw), vb = quantise<BF16>(vw);
-        uint8_t* c = p.a + (size_t)h * (18 * D);
-        store_block<D>(c, p.row, blk, kb);
-        store_block<D>(c + 9 * D, p.row, blk, vb);
-        if (p.b) {
-            c = p.b + (size_t)h * (18 * D);
-            store_block<D>(c, p.row, blk, kb);
-            store_block<D>(c + 9 * D, p.row, blk, vb);
+__global__ void __launch_bounds__(kThreads) write_kernel(const TokenRows in, int64_t n, const Dest dest) {
+    constexpr int kBlocks = D / 16, kTok = 32 / kBlocks, kWays = 2;
+    const int lane = threadIdx.x & 31, blk = lane % kBlocks, h = blockIdx.y;
+    const int64_t step = (int64_t)gridDim.x * (kThreads / 32) * (kTok * kWays);
+    const uint16_t* k = in.k + h * in.k_head + 16 * blk;
+    const uint16_t* v = in.v + h * in.v_head + 16 * blk;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int64_t i0 = ((int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * (kTok * kWays) + lane / kBlocks; i0 < n; i0 += step) {
+        uint32_t kw[kWays][8], vw[kWays][8];
+        Place p[kWays];
+#pragma unroll
+        for (int w = 0; w < kWays; ++w) {
+            const int64_t i = i0 + w * kTok;
+            p[w].row = -1;
+            if (i >= n) continue;
+            load_block(kw[w], k + i * in.k_token);
+            load_block(vw[w], v + i * in.v_token);
+            p[w] = dest(i, h == 0 && blk == 0);
+        }
+#pragma unroll
+        for (int w = 0; w < kWays; ++w) {
+            if (p[w].row < 0) continue;
+            const Block kb = quantise<BF16>(kw[w]), vb = quantise<BF16>(vw[w]);
+            uint8_t* c = p[w].a + (size_t)h * (18 * D);
+            store_block<D>(c, p[w].row, blk, kb);
+            store_block<D>(c + 9 * D, p[w].row, blk, vb);
+            if (p[w].b) {
+                c = p[w].b + (size_t)h * (18 * D);
+                store_block<D>(c, p[w].row, blk, kb);
+                store_block<D>(c + 9 * D, p[w].row, blk, vb);
+            }
         }
     }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // Two codes of a byte to two halves (exact).
@@ -212,64 +222,78 @@ __device__ __forceinline__ uint4 decode8(uint32_t w, uint32_t u) {
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-// Warp unit: 512 / D tokens of one head of one selected page.
+// A warp takes a tile of 16 tokens of one head (blockIdx.y) of a selected page, all its loads
+// in flight at once. Tiles: every page of [B][n] in turn.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreads)
-read_kernel(const uint8_t* __restrict__ pages, int S, const int32_t* __restrict__ slots, int64_t total, int n, int tokens,
-            int heads, size_t page_bytes, uint16_t* __restrict__ ko, uint16_t* __restrict__ vo, uint32_t* status) {
-    constexpr int kBlocks = D / 16, kTok = 32 / kBlocks;
-    const int lane = threadIdx.x & 31, blk = lane % kBlocks;
-    const int per_page = tokens / kTok * heads;
-    const int64_t units = total * per_page;  // total: selected pages of all requests
-    for (int64_t u = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); u < units;
-         u += (int64_t)gridDim.x * (kThreads / 32)) {
-        const int64_t j = u / per_page;  // page of [B][n]
-        const int in = (int)(u - j * per_page), grp = in / heads, h = in - grp * heads;
-        const int off = grp * kTok + lane / kBlocks;
+read_kernel(const uint8_t* __restrict__ pages, int S, const int32_t* __restrict__ slots, int64_t ntiles, int n, int tiles,
+            int heads, uint16_t* __restrict__ ko, uint16_t* __restrict__ vo, uint32_t* status) {
+    constexpr int kBlocks = D / 16, kTok = 32 / kBlocks, kWays = kTile / kTok;
+    const int lane = threadIdx.x & 31, blk = lane % kBlocks, h = blockIdx.y;
+    const int64_t step = (int64_t)gridDim.x * (kThreads / 32);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int64_t x = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); x < ntiles; x += step) {
+        const int64_t j = tiles == 1 ? x : x / tiles;  // page of [B][n]
+        const int tile = (int)(x - j * tiles);
         const int32_t s = __ldg(slots + j);
-        uint4 k0 = make_uint4(0, 0, 0, 0), k1 = k0, v0 = k0, v1 = k0;
-        if (s >= S) {
-            if (in == 0 && lane == 0 && status) atomicOr(status, 1u /* HS_STATUS_RANGE */);
-        } else if (s >= 0) {
-            const int64_t b = j / n;
-            const uint8_t* c = pages + (size_t)(b * S + s) * page_bytes + ((size_t)(off / kTile) * heads + h) * (18 * D);
-            const int r = off % kTile;
-            const uint2 kc = __ldg(reinterpret_cast<const uint2*>(c + r * (D / 2) + 8 * blk));
-            const uint2 vc = __ldg(reinterpret_cast<const uint2*>(c + 9 * D + r * (D / 2) + 8 * blk));
-            const uint32_t ku = __ldg(c + 8 * D + r * (D / 16) + blk), vu = __ldg(c + 17 * D + r * (D / 16) + blk);
-            k0 = decode8<BF16>(kc.x, ku);
-            k1 = decode8<BF16>(kc.y, ku);
-            v0 = decode8<BF16>(vc.x, vu);
-            v1 = decode8<BF16>(vc.y, vu);
+        const bool live = s >= 0 && s < S;
+        if (s >= S && status && tile == 0 && h == 0 && lane == 0) atomicOr(status, 1u /* HS_STATUS_RANGE */);
+        const int64_t b = live ? j / n : 0;
+        const uint8_t* c = pages + ((size_t)((b * S + (live ? s : 0)) * tiles + tile) * heads + h) * (18 * D);
+        uint2 kc[kWays], vc[kWays];
+        uint32_t ku[kWays], vu[kWays];
+#pragma unroll
+        for (int w = 0; w < kWays; ++w) {
+            const int r = w * kTok + lane / kBlocks;
+            kc[w] = vc[w] = make_uint2(0, 0);
+            ku[w] = vu[w] = 0;
+            if (live) {
+                kc[w] = __ldg(reinterpret_cast<const uint2*>(c + r * (D / 2) + 8 * blk));
+                vc[w] = __ldg(reinterpret_cast<const uint2*>(c + 9 * D + r * (D / 2) + 8 * blk));
+                ku[w] = __ldg(c + 8 * D + r * (D / 16) + blk);
+                vu[w] = __ldg(c + 17 * D + r * (D / 16) + blk);
+            }
         }
-        const size_t at = ((size_t)(j * tokens + off) * heads + h) * D + 16 * blk;
-        reinterpret_cast<uint4*>(ko + at)[0] = k0;
-        reinterpret_cast<uint4*>(ko + at)[1] = k1;
-        reinterpret_cast<uint4*>(vo + at)[0] = v0;
-        reinterpret_cast<uint4*>(vo + at)[1] = v1;
+#pragma unroll
+        for (int w = 0; w < kWays; ++w) {
+            const size_t at = ((size_t)(x * kTile + w * kTok + lane / kBlocks) * heads + h) * D + 16 * blk;
+            reinterpret_cast<uint4*>(ko + at)[0] = decode8<BF16>(kc[w].x, ku[w]);
+            reinterpret_cast<uint4*>(ko + at)[1] = decode8<BF16>(kc[w].y, ku[w]);
+            reinterpret_cast<uint4*>(vo + at)[0] = decode8<BF16>(vc[w].x, vu[w]);
+            reinterpret_cast<uint4*>(vo + at)[1] = decode8<BF16>(vc[w].y, vu[w]);
+        }
     }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// CTAs for `units` warp units: one unit a warp, at most eight CTAs an SM (further units in turn).
-unsigned grid_for(int64_t units, int num_sms) {
-    const int64_t ctas = (units + kThreads / 32 - 1) / (kThreads / 32), most = (int64_t)num_sms * 8;
-    return (unsigned)(ctas < most ? ctas : most);
+// Launches `kernel` with enough CTAs for `units` warp units of each of `heads` heads, at most
+// kWave of them an SM (further units in turn), allowed to begin before the kernel ahead of it
+// on the stream is done (the kernels wait for that themselves).
+constexpr int kWave = 16;
+template <class... Params, class... Args>
+cudaError_t launch(cudaStream_t stream, int64_t units, int heads, int num_sms, void (*kernel)(Params...), Args... args) {
+    const int64_t ctas = (units + kThreads / 32 - 1) / (kThreads / 32), most = ((int64_t)num_sms * kWave + heads - 1) / heads;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(ctas < most ? ctas : most), (unsigned)heads);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
 }
 
 template <class Dest>
 cudaError_t write_any(cudaStream_t stream, const PageShape& ps, bool bf16, const TokenRows& rows, int64_t n, const Dest& dest,
                       int num_sms) {
     if (n == 0) return cudaSuccess;
-    const int tok = 512 / ps.dim;
-    const unsigned grid = grid_for((n + tok - 1) / tok * ps.heads, num_sms);
-#define HS_WRITE(D_)                                                                             \
-    (bf16 ? write_kernel<D_, true, Dest><<<grid, kThreads, 0, stream>>>(rows, n, ps.heads, dest)  \
-          : write_kernel<D_, false, Dest><<<grid, kThreads, 0, stream>>>(rows, n, ps.heads, dest))
-    if (ps.dim == 64) HS_WRITE(64);
-    else if (ps.dim == 128) HS_WRITE(128);
-    else HS_WRITE(256);
+    const int64_t units = (n + 1024 / ps.dim - 1) / (1024 / ps.dim);
+#define HS_WRITE(D_) \
+    launch(stream, units, ps.heads, num_sms, bf16 ? write_kernel<D_, true, Dest> : write_kernel<D_, false, Dest>, rows, n, dest)
+    return ps.dim == 64 ? HS_WRITE(64) : ps.dim == 128 ? HS_WRITE(128) : HS_WRITE(256);
 #undef HS_WRITE
-    return cudaGetLastError();
 }
 
 }  // namespace
@@ -289,20 +313,13 @@ cudaError_t launch_append_tokens(const Layout& L, cudaStream_t stream, const Pag
 
 cudaError_t launch_read_pages(cudaStream_t stream, const PageShape& ps, bool bf16, const uint8_t* pages, int B, int S,
                               const int32_t* slots, int n, void* k, void* v, uint32_t* status, int num_sms) {
-    const int64_t total = (int64_t)B * n;
-    if (total == 0) return cudaSuccess;
-    const unsigned grid = grid_for(total * (ps.tokens / (512 / ps.dim)) * ps.heads, num_sms);
-    uint16_t *ko = (uint16_t*)k, *vo = (uint16_t*)v;
-#define HS_READ(D_)                                                                                                   \
-    (bf16 ? read_kernel<D_, true><<<grid, kThreads, 0, stream>>>(pages, S, slots, total, n, ps.tokens, ps.heads,       \
-                                                                 ps.bytes(), ko, vo, status)                           \
-          : read_kernel<D_, false><<<grid, kThreads, 0, stream>>>(pages, S, slots, total, n, ps.tokens, ps.heads,      \
-                                                                  ps.bytes(), ko, vo, status))
-    if (ps.dim == 64) HS_READ(64);
-    else if (ps.dim == 128) HS_READ(128);
-    else HS_READ(256);
+    const int64_t ntiles = (int64_t)B * n * ps.tiles();
+    if (ntiles == 0) return cudaSuccess;
+#define HS_READ(D_)                                                                                                        \
+    launch(stream, ntiles, ps.heads, num_sms, bf16 ? read_kernel<D_, true> : read_kernel<D_, false>, pages, S, slots, ntiles, \
+           n, ps.tiles(), ps.heads, (uint16_t*)k, (uint16_t*)v, status)
+    return ps.dim == 64 ? HS_READ(64) : ps.dim == 128 ? HS_READ(128) : HS_READ(256);
 #undef HS_READ
-    return cudaGetLastError();
 }
 
 }  // namespace hs

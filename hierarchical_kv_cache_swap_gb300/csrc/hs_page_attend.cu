@@ -45,49 +45,73 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <algorithm>
+#include <math.h>
+
 #include <atomic>
+#include <mutex>
 
 #include "hs_page.h"
 
 namespace hs {
 namespace {
 
-constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr int kMaxWarps = 20;
 constexpr int kMaxSplit = 8;           // CTAs that share a selection: the portable cluster size
 constexpr int kList = 64;              // a warp's list of live tiles (a ring; 32 are added at a time)
 constexpr float kRescale = 8.f;        // a row's reference maximum moves when exceeded by 2^8
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
+
+// n / d for 0 <= n < 2^31 by a multiplication (Granlund and Montgomery, 1994).
+struct Divisor {
+    uint32_t d, m, s;
+    Divisor() = default;
+    explicit Divisor(uint32_t by) : d(by), m(0), s(0) {
+        while ((1ull << s) < by) ++s;
+        m = (uint32_t)((((1ull << s) - by) << 32) / by + 1);
+    }
+    __device__ __forceinline__ int operator()(int n) const { return (int)((__umulhi((uint32_t)n, m) + (uint32_t)n) >> s); }
+};
+
+// A call's work split: job (request, KV head, tile of rows) x share.
+struct Split {
+    Divisor shares, row_tiles, heads, tiles, group;  // CTAs of a job; ...; tiles of a page; query heads of a KV head
+    int ntiles;  // of a selection
+    int groups;  // a warp's groups of 32 tiles
+};
 
 template <int D, int NT>
 struct Config {
     static constexpr int kChunk = 18 * D;           // bytes of a tile of one head
     static constexpr int kRows = 8 * NT;            // query rows of a CTA
     static constexpr int kSteps = D / 16;
-    static constexpr int kCtas = NT * D <= 128 ? 4 : NT * D <= 256 ? 3 : 2;  // CTAs an SM: registers
-    static constexpr int kStages = D == 64 ? 6 : D == 128 ? 4 : 3;
-    static constexpr int kRing = kWarps * kStages * kChunk;
-    static constexpr int kPart = kWarps * kRows * D * 4;  // the warps' outputs, over the ring
-    static constexpr int kSpace = kRing > kPart ? kRing : kPart;
+    // Warps of an SM: what the registers allow (96, 128, 168 or 255 of them)
+    static constexpr int kSmWarps = D == 256 ? 8 : NT == 1 ? 20 : NT * D <= 128 ? 16 : NT * D <= 256 ? 12 : 8;
+    static constexpr int kStages = D == 64 ? 4 : 2;  // of two tiles
+    // shared memory of a warp: its ring and its list; over the rings, at the end, the warps'
+    // outputs and the CTA's
+    static constexpr int kRing = kStages * 2 * kChunk, kListBytes = kList * 8;
+    static constexpr int kPart = kRows * D * 4;
+    __host__ __device__ static constexpr int space(int warps) {
+        return warps * kRing > (warps + 1) * kPart ? warps * kRing : (warps + 1) * kPart;
+    }
+    static int smem(int warps);
 };
 
 template <int D, int NT>
-struct Smem {
+struct Fixed {  // followed by the rings and the lists
     using C = Config<D, NT>;
-    alignas(128) uint8_t space[C::kSpace];
     uint2 qf[NT][C::kSteps][32];              // Q as the lanes take it
-    alignas(16) float joined[C::kRows][D];    // this CTA's output, relative to its maxima
-    float qscale[C::kRows], slope[C::kRows];  // of the rows: to log2 units
+    alignas(8) float qscale[C::kRows], slope[C::kRows];  // of the rows: to log2 units
     int qpos[C::kRows];
-    float m[kWarps][C::kRows], l[kWarps][C::kRows];
-    float f[kMaxSplit][C::kRows];             // factors of the warps, then of the shares
-    float cm[C::kRows], cl[C::kRows];         // this CTA's maxima and sums
-    float pm[kMaxSplit][C::kRows], pl[kMaxSplit][C::kRows];  // every share's
-    float inv[C::kRows];
-    int wref[kWarps], cref;                   // positions that biases are relative to
-    uint64_t bar[kWarps][C::kStages];
-    int2 list[kWarps][kList];                 // unit (slot * tiles + tile), position | partial
+    alignas(16) float2 ml[kMaxWarps][C::kRows];  // the warps' maxima and sums
+    alignas(16) float2 cml[C::kRows];            // this CTA's
+    int wref[kMaxWarps], cref;                   // positions that biases are relative to
+    uint64_t bar[kMaxWarps][C::kStages];
 };
+template <int D, int NT>
+int Config<D, NT>::smem(int warps) {
+    return (int)((sizeof(Fixed<D, NT>) + 127) / 128 * 128) + space(warps) + warps * kListBytes;
+}
 
 __device__ __forceinline__ uint32_t su32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ float ex2(float x) {
@@ -100,8 +124,12 @@ __device__ __forceinline__ float lg2(float x) {
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// tanh y = 1 - 2 / (1 + e^(2y)); y2 = 2 y log2 e. Absolute error a few 2^-23.
-__device__ __forceinline__ float tanh_of(float y2) { return 1.f - __fdividef(2.f, 1.f + ex2(y2 > 100.f ? 100.f : y2)); }
+// c tanh y = c - 2 c / (1 + e^(2y)); y2 = 2 y log2 e. Absolute error a few 2^-23 of c.
+__device__ __forceinline__ float capped(float c, float y2) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(y2)));
+    return fmaf(-2.f * c, r, c);
+}
 
 // Four bytes of codes to four pairs of halves (exact).
 __device__ __forceinline__ void decode_word(uint32_t w, uint32_t (&h)[4]) {
@@ -117,13 +145,43 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ uint32_t scale2(uint32_t u) { return u * 0x00800080u; }  // (s, s) of scale byte u
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) { return __byte_perm(a, b, s); }
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// Two f32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{ .reg .b64 a, b, c, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mov.b64 c, {%6, %7}; fma.rn.f32x2 d, a, b, c;"
+        " mov.b64 {%0, %1}, d; }"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{ .reg .b64 a, b, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; add.rn.f32x2 d, a, b; mov.b64 {%0, %1}, d; }"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 mul2f(float2 a, float2 b) {
+    float2 d;
+    asm("{ .reg .b64 a, b, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mul.rn.f32x2 d, a, b; mov.b64 {%0, %1}, d; }"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {  // of the numbers among them
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t r;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
     return r;
 }
 __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
@@ -145,8 +203,10 @@ __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, uint64_t 
     return true;
 }
 // `bytes` (a multiple of 16, both ends 16-byte aligned) into shared memory, counted on `b`.
-__device__ __forceinline__ void copy_in(void* dst, const uint8_t* src, uint32_t bytes, uint64_t* b) {
+__device__ __forceinline__ void expect(uint64_t* b, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(su32(b)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_in(void* dst, const uint8_t* src, uint32_t bytes, uint64_t* b) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(su32(dst)),
                  "l"(src), "r"(bytes), "r"(su32(b))
                  : "memory");
@@ -159,14 +219,14 @@ __device__ __forceinline__ void cluster_sync() {
 __device__ __forceinline__ float peer_float(const float* p, int rank) {
     uint32_t a;
     float v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(su32(p)), "r"(rank));
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(su32(p)), "r"(rank));
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
     return v;
 }
 __device__ __forceinline__ float4 peer_float4(const float* p, int rank) {
     uint32_t a;
     float4 v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(su32(p)), "r"(rank));
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(su32(p)), "r"(rank));
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
     return v;
 }
@@ -176,30 +236,42 @@ __device__ __forceinline__ int peer_int(const int* p, int rank) {
 
 // MOD: scores are capped or biased.
 template <int D, int NT, bool MOD>
-__global__ void __launch_bounds__(kThreads, (Config<D, NT>::kCtas)) attend_pages_kernel(const PageAttention A, int nsplit, int row_tiles, bool bf16) {
+__global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_kernel(const PageAttention A, const Split P, bool bf16) {
     using C = Config<D, NT>;
     extern __shared__ __align__(128) uint8_t raw[];
-    Smem<D, NT>& sm = *reinterpret_cast<Smem<D, NT>*>(raw);
+    Fixed<D, NT>& sm = *reinterpret_cast<Fixed<D, NT>*>(raw);
+    uint8_t* const space = raw + (sizeof(Fixed<D, NT>) + 127) / 128 * 128;
+    const int threads = blockDim.x, warps = threads >> 5;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const uint64_t deadline = global_ns() + A.wait_ns;
-    int job = blockIdx.x / nsplit;
+    const int nsplit = P.shares.d;
+    int job = P.shares((int)blockIdx.x);
     const int split = blockIdx.x - job * nsplit;  // = the rank in the cluster
-    const int rt = job % row_tiles;
-    job /= row_tiles;
-    const int b = job / A.H, h = job - b * A.H;
-    const int rows = A.G * A.Tq, r0 = rt * C::kRows;
+    const int bh = P.row_tiles(job), r0 = (job - bh * (int)P.row_tiles.d) * C::kRows;
+    const int b = P.heads(bh), h = bh - b * A.H;
+    const int rows = A.G * A.Tq;
+    uint8_t* ring = space + warp * C::kRing;
+    uint64_t* bar = sm.bar[warp];
+    int2* list = reinterpret_cast<int2*>(space + C::space(warps) + warp * C::kListBytes);
+    if (lane < C::kStages) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(su32(bar + lane)) : "memory");
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    __syncwarp();
+
+    // The launch may begin before the kernel ahead of it on the stream is done: nothing that
+    // it reads or writes is touched before this.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 
     // ---------------- this warp's tiles: every (nsplit * kWarps)-th of the selection. Lane i
     // looks up the i-th of the next 32; those that hold a visible key go on the warp's list.
     const int32_t* slots = A.slots + (size_t)b * A.k;
     const int32_t* sel = A.sel + (size_t)b * A.k;
-    const int ntiles = A.k * A.tiles, stride = nsplit * kWarps;
-    int next = lane * stride + split * kWarps + warp;  // this lane's tile of the next group
+    const int ntiles = P.ntiles, stride = nsplit * warps;
+    int next = lane * stride + split * warps + warp;  // this lane's tile of the next group
     int gslot = -1, gsel = -1;                          // its page, loaded a group ahead
     auto look_up = [&]() {
         gslot = -1;
         if (next < ntiles) {
-            const int j = next / A.tiles;
+            const int j = P.tiles(next);
             gslot = __ldg(slots + j);
             gsel = __ldg(sel + j);
         }
@@ -213,21 +285,16 @@ __global__ void __launch_bounds__(kThreads, (Config<D, NT>::kCtas)) attend_pages
     const uint8_t* pages = A.pages + ((size_t)b * A.S * A.tiles * A.H + h) * C::kChunk;
     const size_t unit_bytes = (size_t)A.H * C::kChunk;
 
-    uint8_t* ring = sm.space + warp * (C::kStages * C::kChunk);
-    uint64_t* bar = sm.bar[warp];
-    int2* list = sm.list[warp];
-    if (lane < C::kStages) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(su32(bar + lane)) : "memory");
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    __syncwarp();
-
-    int groups = (ntiles + 32 * stride - 1) / (32 * stride);  // not yet on the list
-    uint32_t used = 0, fill = 0, tail = 0;  // listed tiles consumed, copied (or on their way), listed
+    int groups = P.groups;                  // not yet on the list
+    uint32_t fill = 0, used = 0, tail = 0;  // listed tiles copied (or on their way), consumed, listed
+    int fst = 0, ust = 0;                   // the stage of the next copy and of the next wait
+    uint32_t phase = 0;                     // parity of the next wait
     auto append = [&]() {
         bool live = false;
         int2 e;
         if (gslot >= A.S && A.status) atomicOr(A.status, 1u /* HS_STATUS_RANGE */);
         if (gslot >= 0 && gslot < A.S && gsel >= 0) {
-            const int tile = next % A.tiles;
+            const int tile = next - P.tiles(next) * A.tiles;
             const int64_t at = (int64_t)gsel * (A.tiles * kTile) + tile * kTile;
             if (at < length) {
                 const int pos = (int)at, end = pos + (kTile - 1);
@@ -244,41 +311,43 @@ __global__ void __launch_bounds__(kThreads, (Config<D, NT>::kCtas)) attend_pages
         look_up();
         __syncwarp();
     };
-    auto top_up = [&]() {  // keep every stage on its way
-        while (fill - used < C::kStages) {
-            if (fill == tail) {
-                if (groups == 0) break;
-                append();
-                continue;
-            }
-            if (lane == 0) {
-                const int st = fill % C::kStages;
-                copy_in(ring + st * C::kChunk, pages + (size_t)list[fill % kList].x * unit_bytes, C::kChunk, &bar[st]);
-            }
-            ++fill;
+    auto top_up = [&]() {  // put the next two tiles (the last one alone) on their way
+        while (tail - fill < 2 && groups > 0) append();
+        const int n = min(2, (int)(tail - fill));
+        if (lane < n) {
+            const int unit = list[(fill + lane) % kList].x;
+            if (lane == 0) expect(&bar[fst], n * C::kChunk);
+            copy_in(ring + (2 * fst + lane) * C::kChunk, pages + (size_t)unit * unit_bytes, C::kChunk, &bar[fst]);
         }
+        fill += n;
+        fst = fst + 1 == C::kStages ? 0 : fst + 1;
     };
-    top_up();
+#pragma unroll 1
+    for (int i = 0; i < C::kStages; ++i) top_up();
 
     // ---------------- the query rows as halves, in the lanes' order
-    for (int r = warp; r < C::kRows; r += kWarps) {
-        constexpr int N = D / 32;
-        const int row = r0 + r;
-        float x[N], scale = 0.f;
+    for (int r2 = 2 * warp; r2 < C::kRows; r2 += 2 * warps) {  // half a warp a row
+        constexpr int N = D / 16;
+        const int hl = lane & 15, r = r2 + (lane >> 4), row = r0 + r;
+        float x[N], scale = 0.f, amax = 0.f;
+        int tok = 0, head = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = 0.f;
         if (row < rows) {
-            const int tok = row / A.G, head = h * A.G + row - tok * A.G;
-            const uint16_t* src = A.q + b * A.q_batch + tok * A.q_token + head * A.q_head + lane * N;
+            tok = P.group(row);
+            head = h * A.G + row - tok * A.G;
+            const uint16_t* src = A.q + b * A.q_batch + tok * A.q_token + head * A.q_head + hl * N;
             uint32_t w[N / 2];
-            if constexpr (N == 2) {
-                w[0] = __ldg(reinterpret_cast<const uint32_t*>(src));
-            } else if constexpr (N == 4) {
+            if constexpr (N == 4) {
                 const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
                 w[0] = v.x; w[1] = v.y;
             } else {
-                const uint4 v = __ldg(reinterpret_cast<const uint4*>(src));
-                w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+#pragma unroll
+                for (int i = 0; i < N / 8; ++i) {
+                    const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + i);
+                    w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+                }
             }
-            float amax = 0.f;
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const uint32_t u = w[i / 2] >> (16 * (i & 1)) & 0xFFFFu;
@@ -286,57 +355,43 @@ __global__ void __launch_bounds__(kThreads, (Config<D, NT>::kCtas)) attend_pages
                 amax = fmaxf(amax, fabsf(x[i]));
             }
             scale = 1.f;
-            if (bf16) {
+        }
+        if (bf16) {
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                if (amax > 0.f && amax < INFINITY) {
-                    const int e = max((int)(__float_as_uint(amax) >> 23) - 127 - 13, -100);
-                    scale = __uint_as_float((uint32_t)(127 + e) << 23);
-                    const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+            for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            if (amax > 0.f && amax < INFINITY) {
+                const int e = max((int)(__float_as_uint(amax) >> 23) - 127 - 13, -100);
+                scale = __uint_as_float((uint32_t)(127 + e) << 23);
+                const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
-                    for (int i = 0; i < N; ++i) x[i] *= inv;
-                }
-            }
-            if (lane == 0) {
-                // to log2 units; with a cap, to 2 log2 e s / cap
-                sm.qscale[r] = MOD && A.cap > 0.f ? scale * (A.scale * (2.f * kLog2e / A.cap)) : scale * (A.scale * kLog2e);
-                sm.slope[r] = MOD && A.slopes ? __ldg(A.slopes + head) * kLog2e : 0.f;
-                sm.qpos[r] = qpos0 + tok;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < N; ++i) x[i] = 0.f;
-            if (lane == 0) {
-                sm.qscale[r] = sm.slope[r] = 0.f;
-                sm.qpos[r] = qpos0;
+                for (int i = 0; i < N; ++i) x[i] *= inv;
             }
         }
-        // dimension d is taken by lane t = d / (D/4) of row r's group at step d % (D/4) / 4
-#pragma unroll
-        for (int i = 0; i < N; i += 2) {
-            const int d = lane * N + i, dt = d / (D / 4), step = d % (D / 4) / 4;
-            reinterpret_cast<uint32_t*>(&sm.qf[r / 8][step][(r % 8) * 4 + dt])[d % 4 / 2] = pack_half(x[i], x[i + 1]);
+        if (hl == 0) {
+            // to log2 units; with a cap, to 2 log2 e s / cap
+            sm.qscale[r] = MOD && A.cap > 0.f ? scale * (A.scale * (2.f * kLog2e / A.cap)) : scale * (A.scale * kLog2e);
+            sm.slope[r] = MOD && A.slopes && row < rows ? __ldg(A.slopes + head) * kLog2e : 0.f;
+            sm.qpos[r] = qpos0 + tok;
         }
+        // dimension d is taken by lane d / (D/4) of the row's group at step d % (D/4) / 4
+#pragma unroll
+        for (int i = 0; i < N; i += 4)
+            sm.qf[r / 8][((hl & 3) * N + i) / 4][(r & 7) * 4 + (hl >> 2)] = make_uint2(pack_half(x[i], x[i + 1]), pack_half(x[i + 2], x[i + 3]));
     }
     __syncthreads();
 
-    constexpr bool kKeepQ = NT == 1 && D <= 128;  // Q in registers
-    uint2 qreg[kKeepQ ? C::kSteps : 1];
-    if (kKeepQ) {
-#pragma unroll
-        for (int i = 0; i < C::kSteps; ++i) qreg[kKeepQ ? i : 0] = sm.qf[0][i][lane];
-    }
     float2 qs[NT];  // rows 8 n + 2 t, + 1
 #pragma unroll
     for (int n = 0; n < NT; ++n) qs[n] = *reinterpret_cast<const float2*>(&sm.qscale[8 * n + 2 * t]);
     const float cap2 = A.cap * kLog2e;
 
-    float acc[C::kSteps][NT][4];  // O^T: dims g D/8 + 2 i (c = 0, 1), + 1 (2, 3); rows 8 n + 2 t, + 1
-    float m[NT][2], l[NT][2];
+    // O^T: dims g D/8 + 2 i (c = 0, 1), + 1 (2, 3); rows 8 n + 2 t (c = 0, 2), + 1 (1, 3)
+    float acc[C::kSteps][NT][4];
+    float2 m[NT], l[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        m[n][0] = m[n][1] = -INFINITY;
-        l[n][0] = l[n][1] = 0.f;
+        m[n] = make_float2(-INFINITY, -INFINITY);
+        l[n] = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < C::kSteps; ++i)
 #pragma unroll
@@ -353,29 +408,20 @@ __global__ void __launch_bounds__(kThreads, (Config<D, NT>::kCtas)) attend_pages
 #pragma unroll 1
     while (used != fill) {
         const bool two = fill - used >= 2;
-        const uint8_t* tile[2];
-        int pos[2];
-        bool partial = !two;
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const uint32_t at = used + (two ? u : 0), st = at % C::kStages;
-            tile[u] = ring + st * C::kChunk;
-            const int word = list[at % kList].y;
-            pos[u] = word & ~15;
-            partial |= word & 1;
-            if (!__all_sync(0xffffffffu, bar_wait(&bar[st], (at / C::kStages) & 1u, deadline))) ok = false;
+        const int4 e = *reinterpret_cast<const int4*>(&list[used % kList]);
+        const uint8_t* tile[2] = {ring + ust * (2 * C::kChunk), ring + ust * (2 * C::kChunk) + (two ? C::kChunk : 0)};
+        const int pos[2] = {e.y & ~15, (two ? e.w : e.y) & ~15};
+        const bool partial = !two || ((e.y | e.w) & 1);
+        if (!__all_sync(0xffffffffu, bar_wait(&bar[ust], phase, deadline))) {
+            ok = false;
+            break;
         }
-        if (!ok) break;
 
         // ---------------- S^T = K Q^T
         float s[2][NT][4];
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int n = 0; n < NT; ++n) s[u][n][0] = s[u][n][1] = s[u][n][2] = s[u][n][3] = 0.f;
         {
             constexpr int W = D / 32;  // words of codes: D/8 bytes of the keys in places g and g + 8
-            uint32_t kw[2][2][W], ku[2][2];
+            uint32_t kw[2][2][W], ku[2][2][D / 64];
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -386,21 +432,21 @@ __global__ void __launch_bounds__(kThreads, (Config<D, NT>::kCtas)) attend_pages
                     if constexpr (D == 64) {
                         const uint2 v = *reinterpret_cast<const uint2*>(src);
                         kw[u][c][0] = v.x; kw[u][c][1] = v.y;
-                        ku[u][c] = *us;
                     } else {
 #pragma unroll
                         for (int i = 0; i < D / 128; ++i) {
                             const uint4 v = reinterpret_cast<const uint4*>(src)[i];
                             kw[u][c][4 * i] = v.x; kw[u][c][4 * i + 1] = v.y; kw[u][c][4 * i + 2] = v.z; kw[u][c][4 * i + 3] = v.w;
                         }
-                        ku[u][c] = D == 128 ? *reinterpret_cast<const uint16_t*>(us) : *reinterpret_cast<const uint32_t*>(us);
                     }
+#pragma unroll
+                    for (int i = 0; i < D / 64; ++i) ku[u][c][i] = us[i];
                 }
 #pragma unroll
             for (int w = 0; w < W; ++w) {  // a word: 8 dims, two steps
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const uint32_t sc0 = scale2(ku[u][0] >> (8 * (w / 2)) & 0xFFu), sc1 = scale2(ku[u][1] >> (8 * (w / 2)) & 0xFFu);
+                    const uint32_t sc0 = scale2(ku[u][0][w / 2]), sc1 = scale2(ku[u][1][w / 2]);
                     uint32_t a[4], c[4];
                     decode_word(kw[u][0][w], a);
                     decode_word(kw[u][1][w], c);
@@ -411,46 +457,52 @@ __global__ void __launch_bounds__(kThreads, (Config<D, NT>::kCtas)) attend_pages
                     }
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        const uint2 q0 = kKeepQ ? qreg[kKeepQ ? 2 * w : 0] : sm.qf[n][2 * w][lane];
-                        const uint2 q1 = kKeepQ ? qreg[kKeepQ ? 2 * w + 1 : 0] : sm.qf[n][2 * w + 1][lane];
-                        mma(s[u][n], a[0], c[0], a[1], c[1], q0.x, q0.y);
+                        const uint2 q0 = sm.qf[n][2 * w][lane], q1 = sm.qf[n][2 * w + 1][lane];
+                        if (w == 0) mma_first(s[u][n], a[0], c[0], a[1], c[1], q0.x, q0.y);
+                        else mma(s[u][n], a[0], c[0], a[1], c[1], q0.x, q0.y);
                         mma(s[u][n], a[2], c[2], a[3], c[3], q1.x, q1.y);
                     }
                 }
             }
         }
 
-        // ---------------- scores in log2 units, masked; s[u][n][c + 2 k]: row c, place g + 8 k
+        // ---------------- scores less the rows' reference maxima, in log2 units; masked.
+        // z[u][n][k]: rows (8 n + 2 t, + 1), place g + 8 k
+        float2 z[2][NT][2], x[2][NT][2];
         if (MOD) {
-            const int last = max(pos[0], pos[1]) + (kTile - 1), moved = last - ref;
-            if (A.slopes && moved > 0) {  // move the origin of the biases
-                ref = last;
+            if (A.slopes) {  // the origin of the biases moves to the last tile so far, the maxima with it
+                const int moved = max(max(pos[0], pos[1]) + (kTile - 1) - ref, 0);
+                ref += moved;
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) m[n][c] -= sm.slope[8 * n + 2 * t + c] * (float)moved;
+                for (int n = 0; n < NT; ++n) {
+                    const float2 sl = *reinterpret_cast<const float2*>(&sm.slope[8 * n + 2 * t]);
+                    m[n] = fma2(sl, make_float2(-(float)moved, -(float)moved), m[n]);
+                }
             }
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const float2 sl = *reinterpret_cast<const float2*>(&sm.slope[8 * n + 2 * t]);
+            for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
+                for (int k = 0; k < 2; ++k) {
+                    const float back = -(float)(ref - (pos[u] + order(g) + 8 * k));
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        float y = s[u][n][c] * (c & 1 ? qs[n].y : qs[n].x);
-                        if (A.cap > 0.f) y = cap2 * tanh_of(y);
-                        s[u][n][c] = y - (c & 1 ? sl.y : sl.x) * (float)(ref - (pos[u] + order(g) + 8 * (c >> 1)));
+                    for (int n = 0; n < NT; ++n) {
+                        float2 y = mul2f(make_float2(s[u][n][2 * k], s[u][n][2 * k + 1]), qs[n]);
+                        if (A.cap > 0.f) y = make_float2(capped(cap2, y.x), capped(cap2, y.y));
+                        if (A.slopes) y = fma2(*reinterpret_cast<const float2*>(&sm.slope[8 * n + 2 * t]), make_float2(back, back), y);
+                        x[u][n][k] = y;
+                        z[u][n][k] = make_float2(y.x - m[n].x, y.y - m[n].y);
                     }
-            }
+                }
         } else {
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) s[u][n][c] *= c & 1 ? qs[n].y : qs[n].x;
+                    for (int k = 0; k < 2; ++k)
+                        z[u][n][k] = fma2(make_float2(s[u][n][2 * k], s[u][n][2 * k + 1]), qs[n], make_float2(-m[n].x, -m[n].y));
         }
-        if (partial) {
+        auto mask = [&]() {  // -inf where a row does not see a key
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -458,66 +510,83 @@ __global__ void __launch_bounds__(kThreads, (Config<D, NT>::kCtas)) attend_pages
                     const int p = pos[u] + order(g) + 8 * k;
                     const bool in = (u == 0 || two) && (!A.start || p >= start || p < prefix);
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int c = 0; c < 2; ++c)
-                            if (!in || p > sm.qpos[8 * n + 2 * t + c]) s[u][n][c + 2 * k] = -INFINITY;
+                    for (int n = 0; n < NT; ++n) {
+                        const int2 at = *reinterpret_cast<const int2*>(&sm.qpos[8 * n + 2 * t]);
+                        if (!in || p > at.x) z[u][n][k].x = -INFINITY;
+                        if (!in || p > at.y) z[u][n][k].y = -INFINITY;
+                    }
                 }
-        }
+        };
+        if (partial) mask();
         bool more = false;
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-                more |= !(fmaxf(fmaxf(s[0][n][c], s[0][n][c + 2]), fmaxf(s[1][n][c], s[1][n][c + 2])) <= m[n][c] + kRescale);
+        for (int n = 0; n < NT; ++n) {
+            const float a = max3(z[0][n][0].x, z[0][n][0].y, z[0][n][1].x), b = max3(z[0][n][1].y, z[1][n][0].x, z[1][n][0].y);
+            more |= !(max3(fmaxf(a, b), z[1][n][1].x, z[1][n][1].y) <= kRescale);
+        }
         if (__any_sync(0xffffffffu, more)) {  // a row's maximum has grown: move every row's reference
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    float top = m[n][c];
+            for (int n = 0; n < NT; ++n) {
+                if (!MOD) {
 #pragma unroll
                     for (int u = 0; u < 2; ++u)
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {  // a NaN counts as +inf, so that the joins keep the row
-                            const float y = s[u][n][c + 2 * k];
-                            top = fmaxf(top, y == y ? y : INFINITY);
-                        }
-#pragma unroll
-                    for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    const float f = top > -INFINITY ? ex2(m[n][c] - top) : 1.f;
-                    m[n][c] = top;
-                    l[n][c] *= f;
-#pragma unroll
-                    for (int i = 0; i < C::kSteps; ++i) {
-                        acc[i][n][c] *= f;
-                        acc[i][n][c + 2] *= f;
-                    }
+                        for (int k = 0; k < 2; ++k) x[u][n][k] = mul2f(make_float2(s[u][n][2 * k], s[u][n][2 * k + 1]), qs[n]);
                 }
+                float2 top = m[n];
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        // a NaN counts as +inf, so that the joins keep the row; a masked key not at all
+                        const float2 y = x[u][n][k], w = z[u][n][k];
+                        if (w.x != -INFINITY) top.x = fmaxf(top.x, y.x == y.x ? y.x : INFINITY);
+                        if (w.y != -INFINITY) top.y = fmaxf(top.y, y.y == y.y ? y.y : INFINITY);
+                    }
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) {
+                    top.x = fmaxf(top.x, __shfl_xor_sync(0xffffffffu, top.x, o));
+                    top.y = fmaxf(top.y, __shfl_xor_sync(0xffffffffu, top.y, o));
+                }
+                const float2 f = make_float2(top.x > -INFINITY ? ex2(m[n].x - top.x) : 1.f, top.y > -INFINITY ? ex2(m[n].y - top.y) : 1.f);
+                m[n] = top;
+                l[n].x *= f.x;
+                l[n].y *= f.y;
+#pragma unroll
+                for (int i = 0; i < C::kSteps; ++i) {
+                    acc[i][n][0] *= f.x;
+                    acc[i][n][1] *= f.y;
+                    acc[i][n][2] *= f.x;
+                    acc[i][n][3] *= f.y;
+                }
+                // a row without a key yet has m = -inf: its weights become 0, not NaN
+                const float2 less = make_float2(top.x > -INFINITY ? top.x : 0.f, top.y > -INFINITY ? top.y : 0.f);
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) z[u][n][k] = make_float2(x[u][n][k].x - less.x, x[u][n][k].y - less.y);
+            }
+            if (partial) mask();
         }
         uint32_t pf[2][NT][2];
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float w[4];
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    w[c] = ex2(s[u][n][c] - m[n][c & 1]);
-                    if (partial && s[u][n][c] == -INFINITY) w[c] = 0.f;  // m is -inf too in a row without a key yet
+                for (int k = 0; k < 2; ++k) {
+                    const float2 w = make_float2(ex2(z[u][n][k].x), ex2(z[u][n][k].y));
+                    l[n] = add2(l[n], w);
+                    pf[u][n][k] = transpose8x8(pack_half(w.x, w.y));
                 }
-                l[n][0] += w[0] + w[2];
-                l[n][1] += w[1] + w[3];
-                pf[u][n][0] = transpose8x8(pack_half(w[0], w[1]));
-                pf[u][n][1] = transpose8x8(pack_half(w[2], w[3]));
-            }
 
         // ---------------- O^T += V^T P
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             if (u == 1 && !two) break;
             constexpr int W = D / 64;  // words of codes of a token: D/8 dims
-            uint32_t vw[4][W], vs[4];  // of the tokens in places 2t, 2t + 1, 2t + 8, 2t + 9
+            constexpr int B = D > 128 ? D / 128 : 1;  // blocks of a lane's dims (D = 64: half of one)
+            uint32_t vw[4][W], vs[4][B];  // of the tokens in places 2t, 2t + 1, 2t + 8, 2t + 9
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const int tok = order(2 * t + (c & 1)) + 8 * (c >> 1);
@@ -525,15 +594,16 @@ __global__ void __launch_bounds__(kThreads, (Config<D, NT>::kCtas)) attend_pages
                 const uint8_t* us = tile[u] + 17 * D + tok * (D / 16);
                 if constexpr (D == 64) {
                     vw[c][0] = *reinterpret_cast<const uint32_t*>(src);
-                    vs[c] = us[g >> 1];
+                    vs[c][0] = us[g >> 1];
                 } else if constexpr (D == 128) {
                     const uint2 v = *reinterpret_cast<const uint2*>(src);
                     vw[c][0] = v.x; vw[c][1] = v.y;
-                    vs[c] = us[g];
+                    vs[c][0] = us[g];
                 } else {
                     const uint4 v = *reinterpret_cast<const uint4*>(src);
                     vw[c][0] = v.x; vw[c][1] = v.y; vw[c][2] = v.z; vw[c][3] = v.w;
-                    vs[c] = *reinterpret_cast<const uint16_t*>(us + 2 * g);
+                    vs[c][0] = us[2 * g];
+                    vs[c][B - 1] = us[2 * g + 1];
                 }
             }
             if (partial) {
@@ -541,13 +611,16 @@ __global__ void __launch_bounds__(kThreads, (Config<D, NT>::kCtas)) attend_pages
                 // weight of 0 would not undo a NaN. One that only later rows see has been
                 // written, but its NaNs must not reach the rows before it: they are taken
                 // out of the product and set in the outputs of the rows that see them.
-                uint32_t nans = 0;  // bit 16 (half of the dims) + token
+                uint32_t nans = 0;  // bit 16 block + token
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     const int tok = order(2 * t + (c & 1)) + 8 * (c >> 1), p = pos[u] + tok;
-                    if (p >= length || (A.start && p < start && p >= prefix)) vs[c] = 0;
-                    if ((vs[c] & 0xFFu) >= 0xF8u) { vs[c] &= 0xFF00u; nans |= 1u << tok; }
-                    if (D == 256 && vs[c] >= 0xF800u) { vs[c] &= 0xFFu; nans |= 0x10000u << tok; }
+                    const bool hidden = p >= length || (A.start && p < start && p >= prefix);
+#pragma unroll
+                    for (int i = 0; i < B; ++i) {
+                        if (!hidden && vs[c][i] >= 0xF8u) nans |= (0x10000u * i + 1u - (uint32_t)i) << tok;
+                        if (hidden || vs[c][i] >= 0xF8u) vs[c][i] = 0;
+                    }
                 }
                 if (__any_sync(0xffffffffu, nans != 0)) {
                     nans |= __shfl_xor_sync(0xffffffffu, nans, 1);
@@ -570,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, (Config<D, NT>::kCtas)) attend_pages
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     decode_word(vw[c][w], d[c]);
-                    const uint32_t sc = scale2(D == 256 ? vs[c] >> (8 * (w / 2)) & 0xFFu : vs[c]);
+                    const uint32_t sc = scale2(vs[c][w / 2]);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) d[c][i] = mul2(d[c][i], sc);
                 }
@@ -585,182 +658,240 @@ __global__ void __launch_bounds__(kThreads, (Config<D, NT>::kCtas)) attend_pages
         }
         __syncwarp();  // every lane has read the stages: refill them
         used += two ? 2 : 1;
+        ust = ust + 1 == C::kStages ? 0 : ust + 1;
+        if (ust == 0) phase ^= 1;
         top_up();
     }
     if (!ok) {
         if (A.status && lane == 0) atomicOr(A.status, 8u /* HS_STATUS_TIMEOUT */);
         // no copy may still be landing when the CTA exits: wait for them, bounded again
         const uint64_t by = global_ns() + kDefaultWaitNs;
-        for (; used != fill; ++used) bar_wait(&bar[used % C::kStages], (used / C::kStages) & 1u, by);
+        for (; used < fill; used += 2) {
+            bar_wait(&bar[ust], phase, by);
+            ust = ust + 1 == C::kStages ? 0 : ust + 1;
+            if (ust == 0) phase ^= 1;
+        }
     }
 
-    // ---------------- join the warps: their outputs in the lanes' order, over the ring
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    // ---------------- join the warps: their outputs in the lanes' order, over the rings
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            float sum = l[n][c];
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (g == 0) {
-                sm.m[warp][8 * n + 2 * t + c] = m[n][c];
-                sm.l[warp][8 * n + 2 * t + c] = sum;
-            }
+        for (int o = 4; o < 32; o <<= 1) {
+            l[n].x += __shfl_xor_sync(0xffffffffu, l[n].x, o);
+            l[n].y += __shfl_xor_sync(0xffffffffu, l[n].y, o);
         }
-    if (lane == 0) sm.wref[warp] = ref;
+        if (g == 0) *reinterpret_cast<float4*>(&sm.ml[warp][8 * n + 2 * t]) = make_float4(m[n].x, l[n].x, m[n].y, l[n].y);
+    }
+    if (MOD && lane == 0) sm.wref[warp] = ref;
     __syncthreads();  // every warp is done with its ring
-    constexpr int kFrags = C::kSteps * NT * 32;
-    float4* part = reinterpret_cast<float4*>(sm.space);  // [warp][step][n][lane]
+    constexpr int kFrags = C::kSteps * NT * 32, kItems = kFrags / 2;
+    float4* part = reinterpret_cast<float4*>(space);  // [warp][step][n][lane], and the CTA's at [warps]
 #pragma unroll
     for (int i = 0; i < C::kSteps; ++i)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
             part[warp * kFrags + (i * NT + n) * 32 + lane] = make_float4(acc[i][n][0], acc[i][n][1], acc[i][n][2], acc[i][n][3]);
-    if (tid < C::kRows) {
-        int last = sm.wref[0];
-        if (MOD)
-            for (int w = 1; w < kWarps; ++w) last = max(last, sm.wref[w]);
-        float mw[kWarps], top = -INFINITY, sum = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            mw[w] = sm.m[w][tid];
-            if (MOD) mw[w] -= sm.slope[tid] * (float)(last - sm.wref[w]);
-            top = fmaxf(top, mw[w]);
-        }
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float f = mw[w] == -INFINITY ? 0.f : ex2(mw[w] - top);  // -inf: the warp saw no key of the row
-            sm.f[w][tid] = f;
-            sum += f * sm.l[w][tid];
-        }
-        sm.cm[tid] = top;
-        sm.cl[tid] = sum;
-        sm.inv[tid] = top > -INFINITY ? 1.f / sum : 0.f;
-        if (tid == 0) sm.cref = last;
-    }
-    __syncthreads();
-    for (int x = tid; x < kFrags; x += kThreads) {
-        const int ln = x % 32, n = x / 32 % NT, i = x / 32 / NT, r = 8 * n + 2 * (ln & 3), d = (ln >> 2) * (D / 8) + 2 * i;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float4 v = part[w * kFrags + x];
-            const float2 f = *reinterpret_cast<const float2*>(&sm.f[w][r]);
-            o.x += f.x * v.x; o.y += f.y * v.y; o.z += f.x * v.z; o.w += f.y * v.w;
-        }
-        *reinterpret_cast<float2*>(&sm.joined[r][d]) = make_float2(o.x, o.z);
-        *reinterpret_cast<float2*>(&sm.joined[r + 1][d]) = make_float2(o.y, o.w);
-    }
-    // ---------------- join the shares, each CTA a part of the rows' elements, and write
     int last = 0;
-    if (nsplit > 1) {
-        cluster_sync();
-        if (MOD) {
-            last = sm.cref;
-            for (int s = 0; s < nsplit; ++s) last = max(last, peer_int(&sm.cref, s));
-        }
-        for (int x = tid; x < nsplit * C::kRows; x += kThreads) {
-            const int s = x / C::kRows, r = x % C::kRows;
-            float ms = peer_float(&sm.cm[r], s);
-            if (MOD) ms -= sm.slope[r] * (float)(last - peer_int(&sm.cref, s));
-            sm.pm[s][r] = ms;
-            sm.pl[s][r] = peer_float(&sm.cl[r], s);
-        }
-        __syncthreads();
-        if (tid < C::kRows) {
-            float top = -INFINITY, sum = 0.f;
-            for (int s = 0; s < nsplit; ++s) top = fmaxf(top, sm.pm[s][tid]);
-            for (int s = 0; s < nsplit; ++s) {
-                const float f = sm.pm[s][tid] == -INFINITY ? 0.f : ex2(sm.pm[s][tid] - top);  // no key in the share
-                sm.f[s][tid] = f;
-                sum += f * sm.pl[s][tid];
+    __syncthreads();
+    if (MOD && A.slopes)
+        for (int w = 0; w < warps; ++w) last = max(last, sm.wref[w]);
+
+    // The sum over `count` partial results of item x -- steps 2 j, 2 j + 1 of a lane: 4
+    // dimensions of rows r, r + 1 -- relative to their largest maxima.
+    struct Joined {
+        float4 a, b;         // steps 2 j and 2 j + 1
+        float2 top, sum;     // of rows r and r + 1
+    };
+    auto join = [&](int x, int count, auto ml_of, auto ref_of, auto frag_of) {
+        const int ln = x & 31, n = x / 32 % NT, j = x / 32 / NT, r = 8 * n + 2 * (ln & 3);
+        const int at = (2 * j * NT + n) * 32 + ln;
+        Joined o;
+        o.a = o.b = make_float4(0.f, 0.f, 0.f, 0.f);
+        o.top = make_float2(-INFINITY, -INFINITY);
+        o.sum = make_float2(0.f, 0.f);
+        const float2 sl = MOD ? *reinterpret_cast<const float2*>(&sm.slope[r]) : make_float2(0.f, 0.f);
+        auto shifted = [&](int w) {  // maxima as from the common origin of the biases, and sums
+            float4 v = ml_of(w, r);
+            if (MOD && A.slopes) {
+                const float back = (float)(last - ref_of(w));
+                v.x -= sl.x * back;
+                v.z -= sl.y * back;
             }
-            sm.pm[0][tid] = top;  // this CTA's own copies: cm and cl are still read by the peers
-            sm.pl[0][tid] = sum;
-            sm.inv[tid] = top > -INFINITY ? 1.f / sum : 0.f;
+            return v;
+        };
+#pragma unroll 4
+        for (int w = 0; w < count; ++w) {
+            const float4 v = shifted(w);
+            o.top = make_float2(fmaxf(o.top.x, v.x), fmaxf(o.top.y, v.z));
         }
-        __syncthreads();
-    } else {
-        if (MOD) last = sm.cref;
-        __syncthreads();
-    }
-    const int todo = min(C::kRows, rows - r0) * (D / 4);
-    for (int x = split * kThreads + tid; x < todo; x += nsplit * kThreads) {
-        const int r = x / (D / 4), d = x % (D / 4) * 4, row = r0 + r;
-        const int tok = row / A.G, head = h * A.G + row - tok * A.G;
-        float4 o;
-        if (nsplit == 1) {
-            o = *reinterpret_cast<const float4*>(&sm.joined[r][d]);
-        } else {
-            o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int w = 0; w < count; ++w) {
+            const float4 v = shifted(w), a = frag_of(w, at), c = frag_of(w, at + NT * 32);
+            // -inf: no key of the row there
+            const float fx = v.x == -INFINITY ? 0.f : ex2(v.x - o.top.x), fy = v.z == -INFINITY ? 0.f : ex2(v.z - o.top.y);
+            o.sum.x += fx * v.y;
+            o.sum.y += fy * v.w;
+            o.a.x += fx * a.x; o.a.y += fy * a.y; o.a.z += fx * a.z; o.a.w += fy * a.w;
+            o.b.x += fx * c.x; o.b.y += fy * c.y; o.b.z += fx * c.z; o.b.w += fy * c.w;
+        }
+        return o;
+    };
+    auto write = [&](int x, const Joined& o) {
+        const int ln = x & 31, n = x / 32 % NT, j = x / 32 / NT, r = 8 * n + 2 * (ln & 3), d = (ln >> 2) * (D / 8) + 4 * j;
 #pragma unroll
-            for (int s = 0; s < kMaxSplit; ++s) {
-                if (s >= nsplit) break;
-                const float4 v = peer_float4(&sm.joined[r][d], s);
-                const float f = sm.f[s][r];
-                o.x += f * v.x; o.y += f * v.y; o.z += f * v.z; o.w += f * v.w;
+        for (int c = 0; c < 2; ++c) {
+            const int row = r0 + r + c;
+            if (row >= rows) break;
+            const int tok = P.group(row), head = h * A.G + row - tok * A.G;
+            const float top = c ? o.top.y : o.top.x, sum = c ? o.sum.y : o.sum.x, inv = top > -INFINITY ? 1.f / sum : 0.f;
+            const float y0 = (c ? o.a.y : o.a.x) * inv, y1 = (c ? o.a.w : o.a.z) * inv, y2 = (c ? o.b.y : o.b.x) * inv,
+                        y3 = (c ? o.b.w : o.b.z) * inv;
+            uint2 w;
+            if (bf16) {
+                const __nv_bfloat162 lo = __floats2bfloat162_rn(y0, y1), hi = __floats2bfloat162_rn(y2, y3);
+                w = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+            } else {
+                w = make_uint2(pack_half(y0, y1), pack_half(y2, y3));
+            }
+            *reinterpret_cast<uint2*>(A.o + b * A.o_batch + tok * A.o_token + head * A.o_head + d) = w;
+            if (d == 0) {
+                float e = -INFINITY;
+                if (top > -INFINITY) {
+                    e = (top + lg2(sum)) * kLn2;
+                    if (MOD && A.slopes) e -= __ldg(A.slopes + head) * (float)(qpos0 + tok - last);
+                }
+                A.lse[((size_t)b * A.Tq + tok) * A.H * A.G + head] = e;
             }
         }
-        const float inv = sm.inv[r];
-        o.x *= inv; o.y *= inv; o.z *= inv; o.w *= inv;
-        uint2 w;
-        if (bf16) {
-            const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x, o.y), hi = __floats2bfloat162_rn(o.z, o.w);
-            w = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-        } else {
-            w = make_uint2(pack_half(o.x, o.y), pack_half(o.z, o.w));
-        }
-        *reinterpret_cast<uint2*>(A.o + b * A.o_batch + tok * A.o_token + head * A.o_head + d) = w;
-        if (d == 0) {
-            const float top = nsplit == 1 ? sm.cm[r] : sm.pm[0][r], sum = nsplit == 1 ? sm.cl[r] : sm.pl[0][r];
-            float e = -INFINITY;
-            if (top > -INFINITY) {
-                e = (top + lg2(sum)) * kLn2;
-                if (MOD && A.slopes) e -= __ldg(A.slopes + head) * (float)(qpos0 + tok - last);
-            }
-            A.lse[((size_t)b * A.Tq + tok) * A.H * A.G + head] = e;
-        }
+    };
+    auto warp_ml = [&](int w, int r) { return *reinterpret_cast<const float4*>(&sm.ml[w][r]); };
+    auto warp_ref = [&](int w) { return sm.wref[w]; };
+    auto warp_frag = [&](int w, int at) { return part[w * kFrags + at]; };
+    if (nsplit == 1) {
+        for (int x = tid; x < kItems; x += threads) write(x, join(x, warps, warp_ml, warp_ref, warp_frag));
+        return;
     }
-    if (nsplit > 1) cluster_sync();  // no CTA may exit while a peer reads its shared memory
+    // ---------------- join the shares, each CTA a part of the items
+    float4* mine = part + warps * kFrags;
+    for (int x = tid; x < kItems; x += threads) {
+        const Joined o = join(x, warps, warp_ml, warp_ref, warp_frag);
+        const int ln = x & 31, n = x / 32 % NT, j = x / 32 / NT, at = (2 * j * NT + n) * 32 + ln;
+        mine[at] = o.a;
+        mine[at + NT * 32] = o.b;
+        if (j == 0 && ln < 4) *reinterpret_cast<float4*>(&sm.cml[8 * n + 2 * ln]) = make_float4(o.top.x, o.sum.x, o.top.y, o.sum.y);
+    }
+    if (tid == 0) sm.cref = last;
+    cluster_sync();
+    if (MOD && A.slopes)
+        for (int s = 0; s < nsplit; ++s) last = max(last, peer_int(&sm.cref, s));
+    for (int x = tid * nsplit + split; x < kItems; x += threads * nsplit)
+        write(x, join(x, nsplit, [&](int s, int r) { return peer_float4(reinterpret_cast<const float*>(&sm.cml[r]), s); },
+                      [&](int s) { return peer_int(&sm.cref, s); },
+                      [&](int s, int at) { return peer_float4(reinterpret_cast<const float*>(mine + at), s); }));
+    cluster_sync();  // no CTA may exit while a peer reads its shared memory
 }
 
-// The shares of a selection: as many as fill the GPU in one wave, at most 8 (the portable
-// cluster size), and no share below two tiles a warp.
-int plan_splits(int64_t jobs, int64_t tiles, int slots) {
-    const int64_t n = std::min((int64_t)slots / (jobs > 0 ? jobs : 1), tiles / (2 * kWarps));
-    return (int)(n < 1 ? 1 : n > kMaxSplit ? kMaxSplit : n);
+// How many clusters of n CTAs of 4 w warps the device holds at once, by [w - 1][n - 1].
+struct Room {
+    int clusters[kMaxWarps / 4][kMaxSplit];
+};
+
+template <int D, int NT, bool MOD>
+cudaError_t set_up(Room* room) {
+    const auto kernel = attend_pages_kernel<D, NT, MOD>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Config<D, NT>::smem(Config<D, NT>::kSmWarps));
+    for (int w = 1; e == cudaSuccess && 4 * w <= Config<D, NT>::kSmWarps; ++w)
+        for (int n = 1; e == cudaSuccess && n <= kMaxSplit; ++n) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(n);
+            cfg.blockDim = dim3(4 * w * 32);
+            cfg.dynamicSmemBytes = Config<D, NT>::smem(4 * w);
+            cudaLaunchAttribute at;
+            at.id = cudaLaunchAttributeClusterDimension;
+            at.val.clusterDim.x = n;
+            at.val.clusterDim.y = at.val.clusterDim.z = 1;
+            cfg.attrs = &at;
+            cfg.numAttrs = 1;
+            e = cudaOccupancyMaxActiveClusters(&room->clusters[w - 1][n - 1], kernel, &cfg);
+        }
+    return e;
+}
+
+// Warps of a CTA and CTAs that share a selection: the pair with the least estimated time, in
+// cycles. A tile takes an SM about `tile` cycles (what its instructions cost at the rate
+// reached with many warps) and a warp's own tiles follow each other at `delay`; a warp's
+// start and end cost about 600 cycles of its SM's time and a CTA 3000 of delay, a cluster's
+// join 1500 more of both. With few jobs the delays decide and more, smaller shares win until a
+// second wave of clusters would be needed: one request, 8 heads, 128 tiles: 64 CTAs of 8
+// warps 6.3 us, of 4 warps 7.0, of 16 warps 7.8. With many the work does and shares only
+// cost: 512 jobs of 128 tiles: whole ones 37.2 us, halves 39.7, quarters 58.
+void plan(const Room& room, int sm_warps, int num_sms, int D, int NT, int64_t jobs, int64_t tiles, int* warps, int* shares) {
+    const float tile = 12.f + 0.55f * D + NT * (14.f + 0.16f * D), delay = 750.f + 200.f * NT;
+    float best = INFINITY;
+    *warps = 4;
+    *shares = 1;
+    for (int n = 1; n <= kMaxSplit; ++n)
+        for (int w = 4; w <= sm_warps; w += 4) {
+            const int fit = room.clusters[w / 4 - 1][n - 1];
+            if (fit < 1 || ((n > 1 || w > 4) && 2 * (int64_t)n * w > tiles)) continue;
+            const float ctas = (float)jobs * n, share = (float)tiles / n;
+            const float work = ceilf(ctas / num_sms) * (share * tile + 600.f * w + (n > 1 ? 1500.f : 0.f));
+            const float chain = ceilf(ctas / (fit * n)) * (3000.f + (n > 1 ? 1500.f : 0.f) + ceilf(share / w) * delay);
+            const float time = fmaxf(work, chain);
+            if (time < best) {
+                best = time;
+                *warps = w;
+                *shares = n;
+            }
+        }
 }
 
 template <int D, int NT, bool MOD>
 cudaError_t launch(cudaStream_t stream, bool bf16, const PageAttention& a, int num_sms) {
     using C = Config<D, NT>;
-    const auto kernel = attend_pages_kernel<D, NT, MOD>;
-    constexpr int smem = sizeof(Smem<D, NT>);
-    static_assert(smem * C::kCtas <= 227 * 1024, "shared memory");
-    static std::atomic<uint64_t> done{0};  // devices on which the kernel may use this much shared memory
+    constexpr int kDevices = 64;
+    static std::mutex lock;
+    static std::atomic<bool> ready[kDevices];
+    static Room rooms[kDevices];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (dev >= 64 || !(done.load() >> dev & 1)) {
-        if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
-        if (dev < 64) done.fetch_or(1ull << dev);
+    if (dev >= kDevices) return cudaErrorInvalidDevice;
+    if (!ready[dev].load(std::memory_order_acquire)) {
+        std::lock_guard<std::mutex> hold(lock);
+        if ((e = set_up<D, NT, MOD>(&rooms[dev])) != cudaSuccess) return e;
+        ready[dev].store(true, std::memory_order_release);
     }
     const int row_tiles = (a.G * a.Tq + C::kRows - 1) / C::kRows;
-    const int64_t jobs = (int64_t)a.B * a.H * row_tiles;
-    const int nsplit = plan_splits(jobs, (int64_t)a.k * a.tiles, num_sms * C::kCtas);
-    if (jobs * nsplit > 0x7fffffff) return cudaErrorInvalidValue;
+    const int64_t jobs = (int64_t)a.B * a.H * row_tiles, tiles = (int64_t)a.k * a.tiles;
+    int warps, shares;
+    plan(rooms[dev], C::kSmWarps, num_sms, D, NT, jobs, tiles, &warps, &shares);
+    if (jobs * shares > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    Split p;
+    p.shares = Divisor(shares);
+    p.row_tiles = Divisor(row_tiles);
+    p.heads = Divisor(a.H);
+    p.tiles = Divisor(a.tiles);
+    p.group = Divisor(a.G);
+    p.ntiles = (int)tiles;
+    p.groups = (int)((tiles + 32 * shares * warps - 1) / (32 * shares * warps));
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(jobs * nsplit));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.gridDim = dim3((unsigned)(jobs * shares));
+    cfg.blockDim = dim3(warps * 32);
+    cfg.dynamicSmemBytes = C::smem(warps);
     cfg.stream = stream;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)nsplit;
+    at[0].val.clusterDim.x = (unsigned)shares;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, a, nsplit, row_tiles, bf16);
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, attend_pages_kernel<D, NT, MOD>, a, p, bf16);
 }
 
 template <int D, bool MOD>
