@@ -25,6 +25,19 @@ struct PageShape {
     }
 };
 
+#ifdef __CUDACC__
+// n / d for 0 <= n < 2^31 by a multiplication (Granlund and Montgomery, 1994).
+struct Divisor {
+    uint32_t d, m, s;
+    Divisor() = default;
+    explicit Divisor(uint32_t by) : d(by), m(0), s(0) {
+        while ((1ull << s) < by) ++s;
+        m = (uint32_t)((((1ull << s) - by) << 32) / by + 1);
+    }
+    __device__ __forceinline__ int operator()(int n) const { return (int)((__umulhi((uint32_t)n, m) + (uint32_t)n) >> s); }
+};
+#endif
+
 // K and V rows of n tokens, 16-bit floats: row (token i, head h) starts i * token + h * head
 // elements into the tensor, 16-byte aligned.
 struct TokenRows {

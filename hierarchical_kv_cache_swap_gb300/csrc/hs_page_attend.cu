@@ -61,17 +61,6 @@ constexpr int kList = 64;              // a warp's list of live tiles (a ring; 3
 constexpr float kRescale = 8.f;        // a row's reference maximum moves when exceeded by 2^8
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 
-// n / d for 0 <= n < 2^31 by a multiplication (Granlund and Montgomery, 1994).
-struct Divisor {
-    uint32_t d, m, s;
-    Divisor() = default;
-    explicit Divisor(uint32_t by) : d(by), m(0), s(0) {
-        while ((1ull << s) < by) ++s;
-        m = (uint32_t)((((1ull << s) - by) << 32) / by + 1);
-    }
-    __device__ __forceinline__ int operator()(int n) const { return (int)((__umulhi((uint32_t)n, m) + (uint32_t)n) >> s); }
-};
-
 // A call's work split: job (request, KV head, tile of rows) x share.
 struct Split {
     Divisor shares, row_tiles, heads, tiles, group;  // CTAs of a job; ...; tiles of a page; query heads of a KV head
