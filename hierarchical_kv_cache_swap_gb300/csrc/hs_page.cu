@@ -34,23 +34,26 @@ __device__ __forceinline__ float to_float(uint16_t bits) {
 
 __device__ __forceinline__ float scale_value(uint32_t u) { return __half2float(__ushort_as_half((uint16_t)(u << 7))); }
 
-// The scale byte nearest to t >= 0. In the normal range the byte is the top of t's own bits
-// (re-biased), rounded to three fraction bits; below it the scales are multiples of 2^-17.
-__device__ __forceinline__ uint32_t scale_byte(float t) {
-    const uint32_t b = __float_as_uint(t);
-    uint32_t u;
-    if (t >= 6.103515625e-5f) {  // 2^-14
-        u = ((b + 0x7FFFFu + ((b >> 20) & 1u)) >> 20) - ((127 - 15) << 3);
-    } else {
-        u = (uint32_t)__float2int_rn(t * 131072.f);  // 2^17
-    }
+// The scale byte nearest to a / 6, a >= 0 a 16-bit float. a times the rounded sixth is off by
+// 2^-23; a quotient half-way between two scales has at most eight significant bits and any
+// other differs from it by 2^-12, so bringing the product to 16 bits first restores the ties.
+// In the normal range the byte is then the top of the quotient's own bits (re-biased), rounded
+// to three fraction bits; below it the scales are multiples of 2^-17.
+__device__ __forceinline__ uint32_t scale_byte(float a) {
+    const uint32_t b = (__float_as_uint(a * (1.f / 6.f)) + 0x80u) & 0xFFFFFF00u;
+    const float t = __uint_as_float(b);
+    const uint32_t normal = ((b + 0x7FFFFu + ((b >> 20) & 1u)) >> 20) - ((127 - 15) << 3);
+    const uint32_t u = t >= 6.103515625e-5f /* 2^-14 */ ? normal : (uint32_t)__float2int_rn(t * 131072.f /* 2^17 */);
     return min(u, (uint32_t)kTopScale);
 }
 
-// Two values to two codes in a byte (a: low half).
-__device__ __forceinline__ uint32_t codes2(float a, float b) {
+// Eight values, in pairs, to eight codes (the first in the lowest bits).
+__device__ __forceinline__ uint32_t codes8(const float2 (&y)[4]) {
     uint32_t r;
-    asm("{ .reg .b8 c; cvt.rn.satfinite.e2m1x2.f32 c, %2, %1; mov.b32 %0, {c, 0, 0, 0}; }" : "=r"(r) : "f"(a), "f"(b));
+    asm("{ .reg .b8 a, b, c, d; cvt.rn.satfinite.e2m1x2.f32 a, %2, %1; cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;"
+        " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5; cvt.rn.satfinite.e2m1x2.f32 d, %8, %7; mov.b32 %0, {a, b, c, d}; }"
+        : "=r"(r)
+        : "f"(y[0].x), "f"(y[0].y), "f"(y[1].x), "f"(y[1].y), "f"(y[2].x), "f"(y[2].y), "f"(y[3].x), "f"(y[3].y));
     return r;
 }
 
@@ -58,6 +61,15 @@ __device__ __forceinline__ uint32_t codes2(float a, float b) {
 __device__ __forceinline__ uint32_t one_zero(uint32_t w) {
     const uint32_t some = (w | w >> 1 | w >> 2) & 0x11111111u;  // magnitudes that are not zero
     return w & (0x77777777u | some << 3);
+}
+
+// x * inv to multiples of 2^-13, two values at a time.
+__device__ __forceinline__ float2 round13(float2 x, float inv) {
+    float2 y;
+    asm("{ .reg .b64 a, b, c, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %4}; mov.b64 c, {%5, %5}; fma.rn.f32x2 d, a, b, c;"
+        " mov.b64 c, {%6, %6}; add.rn.f32x2 d, d, c; mov.b64 {%0, %1}, d; }"
+        : "=f"(y.x), "=f"(y.y) : "f"(x.x), "f"(x.y), "f"(inv), "f"(1536.f), "f"(-1536.f));
+    return y;
 }
 
 struct Block {
@@ -69,28 +81,31 @@ struct Block {
 template <bool BF16>
 __device__ __forceinline__ Block quantise(const uint32_t (&w)[8]) {
     // the magnitudes' bits order like the magnitudes, infinities and NaNs above every number
-    uint32_t m = 0;
+    uint32_t m = w[0] & 0x7FFF7FFFu;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+    for (int i = 1; i < 7; i += 2) m = __vimax3_u16x2(m, w[i] & 0x7FFF7FFFu, w[i + 1] & 0x7FFF7FFFu);
+    m = __vmaxu2(m, w[7] & 0x7FFF7FFFu);
     m = max(m & 0xFFFFu, m >> 16);
     const bool bad = m >= (BF16 ? 0x7F80u : 0x7C00u);
     Block r;
-    r.u = bad ? 0u : scale_byte(to_float<BF16>((uint16_t)m) / 6.f);
-    const float inv = r.u ? 1.f / scale_value(r.u) : 0.f;
+    r.u = bad ? 0u : scale_byte(to_float<BF16>((uint16_t)m));
+    float inv = 0.f;
+    if (r.u) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(scale_value(r.u)));
     // x / s decides ties exactly although 1 / s is rounded: x * inv is brought to multiples of
     // 2^-13 (adding 1536 leaves 13 fraction bits), which every border between codes is. A
-    // quotient on a border is off by 2^-24 relative before that and lands on it again; one that
+    // quotient on a border is off by 2^-22 relative before that and lands on it again; one that
     // is not differs from the border t s by at least one unit of x's last place, so by 2^-11
     // relative, 2^-13 at the smallest border (1/4): it stays on its side.
-    uint32_t c[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float a = __fmaf_rn(to_float<BF16>((uint16_t)w[i]), inv, 1536.f) - 1536.f;
-        const float b = __fmaf_rn(to_float<BF16>((uint16_t)(w[i] >> 16)), inv, 1536.f) - 1536.f;
-        c[i] = codes2(a, b);
+    for (int c = 0; c < 2; ++c) {
+        float2 y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t x = w[4 * c + i];
+            y[i] = round13(make_float2(to_float<BF16>((uint16_t)x), to_float<BF16>((uint16_t)(x >> 16))), inv);
+        }
+        (c ? r.hi : r.lo) = one_zero(codes8(y));
     }
-    r.lo = one_zero(c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24);
-    r.hi = one_zero(c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24);
     if (bad) {
         r.lo = r.hi = 0;
         r.u = kBadScale;
@@ -284,8 +299,8 @@ cudaError_t write_any(cudaStream_t stream, const PageShape& ps, bool bf16, const
                       int num_sms) {
     if (n == 0) return cudaSuccess;
     // One group of tokens a warp, but at most kWave CTAs an SM, which then take further groups:
-    // 131072 tokens, 8 heads of 128: 112 us with 16, 114 with 8, 131 without a limit.
-    constexpr int kWave = 16;
+    // 131072 tokens, 8 heads of 128: 112.5 us with 16, 105.0 (6.55 TB/s) with 32, 107.6 with 128.
+    constexpr int kWave = 32;
     const int64_t per = (int64_t)(kThreads / 32) * (512 / ps.dim);
     const int64_t ctas = (n + per - 1) / per, most = ((int64_t)num_sms * kWave + ps.heads - 1) / ps.heads;
     const dim3 grid((unsigned)(ctas < most ? ctas : most), (unsigned)ps.heads);
