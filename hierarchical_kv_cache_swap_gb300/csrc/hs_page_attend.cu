@@ -76,30 +76,26 @@ struct Config {
     // Warps of an SM: what the registers allow (96, 128, 168 or 255 of them)
     static constexpr int kSmWarps = D == 256 ? 8 : NT == 1 ? 20 : NT * D <= 128 ? 16 : NT * D <= 256 ? 12 : 8;
     static constexpr int kStages = D == 64 ? 4 : 2;  // of two tiles
-    // shared memory of a warp: its ring and its list; over the rings, at the end, the warps'
-    // outputs and the CTA's
-    static constexpr int kRing = kStages * 2 * kChunk, kListBytes = kList * 8;
-    static constexpr int kPart = kRows * D * 4;
-    __host__ __device__ static constexpr int space(int warps) {
-        return warps * kRing > (warps + 1) * kPart ? warps * kRing : (warps + 1) * kPart;
-    }
-    static int smem(int warps);
+    // shared memory of a warp: its ring, over it at the end its outputs, and its list
+    static constexpr int kRing = kStages * 2 * kChunk, kPart = kRows * D * 4, kListBytes = kList * 8;
+    static constexpr int kSpace = (kRing > kPart ? kRing : kPart) + kListBytes;
+    static int smem(int warps, int shares);
 };
 
 template <int D, int NT>
-struct Fixed {  // followed by the rings and the lists
+struct Fixed {  // followed by the warps' regions and, with several shares, theirs (kPart and a little)
     using C = Config<D, NT>;
     uint2 qf[NT][C::kSteps][32];              // Q as the lanes take it
     alignas(8) float qscale[C::kRows], slope[C::kRows];  // of the rows: to log2 units
     int qpos[C::kRows];
     alignas(16) float2 ml[kMaxWarps][C::kRows];  // the warps' maxima and sums
-    alignas(16) float2 cml[C::kRows];            // this CTA's
-    int wref[kMaxWarps], cref;                   // positions that biases are relative to
+    alignas(16) float2 xml[kMaxSplit][C::kRows]; // the shares'
+    int wref[kMaxWarps], xref[kMaxSplit];        // positions that biases are relative to
     uint64_t bar[kMaxWarps][C::kStages];
 };
 template <int D, int NT>
-int Config<D, NT>::smem(int warps) {
-    return (int)((sizeof(Fixed<D, NT>) + 127) / 128 * 128) + space(warps) + warps * kListBytes;
+int Config<D, NT>::smem(int warps, int shares) {
+    return (int)((sizeof(Fixed<D, NT>) + 127) / 128 * 128) + warps * kSpace + (shares > 1 ? kPart + shares * 32 : 0);
 }
 
 __device__ __forceinline__ uint32_t su32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -201,26 +197,19 @@ __device__ __forceinline__ void copy_in(void* dst, const uint8_t* src, uint32_t 
                  : "memory");
 }
 
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.aligned; barrier.cluster.wait.aligned;" ::: "memory");
-}
-// A float of another CTA of the cluster, at the place of this CTA's `p`.
-__device__ __forceinline__ float peer_float(const float* p, int rank) {
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// Stores to the place of `p` in another CTA of the cluster.
+__device__ __forceinline__ uint32_t peer(const void* p, int rank) {
     uint32_t a;
-    float v;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(su32(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-    return v;
+    return a;
 }
-__device__ __forceinline__ float4 peer_float4(const float* p, int rank) {
-    uint32_t a;
-    float4 v;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(su32(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
-    return v;
+__device__ __forceinline__ void peer_store(void* p, int rank, const float4& v) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(peer(p, rank)), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
 }
-__device__ __forceinline__ int peer_int(const int* p, int rank) {
-    return __float_as_int(peer_float(reinterpret_cast<const float*>(p), rank));
+__device__ __forceinline__ void peer_store(int* p, int rank, int v) {
+    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(peer(p, rank)), "r"(v) : "memory");
 }
 
 // MOD: scores are capped or biased.
@@ -239,15 +228,17 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
     const int bh = P.row_tiles(job), r0 = (job - bh * (int)P.row_tiles.d) * C::kRows;
     const int b = P.heads(bh), h = bh - b * A.H;
     const int rows = A.G * A.Tq;
-    uint8_t* ring = space + warp * C::kRing;
+    uint8_t* ring = space + warp * C::kSpace;
     uint64_t* bar = sm.bar[warp];
-    int2* list = reinterpret_cast<int2*>(space + C::space(warps) + warp * C::kListBytes);
+    int2* list = reinterpret_cast<int2*>(ring + C::kSpace - C::kListBytes);
     if (lane < C::kStages) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(su32(bar + lane)) : "memory");
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     __syncwarp();
 
+    if (nsplit > 1) cluster_arrive();  // waited for before the first store to another CTA
     // The launch may begin before the kernel ahead of it on the stream is done: nothing that
     // it reads or writes is touched before this.
+    asm volatile("" ::"l"(A.slots), "l"(A.sel), "l"(A.lengths), "l"(A.q), "l"(A.pages), "r"(P.ntiles), "r"(P.tiles.m), "r"(P.group.m));
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
     // ---------------- this warp's tiles: every (nsplit * kWarps)-th of the selection. Lane i
@@ -273,6 +264,26 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
     const int qpos0 = length - A.Tq;  // may be negative
     const uint8_t* pages = A.pages + ((size_t)b * A.S * A.tiles * A.H + h) * C::kChunk;
     const size_t unit_bytes = (size_t)A.H * C::kChunk;
+
+    // the first of this warp's query rows (half a warp a row), on their way meanwhile
+    constexpr int kQ = D / 16;  // values of a lane
+    const int hl = lane & 15;
+    uint32_t qw[kQ / 2];
+    auto load_q = [&](int r) {
+        const int row = min(r0 + r, rows - 1), tok = P.group(row), head = h * A.G + row - tok * A.G;
+        const uint16_t* src = A.q + b * A.q_batch + tok * A.q_token + head * A.q_head + hl * kQ;
+        if constexpr (kQ == 4) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
+            qw[0] = v.x; qw[1] = v.y;
+        } else {
+#pragma unroll
+            for (int i = 0; i < kQ / 8; ++i) {
+                const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + i);
+                qw[4 * i] = v.x; qw[4 * i + 1] = v.y; qw[4 * i + 2] = v.z; qw[4 * i + 3] = v.w;
+            }
+        }
+    };
+    if (2 * warp < C::kRows) load_q(2 * warp + (lane >> 4));
 
     int groups = P.groups;                  // not yet on the list
     uint32_t fill = 0, used = 0, tail = 0;  // listed tiles copied (or on their way), consumed, listed
@@ -315,31 +326,16 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
     for (int i = 0; i < C::kStages; ++i) top_up();
 
     // ---------------- the query rows as halves, in the lanes' order
-    for (int r2 = 2 * warp; r2 < C::kRows; r2 += 2 * warps) {  // half a warp a row
-        constexpr int N = D / 16;
-        const int hl = lane & 15, r = r2 + (lane >> 4), row = r0 + r;
-        float x[N], scale = 0.f, amax = 0.f;
-        int tok = 0, head = 0;
+    for (int r2 = 2 * warp; r2 < C::kRows; r2 += 2 * warps) {
+        const int r = r2 + (lane >> 4), row = r0 + r, tok = P.group(min(row, rows - 1));
+        float x[kQ], scale = 0.f, amax = 0.f;
+        if (r2 != 2 * warp) load_q(r);
 #pragma unroll
-        for (int i = 0; i < N; ++i) x[i] = 0.f;
+        for (int i = 0; i < kQ; ++i) x[i] = 0.f;
         if (row < rows) {
-            tok = P.group(row);
-            head = h * A.G + row - tok * A.G;
-            const uint16_t* src = A.q + b * A.q_batch + tok * A.q_token + head * A.q_head + hl * N;
-            uint32_t w[N / 2];
-            if constexpr (N == 4) {
-                const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
-                w[0] = v.x; w[1] = v.y;
-            } else {
 #pragma unroll
-                for (int i = 0; i < N / 8; ++i) {
-                    const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + i);
-                    w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const uint32_t u = w[i / 2] >> (16 * (i & 1)) & 0xFFFFu;
+            for (int i = 0; i < kQ; ++i) {
+                const uint32_t u = qw[i / 2] >> (16 * (i & 1)) & 0xFFFFu;
                 x[i] = bf16 ? __uint_as_float(u << 16) : __half2float(__ushort_as_half((uint16_t)u));
                 amax = fmaxf(amax, fabsf(x[i]));
             }
@@ -353,19 +349,19 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
                 scale = __uint_as_float((uint32_t)(127 + e) << 23);
                 const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
-                for (int i = 0; i < N; ++i) x[i] *= inv;
+                for (int i = 0; i < kQ; ++i) x[i] *= inv;
             }
         }
         if (hl == 0) {
             // to log2 units; with a cap, to 2 log2 e s / cap
             sm.qscale[r] = MOD && A.cap > 0.f ? scale * (A.scale * (2.f * kLog2e / A.cap)) : scale * (A.scale * kLog2e);
-            sm.slope[r] = MOD && A.slopes && row < rows ? __ldg(A.slopes + head) * kLog2e : 0.f;
+            sm.slope[r] = MOD && A.slopes && row < rows ? __ldg(A.slopes + h * A.G + row - tok * A.G) * kLog2e : 0.f;
             sm.qpos[r] = qpos0 + tok;
         }
         // dimension d is taken by lane d / (D/4) of the row's group at step d % (D/4) / 4
 #pragma unroll
-        for (int i = 0; i < N; i += 4)
-            sm.qf[r / 8][((hl & 3) * N + i) / 4][(r & 7) * 4 + (hl >> 2)] = make_uint2(pack_half(x[i], x[i + 1]), pack_half(x[i + 2], x[i + 3]));
+        for (int i = 0; i < kQ; i += 4)
+            sm.qf[r / 8][((hl & 3) * kQ + i) / 4][(r & 7) * 4 + (hl >> 2)] = make_uint2(pack_half(x[i], x[i + 1]), pack_half(x[i + 2], x[i + 3]));
     }
     __syncthreads();
 
@@ -675,56 +671,68 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
         if (g == 0) *reinterpret_cast<float4*>(&sm.ml[warp][8 * n + 2 * t]) = make_float4(m[n].x, l[n].x, m[n].y, l[n].y);
     }
     if (MOD && lane == 0) sm.wref[warp] = ref;
-    __syncthreads();  // every warp is done with its ring
     constexpr int kFrags = C::kSteps * NT * 32, kItems = kFrags / 2;
-    float4* part = reinterpret_cast<float4*>(space);  // [warp][step][n][lane], and the CTA's at [warps]
+    auto part = [&](int w) { return reinterpret_cast<float4*>(space + w * C::kSpace); };  // of a warp: [step][n][lane]
 #pragma unroll
     for (int i = 0; i < C::kSteps; ++i)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-            part[warp * kFrags + (i * NT + n) * 32 + lane] = make_float4(acc[i][n][0], acc[i][n][1], acc[i][n][2], acc[i][n][3]);
+            part(warp)[(i * NT + n) * 32 + lane] = make_float4(acc[i][n][0], acc[i][n][1], acc[i][n][2], acc[i][n][3]);
     int last = 0;
     __syncthreads();
     if (MOD && A.slopes)
         for (int w = 0; w < warps; ++w) last = max(last, sm.wref[w]);
 
-    // The sum over `count` partial results of item x -- steps 2 j, 2 j + 1 of a lane: 4
-    // dimensions of rows r, r + 1 -- relative to their largest maxima.
+    // The sum of partial results of item x -- steps 2 j, 2 j + 1 of a lane: 4 dimensions of rows
+    // r, r + 1 -- relative to their largest maxima, kBatch of them at a time (their loads are
+    // all on their way before the first is used).
     struct Joined {
-        float4 a, b;         // steps 2 j and 2 j + 1
-        float2 top, sum;     // of rows r and r + 1
+        float4 a, b;      // steps 2 j and 2 j + 1
+        float2 top, sum;  // of rows r and r + 1
     };
+    constexpr int kBatch = 4;
     auto join = [&](int x, int count, auto ml_of, auto ref_of, auto frag_of) {
-        const int ln = x & 31, n = x / 32 % NT, j = x / 32 / NT, r = 8 * n + 2 * (ln & 3);
-        const int at = (2 * j * NT + n) * 32 + ln;
+        const int n = x / 32 % NT, r = 8 * n + 2 * (x & 3);
         Joined o;
         o.a = o.b = make_float4(0.f, 0.f, 0.f, 0.f);
         o.top = make_float2(-INFINITY, -INFINITY);
         o.sum = make_float2(0.f, 0.f);
         const float2 sl = MOD ? *reinterpret_cast<const float2*>(&sm.slope[r]) : make_float2(0.f, 0.f);
-        auto shifted = [&](int w) {  // maxima as from the common origin of the biases, and sums
-            float4 v = ml_of(w, r);
-            if (MOD && A.slopes) {
-                const float back = (float)(last - ref_of(w));
-                v.x -= sl.x * back;
-                v.z -= sl.y * back;
+        for (int w0 = 0; w0 < count; w0 += kBatch) {
+            float4 v[kBatch], a[kBatch], c[kBatch];
+            int back[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int w = min(w0 + i, count - 1);
+                v[i] = ml_of(w, r);
+                a[i] = frag_of(w, x, 0);
+                c[i] = frag_of(w, x, 1);
+                back[i] = MOD ? last - ref_of(w) : 0;
             }
-            return v;
-        };
-#pragma unroll 4
-        for (int w = 0; w < count; ++w) {
-            const float4 v = shifted(w);
-            o.top = make_float2(fmaxf(o.top.x, v.x), fmaxf(o.top.y, v.z));
-        }
-#pragma unroll 4
-        for (int w = 0; w < count; ++w) {
-            const float4 v = shifted(w), a = frag_of(w, at), c = frag_of(w, at + NT * 32);
+            float2 top = o.top;
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                if (MOD) {  // as from the common origin of the biases
+                    v[i].x -= sl.x * (float)back[i];
+                    v[i].z -= sl.y * (float)back[i];
+                }
+                if (w0 + i >= count) v[i].x = v[i].z = -INFINITY;
+                top = make_float2(fmaxf(top.x, v[i].x), fmaxf(top.y, v[i].z));
+            }
             // -inf: no key of the row there
-            const float fx = v.x == -INFINITY ? 0.f : ex2(v.x - o.top.x), fy = v.z == -INFINITY ? 0.f : ex2(v.z - o.top.y);
-            o.sum.x += fx * v.y;
-            o.sum.y += fy * v.w;
-            o.a.x += fx * a.x; o.a.y += fy * a.y; o.a.z += fx * a.z; o.a.w += fy * a.w;
-            o.b.x += fx * c.x; o.b.y += fy * c.y; o.b.z += fx * c.z; o.b.w += fy * c.w;
+            const float ox = o.top.x == -INFINITY ? 0.f : ex2(o.top.x - top.x), oy = o.top.y == -INFINITY ? 0.f : ex2(o.top.y - top.y);
+            o.top = top;
+            o.sum = make_float2(o.sum.x * ox, o.sum.y * oy);
+            o.a = make_float4(o.a.x * ox, o.a.y * oy, o.a.z * ox, o.a.w * oy);
+            o.b = make_float4(o.b.x * ox, o.b.y * oy, o.b.z * ox, o.b.w * oy);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const float fx = v[i].x == -INFINITY ? 0.f : ex2(v[i].x - top.x), fy = v[i].z == -INFINITY ? 0.f : ex2(v[i].z - top.y);
+                o.sum.x += fx * v[i].y;
+                o.sum.y += fy * v[i].w;
+                o.a.x += fx * a[i].x; o.a.y += fy * a[i].y; o.a.z += fx * a[i].z; o.a.w += fy * a[i].w;
+                o.b.x += fx * c[i].x; o.b.y += fy * c[i].y; o.b.z += fx * c[i].z; o.b.w += fy * c[i].w;
+            }
         }
         return o;
     };
@@ -758,29 +766,33 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
     };
     auto warp_ml = [&](int w, int r) { return *reinterpret_cast<const float4*>(&sm.ml[w][r]); };
     auto warp_ref = [&](int w) { return sm.wref[w]; };
-    auto warp_frag = [&](int w, int at) { return part[w * kFrags + at]; };
+    auto warp_frag = [&](int w, int x, int k) { return part(w)[((2 * (x / 32 / NT) + k) * NT + x / 32 % NT) * 32 + (x & 31)]; };
     if (nsplit == 1) {
         for (int x = tid; x < kItems; x += threads) write(x, join(x, warps, warp_ml, warp_ref, warp_frag));
         return;
     }
-    // ---------------- join the shares, each CTA a part of the items
-    float4* mine = part + warps * kFrags;
+    // ---------------- join the shares: item x is sent to CTA x % nsplit, which joins and writes it
+    const int per = (kItems + nsplit - 1) / nsplit;
+    float4* frags = reinterpret_cast<float4*>(space + warps * C::kSpace);  // [share][item / nsplit][2]
+    cluster_wait();
     for (int x = tid; x < kItems; x += threads) {
         const Joined o = join(x, warps, warp_ml, warp_ref, warp_frag);
-        const int ln = x & 31, n = x / 32 % NT, j = x / 32 / NT, at = (2 * j * NT + n) * 32 + ln;
-        mine[at] = o.a;
-        mine[at + NT * 32] = o.b;
-        if (j == 0 && ln < 4) *reinterpret_cast<float4*>(&sm.cml[8 * n + 2 * ln]) = make_float4(o.top.x, o.sum.x, o.top.y, o.sum.y);
+        const int ix = P.shares(x), to = x - ix * nsplit;
+        peer_store(frags + (split * per + ix) * 2, to, o.a);
+        peer_store(frags + (split * per + ix) * 2 + 1, to, o.b);
+        if (x / 32 / NT == 0 && (x & 31) < 4)  // the row pair's first item
+            for (int s = 0; s < nsplit; ++s)
+                peer_store(reinterpret_cast<float4*>(&sm.xml[split][8 * (x / 32) + 2 * (x & 3)]), s, make_float4(o.top.x, o.sum.x, o.top.y, o.sum.y));
     }
-    if (tid == 0) sm.cref = last;
-    cluster_sync();
-    if (MOD && A.slopes)
-        for (int s = 0; s < nsplit; ++s) last = max(last, peer_int(&sm.cref, s));
-    for (int x = tid * nsplit + split; x < kItems; x += threads * nsplit)
-        write(x, join(x, nsplit, [&](int s, int r) { return peer_float4(reinterpret_cast<const float*>(&sm.cml[r]), s); },
-                      [&](int s) { return peer_int(&sm.cref, s); },
-                      [&](int s, int at) { return peer_float4(reinterpret_cast<const float*>(mine + at), s); }));
-    cluster_sync();  // no CTA may exit while a peer reads its shared memory
+    if (MOD && tid < nsplit) peer_store(&sm.xref[split], tid, last);
+    cluster_arrive();
+    cluster_wait();
+    if (MOD)
+        for (int s = 0; s < nsplit; ++s) last = max(last, sm.xref[s]);
+    for (int ix = tid; ix * nsplit + split < kItems; ix += threads)
+        write(ix * nsplit + split, join(ix * nsplit + split, nsplit, [&](int s, int r) { return *reinterpret_cast<const float4*>(&sm.xml[s][r]); },
+                                        [&](int s) { return sm.xref[s]; },
+                                        [&](int s, int, int k) { return frags[(s * per + ix) * 2 + k]; }));
 }
 
 // How many clusters of n CTAs of 4 w warps the device holds at once, by [w - 1][n - 1].
@@ -791,13 +803,13 @@ struct Room {
 template <int D, int NT, bool MOD>
 cudaError_t set_up(Room* room) {
     const auto kernel = attend_pages_kernel<D, NT, MOD>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Config<D, NT>::smem(Config<D, NT>::kSmWarps));
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Config<D, NT>::smem(Config<D, NT>::kSmWarps, kMaxSplit));
     for (int w = 1; e == cudaSuccess && 4 * w <= Config<D, NT>::kSmWarps; ++w)
         for (int n = 1; e == cudaSuccess && n <= kMaxSplit; ++n) {
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3(n);
             cfg.blockDim = dim3(4 * w * 32);
-            cfg.dynamicSmemBytes = Config<D, NT>::smem(4 * w);
+            cfg.dynamicSmemBytes = Config<D, NT>::smem(4 * w, n);
             cudaLaunchAttribute at;
             at.id = cudaLaunchAttributeClusterDimension;
             at.val.clusterDim.x = n;
@@ -870,7 +882,7 @@ cudaError_t launch(cudaStream_t stream, bool bf16, const PageAttention& a, int n
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(jobs * shares));
     cfg.blockDim = dim3(warps * 32);
-    cfg.dynamicSmemBytes = C::smem(warps);
+    cfg.dynamicSmemBytes = C::smem(warps, shares);
     cfg.stream = stream;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
