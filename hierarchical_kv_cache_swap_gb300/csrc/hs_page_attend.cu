@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
     Fixed<D, NT>& sm = *reinterpret_cast<Fixed<D, NT>*>(raw);
     uint8_t* const space = raw + (sizeof(Fixed<D, NT>) + 127) / 128 * 128;
     const int threads = blockDim.x, warps = threads >> 5;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0) /* uniform: so are the loops */, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const uint64_t deadline = global_ns() + A.wait_ns;
     const int nsplit = P.shares.d;
     int job = P.shares((int)blockIdx.x);
