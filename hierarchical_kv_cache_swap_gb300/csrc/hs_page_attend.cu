@@ -824,13 +824,16 @@ cudaError_t set_up(Room* room) {
 // Warps of a CTA and CTAs that share a selection: the pair with the least estimated time, in
 // cycles. A tile takes an SM about `tile` cycles (what its instructions cost at the rate
 // reached with many warps) and a warp's own tiles follow each other at `delay`; a warp's
-// start and end cost about 600 cycles of its SM's time and a CTA 3000 of delay, a cluster's
-// join 1500 more of both. With few jobs the delays decide and more, smaller shares win until a
-// second wave of clusters would be needed: one request, 8 heads, 128 tiles: 64 CTAs of 8
-// warps 6.3 us, of 4 warps 7.0, of 16 warps 7.8. With many the work does and shares only
-// cost: 512 jobs of 128 tiles: whole ones 37.2 us, halves 39.7, quarters 58.
+// start and end cost about 350 cycles of its SM's time and a CTA 3000 of delay, a cluster's
+// join 1500 more of both. With few jobs the delays decide and more, smaller shares win until
+// a second wave of clusters would be needed (us a call):
+//   1 request, 8 heads, 128 tiles:    8 CTAs of 8 warps 5.4, of 4 warps 5.9, of 16 warps 6.7
+//   96 jobs of 400 tiles, D = 64:     3 CTAs of 8 warps 13.8, 7 of 4 warps 14.6, 2 of 12 21.3
+//   16 jobs of 512 tiles, 16 rows:    6 CTAs of 12 warps 14.3, of 8 warps 15.6, 7 of 12 26.0
+// With many the work does, and shares only cost: 512 jobs of 128 tiles: whole ones 35.6,
+// halves 36.8, thirds 44.9.
 void plan(const Room& room, int sm_warps, int num_sms, int D, int NT, int64_t jobs, int64_t tiles, int* warps, int* shares) {
-    const float tile = 12.f + 0.55f * D + NT * (14.f + 0.16f * D), delay = 750.f + 200.f * NT;
+    const float tile = 12.f + 0.55f * D + NT * (14.f + 0.16f * D), delay = 1000.f + 250.f * NT;
     float best = INFINITY;
     *warps = 4;
     *shares = 1;
@@ -839,7 +842,7 @@ void plan(const Room& room, int sm_warps, int num_sms, int D, int NT, int64_t jo
             const int fit = room.clusters[w / 4 - 1][n - 1];
             if (fit < 1 || ((n > 1 || w > 4) && 2 * (int64_t)n * w > tiles)) continue;
             const float ctas = (float)jobs * n, share = (float)tiles / n;
-            const float work = ceilf(ctas / num_sms) * (share * tile + 600.f * w + (n > 1 ? 1500.f : 0.f));
+            const float work = ceilf(ctas / num_sms) * (share * tile + 350.f * w + (n > 1 ? 1500.f : 0.f));
             const float chain = ceilf(ctas / (fit * n)) * (3000.f + (n > 1 ? 1500.f : 0.f) + ceilf(share / w) * delay);
             const float time = fmaxf(work, chain);
             if (time < best) {
