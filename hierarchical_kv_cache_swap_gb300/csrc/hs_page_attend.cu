@@ -10,7 +10,7 @@
 //
 // What bounds it: each key and head costs 9/8 D bytes of HBM and 4 D multiply-adds a row, so
 // up to about 16 rows the stream of pages is the floor, and the work per byte -- two
-// conversions, two scalings and half a register shuffle for each pair of codes -- has to stay
+// conversions and two scalings for each pair of codes and row -- has to stay
 // under it. So nothing decoded goes through shared memory: a warp decodes its tile's codes
 // straight into the registers in which the tensor cores (mma.sync m16n8k16, f16 operands, f32
 // sums) take them. Both products are formed transposed, keys (or dimensions) along the 16
@@ -29,8 +29,9 @@
 //                t D/4 + 4 i ... of keys g and g + 8 at step i, so its codes are D/8
 //                contiguous bytes of a row and its scales D/64 bytes.
 //   O^T = V^T P  A: 16 dims x 16 keys. Lane (g, t) needs pairs of keys (2t, 2t+1) and (2t+8,
-//                2t+9) for the same dimension: it decodes the same bytes of four tokens and
-//                interleaves them. At step i it holds dimensions g D/8 + 2 i and + 1.
+//                2t+9) for the same dimension: it takes the same bytes of four tokens and
+//                interleaves their codes before decoding them. At step i it holds dimensions
+//                g D/8 + 2 i and + 1.
 //   P            leaves S^T's layout (a lane has keys g, g + 8 of rows 2t, 2t + 1) for the
 //                other operand's (keys 2t, 2t + 1 of row g) by a transposing register move.
 //
@@ -128,7 +129,6 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
     return r;
 }
 __device__ __forceinline__ uint32_t scale2(uint32_t u) { return u * 0x00800080u; }  // (s, s) of scale byte u
-__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) { return __byte_perm(a, b, s); }
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -624,20 +624,26 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
             }
 #pragma unroll
             for (int w = 0; w < W; ++w) {
-                uint32_t d[4][4];
+                // two tokens' codes for one dimension into a byte, which decodes to the pair of
+                // halves that the product takes: e their even dimensions, o the odd ones
+                constexpr uint32_t kLow = 0x0F0F0F0Fu;
+                uint32_t e[2][4], o[2][4];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    decode_word(vw[c][w], d[c]);
-                    const uint32_t sc = scale2(vs[c][w / 2]);
+                for (int c = 0; c < 2; ++c) {
+                    const uint32_t x = vw[2 * c][w], y = vw[2 * c + 1][w];
+                    const uint32_t sc = vs[2 * c][w / 2] * 0x80u + (vs[2 * c + 1][w / 2] << 23);
+                    decode_word((x & kLow) | (y << 4 & ~kLow), e[c]);
+                    decode_word((x >> 4 & kLow) | (y & ~kLow), o[c]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) d[c][i] = mul2(d[c][i], sc);
+                    for (int i = 0; i < 4; ++i) {
+                        e[c][i] = mul2(e[c][i], sc);
+                        o[c][i] = mul2(o[c][i], sc);
+                    }
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const uint32_t a0 = prmt(d[0][i], d[1][i], 0x5410), a1 = prmt(d[0][i], d[1][i], 0x7632);
-                    const uint32_t a2 = prmt(d[2][i], d[3][i], 0x5410), a3 = prmt(d[2][i], d[3][i], 0x7632);
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) mma(acc[4 * w + i][n], a0, a1, a2, a3, pf[u][n][0], pf[u][n][1]);
+                    for (int n = 0; n < NT; ++n) mma(acc[4 * w + i][n], e[0][i], o[0][i], e[1][i], o[1][i], pf[u][n][0], pf[u][n][1]);
                 }
             }
         }
