@@ -19,8 +19,8 @@
 //
 // Work split: one CTA per (request, KV head, tile of query rows, share of the selection); a
 // selection is shared by up to 8 CTAs, one thread-block cluster, when there are few requests
-// and heads. Each of the CTA's warps takes 16-token tiles in turn (18 D contiguous bytes: one
-// bulk copy into the warp's own ring of stages, no barrier between warps) and keeps its own
+// and heads. Each of the CTA's warps takes 16-token tiles in turn (18 D contiguous bytes,
+// copied asynchronously into the warp's own ring of stages: no barrier between warps) and keeps its own
 // maxima, sums and outputs; the warps are joined through shared memory at the end and the
 // CTAs of a cluster through distributed shared memory, so no workspace and no second kernel.
 //
@@ -92,7 +92,6 @@ struct Fixed {  // followed by the warps' regions and, with several shares, thei
     alignas(16) float2 ml[kMaxWarps][C::kRows];  // the warps' maxima and sums
     alignas(16) float2 xml[kMaxSplit][C::kRows]; // the shares'
     int wref[kMaxWarps], xref[kMaxSplit];        // positions that biases are relative to
-    uint64_t bar[kMaxWarps][C::kStages];
 };
 template <int D, int NT>
 int Config<D, NT>::smem(int warps, int shares) {
@@ -175,27 +174,13 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
     return r;
 }
 
-__device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t parity) {
-    uint32_t ok;
-    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-                 : "=r"(ok) : "r"(su32(b)), "r"(parity) : "memory");
-    return ok != 0;
+// 16 bytes into shared memory, asynchronously; copies are waited for by groups.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-// Waits for a copy to land; gives up once the global timer passes `deadline`.
-__device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, uint64_t deadline) {
-    while (!bar_try(b, parity))
-        if (global_ns() > deadline) return false;
-    return true;
-}
-// `bytes` (a multiple of 16, both ends 16-byte aligned) into shared memory, counted on `b`.
-__device__ __forceinline__ void expect(uint64_t* b, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(su32(b)), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void copy_in(void* dst, const uint8_t* src, uint32_t bytes, uint64_t* b) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(su32(dst)),
-                 "l"(src), "r"(bytes), "r"(su32(b))
-                 : "memory");
-}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory"); }
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
@@ -221,7 +206,6 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
     uint8_t* const space = raw + (sizeof(Fixed<D, NT>) + 127) / 128 * 128;
     const int threads = blockDim.x, warps = threads >> 5;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0) /* uniform: so are the loops */, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    const uint64_t deadline = global_ns() + A.wait_ns;
     const int nsplit = P.shares.d;
     int job = P.shares((int)blockIdx.x);
     const int split = blockIdx.x - job * nsplit;  // = the rank in the cluster
@@ -229,12 +213,7 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
     const int b = P.heads(bh), h = bh - b * A.H;
     const int rows = A.G * A.Tq;
     uint8_t* ring = space + warp * C::kSpace;
-    uint64_t* bar = sm.bar[warp];
     int2* list = reinterpret_cast<int2*>(ring + C::kSpace - C::kListBytes);
-    if (lane < C::kStages) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(su32(bar + lane)) : "memory");
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    __syncwarp();
-
     if (nsplit > 1) cluster_arrive();  // waited for before the first store to another CTA
     // The launch may begin before the kernel ahead of it on the stream is done: nothing that
     // it reads or writes is touched before this.
@@ -288,7 +267,6 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
     int groups = P.groups;                  // not yet on the list
     uint32_t fill = 0, used = 0, tail = 0;  // listed tiles copied (or on their way), consumed, listed
     int fst = 0, ust = 0;                   // the stage of the next copy and of the next wait
-    uint32_t phase = 0;                     // parity of the next wait
     auto append = [&]() {
         bool live = false;
         int2 e;
@@ -311,14 +289,23 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
         look_up();
         __syncwarp();
     };
-    auto top_up = [&]() {  // put the next two tiles (the last one alone) on their way
+    auto top_up = [&]() {  // put the next two tiles (the last one alone) on their way, as one group
         while (tail - fill < 2 && groups > 0) append();
         const int n = min(2, (int)(tail - fill));
-        if (lane < n) {
-            const int unit = list[(fill + lane) % kList].x;
-            if (lane == 0) expect(&bar[fst], n * C::kChunk);
-            copy_in(ring + (2 * fst + lane) * C::kChunk, pages + (size_t)unit * unit_bytes, C::kChunk, &bar[fst]);
+        if (n > 0) {
+            constexpr int kParts = C::kChunk / 16;
+            const int4 e = *reinterpret_cast<const int4*>(&list[fill % kList]);
+            const uint8_t* from0 = pages + (size_t)e.x * unit_bytes + 16 * lane;
+            const uint8_t* from1 = pages + (size_t)e.z * unit_bytes + 16 * lane - C::kChunk;
+            const uint32_t to = su32(ring) + fst * (2 * C::kChunk) + 16 * lane;
+#pragma unroll
+            for (int i = 0; i < (2 * kParts + 31) / 32; ++i) {  // part 32 i + lane of the two tiles
+                const bool first = 32 * i + 31 < kParts || (32 * i < kParts && 32 * i + lane < kParts);
+                if (first) copy16(to + 512 * i, from0 + 512 * i);
+                else if (n == 2 && (32 * i + 31 < 2 * kParts || 32 * i + lane < 2 * kParts)) copy16(to + 512 * i, from1 + 512 * i);
+            }
         }
+        copy_commit();
         fill += n;
         fst = fst + 1 == C::kStages ? 0 : fst + 1;
     };
@@ -387,7 +374,6 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
     // four tokens of V (places 2t, 2t + 1, + 8) then lie in both halves of the 128 bytes that
     // the shared memory banks cover, and its keys still do.
     auto order = [](int r) { return r ^ (r >> 1 & 1); };
-    bool ok = true;
 
     // ---------------- two tiles at a time: their chains of products are independent
 #pragma unroll 1
@@ -397,10 +383,8 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
         const uint8_t* tile[2] = {ring + ust * (2 * C::kChunk), ring + ust * (2 * C::kChunk) + (two ? C::kChunk : 0)};
         const int pos[2] = {e.y & ~15, (two ? e.w : e.y) & ~15};
         const bool partial = !two || ((e.y | e.w) & 1);
-        if (!__all_sync(0xffffffffu, bar_wait(&bar[ust], phase, deadline))) {
-            ok = false;
-            break;
-        }
+        copy_wait<C::kStages - 1>();
+        __syncwarp();
 
         // ---------------- S^T = K Q^T
         float s[2][NT][4];
@@ -450,6 +434,32 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
                 }
             }
         }
+
+        // ---------------- V's bytes, to be there when the weights are
+        constexpr int WV = D / 64;                // words of codes of a token: D/8 dims
+        constexpr int B = D > 128 ? D / 128 : 1;  // blocks of those dims (D = 64: half of one)
+        uint32_t vw[2][4][WV], vs[2][4][B];       // of the tokens in places 2t, 2t + 1, 2t + 8, 2t + 9
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int tok = order(2 * t + (c & 1)) + 8 * (c >> 1);
+                const uint8_t* src = tile[u] + 9 * D + tok * (D / 2) + g * (D / 16);
+                const uint8_t* us = tile[u] + 17 * D + tok * (D / 16);
+                if constexpr (D == 64) {
+                    vw[u][c][0] = *reinterpret_cast<const uint32_t*>(src);
+                    vs[u][c][0] = us[g >> 1];
+                } else if constexpr (D == 128) {
+                    const uint2 v = *reinterpret_cast<const uint2*>(src);
+                    vw[u][c][0] = v.x; vw[u][c][1] = v.y;
+                    vs[u][c][0] = us[g];
+                } else {
+                    const uint4 v = *reinterpret_cast<const uint4*>(src);
+                    vw[u][c][0] = v.x; vw[u][c][1] = v.y; vw[u][c][2] = v.z; vw[u][c][3] = v.w;
+                    vs[u][c][0] = us[2 * g];
+                    vs[u][c][B - 1] = us[2 * g + 1];
+                }
+            }
 
         // ---------------- scores less the rows' reference maxima, in log2 units; masked.
         // z[u][n][k]: rows (8 n + 2 t, + 1), place g + 8 k
@@ -567,30 +577,7 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
 
         // ---------------- O^T += V^T P
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            if (u == 1 && !two) break;
-            constexpr int W = D / 64;  // words of codes of a token: D/8 dims
-            constexpr int B = D > 128 ? D / 128 : 1;  // blocks of a lane's dims (D = 64: half of one)
-            uint32_t vw[4][W], vs[4][B];  // of the tokens in places 2t, 2t + 1, 2t + 8, 2t + 9
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const int tok = order(2 * t + (c & 1)) + 8 * (c >> 1);
-                const uint8_t* src = tile[u] + 9 * D + tok * (D / 2) + g * (D / 16);
-                const uint8_t* us = tile[u] + 17 * D + tok * (D / 16);
-                if constexpr (D == 64) {
-                    vw[c][0] = *reinterpret_cast<const uint32_t*>(src);
-                    vs[c][0] = us[g >> 1];
-                } else if constexpr (D == 128) {
-                    const uint2 v = *reinterpret_cast<const uint2*>(src);
-                    vw[c][0] = v.x; vw[c][1] = v.y;
-                    vs[c][0] = us[g];
-                } else {
-                    const uint4 v = *reinterpret_cast<const uint4*>(src);
-                    vw[c][0] = v.x; vw[c][1] = v.y; vw[c][2] = v.z; vw[c][3] = v.w;
-                    vs[c][0] = us[2 * g];
-                    vs[c][B - 1] = us[2 * g + 1];
-                }
-            }
+        for (int u = 0; u < 2; ++u) {  // a second tile that is not there has weights of zero
             if (partial) {
                 // a key that no row sees may hold anything: its values become zeros, since a
                 // weight of 0 would not undo a NaN. One that only later rows see has been
@@ -603,8 +590,8 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
                     const bool hidden = p >= length || (A.start && p < start && p >= prefix);
 #pragma unroll
                     for (int i = 0; i < B; ++i) {
-                        if (!hidden && vs[c][i] >= 0xF8u) nans |= (0x10000u * i + 1u - (uint32_t)i) << tok;
-                        if (hidden || vs[c][i] >= 0xF8u) vs[c][i] = 0;
+                        if (!hidden && vs[u][c][i] >= 0xF8u) nans |= (0x10000u * i + 1u - (uint32_t)i) << tok;
+                        if (hidden || vs[u][c][i] >= 0xF8u) vs[u][c][i] = 0;
                     }
                 }
                 if (__any_sync(0xffffffffu, nans != 0)) {
@@ -623,15 +610,15 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
                 }
             }
 #pragma unroll
-            for (int w = 0; w < W; ++w) {
+            for (int w = 0; w < WV; ++w) {
                 // two tokens' codes for one dimension into a byte, which decodes to the pair of
                 // halves that the product takes: e their even dimensions, o the odd ones
                 constexpr uint32_t kLow = 0x0F0F0F0Fu;
                 uint32_t e[2][4], o[2][4];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const uint32_t x = vw[2 * c][w], y = vw[2 * c + 1][w];
-                    const uint32_t sc = vs[2 * c][w / 2] * 0x80u + (vs[2 * c + 1][w / 2] << 23);
+                    const uint32_t x = vw[u][2 * c][w], y = vw[u][2 * c + 1][w];
+                    const uint32_t sc = vs[u][2 * c][w / 2] * 0x80u + (vs[u][2 * c + 1][w / 2] << 23);
                     decode_word((x & kLow) | (y << 4 & ~kLow), e[c]);
                     decode_word((x >> 4 & kLow) | (y & ~kLow), o[c]);
 #pragma unroll
@@ -650,20 +637,8 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
         __syncwarp();  // every lane has read the stages: refill them
         used += two ? 2 : 1;
         ust = ust + 1 == C::kStages ? 0 : ust + 1;
-        if (ust == 0) phase ^= 1;
         top_up();
     }
-    if (!ok) {
-        if (A.status && lane == 0) atomicOr(A.status, 8u /* HS_STATUS_TIMEOUT */);
-        // no copy may still be landing when the CTA exits: wait for them, bounded again
-        const uint64_t by = global_ns() + kDefaultWaitNs;
-        for (; used < fill; used += 2) {
-            bar_wait(&bar[ust], phase, by);
-            ust = ust + 1 == C::kStages ? 0 : ust + 1;
-            if (ust == 0) phase ^= 1;
-        }
-    }
-
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // ---------------- join the warps: their outputs in the lanes' order, over the rings
