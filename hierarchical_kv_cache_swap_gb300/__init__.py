@@ -72,7 +72,7 @@ class _PageAttention(ctypes.Structure):
                 ("q_head_stride", _I64), ("o", _VP), ("o_batch_stride", _I64), ("o_token_stride", _I64),
                 ("o_head_stride", _I64), ("lse", _VP), ("pages", _VP), ("slots", _VP), ("selections", _VP),
                 ("lengths", _VP), ("sm_scale", ctypes.c_float), ("softcap", ctypes.c_float), ("slopes", _VP),
-                ("start", _VP), ("prefix", _VP), ("status", _VP), ("wait_ns", ctypes.c_uint64)]
+                ("start", _VP), ("prefix", _VP), ("status", _VP)]
 
 
 SIGNATURES = {
@@ -251,7 +251,7 @@ def read_pages(shape, pages, slots, k, v, status=None, stream=None) -> None:
 
 
 def attend_pages(shape, q, pages, slots, selections, lengths, o, lse, sm_scale: float, softcap: float = 0.0,
-                 slopes=None, start=None, prefix=None, status=None, stream=None, wait_ns: int = 0) -> None:
+                 slopes=None, start=None, prefix=None, status=None, stream=None) -> None:
     """hs_attend_pages: q [B, q_tokens, q_heads, head_dim], bf16 or fp16, over the pages
     [B, S, page bytes] in slots int32 [B, k], which are the pages numbered selections int32
     [B, k] of sequences of lengths int32 [B] tokens; into o (as q) and lse float32 [B,
@@ -259,7 +259,7 @@ def attend_pages(shape, q, pages, slots, selections, lengths, o, lse, sm_scale: 
     distance bias; start, prefix: int32 [B], keys before start are masked but for the first
     prefix; status: a device int32 word [1]."""
     (_torch_binding or _native()).attend_pages(shape, q, pages, slots, selections, lengths, o, lse, sm_scale, softcap,
-                                               slopes, start, prefix, status, stream, wait_ns)
+                                               slopes, start, prefix, status, stream)
 
 
 class Pool:
@@ -306,7 +306,6 @@ class Context:
         self._lib = load_library()
         self.R, self.C, self.S, self.E = num_requests, context_len, slots, entry_bytes
         self.pool_rows = 0
-        self._wait_ns = 0  # the library's default
         if pool is not None:
             addr, rows, stride = pool
             self.pool_rows = rows
@@ -425,9 +424,9 @@ class Context:
 
     def attend_pages(self, shape, q, out_slots, selections, lengths, o, lse, sm_scale: float, softcap: float = 0.0,
                      slopes=None, start=None, prefix=None, stream=None) -> None:
-        """attend_pages() over this context's device buffer, status word and wait limit."""
+        """attend_pages() over this context's device buffer and status word."""
         _native().attend_pages(shape, q, self._pages(shape), out_slots, selections, lengths, o, lse, sm_scale, softcap,
-                               slopes, start, prefix, self._lib.hs_status_word(self._h), stream, self._wait_ns)
+                               slopes, start, prefix, self._lib.hs_status_word(self._h), stream)
 
     def reset(self, stream=None) -> None:
         self._check(self._lib.hs_reset(self._h, _stream(stream)), "hs_reset")
@@ -442,7 +441,6 @@ class Context:
     def set_wait_limit(self, ns: int) -> None:
         """Time limit (global-timer ns from a CTA's start) of the kernels' device waits."""
         self._check(self._lib.hs_set_wait_limit(self._h, int(ns)), "hs_set_wait_limit")
-        self._wait_ns = int(ns)
 
     def kernels_per_call(self) -> int:
         return int(self._lib.hs_kernels_per_call(self._h))

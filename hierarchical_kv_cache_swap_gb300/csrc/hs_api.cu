@@ -601,9 +601,6 @@ int hs_attend_pages(hs_stream_t stream, const hs_page_attention* a) {
         return fail(HS_ERR_INVALID, "q, o and pages must be 16-byte aligned");
     if ((a->q_batch_stride | a->q_token_stride | a->q_head_stride | a->o_batch_stride | a->o_token_stride | a->o_head_stride) & 7)
         return fail(HS_ERR_INVALID, "rows of q and o must be 16-byte aligned");
-    if (a->wait_ns != 0 && (a->wait_ns < hs::kMinWaitNs || a->wait_ns > hs::kMaxWaitNs))
-        return fail(HS_ERR_INVALID, "wait limit %llu ns outside [%llu, %llu]", (unsigned long long)a->wait_ns,
-                    (unsigned long long)hs::kMinWaitNs, (unsigned long long)hs::kMaxWaitNs);
     if ((rc = sm_count(&sms)) != HS_OK) return rc;
     hs::PageAttention p;
     p.q = (const uint16_t*)a->q;
@@ -632,7 +629,6 @@ int hs_attend_pages(hs_stream_t stream, const hs_page_attention* a) {
     p.tiles = ps.tiles();
     p.scale = a->sm_scale;
     p.cap = a->softcap;
-    p.wait_ns = a->wait_ns ? a->wait_ns : hs::kDefaultWaitNs;
     cudaError_t e = hs::launch_attend_pages((cudaStream_t)stream, ps, a->dtype == HS_BF16, p, sms);
     if (e != cudaSuccess) return cuda_fail(e, "page attention kernel launch");
     g_err[0] = 0;

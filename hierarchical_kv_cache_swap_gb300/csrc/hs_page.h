@@ -74,7 +74,6 @@ struct PageAttention {
     int B, S, k, H, G, Tq;   // H KV heads, G query heads to each
     int tiles;               // 16-token tiles of a page
     float scale, cap;
-    uint64_t wait_ns;
 };
 cudaError_t launch_attend_pages(cudaStream_t stream, const PageShape& ps, bool bf16, const PageAttention& a, int num_sms);
 

@@ -248,9 +248,9 @@ PyObject* read_pages(PyObject*, PyObject* const* a, Py_ssize_t na) {
 }
 
 // attend_pages(shape, q, pages, slots, selections, lengths, o, lse, sm_scale, softcap, slopes,
-//              start, prefix, status, stream, wait_ns)
+//              start, prefix, status, stream)
 PyObject* attend_pages(PyObject*, PyObject* const* a, Py_ssize_t na) {
-    if (!arity(na, 16)) return nullptr;
+    if (!arity(na, 15)) return nullptr;
     return guarded([&] {
         hs_page_attention p{};
         p.shape = shape_of(a[0]);
@@ -300,7 +300,6 @@ PyObject* attend_pages(PyObject*, PyObject* const* a, Py_ssize_t na) {
         p.start = start ? (const int32_t*)start->data_ptr() : nullptr;
         p.prefix = prefix ? (const int32_t*)prefix->data_ptr() : nullptr;
         p.status = status_of(a[13]);
-        p.wait_ns = (uint64_t)integer(a[15]);
         return done(hs_attend_pages(stream_of(a[14]), &p), "hs_attend_pages");
     });
 }

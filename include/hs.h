@@ -371,6 +371,8 @@ int hs_set_extents(hs_ctx* ctx, hs_stream_t stream, const int64_t* base, const i
  * that a resolution left in its slots. A context that holds them has entry_bytes =
  * hs_page_bytes(). All of them are enqueue-only and graph-capturable, allocate nothing and
  * need no workspace; their device pointers belong to the calling thread's current device.
+ * Their kernels are programmatic dependents of the kernel before them on the stream: they
+ * may be launched while it runs, and wait for it before they read or write anything.
  *
  * Layout: for tile i (tokens 16 i .. 16 i + 15 of the page) and head h, the 18 * head_dim
  * bytes at (i * kv_heads + h) * 18 * head_dim hold K codes [16][head_dim / 2], K scales
@@ -474,9 +476,8 @@ typedef struct {
     const float* slopes;     /* device [q_heads], or NULL */
     const int32_t* start;    /* device [B], or NULL (no document mask; prefix is then ignored) */
     const int32_t* prefix;   /* device [B], or NULL (0) */
-    uint32_t* status;        /* device word: HS_STATUS_RANGE (a slot >= S; its page is left out) and
-                                HS_STATUS_TIMEOUT are set in it; or NULL */
-    uint64_t wait_ns;        /* limit of the device waits (hs_set_wait_limit), 0: its default */
+    uint32_t* status;        /* device word, or NULL: HS_STATUS_RANGE is set in it by a slot >= S,
+                                whose page is left out */
 } hs_page_attention;
 int hs_attend_pages(hs_stream_t stream, const hs_page_attention* args);
 

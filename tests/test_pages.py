@@ -133,7 +133,7 @@ def _attention(**change):
     a = dict(shape=GOOD, dtype=0, B=1, S=4, k=2, q_heads=16, q_tokens=1, q=16, q_batch_stride=2048, q_token_stride=2048,
              q_head_stride=128, o=16, o_batch_stride=2048, o_token_stride=2048, o_head_stride=128, lse=4, pages=16,
              slots=4, selections=4, lengths=4, sm_scale=0.1, softcap=0.0, slopes=None, start=None, prefix=None,
-             status=None, wait_ns=0)
+             status=None)
     a.update(change)
     return hs._PageAttention(**a)
 
@@ -159,7 +159,6 @@ def _attention(**change):
     ("null pages", {"pages": None}, hs.HS_ERR_INVALID),
     ("aligned", {"q": 24}, hs.HS_ERR_INVALID),
     ("aligned", {"o_head_stride": 4}, hs.HS_ERR_INVALID),
-    ("wait limit", {"wait_ns": 10}, hs.HS_ERR_INVALID),
 ])
 def test_attend_pages_refuses_before_touching_cuda(lib, what, change, code):
     assert lib.hs_attend_pages(None, _ref(_attention(**change))) == code
