@@ -62,11 +62,13 @@ constexpr int kList = 64;              // a warp's list of live tiles (a ring; 3
 constexpr float kRescale = 8.f;        // a row's reference maximum moves when exceeded by 2^8
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 
-// A call's work split: job (request, KV head, tile of rows) x share.
+// A call's work split. Jobs are (request, KV head, tile of rows); a cluster of `shares` CTAs
+// takes that many whole jobs while there are any and then shares one.
 struct Split {
-    Divisor shares, row_tiles, heads, tiles, group;  // CTAs of a job; ...; tiles of a page; query heads of a KV head
-    int ntiles;  // of a selection
-    int groups;  // a warp's groups of 32 tiles
+    Divisor shares, row_tiles, heads, tiles, group;  // CTAs of a cluster; ...; tiles of a page; query heads of a KV head
+    int whole;             // clusters of whole jobs
+    int ntiles;            // of a selection
+    int groups, groups_1;  // a warp's groups of 32 tiles, of a shared job and of a whole one
 };
 
 template <int D, int NT>
@@ -206,9 +208,10 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
     uint8_t* const space = raw + (sizeof(Fixed<D, NT>) + 127) / 128 * 128;
     const int threads = blockDim.x, warps = threads >> 5;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0) /* uniform: so are the loops */, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    const int nsplit = P.shares.d;
-    int job = P.shares((int)blockIdx.x);
-    const int split = blockIdx.x - job * nsplit;  // = the rank in the cluster
+    const int cluster = P.shares((int)blockIdx.x), rank = blockIdx.x - cluster * P.shares.d;
+    const bool whole = cluster < P.whole;
+    const int nsplit = whole ? 1 : P.shares.d, split = whole ? 0 : rank;
+    const int job = whole ? cluster * (int)P.shares.d + rank : P.whole * ((int)P.shares.d - 1) + cluster;
     const int bh = P.row_tiles(job), r0 = (job - bh * (int)P.row_tiles.d) * C::kRows;
     const int b = P.heads(bh), h = bh - b * A.H;
     const int rows = A.G * A.Tq;
@@ -264,9 +267,9 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
     };
     if (2 * warp < C::kRows) load_q(2 * warp + (lane >> 4));
 
-    int groups = P.groups;                  // not yet on the list
-    uint32_t fill = 0, used = 0, tail = 0;  // listed tiles copied (or on their way), consumed, listed
-    int fst = 0, ust = 0;                   // the stage of the next copy and of the next wait
+    int groups = whole ? P.groups_1 : P.groups;  // not yet on the list
+    uint32_t fill = 0, used = 0, tail = 0;       // listed tiles copied (or on their way), consumed, listed
+    int fst = 0, ust = 0;                        // the stage of the next copy and of the next wait
     auto append = [&]() {
         bool live = false;
         int2 e;
@@ -811,13 +814,16 @@ cudaError_t set_up(Room* room) {
 //   1 request, 8 heads, 128 tiles:    8 CTAs of 8 warps 5.4, of 4 warps 5.9, of 16 warps 6.7
 //   96 jobs of 400 tiles, D = 64:     3 CTAs of 8 warps 13.8, 7 of 4 warps 14.6, 2 of 12 21.3
 //   16 jobs of 512 tiles, 16 rows:    6 CTAs of 12 warps 14.3, of 8 warps 15.6, 7 of 12 26.0
-// With many the work does, and shares only cost: 512 jobs of 128 tiles: whole ones 35.6,
-// halves 36.8, thirds 44.9.
-void plan(const Room& room, int sm_warps, int num_sms, int D, int NT, int64_t jobs, int64_t tiles, int* warps, int* shares) {
+// With many the work does, and shares only cost, but for the jobs that some SMs have more of
+// than others: 512 jobs of 128 tiles: whole 34.5, all halved 36.8, 456 whole and 56 halved
+// 33.1; in clusters of 3, 4 or 8 these mixtures took 37.1, 34.1 and 35.3.
+void plan(const Room& room, int sm_warps, int num_sms, int D, int NT, int64_t jobs, int64_t tiles, int* warps, int* shares,
+          int64_t* whole) {
     const float tile = 12.f + 0.55f * D + NT * (14.f + 0.16f * D), delay = 1000.f + 250.f * NT;
     float best = INFINITY;
     *warps = 4;
     *shares = 1;
+    *whole = jobs;
     for (int n = 1; n <= kMaxSplit; ++n)
         for (int w = 4; w <= sm_warps; w += 4) {
             const int fit = room.clusters[w / 4 - 1][n - 1];
@@ -830,6 +836,18 @@ void plan(const Room& room, int sm_warps, int num_sms, int D, int NT, int64_t jo
                 best = time;
                 *warps = w;
                 *shares = n;
+                *whole = n == 1 ? jobs : 0;
+            }
+            // as many whole jobs as every SM can have alike, the others halved
+            const int64_t even = n == 2 ? jobs / num_sms * num_sms / n * n : 0;
+            if (even == 0) continue;
+            const float mixed = (float)(even / num_sms) * ((float)tiles * tile + 350.f * w) +
+                                ceilf((float)(jobs - even) * n / num_sms) * (share * tile + 350.f * w + 1500.f);
+            if (mixed < best) {
+                best = mixed;
+                *warps = w;
+                *shares = n;
+                *whole = even;
             }
         }
 }
@@ -853,18 +871,22 @@ cudaError_t launch(cudaStream_t stream, bool bf16, const PageAttention& a, int n
     const int row_tiles = (a.G * a.Tq + C::kRows - 1) / C::kRows;
     const int64_t jobs = (int64_t)a.B * a.H * row_tiles, tiles = (int64_t)a.k * a.tiles;
     int warps, shares;
-    plan(rooms[dev], C::kSmWarps, num_sms, D, NT, jobs, tiles, &warps, &shares);
-    if (jobs * shares > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    int64_t whole;  // jobs that are not shared, a multiple of shares
+    plan(rooms[dev], C::kSmWarps, num_sms, D, NT, jobs, tiles, &warps, &shares, &whole);
+    const int64_t ctas = whole + (jobs - whole) * shares;
+    if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
     Split p;
     p.shares = Divisor(shares);
     p.row_tiles = Divisor(row_tiles);
     p.heads = Divisor(a.H);
     p.tiles = Divisor(a.tiles);
     p.group = Divisor(a.G);
+    p.whole = (int)(whole / shares);
     p.ntiles = (int)tiles;
     p.groups = (int)((tiles + 32 * shares * warps - 1) / (32 * shares * warps));
+    p.groups_1 = (int)((tiles + 32 * warps - 1) / (32 * warps));
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(jobs * shares));
+    cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3(warps * 32);
     cfg.dynamicSmemBytes = C::smem(warps, shares);
     cfg.stream = stream;
