@@ -111,12 +111,13 @@ __device__ __forceinline__ float lg2(float x) {
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// c tanh y = c - 2 c / (1 + e^(2y)); y2 = 2 y log2 e. Absolute error a few 2^-23 of c.
-__device__ __forceinline__ float capped(float c, float y2) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(y2)));
-    return fmaf(-2.f * c, r, c);
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
+// c tanh y = c - 2 c / (1 + e^(2y)); y2 = 2 y log2 e. Absolute error a few 2^-23 of c.
+__device__ __forceinline__ float capped(float c, float y2) { return fmaf(-2.f * c, rcp(1.f + ex2(y2)), c); }
 
 // Four bytes of codes to four pairs of halves (exact).
 __device__ __forceinline__ void decode_word(uint32_t w, uint32_t (&h)[4]) {
@@ -727,7 +728,7 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
             const int row = r0 + r + c;
             if (row >= rows) break;
             const int tok = P.group(row), head = h * A.G + row - tok * A.G;
-            const float top = c ? o.top.y : o.top.x, sum = c ? o.sum.y : o.sum.x, inv = top > -INFINITY ? 1.f / sum : 0.f;
+            const float top = c ? o.top.y : o.top.x, sum = c ? o.sum.y : o.sum.x, inv = top > -INFINITY ? rcp(sum) : 0.f;
             const float y0 = (c ? o.a.y : o.a.x) * inv, y1 = (c ? o.a.w : o.a.z) * inv, y2 = (c ? o.b.y : o.b.x) * inv,
                         y3 = (c ? o.b.w : o.b.z) * inv;
             uint2 w;
