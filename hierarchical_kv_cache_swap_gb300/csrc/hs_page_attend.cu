@@ -8,10 +8,10 @@
 // over the keys with a valid slot, p_j <= qpos_t and (p_j >= start or p_j < prefix). A row
 // that sees no key gets o = 0, lse = -inf.
 //
-// What bounds it: each key and head costs 9/8 D bytes of HBM and 4 D multiply-adds a row, so
-// up to about 16 rows the stream of pages is the floor, and the work per byte -- two
-// conversions and two scalings for each pair of codes and row -- has to stay
-// under it. So nothing decoded goes through shared memory: a warp decodes its tile's codes
+// What bounds it: each key and head costs 9/8 D bytes of HBM and 2 D multiply-adds a row, so
+// up to about 16 rows the stream of pages is the floor, and the work per byte -- a conversion
+// and a scaling for each pair of codes, and their instructions' issue rather than any one
+// pipe -- has to stay under it. So nothing decoded goes through shared memory: a warp decodes its tile's codes
 // straight into the registers in which the tensor cores (mma.sync m16n8k16, f16 operands, f32
 // sums) take them. Both products are formed transposed, keys (or dimensions) along the 16
 // rows of the instruction and the query rows along its 8 columns, so that a group of up to 8
@@ -20,9 +20,10 @@
 // Work split: one CTA per (request, KV head, tile of query rows, share of the selection); a
 // selection is shared by up to 8 CTAs, one thread-block cluster, when there are few requests
 // and heads. Each of the CTA's warps takes 16-token tiles in turn (18 D contiguous bytes,
-// copied asynchronously into the warp's own ring of stages: no barrier between warps) and keeps its own
-// maxima, sums and outputs; the warps are joined through shared memory at the end and the
-// CTAs of a cluster through distributed shared memory, so no workspace and no second kernel.
+// copied asynchronously into the warp's own ring of stages: no barrier between warps) and
+// keeps its own maxima, sums and outputs; the warps are joined through shared memory at the
+// end and the CTAs of a cluster through distributed shared memory, so no workspace and no
+// second kernel.
 //
 //   S^T = K Q^T  A: 16 keys x 16 dims. Which 4 dimensions a lane holds at a step is free as
 //                long as Q's do the same: lane (g, t) = (lane / 4, lane % 4) takes dimensions
@@ -41,6 +42,13 @@
 // the largest; what is below is rounded by at most 2^-38 of the largest. Softmax weights are
 // rounded to half (2^-11 relative, unless below 2^-14 of the largest) for the second product
 // only; the sums that normalise them add the unrounded ones in f32.
+//
+// Measured (16-token pages, 8 heads of 128 with 8 queries each, 128 pages a request; us a
+// call in a graph): 256 requests 105 (5.82 TB/s, 87 % of a copy's rate), of which the copies
+// alone take 91.5 and the arithmetic alone about 100; 64 requests 33 (4.65 TB/s: 512 jobs do
+// not spread evenly over 152 SMs), 1 request 5.1 and one of five tokens 3.6 (the chain of
+// loads, one pair of tiles and the joins). 32 rows (four drafted tokens) over 16 requests take
+// 21.5, where the products alone would take 8.5 on all SMs.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -208,7 +216,8 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
     Fixed<D, NT>& sm = *reinterpret_cast<Fixed<D, NT>*>(raw);
     uint8_t* const space = raw + (sizeof(Fixed<D, NT>) + 127) / 128 * 128;
     const int threads = blockDim.x, warps = threads >> 5;
-    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0) /* uniform: so are the loops */, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known uniform, so that its loops and addresses are
     const int cluster = P.shares((int)blockIdx.x), rank = blockIdx.x - cluster * P.shares.d;
     const bool whole = cluster < P.whole;
     const int nsplit = whole ? 1 : P.shares.d, split = whole ? 0 : rank;
@@ -224,7 +233,7 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
     asm volatile("" ::"l"(A.slots), "l"(A.sel), "l"(A.lengths), "l"(A.q), "l"(A.pages), "r"(P.ntiles), "r"(P.tiles.m), "r"(P.group.m));
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    // ---------------- this warp's tiles: every (nsplit * kWarps)-th of the selection. Lane i
+    // ---------------- this warp's tiles: every (nsplit * warps)-th of the selection. Lane i
     // looks up the i-th of the next 32; those that hold a visible key go on the warp's list.
     const int32_t* slots = A.slots + (size_t)b * A.k;
     const int32_t* sel = A.sel + (size_t)b * A.k;
@@ -812,12 +821,12 @@ cudaError_t set_up(Room* room) {
 // start and end cost about 350 cycles of its SM's time and a CTA 3000 of delay, a cluster's
 // join 1500 more of both. With few jobs the delays decide and more, smaller shares win until
 // a second wave of clusters would be needed (us a call):
-//   1 request, 8 heads, 128 tiles:    8 CTAs of 8 warps 5.4, of 4 warps 5.9, of 16 warps 6.7
-//   96 jobs of 400 tiles, D = 64:     3 CTAs of 8 warps 13.8, 7 of 4 warps 14.6, 2 of 12 21.3
-//   16 jobs of 512 tiles, 16 rows:    6 CTAs of 12 warps 14.3, of 8 warps 15.6, 7 of 12 26.0
+//   1 request, 8 heads, 128 tiles:    8 CTAs of 8 warps 5.1, of 4 warps 5.5, of 16 warps 7.3
+//   96 jobs of 400 tiles, D = 64:     3 CTAs of 8 warps 14.1, 7 of 4 warps 15.1, 2 of 12 21.1
+//   16 jobs of 512 tiles, 16 rows:    6 CTAs of 12 warps 14.8, of 8 warps 15.6, 7 of 12 26.6
 // With many the work does, and shares only cost, but for the jobs that some SMs have more of
-// than others: 512 jobs of 128 tiles: whole 34.5, all halved 36.8, 456 whole and 56 halved
-// 33.1; in clusters of 3, 4 or 8 these mixtures took 37.1, 34.1 and 35.3.
+// than others: 512 jobs of 128 tiles: whole 34.5, all halved 35.6, 456 whole and 56 halved
+// 32.9; in clusters of 3, 4 or 8 these mixtures took 37.0, 34.1 and 35.2.
 void plan(const Room& room, int sm_warps, int num_sms, int D, int NT, int64_t jobs, int64_t tiles, int* warps, int* shares,
           int64_t* whole) {
     const float tile = 12.f + 0.55f * D + NT * (14.f + 0.16f * D), delay = 1000.f + 250.f * NT;

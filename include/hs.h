@@ -425,7 +425,7 @@ int hs_write_tokens(hs_stream_t stream, const hs_page_shape* shape, int dtype, c
  * tokens of page position / tokens. It is written into the host store and, when the page is
  * resident, into its slot as well, so the cache stays exact; the replacement state does not
  * change. A page >= context_len (or the request's extent), or a request >= num_requests, is
- * skipped and sets HS_STATUS_RANGE. Distinct (request, position) pairs only. Stream ordered
+ * skipped and sets HS_STATUS_RANGE; a negative request is skipped like a negative position. Distinct (request, position) pairs only. Stream ordered
  * with the context's other calls.
  */
 int hs_append_tokens(hs_ctx* ctx, hs_stream_t stream, const hs_page_shape* shape, int dtype, const hs_token_rows* rows,

@@ -119,6 +119,31 @@ def test_strides_padding_range_and_pinned_pages():
     assert int(word) == hs.HS_STATUS_RANGE and not out[:, :16].any()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_rows_that_are_16_byte_but_not_32_byte_aligned(dtype):
+    shape, n = (32, 2, 128), 37
+    base = tokens(n, 3, 128, dtype, 6).reshape(-1).cuda()
+    k = base[8:8 + n * 256].view(n, 2, 128)
+    v = torch.as_strided(base, (n, 2, 128), (264, 128, 1), 16)  # token stride of 33 times 16 bytes
+    assert k.data_ptr() % 32 == 16
+    dest = torch.arange(n) + 5
+    ref = pm.random_pages(2, shape, 3)
+    pages = ref.cuda()
+    hs.write_tokens(shape, k, v, dest.cuda(), pages)
+    pm.write(ref, shape, k.cpu(), v.cpu(), dest)
+    assert torch.equal(pages.cpu(), ref)
+    out = torch.zeros(2, 64 * 256 + 16, dtype=dtype, device="cuda")
+    ko, vo = (x[8:8 + 64 * 256].view(1, 64, 2, 128) for x in out)
+    slots = torch.tensor([[1, 0]], dtype=torch.int32, device="cuda")
+    hs.read_pages(shape, pages[None], slots, ko, vo)
+    for got, want in zip((ko, vo), pm.read(ref, shape)):
+        assert torch.equal(got.cpu().double()[0], want[[1, 0]].flatten(0, 1))
+    assert not out[:, :8].any() and not out[:, -8:].any()
+    odd = torch.zeros(n * 256 + 8, dtype=dtype, device="cuda")[4:4 + n * 256].view(n, 2, 128)
+    with pytest.raises(hs.HsError, match="aligned"):
+        hs.write_tokens(shape, odd, odd, dest.cuda(), pages)
+
+
 def test_refuses_tensors_that_are_not_on_the_device():
     shape = (16, 1, 64)
     k = torch.zeros((1, 1, 64), dtype=torch.bfloat16)
@@ -554,4 +579,46 @@ def test_decode_steps_over_a_paged_context():
         ctx.append_tokens(shape, kn[:2].cuda(), vn[:2].cuda(), bad[:2])  # two tokens for three requests
     with pytest.raises(hs.HsError):
         ctx.append_tokens((32, 2, 128), kn.cuda(), vn.cuda(), bad)  # not this context's pages
+    ctx.close()
+
+
+def test_tokens_join_extents_of_a_shared_pool():
+    """Appended tokens land in each request's own extent of a pooled context's host store, and
+    in its resident slots; pages past an extent are refused."""
+    shape, rows, S, k = (32, 1, 64), 40, 4, 3
+    T, H, D = shape
+    E = hs.PageShape(*shape).bytes
+    mem = torch.zeros(rows * E, dtype=torch.uint8).pin_memory()
+    ctx = hs.Context(2, 16, S, E, pool=(mem.data_ptr(), rows, E))
+    base, pages = [21, 3], [5, 9]
+    ctx.set_extents(base, pages)
+    ref = torch.zeros((rows, E), dtype=torch.uint8)
+    n = [150, 288]
+    req = torch.cat([torch.full((x,), b) for b, x in enumerate(n)])
+    pos = torch.cat([torch.arange(x) for x in n])
+    kk, vv = tokens(sum(n), H, D, torch.float16, 1), tokens(sum(n), H, D, torch.float16, 2)
+    ctx.append_tokens(shape, kk.cuda(), vv.cuda(), pos.int().cuda(), requests=req.int().cuda())
+    torch.cuda.synchronize()
+    pm.write(ref, shape, kk, vv, torch.tensor(base)[req] * T + pos)
+    assert torch.equal(mem.view(rows, E), ref) and ctx.status() == 0
+    sel = torch.tensor([[4, 0, 2], [8, 1, 5]], dtype=torch.int32)
+    out, miss = torch.empty((2, k), dtype=torch.int32, device="cuda"), torch.empty(2, dtype=torch.int32, device="cuda")
+    ctx.resolve(sel.cuda(), out, miss)
+    # a token of a resident page is written in both places; one past the extent nowhere
+    k1, v1 = tokens(2, H, D, torch.float16, 3), tokens(2, H, D, torch.float16, 4)
+    ctx.append_tokens(shape, k1.cuda(), v1.cuda(), torch.tensor([5 * T, 8 * T + 31], dtype=torch.int32, device="cuda"))
+    ctx.resolve(sel.cuda(), out, miss)
+    q = torch.randn((2, 1, 3, D)).to(torch.float16)
+    o, lse = torch.empty_like(q, device="cuda"), torch.empty((2, 1, 3), device="cuda")
+    lengths = torch.tensor([150, 288], dtype=torch.int32)
+    ctx.attend_pages(shape, q.cuda(), out, sel.cuda(), lengths.cuda(), o, lse, 0.2)
+    torch.cuda.synchronize()
+    assert ctx.status() == hs.HS_STATUS_RANGE and not miss.any()
+    pm.write(ref, shape, k1[1:], v1[1:], torch.tensor([(base[1] + 8) * T + 31]))
+    assert torch.equal(mem.view(rows, E), ref)
+    hist = torch.stack([torch.nn.functional.pad(ref[b:b + x], (0, 0, 0, 16 - x)) for b, x in zip(base, pages)])
+    ro, rl, to, tl = pm.attend(shape, q, hist, sel, sel, lengths, 0.2)
+    for got, want, tol in ((o, ro, to), (lse, rl, tl)):  # the rows hold overflows: NaN blocks
+        got, nan = got.cpu().double(), torch.isnan(want)
+        assert torch.equal(torch.isnan(got), nan) and ((got - want).abs()[~nan] <= tol[~nan]).all()
     ctx.close()
