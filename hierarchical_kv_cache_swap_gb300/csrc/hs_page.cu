@@ -117,7 +117,7 @@ __device__ __forceinline__ Block quantise(const uint32_t (&w)[8]) {
 }
 
 __device__ __forceinline__ void load_block(uint32_t (&w)[8], const uint16_t* p) {
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(p)), b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+    const uint4 a = load(reinterpret_cast<const uint4*>(p)), b = load(reinterpret_cast<const uint4*>(p) + 1);
     w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
     w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
 }
@@ -154,7 +154,7 @@ struct ToPages {
     size_t tile_bytes;  // the tiles of all pages lie one after the other
     uint32_t* status;
     __device__ __forceinline__ Place operator()(int64_t i, bool first) const {
-        const int64_t d = __ldg(dest + i);
+        const int64_t d = load(dest + i);
         if (d < 0) return {nullptr, nullptr, -1};
         if (d >= slots) {
             if (first && status) atomicOr(status, 1u /* HS_STATUS_RANGE */);
@@ -171,15 +171,15 @@ struct ToContext {
     int tokens;
     size_t tile_bytes;
     __device__ __forceinline__ Place operator()(int64_t i, bool first) const {
-        const int32_t p = __ldg(positions + i);
-        const int64_t b = requests ? (int64_t)__ldg(requests + i) : i;
+        const int32_t p = load(positions + i);
+        const int64_t b = requests ? (int64_t)load(requests + i) : i;
         if (p < 0 || b < 0) return {nullptr, nullptr, -1};
         const int32_t page = p / tokens, off = p - page * tokens;
-        if (b >= L.R || page >= (L.row_len ? __ldg(L.row_len + b) : L.C)) {
+        if (b >= L.R || page >= (L.row_len ? load(L.row_len + b) : L.C)) {
             if (first) atomicOr(L.status, 1u /* HS_STATUS_RANGE */);
             return {nullptr, nullptr, -1};
         }
-        const int64_t row = (L.row_base ? __ldg(L.row_base + b) : b * L.C) + page;
+        const int64_t row = (L.row_base ? load(L.row_base + b) : b * L.C) + page;
         const int32_t s = L.pt[(size_t)b * L.C + page];
         const size_t in = (size_t)(off / kTile) * tile_bytes;
         return {const_cast<uint8_t*>(L.host) + (size_t)row * L.host_stride + in,
@@ -246,8 +246,8 @@ __device__ __forceinline__ uint4 decode8(uint32_t w, uint32_t u) {
 // the same bytes took 139 us instead of 104 (131072 tokens, 8 heads of 128).
 template <int D, bool BF16, bool WIDE>
 __global__ void __launch_bounds__(kThreads)
-read_kernel(const uint8_t* __restrict__ pages, int S, const int32_t* __restrict__ slots, int units, Divisor n, Divisor per_page,
-            Divisor heads, uint16_t* __restrict__ ko, uint16_t* __restrict__ vo, uint32_t* status) {
+read_kernel(const uint8_t* pages, int S, const int32_t* slots, int units, Divisor n, Divisor per_page,
+            Divisor heads, uint16_t* ko, uint16_t* vo, uint32_t* status) {
     constexpr int kBlocks = D / 16, kTok = 32 / kBlocks;
     const int lane = threadIdx.x & 31, blk = lane % kBlocks, u = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -255,7 +255,7 @@ read_kernel(const uint8_t* __restrict__ pages, int S, const int32_t* __restrict_
         const int j = per_page(u);  // page of [B][n]
         const int in = u - j * (int)per_page.d, grp = heads(in), h = in - grp * (int)heads.d;
         const int off = grp * kTok + lane / kBlocks;
-        const int32_t s = __ldg(slots + j);
+        const int32_t s = load(slots + j);
         uint2 kc = make_uint2(0, 0), vc = kc;
         uint32_t ku = 0, vu = 0;
         if (s >= S) {
@@ -264,10 +264,10 @@ read_kernel(const uint8_t* __restrict__ pages, int S, const int32_t* __restrict_
             const int tiles = (int)per_page.d / (int)heads.d / (kTile / kTok);
             const uint8_t* c = pages + (((size_t)n(j) * S + s) * tiles + off / kTile) * heads.d * (18 * D) + (size_t)h * (18 * D);
             const int r = off % kTile;
-            kc = __ldg(reinterpret_cast<const uint2*>(c + r * (D / 2) + 8 * blk));
-            vc = __ldg(reinterpret_cast<const uint2*>(c + 9 * D + r * (D / 2) + 8 * blk));
-            ku = __ldg(c + 8 * D + r * (D / 16) + blk);
-            vu = __ldg(c + 17 * D + r * (D / 16) + blk);
+            kc = load(reinterpret_cast<const uint2*>(c + r * (D / 2) + 8 * blk));
+            vc = load(reinterpret_cast<const uint2*>(c + 9 * D + r * (D / 2) + 8 * blk));
+            ku = load(c + 8 * D + r * (D / 16) + blk);
+            vu = load(c + 17 * D + r * (D / 16) + blk);
         }
         const size_t at = (((size_t)j * (per_page.d / heads.d) + grp) * kTok + lane / kBlocks) * heads.d * D + (size_t)h * D + 16 * blk;
         store_values<WIDE>(ko + at, decode8<BF16>(kc.x, ku), decode8<BF16>(kc.y, ku));
@@ -341,10 +341,11 @@ cudaError_t launch_read_pages(cudaStream_t stream, const PageShape& ps, bool bf1
             const uint8_t* from = pages + (size_t)b * S * ps.bytes();
             uint16_t *ko = (uint16_t*)k + (b * n + j) * values, *vo = (uint16_t*)v + (b * n + j) * values;
             cudaError_t e;
-#define HS_READ(D_)                                                                                                           \
-    launch(stream, grid, bf16 ? (wide ? read_kernel<D_, true, true> : read_kernel<D_, true, false>)                            \
-                              : (wide ? read_kernel<D_, false, true> : read_kernel<D_, false, false>), from, S,                 \
-           slots + b * n + j, units, Divisor(n), Divisor(per_page), Divisor(ps.heads), ko, vo, status)
+#define HS_READ(D_)                                                                                               \
+    launch(stream, grid,                                                                                          \
+           bf16 ? (wide ? read_kernel<D_, true, true> : read_kernel<D_, true, false>)                             \
+                : (wide ? read_kernel<D_, false, true> : read_kernel<D_, false, false>),                          \
+           from, S, slots + b * n + j, units, Divisor(n), Divisor(per_page), Divisor(ps.heads), ko, vo, status)
             e = ps.dim == 64 ? HS_READ(64) : ps.dim == 128 ? HS_READ(128) : HS_READ(256);
 #undef HS_READ
             if (e != cudaSuccess) return e;

@@ -26,6 +26,11 @@ struct PageShape {
 };
 
 #ifdef __CUDACC__
+// What a kernel reads that another may still have been writing when it was launched (a
+// programmatic dependent): an ordinary load, never one through the read-only path.
+template <class T>
+__device__ __forceinline__ T load(const T* p) { return *p; }
+
 // n / d for 0 <= n < 2^31 by a multiplication (Granlund and Montgomery, 1994).
 struct Divisor {
     uint32_t d, m, s;

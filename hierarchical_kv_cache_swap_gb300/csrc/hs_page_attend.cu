@@ -46,7 +46,7 @@
 // Measured (16-token pages, 8 heads of 128 with 8 queries each, 128 pages a request; us a
 // call in a graph): 256 requests 105 (5.82 TB/s, 87 % of a copy's rate), of which the copies
 // alone take 91.5 and the arithmetic alone about 100; 64 requests 33 (4.65 TB/s: 512 jobs do
-// not spread evenly over 152 SMs), 1 request 5.1 and one of five tokens 3.6 (the chain of
+// not spread evenly over 152 SMs), 1 request 5.2 and one of five tokens 3.7 (the chain of
 // loads, one pair of tiles and the joins). 32 rows (four drafted tokens) over 16 requests take
 // 21.5, where the products alone would take 8.5 on all SMs.
 #include <cuda_bf16.h>
@@ -244,15 +244,15 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
         gslot = -1;
         if (next < ntiles) {
             const int j = P.tiles(next);
-            gslot = __ldg(slots + j);
-            gsel = __ldg(sel + j);
+            gslot = load(slots + j);
+            gsel = load(sel + j);
         }
     };
     look_up();
     // the request's mask: query token t sees p <= length - Tq + t and (p >= start or p < prefix)
-    const int length = __ldg(A.lengths + b);
-    const int start = A.start ? __ldg(A.start + b) : 0;
-    const int prefix = A.prefix ? __ldg(A.prefix + b) : 0;
+    const int length = load(A.lengths + b);
+    const int start = A.start ? load(A.start + b) : 0;
+    const int prefix = A.prefix ? load(A.prefix + b) : 0;
     const int qpos0 = length - A.Tq;  // may be negative
     const uint8_t* pages = A.pages + ((size_t)b * A.S * A.tiles * A.H + h) * C::kChunk;
     const size_t unit_bytes = (size_t)A.H * C::kChunk;
@@ -265,12 +265,12 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
         const int row = min(r0 + r, rows - 1), tok = P.group(row), head = h * A.G + row - tok * A.G;
         const uint16_t* src = A.q + b * A.q_batch + tok * A.q_token + head * A.q_head + hl * kQ;
         if constexpr (kQ == 4) {
-            const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
+            const uint2 v = load(reinterpret_cast<const uint2*>(src));
             qw[0] = v.x; qw[1] = v.y;
         } else {
 #pragma unroll
             for (int i = 0; i < kQ / 8; ++i) {
-                const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + i);
+                const uint4 v = load(reinterpret_cast<const uint4*>(src) + i);
                 qw[4 * i] = v.x; qw[4 * i + 1] = v.y; qw[4 * i + 2] = v.z; qw[4 * i + 3] = v.w;
             }
         }
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
         if (hl == 0) {
             // to log2 units; with a cap, to 2 log2 e s / cap
             sm.qscale[r] = MOD && A.cap > 0.f ? scale * (A.scale * (2.f * kLog2e / A.cap)) : scale * (A.scale * kLog2e);
-            sm.slope[r] = MOD && A.slopes && row < rows ? __ldg(A.slopes + h * A.G + row - tok * A.G) * kLog2e : 0.f;
+            sm.slope[r] = MOD && A.slopes && row < rows ? load(A.slopes + h * A.G + row - tok * A.G) * kLog2e : 0.f;
             sm.qpos[r] = qpos0 + tok;
         }
         // dimension d is taken by lane d / (D/4) of the row's group at step d % (D/4) / 4
@@ -752,7 +752,7 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
                 float e = -INFINITY;
                 if (top > -INFINITY) {
                     e = (top + lg2(sum)) * kLn2;
-                    if (MOD && A.slopes) e -= __ldg(A.slopes + head) * (float)(qpos0 + tok - last);
+                    if (MOD && A.slopes) e -= load(A.slopes + head) * (float)(qpos0 + tok - last);
                 }
                 A.lse[((size_t)b * A.Tq + tok) * A.H * A.G + head] = e;
             }
