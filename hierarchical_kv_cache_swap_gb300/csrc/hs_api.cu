@@ -601,6 +601,9 @@ int hs_attend_pages(hs_stream_t stream, const hs_page_attention* a) {
         return fail(HS_ERR_INVALID, "q, o and pages must be 16-byte aligned");
     if ((a->q_batch_stride | a->q_token_stride | a->q_head_stride | a->o_batch_stride | a->o_token_stride | a->o_head_stride) & 7)
         return fail(HS_ERR_INVALID, "rows of q and o must be 16-byte aligned");
+    auto overlap = [&](int64_t n, int64_t stride) { return n > 1 && stride > -ps.dim && stride < ps.dim; };
+    if (overlap(a->B, a->o_batch_stride) || overlap(a->q_tokens, a->o_token_stride) || overlap(a->q_heads, a->o_head_stride))
+        return fail(HS_ERR_INVALID, "rows of o overlap");
     if ((rc = sm_count(&sms)) != HS_OK) return rc;
     hs::PageAttention p;
     p.q = (const uint16_t*)a->q;

@@ -137,7 +137,13 @@ uint32_t* status_of(PyObject* o) {
     return (uint32_t*)x.data_ptr();
 }
 
-PyObject* done(int rc, const char* what) {
+// Makes the C call without the interpreter's lock: a launch may block while the queue is full
+// of work that waits for a callback into Python.
+template <class F>
+PyObject* done(const char* what, F&& call) {
+    PyThreadState* state = PyEval_SaveThread();
+    const int rc = call();
+    PyEval_RestoreThread(state);
     if (rc == HS_OK) Py_RETURN_NONE;
     PyErr_Format(g_error ? g_error : PyExc_RuntimeError, "%s failed (%d): %s", what, rc, hs_last_error());
     return nullptr;
@@ -162,6 +168,9 @@ bool arity(Py_ssize_t got, Py_ssize_t want) {
     return got == want;
 }
 
+// The stride of dimension i; a dimension of one has none that matters.
+int64_t stride(const at::Tensor& x, int i) { return x.size(i) > 1 ? x.stride(i) : 0; }
+
 // k and v [n, kv_heads, head_dim] with contiguous rows.
 hs_token_rows rows_of(const hs_page_shape& s, const at::Tensor& k, const at::Tensor& v) {
     const int64_t n = k.dim() == 3 ? k.size(0) : 0;
@@ -170,7 +179,7 @@ hs_token_rows rows_of(const hs_page_shape& s, const at::Tensor& k, const at::Ten
             (t.x->stride(2) != 1 && t.x->numel() > 0))
             refuse("%s must have shape [%lld, %d, %d] with contiguous rows", t.name, (long long)n, s.kv_heads, s.head_dim);
     if (v.scalar_type() != k.scalar_type()) refuse("k and v must have one dtype");
-    return hs_token_rows{k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), v.stride(0), v.stride(1)};
+    return hs_token_rows{k.data_ptr(), v.data_ptr(), stride(k, 0), stride(k, 1), stride(v, 0), stride(v, 1)};
 }
 
 // write_tokens(shape, k, v, dest, pages, status, stream)
@@ -184,9 +193,12 @@ PyObject* write_tokens(PyObject*, PyObject* const* a, Py_ssize_t na) {
         vector(dest, "dest", at::kLong, {k.size(0)});
         vector(pages, "pages", at::kByte, {-1, (int64_t)hs_page_bytes(&s)});
         on_device({{"k", &k}, {"v", &v}, {"dest", &dest}, {"pages", pages.is_cpu() && pages.is_pinned() ? nullptr : &pages}});
-        return done(hs_write_tokens(stream_of(a[6]), &s, type, &rows, k.size(0), (const int64_t*)dest.data_ptr(),
-                                    (uint8_t*)pages.data_ptr(), pages.size(0), status_of(a[5])),
-                    "hs_write_tokens");
+        uint32_t* const status = status_of(a[5]);
+        const hs_stream_t stream = stream_of(a[6]);
+        return done("hs_write_tokens", [&] {
+            return hs_write_tokens(stream, &s, type, &rows, k.size(0), (const int64_t*)dest.data_ptr(),
+                                   (uint8_t*)pages.data_ptr(), pages.size(0), status);
+        });
     });
 }
 
@@ -202,9 +214,12 @@ PyObject* append_tokens(PyObject*, PyObject* const* a, Py_ssize_t na) {
         vector(pos, "positions", at::kInt, {k.size(0)});
         if (req) vector(*req, "requests", at::kInt, {k.size(0)});
         on_device({{"k", &k}, {"v", &v}, {"positions", &pos}, {"requests", req}});
-        return done(hs_append_tokens((hs_ctx*)(uintptr_t)integer(a[0]), stream_of(a[6]), &s, type, &rows, k.size(0),
-                                     req ? (const int32_t*)req->data_ptr() : nullptr, (const int32_t*)pos.data_ptr()),
-                    "hs_append_tokens");
+        hs_ctx* const ctx = (hs_ctx*)(uintptr_t)integer(a[0]);
+        const hs_stream_t stream = stream_of(a[6]);
+        return done("hs_append_tokens", [&] {
+            return hs_append_tokens(ctx, stream, &s, type, &rows, k.size(0), req ? (const int32_t*)req->data_ptr() : nullptr,
+                                    (const int32_t*)pos.data_ptr());
+        });
     });
 }
 
@@ -241,9 +256,13 @@ PyObject* read_pages(PyObject*, PyObject* const* a, Py_ssize_t na) {
         const Pages p = pages_of(a[1], s);
         if (p.B != B) refuse("pages of %lld requests, slots of %lld", (long long)p.B, (long long)B);
         on_device({{"slots", &slots}, {"k", &k}, {"v", &v}});
-        return done(hs_read_pages(stream_of(a[6]), &s, type, p.at, int_of(B, "B"), int_of(p.S, "S"),
-                                  (const int32_t*)slots.data_ptr(), int_of(n, "n"), k.data_ptr(), v.data_ptr(), status_of(a[5])),
-                    "hs_read_pages");
+        const int requests = int_of(B, "B"), S = int_of(p.S, "S"), count = int_of(n, "n");
+        uint32_t* const status = status_of(a[5]);
+        const hs_stream_t stream = stream_of(a[6]);
+        return done("hs_read_pages", [&] {
+            return hs_read_pages(stream, &s, type, p.at, requests, S, (const int32_t*)slots.data_ptr(), count, k.data_ptr(),
+                                 v.data_ptr(), status);
+        });
     });
 }
 
@@ -282,13 +301,13 @@ PyObject* attend_pages(PyObject*, PyObject* const* a, Py_ssize_t na) {
         p.q_heads = int_of(Hq, "q_heads");
         p.q_tokens = int_of(T, "q_tokens");
         p.q = q.data_ptr();
-        p.q_batch_stride = q.stride(0);
-        p.q_token_stride = q.stride(1);
-        p.q_head_stride = q.stride(2);
+        p.q_batch_stride = stride(q, 0);
+        p.q_token_stride = stride(q, 1);
+        p.q_head_stride = stride(q, 2);
         p.o = o.data_ptr();
-        p.o_batch_stride = o.stride(0);
-        p.o_token_stride = o.stride(1);
-        p.o_head_stride = o.stride(2);
+        p.o_batch_stride = stride(o, 0);
+        p.o_token_stride = stride(o, 1);
+        p.o_head_stride = stride(o, 2);
         p.lse = (float*)lse.data_ptr();
         p.pages = pages.at;
         p.slots = (const int32_t*)slots.data_ptr();
@@ -300,7 +319,8 @@ PyObject* attend_pages(PyObject*, PyObject* const* a, Py_ssize_t na) {
         p.start = start ? (const int32_t*)start->data_ptr() : nullptr;
         p.prefix = prefix ? (const int32_t*)prefix->data_ptr() : nullptr;
         p.status = status_of(a[13]);
-        return done(hs_attend_pages(stream_of(a[14]), &p), "hs_attend_pages");
+        const hs_stream_t stream = stream_of(a[14]);
+        return done("hs_attend_pages", [&] { return hs_attend_pages(stream, &p); });
     });
 }
 

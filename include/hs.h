@@ -372,7 +372,7 @@ int hs_set_extents(hs_ctx* ctx, hs_stream_t stream, const int64_t* base, const i
  * hs_page_bytes(). All of them are enqueue-only and graph-capturable, allocate nothing and
  * need no workspace; their device pointers belong to the calling thread's current device.
  * Their kernels are programmatic dependents of the kernel before them on the stream: they
- * may be launched while it runs, and wait for it before they read or write anything.
+ * may be launched while it runs, and wait for it to end before they read or write anything.
  *
  * Layout: for tile i (tokens 16 i .. 16 i + 15 of the page) and head h, the 18 * head_dim
  * bytes at (i * kv_heads + h) * 18 * head_dim hold K codes [16][head_dim / 2], K scales
@@ -425,8 +425,8 @@ int hs_write_tokens(hs_stream_t stream, const hs_page_shape* shape, int dtype, c
  * tokens of page position / tokens. It is written into the host store and, when the page is
  * resident, into its slot as well, so the cache stays exact; the replacement state does not
  * change. A page >= context_len (or the request's extent), or a request >= num_requests, is
- * skipped and sets HS_STATUS_RANGE; a negative request is skipped like a negative position. Distinct (request, position) pairs only. Stream ordered
- * with the context's other calls.
+ * skipped and sets HS_STATUS_RANGE; a negative request is skipped like a negative position.
+ * Distinct (request, position) pairs only. Stream ordered with the context's other calls.
  */
 int hs_append_tokens(hs_ctx* ctx, hs_stream_t stream, const hs_page_shape* shape, int dtype, const hs_token_rows* rows,
                      int64_t n, const int32_t* requests, const int32_t* positions);
@@ -453,7 +453,8 @@ int hs_read_pages(hs_stream_t stream, const hs_page_shape* shape, int dtype, con
  * sees no key gets o = 0 and lse = -inf. Keys that no query sees are not read into the
  * result, whatever their bytes hold; a page selected twice counts twice.
  * Rows of q and o are contiguous and 16-byte aligned: (b, t, head) starts b * batch_stride +
- * t * token_stride + head * head_stride elements in. The products run on the tensor cores
+ * t * token_stride + head * head_stride elements in; rows of o do not overlap. A score that
+ * is -inf in f32 counts as unseen. The products run on the tensor cores
  * with f32 sums; the queries enter them as halves (bf16 ones scaled by a power of two per
  * row) and the softmax weights are rounded to half for the product with V.
  */

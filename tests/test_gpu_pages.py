@@ -436,6 +436,60 @@ def test_another_stream_and_a_captured_graph():
         assert torch.equal(ko.cpu().double(), want)
 
 
+def test_dimensions_of_one_may_have_any_stride():
+    c = case(1, 1, 4, 64, 16, 3, 3, [40])
+    q = torch.as_strided(c["q"].cuda(), (1, 1, 4, 64), (3, 5, 64, 1))
+    o, lse = torch.empty(4 * 64, dtype=q.dtype, device="cuda"), torch.empty((1, 1, 4), device="cuda")
+    hs.attend_pages(c["shape"], q, *(c[n].cuda() for n in ("pages", "slots", "sel", "lengths")),
+                    torch.as_strided(o, (1, 1, 4, 64), (1, 7, 64, 1)), lse, 0.1)
+    check(c, 0.1, got=(o.view(1, 1, 4, 64).cpu().double(), lse.cpu().double()))
+    k = torch.as_strided(tokens(1, 1, 64, torch.bfloat16, 1).cuda(), (1, 1, 64), (1, 2, 1))
+    ref = torch.zeros((1, 1152), dtype=torch.uint8)
+    pages = ref.cuda()
+    hs.write_tokens((16, 1, 64), k, k, torch.tensor([3], device="cuda"), pages)
+    pm.write(ref, (16, 1, 64), k.cpu(), k.cpu(), torch.tensor([3]))
+    assert torch.equal(pages.cpu(), ref)
+
+
+def test_rows_broadcast_over_tokens_and_heads():
+    k = tokens(1, 1, 128, torch.float16, 2)
+    ref = torch.zeros((2, 16 * 3 * 128 * 9 // 8), dtype=torch.uint8)
+    pages = ref.cuda()
+    dest = torch.tensor([4, 9, 31])
+    hs.write_tokens((16, 3, 128), k.cuda().expand(3, 3, 128), k.cuda().expand(3, 3, 128), dest.cuda(), pages)
+    pm.write(ref, (16, 3, 128), k.expand(3, 3, 128), k.expand(3, 3, 128), dest)
+    assert torch.equal(pages.cpu(), ref)
+
+
+def test_captured_between_a_fork_and_a_join():
+    """Work of another stream, a copy and a fill directly before and after the calls of a graph."""
+    c = case(3, 2, 8, 128, 16, 24, 30, [380, 17, 300])
+    cu = [c[n].cuda() for n in ("q", "pages", "slots", "sel", "lengths")]
+    o, lse = torch.zeros_like(cu[0]), torch.zeros(c["q"].shape[:3], device="cuda")
+    q0, lens0, far, copy = torch.zeros_like(cu[0]), torch.zeros_like(cu[4]), torch.zeros_like(o), torch.zeros_like(o)
+    hs.attend_pages(c["shape"], *cu, o, lse, 0.1)
+    torch.cuda.synchronize()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            lens0.copy_(cu[4])
+            hs.attend_pages(c["shape"], cu[0], *cu[1:4], lens0, far, torch.empty_like(lse), 0.1)
+        q0.copy_(cu[0])
+        main.wait_stream(side)
+        hs.attend_pages(c["shape"], q0, *cu[1:4], lens0, o, lse, 0.1)
+        hs.attend_pages(c["shape"], q0, *cu[1:4], lens0, o, lse, 0.1)
+        copy.copy_(o)
+    for _ in range(3):
+        for x in (o, lse, q0, lens0, far, copy):
+            x.zero_()
+        graph.replay()
+    torch.cuda.synchronize()
+    for x in (o, far, copy):
+        check(c, 0.1, got=(x.cpu().double(), lse.cpu().double()))
+
+
 def test_two_calls_at_once_on_two_streams():
     a, b = case(2, 8, 8, 128, 16, 128, 128, [30000, 2000], seed=1), case(2, 8, 8, 128, 16, 128, 128, [500, 2000], seed=2)
     s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
@@ -621,4 +675,68 @@ def test_tokens_join_extents_of_a_shared_pool():
     for got, want, tol in ((o, ro, to), (lse, rl, tl)):  # the rows hold overflows: NaN blocks
         got, nan = got.cpu().double(), torch.isnan(want)
         assert torch.equal(torch.isnan(got), nan) and ((got - want).abs()[~nan] <= tol[~nan]).all()
+    ctx.close()
+
+
+def test_attention_behind_a_resolution_in_chunks():
+    """More requests than SMs: the resolution and its fetches are several overlapping kernels,
+    and the attention launched behind them must see every page fetched."""
+    shape, B, C, S, k = (16, 1, 64), 400, 12, 5, 4
+    E = hs.PageShape(*shape).bytes
+    ctx = hs.Context(B, C, S, E)
+    hist = pm.random_pages(B * C, shape, 7).view(B, C, E)
+    ctx.host_kv()[..., :E] = hist.numpy()
+    g = torch.Generator().manual_seed(1)
+    lengths = torch.full((B,), C * 16, dtype=torch.int32)
+    q = torch.randn((B, 1, 2, 64), generator=g).to(torch.bfloat16)
+    qd, ld = q.cuda(), lengths.cuda()
+    sels = [torch.stack([torch.randperm(C, generator=g)[:k] for _ in range(B)]).int() for _ in range(6)]
+    dev = [s.cuda() for s in sels]
+    outs = []
+    for s in dev:  # back to back, nothing waits in between
+        out, miss = torch.empty((B, k), dtype=torch.int32, device="cuda"), torch.empty(B, dtype=torch.int32, device="cuda")
+        ctx.resolve(s, out, miss)
+        o, lse = torch.empty_like(qd), torch.empty((B, 1, 2), device="cuda")
+        ctx.attend_pages(shape, qd, out, s, ld, o, lse, 0.2)
+        outs.append((o, lse))
+    assert ctx.status() == 0
+    for s, (o, lse) in zip(sels, outs):
+        ro, rl, to, tl = pm.attend(shape, q, hist, s, s, lengths, 0.2)
+        assert ((o.cpu().double() - ro).abs() <= to).all() and ((lse.cpu().double() - rl).abs() <= tl).all()
+    ctx.close()
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_pages_read_behind_a_resolution_whose_first_chunk_ends_last(captured):
+    """The fetch of a later chunk, with nothing to copy, is done long before the first one's."""
+    shape, B, C, k = (16, 4, 128), 320, 20, 16
+    E = hs.PageShape(*shape).bytes
+    ctx = hs.Context(B, C, k, E)
+    ctx.host_kv()[..., :E] = pm.random_pages(C, shape, 3).numpy()
+    sel = torch.full((B, k), -1, dtype=torch.int32)
+    sel[:B // 3] = torch.arange(k, dtype=torch.int32) + 2
+    sel, out = sel.cuda(), torch.full((B, k), -1, dtype=torch.int32, device="cuda")
+    miss = torch.empty(B, dtype=torch.int32, device="cuda")
+    k1, v1, k2, v2 = (torch.empty((B, k * 16, 4, 128), dtype=torch.float16, device="cuda") for _ in range(4))
+
+    def step():
+        ctx.resolve(sel, out, miss)
+        ctx.read_pages(shape, out, k1, v1)
+
+    if captured:
+        ctx.read_pages(shape, out, k1, v1)  # loads the kernel
+        graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(graph, stream=side):
+            step()
+        step = graph.replay
+    ctx.device_kv().zero_()
+    torch.cuda.synchronize()
+    step()
+    torch.cuda.synchronize()
+    ctx.read_pages(shape, out, k2, v2)
+    assert ctx.status() == 0 and int(miss.sum()) == B // 3 * k
+    assert torch.equal(k1, k2) and torch.equal(v1, v2)
+    n = k * 16
+    got = torch.stack([k2[0].cpu(), k2[B // 3 - 1].cpu()])
+    assert torch.equal(got[0], got[1]) and bool((got[0].abs().amax(dim=(1, 2)) > 0).all()) and got.shape[1] == n
     ctx.close()

@@ -159,6 +159,10 @@ def _attention(**change):
     ("null pages", {"pages": None}, hs.HS_ERR_INVALID),
     ("aligned", {"q": 24}, hs.HS_ERR_INVALID),
     ("aligned", {"o_head_stride": 4}, hs.HS_ERR_INVALID),
+    ("overlap", {"o_head_stride": 0}, hs.HS_ERR_INVALID),
+    ("overlap", {"o_head_stride": -120}, hs.HS_ERR_INVALID),
+    ("overlap", {"q_tokens": 2, "o_token_stride": 64}, hs.HS_ERR_INVALID),
+    ("overlap", {"B": 2, "o_batch_stride": 0}, hs.HS_ERR_INVALID),
 ])
 def test_attend_pages_refuses_before_touching_cuda(lib, what, change, code):
     assert lib.hs_attend_pages(None, _ref(_attention(**change))) == code
