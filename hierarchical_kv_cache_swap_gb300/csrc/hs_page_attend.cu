@@ -815,50 +815,50 @@ cudaError_t set_up(Room* room) {
     return e;
 }
 
-// Warps of a CTA and CTAs that share a selection: the pair with the least estimated time, in
-// cycles. A tile takes an SM about `tile` cycles (what its instructions cost at the rate
-// reached with many warps) and a warp's own tiles follow each other at `delay`; a warp's
-// start and end cost about 350 cycles of its SM's time and a CTA 3000 of delay, a cluster's
-// join 1500 more of both. With few jobs the delays decide and more, smaller shares win until
-// a second wave of clusters would be needed (us a call):
-//   1 request, 8 heads, 128 tiles:    8 CTAs of 8 warps 5.1, of 4 warps 5.5, of 16 warps 7.3
-//   96 jobs of 400 tiles, D = 64:     3 CTAs of 8 warps 14.1, 7 of 4 warps 15.1, 2 of 12 21.1
-//   16 jobs of 512 tiles, 16 rows:    6 CTAs of 12 warps 14.8, of 8 warps 15.6, 7 of 12 26.6
-// With many the work does, and shares only cost, but for the jobs that some SMs have more of
-// than others: 512 jobs of 128 tiles: whole 34.5, all halved 35.6, 456 whole and 56 halved
-// 32.9; in clusters of 3, 4 or 8 these mixtures took 37.0, 34.1 and 35.2.
+// Warps of a CTA, CTAs that share a selection and jobs that are not shared: what has the least
+// estimated time, in cycles, the larger of two bounds. Work: a tile takes an SM about `tile`
+// (what its instructions cost at the rate reached with many warps), a warp's start and end 450,
+// a shared CTA's join 1600 more. Chain: a warp's own pairs of tiles follow each other at `pair`
+// behind 4500 of start and end (1000 more if shared), and again for the CTAs that find no room
+// at first. With few jobs the chain decides and more, smaller shares win; with many the work
+// does, and shares only cost, but for the jobs that some SMs have more of than others. us a call:
+//   1 request, 8 heads, 128 tiles:    8 CTAs of 8 warps 5.2, of 4 warps 5.5, of 12 warps 6.4
+//   16 jobs of 512 tiles, 16 rows:    6 CTAs of 12 warps 14.9, of 8 warps 15.6, 7 of 12 26.6
+//   256 jobs of 128 tiles, 32 rows:   whole 38.2, 152 whole and 104 halved 46.7, all halved 46.8
+//   512 jobs of 128 tiles:            whole 34.5, all halved 35.6, 456 whole and 56 halved 32.9;
+//                                     such mixtures in clusters of 3, 4 or 8: 37.0, 34.1, 35.2
+// The constants are fitted to the times of every split of 110 calls (heads of 64, 128 and 256,
+// 1 to 64 rows, 8 to 2000 jobs of 8 to 1200 tiles): the split taken is 1.2 % slower than the best one
+// on average and 16 % at most.
 void plan(const Room& room, int sm_warps, int num_sms, int D, int NT, int64_t jobs, int64_t tiles, int* warps, int* shares,
           int64_t* whole) {
-    const float tile = 12.f + 0.55f * D + NT * (14.f + 0.16f * D), delay = 1000.f + 250.f * NT;
+    const float tile = 7.f + 0.55f * D + NT * (10.f + 0.12f * D), pair = 2000.f + 290.f / 128 * NT * D;
     float best = INFINITY;
     *warps = 4;
     *shares = 1;
     *whole = jobs;
     for (int n = 1; n <= kMaxSplit; ++n)
         for (int w = 4; w <= sm_warps; w += 4) {
-            const int fit = room.clusters[w / 4 - 1][n - 1];
+            const int64_t fit = (int64_t)room.clusters[w / 4 - 1][n - 1] * n;  // CTAs
             if (fit < 1 || ((n > 1 || w > 4) && 2 * (int64_t)n * w > tiles)) continue;
-            const float ctas = (float)jobs * n, share = (float)tiles / n;
-            const float work = ceilf(ctas / num_sms) * (share * tile + 350.f * w + (n > 1 ? 1500.f : 0.f));
-            const float chain = ceilf(ctas / (fit * n)) * (3000.f + (n > 1 ? 1500.f : 0.f) + ceilf(share / w) * delay);
-            const float time = fmaxf(work, chain);
-            if (time < best) {
-                best = time;
+            const float share = (float)tiles / n, ends = n > 1 ? 5500.f : 4500.f;
+            const float work_1 = tiles * tile + 450.f * w, work_n = share * tile + 450.f * w + (n > 1 ? 1600.f : 0.f);
+            const float chain_1 = ends + ceilf((float)tiles / (2 * w)) * pair, chain_n = ends + ceilf(share / (2 * w)) * pair;
+            auto consider = [&](float work, float chain, int64_t alone) {
+                if (fmaxf(work, chain) >= best) return;
+                best = fmaxf(work, chain);
                 *warps = w;
                 *shares = n;
-                *whole = n == 1 ? jobs : 0;
-            }
+                *whole = alone;
+            };
+            const float ctas = (float)jobs * n;
+            consider(ceilf(ctas / num_sms) * work_n, ceilf(ctas / fit) * chain_n, n == 1 ? jobs : 0);
             // as many whole jobs as every SM can have alike, the others halved
             const int64_t even = n == 2 ? jobs / num_sms * num_sms / n * n : 0;
             if (even == 0) continue;
-            const float mixed = (float)(even / num_sms) * ((float)tiles * tile + 350.f * w) +
-                                ceilf((float)(jobs - even) * n / num_sms) * (share * tile + 350.f * w + 1500.f);
-            if (mixed < best) {
-                best = mixed;
-                *warps = w;
-                *shares = n;
-                *whole = even;
-            }
+            const float halves = (float)(jobs - even) * n;
+            consider((float)(even / num_sms) * work_1 + ceilf(halves / num_sms) * work_n,
+                     chain_1 + (even + halves > fit ? chain_n : 0.f), even);
         }
 }
 
