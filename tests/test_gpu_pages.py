@@ -367,6 +367,26 @@ def test_long_selections(k, H, D):
     check(c, D ** -0.5, start=torch.tensor([9 * k], dtype=torch.int32), prefix=torch.tensor([100], dtype=torch.int32))
 
 
+@pytest.mark.parametrize("H,G,D,Tq,mods", [(8, 8, 128, 1, {}), (4, 2, 128, 1, {"softcap": 9.0}), (2, 16, 128, 1, {}),
+                                           (8, 8, 128, 4, {}), (4, 6, 64, 1, {}), (2, 8, 64, 4, {"softcap": 9.0}),
+                                           (4, 8, 256, 1, {}), (2, 12, 256, 1, {"softcap": 9.0})])
+def test_every_number_of_requests(H, G, D, Tq, mods):
+    """The same two requests over and over: shared, whole and mixed jobs, from a few to many an SM."""
+    k = 67
+    c = case(2, H, G, D, 16, k, k, [67 * 16 - 3, 41 * 16], Tq, seed=D + H)
+    scale = D ** -0.5
+    slopes = 2.0 ** -torch.arange(1.0, H * G + 1) if mods else None
+    ro, rl, to, tl = pm.attend(c["shape"], c["q"], c["pages"], c["slots"], c["sel"], c["lengths"], scale, cap=9.0 if mods else 0.0, slopes=slopes)
+    ro, rl, to, tl = (x.cuda() for x in (ro, rl, to, tl))
+    for n in (2, 4, 8, 10, 14, 20, 24, 26, 40, 60, 78, 100, 140, 200):
+        cu = [c[x].cuda().repeat(n // 2, *[1] * (c[x].dim() - 1)) for x in ("q", "pages", "slots", "sel", "lengths")]
+        o, lse = torch.empty_like(cu[0]), torch.empty(cu[0].shape[:3], device="cuda")
+        hs.attend_pages(c["shape"], *cu, o, lse, scale, slopes=slopes.cuda() if mods else None, **mods)
+        o, lse = o.double().view(n // 2, *ro.shape), lse.double().view(n // 2, *rl.shape)
+        assert ((o - ro).abs() <= to).all(), n
+        assert ((lse - rl).abs() <= tl).all(), n
+
+
 def test_buffer_beyond_four_gigabytes():
     shape, S = (256, 8, 256), 8000  # 589824 bytes a page, 4.7 GB
     E = hs.PageShape(*shape).bytes
