@@ -48,7 +48,7 @@
 // alone take 91.5 and the arithmetic alone about 100; 64 requests 33 (4.65 TB/s: 512 jobs do
 // not spread evenly over 152 SMs), 1 request 5.2 and one of five tokens 3.7 (the chain of
 // loads, one pair of tiles and the joins). 32 rows (four drafted tokens) over 16 requests take
-// 21.5, where the products alone would take 8.5 on all SMs.
+// 21.7, where the products alone would take 8.5 on all SMs.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
