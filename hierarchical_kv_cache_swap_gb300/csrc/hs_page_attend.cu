@@ -124,9 +124,6 @@ __device__ __forceinline__ float rcp(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// c tanh y = c - 2 c / (1 + e^(2y)); y2 = 2 y log2 e. Absolute error a few 2^-23 of c.
-__device__ __forceinline__ float capped(float c, float y2) { return fmaf(-2.f * c, rcp(1.f + ex2(y2)), c); }
-
 // Four bytes of codes to four pairs of halves (exact).
 __device__ __forceinline__ void decode_word(uint32_t w, uint32_t (&h)[4]) {
     asm("{ .reg .b8 a, b, c, d; mov.b32 {a, b, c, d}, %4; cvt.rn.f16x2.e2m1x2 %0, a; cvt.rn.f16x2.e2m1x2 %1, b;"
@@ -168,6 +165,31 @@ __device__ __forceinline__ float2 mul2f(float2 a, float2 b) {
     asm("{ .reg .b64 a, b, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mul.rn.f32x2 d, a, b; mov.b64 {%0, %1}, d; }"
         : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
+}
+// c tanh(x / c) for two scores x in log2 units, within 2^-20 of itself at any c; to_y = 2 log2 e / c,
+// so that y = x to_y has 2^y = e^(2 x / c). c - 2 c / (1 + 2^y) is off by parts of c: it serves
+// from |x| = .4 c, where rounding takes at most 8 x 2^-23 of it. Below, x + x v P(v) with v = y^2
+// keeps x's own precision however large c is: P is the quadratic that brings the sum nearest to
+// the tanh there (least largest error, 2^-23). `far`: some score of the warp is not below; both
+// forms are then made and one is selected. (24 requests with 4 x 6 heads of 64 and a cap that few
+// scores come near: 14.3 us; both always 14.65; both, with the choice left to the compiler 14.9;
+// the first form alone, wrong for large caps, 14.0. Wide heads: 11.6, 11.6, 11.7 and 11.4.)
+constexpr float kNear = 0.39f;  // of the cap
+__device__ __forceinline__ float2 capped(float2 x, float c, float to_y, bool far) {
+    auto both = [](float a) { return make_float2(a, a); };
+    const float2 y = mul2f(x, both(to_y)), v = mul2f(y, y);
+    float2 p = fma2(v, both(-8.2822472e-5f), both(1.9155892e-3f));
+    p = fma2(v, p, both(-0.040036008f));
+    p = fma2(mul2f(x, v), p, x);
+    if (!far) return p;
+    auto one = [&](float y, float p) {
+        const float f = fmaf(-2.f * c, rcp(1.f + ex2(y)), c);
+        float r;
+        asm("{ .reg .pred below; setp.lt.f32 below, %1, 0f3F93BB62; selp.f32 %0, %2, %3, below; }"  // 1.154156, .4 of the cap
+            : "=f"(r) : "f"(fabsf(y)), "f"(p), "f"(f));
+        return r;
+    };
+    return make_float2(one(y.x, p.x), one(y.y, p.y));
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {  // of the numbers among them
     float d;
@@ -353,8 +375,7 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
             }
         }
         if (hl == 0) {
-            // to log2 units; with a cap, to 2 log2 e s / cap
-            sm.qscale[r] = MOD && A.cap > 0.f ? scale * (A.scale * (2.f * kLog2e / A.cap)) : scale * (A.scale * kLog2e);
+            sm.qscale[r] = scale * (A.scale * kLog2e);  // to log2 units
             sm.slope[r] = MOD && A.slopes && row < rows ? load(A.slopes + h * A.G + row - tok * A.G) * kLog2e : 0.f;
             sm.qpos[r] = qpos0 + tok;
         }
@@ -368,7 +389,7 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
     float2 qs[NT];  // rows 8 n + 2 t, + 1
 #pragma unroll
     for (int n = 0; n < NT; ++n) qs[n] = *reinterpret_cast<const float2*>(&sm.qscale[8 * n + 2 * t]);
-    const float cap2 = A.cap * kLog2e;
+    const float cap2 = A.cap * kLog2e, to_y = 2.f / A.cap;
 
     // O^T: dims g D/8 + 2 i (c = 0, 1), + 1 (2, 3); rows 8 n + 2 t (c = 0, 2), + 1 (1, 3)
     float acc[C::kSteps][NT][4];
@@ -487,6 +508,18 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
                     m[n] = fma2(sl, make_float2(-(float)moved, -(float)moved), m[n]);
                 }
             }
+            bool far = false;
+            if (A.cap > 0.f) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float top[2];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        top[c] = max3(fmaxf(fabsf(s[0][n][c]), fabsf(s[0][n][c + 2])), fabsf(s[1][n][c]), fabsf(s[1][n][c + 2]));
+                    far |= !(fabsf(top[0] * qs[n].x) < kNear * cap2 && fabsf(top[1] * qs[n].y) < kNear * cap2);
+                }
+                far = __any_sync(0xffffffffu, far);
+            }
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -495,7 +528,7 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         float2 y = mul2f(make_float2(s[u][n][2 * k], s[u][n][2 * k + 1]), qs[n]);
-                        if (A.cap > 0.f) y = make_float2(capped(cap2, y.x), capped(cap2, y.y));
+                        if (A.cap > 0.f) y = capped(y, cap2, to_y, far);
                         if (A.slopes) y = fma2(*reinterpret_cast<const float2*>(&sm.slope[8 * n + 2 * t]), make_float2(back, back), y);
                         x[u][n][k] = y;
                         z[u][n][k] = make_float2(y.x - m[n].x, y.y - m[n].y);
