@@ -191,9 +191,9 @@ __device__ __forceinline__ float2 capped(float2 x, float c, float to_y, bool far
     };
     return make_float2(one(y.x, p.x), one(y.y, p.y));
 }
-__device__ __forceinline__ float max3(float a, float b, float c) {  // of the numbers among them
+__device__ __forceinline__ float max3(float a, float b, float c) {  // NaN if one of them is
     float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -562,8 +562,9 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
         bool more = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
+            // a NaN too moves the references: a key that is one, or -inf before the row's first key
             const float a = max3(z[0][n][0].x, z[0][n][0].y, z[0][n][1].x), b = max3(z[0][n][1].y, z[1][n][0].x, z[1][n][0].y);
-            more |= !(max3(fmaxf(a, b), z[1][n][1].x, z[1][n][1].y) <= kRescale);
+            more |= !(max3(a, z[1][n][1].x, z[1][n][1].y) <= kRescale && b <= kRescale);
         }
         if (__any_sync(0xffffffffu, more)) {  // a row's maximum has grown: move every row's reference
 #pragma unroll

@@ -110,3 +110,50 @@ def test_attention_with_caps_of_every_size(cap, dtype):
     c = case(2, 1, 16, 64, 32, 6, 6, [192, 33], dtype=dtype, seed=12)
     check(c, 0.125, cap, 2.0 ** -torch.arange(1.0, 17.0))
     check(case(1, 2, 5, 256, 16, 40, 40, [640], dtype=dtype, seed=13), 0.0625, cap)
+
+
+@pytest.mark.parametrize("mods", [{}, {"softcap": 8.0}, {"slopes": 2.0 ** -torch.arange(1.0, 17.0)}])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_a_nan_key_that_no_other_key_precedes(D, mods):
+    """The first key of each sequence is NaN for one head: its rows see nothing else at length 1,
+    and at length 3 the others. Such rows are NaN, not rows without a key."""
+    c = case(4, 2, 8, D, 16, 1, 1, [1, 3, 1, 2], seed=D)
+    want, wl = run(c, 0.1, **mods)
+    _, scale_at = pm.offsets((16, 2, D))
+    for b in range(3):  # the fourth has none
+        c["pages"][b, c["slots"][b, 0], scale_at[0, 0, 0, 0]] = 0xFF
+    o, lse = run(c, 0.1, **mods)
+    assert torch.isnan(o[:3, 0, :8]).all() and torch.isnan(lse[:3, 0, :8]).all()
+    assert torch.equal(o[:, 0, 8:], want[:, 0, 8:]) and torch.equal(lse[:, 0, 8:], wl[:, 0, 8:])
+    assert torch.equal(o[3], want[3]) and torch.equal(lse[3], wl[3])
+
+
+def minus_infinity(lens, k, last):
+    """Requests whose scores are -inf in f32 (-3e38 x 4 x 100) at positions below `last`, 0 from it."""
+    c = case(len(lens), 1, 8, 64, 16, k, k, lens, seed=5)
+    c["q"].zero_()
+    c["q"][..., 0] = -3e38
+    code_at, scale_at = pm.offsets((16, 1, 64))
+    for b in range(len(lens)):
+        for j in range(k):
+            if c["sel"][b, j] >= 0:
+                p = int(c["sel"][b, j]) * 16 + torch.arange(16)
+                page = c["pages"][b, c["slots"][b, j]]
+                page[code_at[0, :, 0, 0]] = torch.where(p < last, 6, 0).to(torch.uint8)  # 4 and, beside it, 0
+                page[scale_at[0, :, 0, 0]] = 0x78
+    return c
+
+
+def test_scores_of_minus_infinity_are_not_seen():
+    """Before any other key is seen, next to masked ones: no NaN, and no part in the result."""
+    slopes = 2.0 ** -torch.arange(8.0, 16.0)
+    c = minus_infinity([1, 9, 40], 4, 1000)
+    for mods in ({}, {"slopes": slopes}):
+        o, lse = run(c, 100.0, **mods)
+        assert not o.any() and torch.isneginf(lse).all()
+    c = minus_infinity([960, 955], 60, 480)
+    mods = dict(slopes=slopes, start=torch.tensor([320, 330]), prefix=torch.tensor([8, 5]))
+    mods = {n: x.int() if n != "slopes" else x for n, x in mods.items()}
+    o, lse = run(c, 100.0, **mods)
+    ro, rl, to, tl = pm.attend(c["shape"], c["q"], c["pages"], c["slots"], c["sel"], c["lengths"], 100.0, **mods)
+    assert ((o - ro).abs() <= to).all() and ((lse - rl).abs() <= tl).all()
