@@ -709,10 +709,15 @@ __device__ __forceinline__ void fetch_role(const Layout& L, const int32_t* out, 
 // only when it finishes, or when it has signalled programmatic completion after writing
 // them), so the first batch is loaded before the wait; nothing the previous call writes
 // is read before that grid (and, through its own wait, the previous resolution) is done.
-// A later chunk of a call's requests (`wait` = 0) does not wait: it is launched behind the
-// first chunk's fetch, which starts only once every CTA of the first chunk has passed its
-// wait -- the previous call is complete by then -- and its requests are disjoint from the
-// earlier chunks', so it runs under their fetch.
+// A later chunk of a call's requests (`wait` = 0) does not wait before its work: it is launched
+// behind the earlier chunk's fetch, which starts only once every CTA of the first chunk has
+// passed its wait -- the previous call is complete by then -- and its requests are disjoint from
+// the earlier chunks', so it runs under their fetch. Its first CTA waits for that fetch at its
+// end: a grid is done when its last CTA is, so this chunk's resolution, and through it its own
+// fetch, ends after the earlier chunk's fetch, and whoever waits for the last grid of a call
+// has waited for all of them. (Every CTA waiting would keep the later fetch, which needs their
+// registers, from running beside the earlier one.) That fetch's CTAs are all resident before
+// this grid starts and wait for nothing behind them, so the wait ends.
 __global__ void __launch_bounds__(kResolveThreads, 2)
 resolve_kernel(const Layout L, const int32_t* __restrict__ sel, int k, int32_t* __restrict__ out,
                int32_t* __restrict__ miss_counts, int fetch, int b0, int wait) {
@@ -728,6 +733,7 @@ resolve_kernel(const Layout L, const int32_t* __restrict__ sel, int k, int32_t* 
     // Flags are raised only when a fetch grid follows (it advances the counters) and no
     // stall is being injected.
     resolve_role(L, smem, b, sel, k, out, miss_counts, fetch != 0 && !L.no_publish, p, (prev & 0xffffu) == 0);
+    if (!wait && blockIdx.x == 0) pdl_wait_prerequisites();
 }
 
 // The fetch of a call, held to 64 registers so that it is resident beside a resolution CTA
@@ -741,8 +747,9 @@ gather_kernel(const Layout L, const int32_t* __restrict__ out, int k, int sync, 
     // waits for this grid to finish before it reads anything).
     pdl_launch_dependents();
     fetch_role(L, out, k, blockIdx.x, gridDim.x, sync != 0, bcast, (uint32_t)b0, (uint32_t)nr);
-    // This grid ends only after the resolution it serves: a successor that waits for this
-    // grid then also sees every table update of that resolution.
+    // This grid ends only after the resolution it serves (and, through a later chunk's, after
+    // the earlier chunks' fetches): a successor that waits for this grid then also sees every
+    // table update of that resolution and every row of the call.
     pdl_wait_prerequisites();
 }
 
