@@ -97,11 +97,12 @@ template <int D, int NT>
 struct Fixed {  // followed by the warps' regions and, with several shares, theirs (kPart and a little)
     using C = Config<D, NT>;
     uint2 qf[NT][C::kSteps][32];              // Q as the lanes take it
-    alignas(8) float qscale[C::kRows], slope[C::kRows];  // of the rows: to log2 units
+    alignas(8) float qscale[C::kRows];           // of the rows: to log2 units
+    alignas(8) float slope[2][C::kRows];         // [0] those from zero up, [1] those below; else 0
     int qpos[C::kRows];
     alignas(16) float2 ml[kMaxWarps][C::kRows];  // the warps' maxima and sums
     alignas(16) float2 xml[kMaxSplit][C::kRows]; // the shares'
-    int wref[kMaxWarps], xref[kMaxSplit];        // positions that biases are relative to
+    int2 wref[kMaxWarps], xref[kMaxSplit];       // positions that biases are relative to
 };
 template <int D, int NT>
 int Config<D, NT>::smem(int warps, int shares) {
@@ -172,8 +173,8 @@ __device__ __forceinline__ float2 mul2f(float2 a, float2 b) {
 // keeps x's own precision however large c is: P is the quadratic that brings the sum nearest to
 // the tanh there (least largest error, 2^-23). `far`: some score of the warp is not below; both
 // forms are then made and one is selected. (24 requests with 4 x 6 heads of 64 and a cap that few
-// scores come near: 14.3 us; both always 14.65; both, with the choice left to the compiler 14.9;
-// the first form alone, wrong for large caps, 14.0. Wide heads: 11.6, 11.6, 11.7 and 11.4.)
+// scores come near, 14.2 us: both forms always .35 us more, and the choice left to the compiler
+// another .25.)
 constexpr float kNear = 0.39f;  // of the cap
 __device__ __forceinline__ float2 capped(float2 x, float c, float to_y, bool far) {
     auto both = [](float a) { return make_float2(a, a); };
@@ -226,8 +227,8 @@ __device__ __forceinline__ uint32_t peer(const void* p, int rank) {
 __device__ __forceinline__ void peer_store(void* p, int rank, const float4& v) {
     asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(peer(p, rank)), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
 }
-__device__ __forceinline__ void peer_store(int* p, int rank, int v) {
-    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(peer(p, rank)), "r"(v) : "memory");
+__device__ __forceinline__ void peer_store(int2* p, int rank, int2 v) {
+    asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(peer(p, rank)), "r"(v.x), "r"(v.y) : "memory");
 }
 
 // MOD: scores are capped or biased.
@@ -348,6 +349,7 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
     for (int i = 0; i < C::kStages; ++i) top_up();
 
     // ---------------- the query rows as halves, in the lanes' order
+    bool below = false;  // some row's slope is below zero
     for (int r2 = 2 * warp; r2 < C::kRows; r2 += 2 * warps) {
         const int r = r2 + (lane >> 4), row = r0 + r, tok = P.group(min(row, rows - 1));
         float x[kQ], scale = 0.f, amax = 0.f;
@@ -376,7 +378,10 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
         }
         if (hl == 0) {
             sm.qscale[r] = scale * (A.scale * kLog2e);  // to log2 units
-            sm.slope[r] = MOD && A.slopes && row < rows ? load(A.slopes + h * A.G + row - tok * A.G) * kLog2e : 0.f;
+            const float slope = MOD && A.slopes && row < rows ? load(A.slopes + h * A.G + row - tok * A.G) * kLog2e : 0.f;
+            below |= slope < 0.f;
+            sm.slope[0][r] = slope < 0.f ? 0.f : slope;
+            sm.slope[1][r] = slope < 0.f ? slope : 0.f;
             sm.qpos[r] = qpos0 + tok;
         }
         // dimension d is taken by lane d / (D/4) of the row's group at step d % (D/4) / 4
@@ -384,7 +389,8 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
         for (int i = 0; i < kQ; i += 4)
             sm.qf[r / 8][((hl & 3) * kQ + i) / 4][(r & 7) * 4 + (hl >> 2)] = make_uint2(pack_half(x[i], x[i + 1]), pack_half(x[i + 2], x[i + 3]));
     }
-    __syncthreads();
+    if (MOD) below = __syncthreads_or(below);
+    else __syncthreads();
 
     float2 qs[NT];  // rows 8 n + 2 t, + 1
 #pragma unroll
@@ -403,7 +409,10 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
 #pragma unroll
             for (int c = 0; c < 4; ++c) acc[i][n][c] = 0.f;
     }
-    int ref = 0;  // biases are relative to this position: the last of the tiles so far
+    // A row's biases are relative to the last position of the tiles so far (x), or to the first
+    // (y) where its slope is negative: the keys with the largest scores keep small biases.
+    int2 ref = make_int2(0, INT_MAX);
+    const bool biased = MOD && A.slopes;
     // The order of a tile's keys along the instruction: place r holds token order(r). A lane's
     // four tokens of V (places 2t, 2t + 1, + 8) then lie in both halves of the 128 bytes that
     // the shared memory banks cover, and its keys still do.
@@ -499,15 +508,6 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
         // z[u][n][k]: rows (8 n + 2 t, + 1), place g + 8 k
         float2 z[2][NT][2], x[2][NT][2];
         if (MOD) {
-            if (A.slopes) {  // the origin of the biases moves to the last tile so far, the maxima with it
-                const int moved = max(max(pos[0], pos[1]) + (kTile - 1) - ref, 0);
-                ref += moved;
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const float2 sl = *reinterpret_cast<const float2*>(&sm.slope[8 * n + 2 * t]);
-                    m[n] = fma2(sl, make_float2(-(float)moved, -(float)moved), m[n]);
-                }
-            }
             bool far = false;
             if (A.cap > 0.f) {
 #pragma unroll
@@ -520,20 +520,42 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
                 }
                 far = __any_sync(0xffffffffu, far);
             }
+            auto each = [&](auto f) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+                for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const float back = -(float)(ref - (pos[u] + order(g) + 8 * k));
+                    for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        float2 y = mul2f(make_float2(s[u][n][2 * k], s[u][n][2 * k + 1]), qs[n]);
-                        if (A.cap > 0.f) y = capped(y, cap2, to_y, far);
-                        if (A.slopes) y = fma2(*reinterpret_cast<const float2*>(&sm.slope[8 * n + 2 * t]), make_float2(back, back), y);
-                        x[u][n][k] = y;
-                        z[u][n][k] = make_float2(y.x - m[n].x, y.y - m[n].y);
-                    }
+                        for (int k = 0; k < 2; ++k) f(u, n, k);
+            };
+            each([&](int u, int n, int k) {
+                x[u][n][k] = mul2f(make_float2(s[u][n][2 * k], s[u][n][2 * k + 1]), qs[n]);
+                if (A.cap > 0.f) x[u][n][k] = capped(x[u][n][k], cap2, to_y, far);
+            });
+            // the biases; their origin moves first, and the maxima with it
+            auto bias = [&](const float (&slope)[C::kRows], int moved, int origin) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const float2 sl = *reinterpret_cast<const float2*>(&slope[8 * n + 2 * t]);
+                    m[n] = fma2(sl, make_float2(-(float)moved, -(float)moved), m[n]);
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const float at = (float)(pos[u] + order(g) + 8 * k - origin);
+                            x[u][n][k] = fma2(sl, make_float2(at, at), x[u][n][k]);
+                        }
                 }
+            };
+            if (biased) {
+                const int moved = max(max(pos[0], pos[1]) + (kTile - 1) - ref.x, 0);
+                bias(sm.slope[0], moved, ref.x += moved);
+            }
+            if (below) {
+                const int moved = min(min(pos[0], pos[1]) - ref.y, 0);
+                bias(sm.slope[1], moved, ref.y += moved);
+            }
+            each([&](int u, int n, int k) { z[u][n][k] = make_float2(x[u][n][k].x - m[n].x, x[u][n][k].y - m[n].y); });
         } else {
 #pragma unroll
             for (int u = 0; u < 2; ++u)
@@ -689,6 +711,24 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // ---------------- join the warps: their outputs in the lanes' order, over the rings
+    int2 last = ref;  // common origins
+    auto reach = [&](const int2* of, int count) {  // of all of them, at most 32
+        const int2 v = lane < count ? of[lane] : make_int2(0, INT_MAX);
+        return make_int2(__reduce_max_sync(0xffffffffu, v.x), __reduce_min_sync(0xffffffffu, v.y));
+    };
+    auto shift = [&](float m, int r, int2 from) {
+        return m - sm.slope[0][r] * (float)(last.x - from.x) - sm.slope[1][r] * (float)(last.y - from.y);
+    };
+    if (biased) {  // the maxima as from the common origins
+        if (lane == 0) sm.wref[warp] = ref;
+        __syncthreads();
+        last = reach(sm.wref, warps);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int r = 8 * n + 2 * t;
+            m[n] = make_float2(shift(m[n].x, r, ref), shift(m[n].y, r + 1, ref));
+        }
+    }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -698,7 +738,6 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
         }
         if (g == 0) *reinterpret_cast<float4*>(&sm.ml[warp][8 * n + 2 * t]) = make_float4(m[n].x, l[n].x, m[n].y, l[n].y);
     }
-    if (MOD && lane == 0) sm.wref[warp] = ref;
     constexpr int kFrags = C::kSteps * NT * 32, kItems = kFrags / 2;
     auto part = [&](int w) { return reinterpret_cast<float4*>(space + w * C::kSpace); };  // of a warp: [step][n][lane]
 #pragma unroll
@@ -706,10 +745,7 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
 #pragma unroll
         for (int n = 0; n < NT; ++n)
             part(warp)[(i * NT + n) * 32 + lane] = make_float4(acc[i][n][0], acc[i][n][1], acc[i][n][2], acc[i][n][3]);
-    int last = 0;
     __syncthreads();
-    if (MOD && A.slopes)
-        for (int w = 0; w < warps; ++w) last = max(last, sm.wref[w]);
 
     // The sum of partial results of item x -- steps 2 j, 2 j + 1 of a lane: 4 dimensions of rows
     // r, r + 1 -- relative to their largest maxima, kBatch of them at a time (their loads are
@@ -719,31 +755,24 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
         float2 top, sum;  // of rows r and r + 1
     };
     constexpr int kBatch = 4;
-    auto join = [&](int x, int count, auto ml_of, auto ref_of, auto frag_of) {
+    auto join = [&](int x, int count, auto ml_of, auto frag_of) {
         const int n = x / 32 % NT, r = 8 * n + 2 * (x & 3);
         Joined o;
         o.a = o.b = make_float4(0.f, 0.f, 0.f, 0.f);
         o.top = make_float2(-INFINITY, -INFINITY);
         o.sum = make_float2(0.f, 0.f);
-        const float2 sl = MOD ? *reinterpret_cast<const float2*>(&sm.slope[r]) : make_float2(0.f, 0.f);
         for (int w0 = 0; w0 < count; w0 += kBatch) {
             float4 v[kBatch], a[kBatch], c[kBatch];
-            int back[kBatch];
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
                 const int w = min(w0 + i, count - 1);
                 v[i] = ml_of(w, r);
                 a[i] = frag_of(w, x, 0);
                 c[i] = frag_of(w, x, 1);
-                back[i] = MOD ? last - ref_of(w) : 0;
             }
             float2 top = o.top;
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
-                if (MOD) {  // as from the common origin of the biases
-                    v[i].x -= sl.x * (float)back[i];
-                    v[i].z -= sl.y * (float)back[i];
-                }
                 if (w0 + i >= count) v[i].x = v[i].z = -INFINITY;
                 top = make_float2(fmaxf(top.x, v[i].x), fmaxf(top.y, v[i].z));
             }
@@ -786,17 +815,19 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
                 float e = -INFINITY;
                 if (top > -INFINITY) {
                     e = (top + lg2(sum)) * kLn2;
-                    if (MOD && A.slopes) e -= load(A.slopes + head) * (float)(qpos0 + tok - last);
+                    if (biased) {
+                        const float sl = load(A.slopes + head);
+                        e -= sl * (float)(qpos0 + tok - (sl < 0.f ? last.y : last.x));
+                    }
                 }
                 A.lse[((size_t)b * A.Tq + tok) * A.H * A.G + head] = e;
             }
         }
     };
     auto warp_ml = [&](int w, int r) { return *reinterpret_cast<const float4*>(&sm.ml[w][r]); };
-    auto warp_ref = [&](int w) { return sm.wref[w]; };
     auto warp_frag = [&](int w, int x, int k) { return part(w)[((2 * (x / 32 / NT) + k) * NT + x / 32 % NT) * 32 + (x & 31)]; };
     if (nsplit == 1) {
-        for (int x = tid; x < kItems; x += threads) write(x, join(x, warps, warp_ml, warp_ref, warp_frag));
+        for (int x = tid; x < kItems; x += threads) write(x, join(x, warps, warp_ml, warp_frag));
         return;
     }
     // ---------------- join the shares: item x is sent to CTA x % nsplit, which joins and writes it
@@ -804,7 +835,7 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
     float4* frags = reinterpret_cast<float4*>(space + warps * C::kSpace);  // [share][item / nsplit][2]
     cluster_wait();
     for (int x = tid; x < kItems; x += threads) {
-        const Joined o = join(x, warps, warp_ml, warp_ref, warp_frag);
+        const Joined o = join(x, warps, warp_ml, warp_frag);
         const int ix = P.shares(x), to = x - ix * nsplit;
         peer_store(frags + (split * per + ix) * 2, to, o.a);
         peer_store(frags + (split * per + ix) * 2 + 1, to, o.b);
@@ -812,14 +843,19 @@ __global__ void __launch_bounds__(Config<D, NT>::kSmWarps * 32, 1) attend_pages_
             for (int s = 0; s < nsplit; ++s)
                 peer_store(reinterpret_cast<float4*>(&sm.xml[split][8 * (x / 32) + 2 * (x & 3)]), s, make_float4(o.top.x, o.sum.x, o.top.y, o.sum.y));
     }
-    if (MOD && tid < nsplit) peer_store(&sm.xref[split], tid, last);
+    if (biased && tid < nsplit) peer_store(&sm.xref[split], tid, last);
     cluster_arrive();
     cluster_wait();
-    if (MOD)
-        for (int s = 0; s < nsplit; ++s) last = max(last, sm.xref[s]);
+    if (biased) {
+        last = reach(sm.xref, nsplit);
+        for (int i = tid; i < nsplit * C::kRows; i += threads) {
+            const int share = i / C::kRows, r = i % C::kRows;
+            sm.xml[share][r].x = shift(sm.xml[share][r].x, r, sm.xref[share]);
+        }
+        __syncthreads();
+    }
     for (int ix = tid; ix * nsplit + split < kItems; ix += threads)
         write(ix * nsplit + split, join(ix * nsplit + split, nsplit, [&](int s, int r) { return *reinterpret_cast<const float4*>(&sm.xml[s][r]); },
-                                        [&](int s) { return sm.xref[s]; },
                                         [&](int s, int, int k) { return frags[(s * per + ix) * 2 + k]; }));
 }
 

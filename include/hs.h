@@ -458,7 +458,10 @@ int hs_read_pages(hs_stream_t stream, const hs_page_shape* shape, int dtype, con
  * every query that sees it NaN, in o and lse. The products run on the tensor cores
  * with f32 sums; the queries enter them as halves (bf16 ones scaled by a power of two per
  * row) and the softmax weights are rounded to half for the product with V. A capped score
- * is within 2^-20 of itself, whatever the cap.
+ * is within 2^-20 of itself, whatever the cap; biases are f32 numbers that count from the
+ * nearest key of the selected pages, or from the farthest where the slope is negative, so that
+ * the keys with the largest scores keep their differences; the exponentials, and lse, are
+ * formed in base 2 by the GPU's approximate instructions (about 2^-22 each).
  */
 typedef struct {
     hs_page_shape shape;

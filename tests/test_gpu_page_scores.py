@@ -157,3 +157,16 @@ def test_scores_of_minus_infinity_are_not_seen():
     o, lse = run(c, 100.0, **mods)
     ro, rl, to, tl = pm.attend(c["shape"], c["q"], c["pages"], c["slots"], c["sel"], c["lengths"], 100.0, **mods)
     assert ((o - ro).abs() <= to).all() and ((lse - rl).abs() <= tl).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("H,G,D", [(2, 4, 64), (1, 8, 128), (1, 12, 256), (1, 24, 64)])
+def test_biases_that_grow_with_the_distance(H, G, D, dtype):
+    """Slopes below zero over 1.6 million tokens, beside ones above: the far keys then carry the
+    weight, and their biases' differences decide."""
+    c = case(2, H, G, D, 16, 64, 64, [1600000, 1400007], dtype=dtype, seed=9)
+    near = (c["sel"] >= 0) & (torch.arange(64) % 4 != 0)
+    c["sel"] = torch.where(near, c["sel"] % 40 + 17, c["sel"])  # several pages share the far end
+    slopes = 2.0 ** -(torch.arange(H * G) % 8).float() * torch.where(torch.arange(H * G) % 3 == 0, 1.0, -1.0)
+    check(c, D ** -0.5, 0.0, slopes)
+    check(c, D ** -0.5, 20.0, slopes)
