@@ -13,6 +13,8 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include <algorithm>
+#include <array>
 #include <new>
 
 #include "hs.h"
@@ -579,6 +581,43 @@ int hs_read_pages(hs_stream_t stream, const hs_page_shape* shape, int dtype, con
     return HS_OK;
 }
 
+// Whether two of the rows of `width` elements that start at the sums of i * stride, 0 <= i < n,
+// of the axes share an element.
+struct Axis {
+    int64_t n, stride;
+};
+static bool rows_overlap(int64_t width, std::array<Axis, 3> axes) {
+    using Wide = __int128;
+    int used = 0;
+    for (Axis x : axes)
+        if (x.n > 1) {  // which end an axis starts from does not matter
+            if (x.stride == INT64_MIN) return true;
+            axes[used++] = Axis{x.n, x.stride < 0 ? -x.stride : x.stride};
+        }
+    std::sort(axes.begin(), axes.begin() + used, [](const Axis& x, const Axis& y) { return x.stride < y.stride; });
+    Wide span = width;  // of what the axes so far reach: the next one steps over it
+    bool nested = true;
+    for (int i = 0; i < used; ++i) {
+        if (axes[i].stride < width) return true;
+        nested &= axes[i].stride >= span;
+        span += (Wide)(axes[i].n - 1) * axes[i].stride;
+    }
+    if (nested) return false;
+    // Interleaved axes: for every step along the two shorter ones, is there one along the longest
+    // that comes back to less than a row? Refused where that would take long.
+    std::sort(axes.begin(), axes.begin() + used, [](const Axis& x, const Axis& y) { return x.n < y.n; });
+    const Axis far = axes[used - 1], x = axes[0], y = used == 3 ? axes[1] : Axis{1, 0};
+    if ((Wide)x.n * y.n > 1 << 20) return true;
+    for (int64_t i = 0; i < x.n; ++i)
+        for (int64_t j = i ? 1 - y.n : 1; j < y.n; ++j) {
+            const Wide off = (Wide)i * x.stride + (Wide)j * y.stride, most = (Wide)(far.n - 1) * far.stride;
+            const Wide at = off < 0 ? -off : off, back = at % far.stride;  // far.stride >= width
+            if (at - back <= most && back < width) return true;
+            if (at - back + far.stride <= most && far.stride - back < width) return true;
+        }
+    return false;
+}
+
 int hs_attend_pages(hs_stream_t stream, const hs_page_attention* a) {
     hs::PageShape ps;
     if (!a) return fail(HS_ERR_INVALID, "null arguments");
@@ -601,8 +640,7 @@ int hs_attend_pages(hs_stream_t stream, const hs_page_attention* a) {
         return fail(HS_ERR_INVALID, "q, o and pages must be 16-byte aligned");
     if ((a->q_batch_stride | a->q_token_stride | a->q_head_stride | a->o_batch_stride | a->o_token_stride | a->o_head_stride) & 7)
         return fail(HS_ERR_INVALID, "rows of q and o must be 16-byte aligned");
-    auto overlap = [&](int64_t n, int64_t stride) { return n > 1 && stride > -ps.dim && stride < ps.dim; };
-    if (overlap(a->B, a->o_batch_stride) || overlap(a->q_tokens, a->o_token_stride) || overlap(a->q_heads, a->o_head_stride))
+    if (rows_overlap(ps.dim, {Axis{a->B, a->o_batch_stride}, Axis{a->q_tokens, a->o_token_stride}, Axis{a->q_heads, a->o_head_stride}}))
         return fail(HS_ERR_INVALID, "rows of o overlap");
     if ((rc = sm_count(&sms)) != HS_OK) return rc;
     hs::PageAttention p;

@@ -453,7 +453,8 @@ int hs_read_pages(hs_stream_t stream, const hs_page_shape* shape, int dtype, con
  * sees no key gets o = 0 and lse = -inf. Keys that no query sees are not read into the
  * result, whatever their bytes hold; a page selected twice counts twice.
  * Rows of q and o are contiguous and 16-byte aligned: (b, t, head) starts b * batch_stride +
- * t * token_stride + head * head_stride elements in; rows of o do not overlap. A score that
+ * t * token_stride + head * head_stride elements in; rows of o that overlap are
+ * refused. A score that
  * is -inf in f32 has a weight of 0, as if unseen (a NaN in its V still shows); a NaN key makes
  * every query that sees it NaN, in o and lse. The products run on the tensor cores
  * with f32 sums; the queries enter them as halves (bf16 ones scaled by a power of two per
