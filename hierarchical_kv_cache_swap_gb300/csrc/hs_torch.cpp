@@ -138,11 +138,12 @@ uint32_t* status_of(PyObject* o) {
 }
 
 // Makes the C call without the interpreter's lock: a launch may block while the queue is full
-// of work that waits for a callback into Python.
+// of work that waits for a callback into Python. Nothing of torch is asked in there: a tensor
+// without memory throws when asked for its pointer, and an error is set under the lock.
 template <class F>
 PyObject* done(const char* what, F&& call) {
     PyThreadState* state = PyEval_SaveThread();
-    const int rc = call();
+    const int rc = [&]() noexcept { return call(); }();
     PyEval_RestoreThread(state);
     if (rc == HS_OK) Py_RETURN_NONE;
     PyErr_Format(g_error ? g_error : PyExc_RuntimeError, "%s failed (%d): %s", what, rc, hs_last_error());
@@ -195,10 +196,9 @@ PyObject* write_tokens(PyObject*, PyObject* const* a, Py_ssize_t na) {
         on_device({{"k", &k}, {"v", &v}, {"dest", &dest}, {"pages", pages.is_cpu() && pages.is_pinned() ? nullptr : &pages}});
         uint32_t* const status = status_of(a[5]);
         const hs_stream_t stream = stream_of(a[6]);
-        return done("hs_write_tokens", [&] {
-            return hs_write_tokens(stream, &s, type, &rows, k.size(0), (const int64_t*)dest.data_ptr(),
-                                   (uint8_t*)pages.data_ptr(), pages.size(0), status);
-        });
+        const int64_t n = k.size(0), num_pages = pages.size(0), *const to = (const int64_t*)dest.data_ptr();
+        uint8_t* const at = (uint8_t*)pages.data_ptr();
+        return done("hs_write_tokens", [&] { return hs_write_tokens(stream, &s, type, &rows, n, to, at, num_pages, status); });
     });
 }
 
@@ -216,10 +216,9 @@ PyObject* append_tokens(PyObject*, PyObject* const* a, Py_ssize_t na) {
         on_device({{"k", &k}, {"v", &v}, {"positions", &pos}, {"requests", req}});
         hs_ctx* const ctx = (hs_ctx*)(uintptr_t)integer(a[0]);
         const hs_stream_t stream = stream_of(a[6]);
-        return done("hs_append_tokens", [&] {
-            return hs_append_tokens(ctx, stream, &s, type, &rows, k.size(0), req ? (const int32_t*)req->data_ptr() : nullptr,
-                                    (const int32_t*)pos.data_ptr());
-        });
+        const int64_t n = k.size(0);
+        const int32_t *const requests = req ? (const int32_t*)req->data_ptr() : nullptr, *const positions = (const int32_t*)pos.data_ptr();
+        return done("hs_append_tokens", [&] { return hs_append_tokens(ctx, stream, &s, type, &rows, n, requests, positions); });
     });
 }
 
@@ -259,10 +258,9 @@ PyObject* read_pages(PyObject*, PyObject* const* a, Py_ssize_t na) {
         const int requests = int_of(B, "B"), S = int_of(p.S, "S"), count = int_of(n, "n");
         uint32_t* const status = status_of(a[5]);
         const hs_stream_t stream = stream_of(a[6]);
-        return done("hs_read_pages", [&] {
-            return hs_read_pages(stream, &s, type, p.at, requests, S, (const int32_t*)slots.data_ptr(), count, k.data_ptr(),
-                                 v.data_ptr(), status);
-        });
+        const int32_t* const from = (const int32_t*)slots.data_ptr();
+        void *const ko = k.data_ptr(), *const vo = v.data_ptr();
+        return done("hs_read_pages", [&] { return hs_read_pages(stream, &s, type, p.at, requests, S, from, count, ko, vo, status); });
     });
 }
 
