@@ -56,9 +56,7 @@
 
 #include <math.h>
 
-#include <atomic>
-#include <mutex>
-
+#include "hs_once.h"
 #include "hs_page.h"
 
 namespace hs {
@@ -935,24 +933,18 @@ void plan(const Room& room, int sm_warps, int num_sms, int D, int NT, int64_t jo
 template <int D, int NT, bool MOD>
 cudaError_t launch(cudaStream_t stream, bool bf16, const PageAttention& a, int num_sms) {
     using C = Config<D, NT>;
-    constexpr int kDevices = 64;
-    static std::mutex lock;
-    static std::atomic<bool> ready[kDevices];
-    static Room rooms[kDevices];
+    static PerDevice<Room> rooms;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (dev >= kDevices) return cudaErrorInvalidDevice;
-    if (!ready[dev].load(std::memory_order_acquire)) {
-        std::lock_guard<std::mutex> hold(lock);
-        if ((e = set_up<D, NT, MOD>(&rooms[dev])) != cudaSuccess) return e;
-        ready[dev].store(true, std::memory_order_release);
-    }
+    if (dev >= PerDevice<Room>::kDevices) return cudaErrorInvalidDevice;
+    const Room* room = nullptr;
+    if ((e = (cudaError_t)rooms.get(dev, set_up<D, NT, MOD>, &room)) != cudaSuccess) return e;
     const int row_tiles = (a.G * a.Tq + C::kRows - 1) / C::kRows;
     const int64_t jobs = (int64_t)a.B * a.H * row_tiles, tiles = (int64_t)a.k * a.tiles;
     int warps, shares;
     int64_t whole;  // jobs that are not shared, a multiple of shares
-    plan(rooms[dev], C::kSmWarps, num_sms, D, NT, jobs, tiles, &warps, &shares, &whole);
+    plan(*room, C::kSmWarps, num_sms, D, NT, jobs, tiles, &warps, &shares, &whole);
     const int64_t ctas = whole + (jobs - whole) * shares;
     if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
     Split p;
