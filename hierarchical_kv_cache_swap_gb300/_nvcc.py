@@ -6,9 +6,11 @@ library next to this file. Nothing is installed into site-packages.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -40,37 +42,56 @@ def _stale(target: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def _torch_command(obj: str) -> list[str]:
-    """The host compiler's command for the torch binding (headers of the torch that runs)."""
-    import sysconfig
+def _torch_dir() -> str:
+    """Where the torch that would be imported is (without importing it)."""
+    return importlib.util.find_spec("torch").submodule_search_locations[0]
 
-    import torch
-    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+
+def _torch_command(obj: str) -> list[str]:
+    """The host compiler's command for the torch binding (headers of the torch that runs), but
+    for the flag of its C++ ABI."""
+    inc = os.path.join(_torch_dir(), "include")
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     dirs = [inc, os.path.join(inc, "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"],
             os.path.join(cuda or "/usr/local/cuda", "include")]
-    return (["g++", "-O2", "-fPIC", "-std=c++17", "-I", os.path.join(ROOT, "include"),
-             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    return (["g++", "-O2", "-fPIC", "-std=c++17", "-I", os.path.join(ROOT, "include")]
             + [x for d in dirs for x in ("-isystem", d)] + ["-c", TORCH_SOURCE, "-o", obj])
 
 
+def _torch_stamp(cmd: list[str]) -> str:
+    """What the binding is compiled with and against, besides its sources: the command, the
+    Python, and the torch, by its library's size and time (its version and ABI with it)."""
+    lib = os.stat(os.path.join(_torch_dir(), "lib", "libtorch_python.so"))
+    return "\n".join([" ".join(cmd), sys.version, f"{lib.st_size} {lib.st_mtime_ns}"])
+
+
 def _link_torch(obj: str) -> None:
-    import torch
-    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    libs = os.path.join(_torch_dir(), "lib")
     tmp = TORCH_LIB + f".tmp{os.getpid()}"
     subprocess.check_call(["g++", "-shared", "-o", tmp, obj, "-L", HERE, "-l:libhs.so", "-Wl,-rpath,$ORIGIN", "-L", libs,
                            f"-Wl,-rpath,{libs}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"])
     os.replace(tmp, TORCH_LIB)
 
 
+def _read(path: str) -> str | None:
+    if not os.path.exists(path):
+        return None
+    with open(path) as f:
+        return f.read()
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link libhs.so and the torch binding if any source or header changed;
-    returns the path of libhs.so."""
+    """Compile and link libhs.so and the torch binding if any source or header changed, the
+    binding also for another torch or Python; returns the path of libhs.so."""
     os.makedirs(OBJDIR, exist_ok=True)
     objs, procs = [], []
     tobj = os.path.join(OBJDIR, "hs_torch.o")
-    if force or _stale(tobj, [TORCH_SOURCE] + HEADERS):
-        cmd, log = _torch_command(tobj), tobj + ".log"
+    tcmd, tstamp = _torch_command(tobj), tobj + ".stamp"
+    stamp = _torch_stamp(tcmd)
+    compile_torch = force or _stale(tobj, [TORCH_SOURCE] + HEADERS) or _read(tstamp) != stamp
+    if compile_torch:
+        import torch
+        cmd, log = tcmd + [f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"], tobj + ".log"
         procs.append((cmd, log, subprocess.Popen(cmd, stdout=open(log, "w"), stderr=subprocess.STDOUT)))
     for src in SOURCES:
         sp = os.path.join(CSRC, src)
@@ -91,8 +112,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
         tmp = LIB + f".tmp{os.getpid()}"
         subprocess.check_call([nvcc()] + ARCH + ["-shared", "-o", tmp] + objs)
         os.replace(tmp, LIB)
-    if force or _stale(TORCH_LIB, [tobj]):
+    if compile_torch or _stale(TORCH_LIB, [tobj]):
         _link_torch(tobj)
+        with open(tstamp, "w") as f:
+            f.write(stamp)
     return LIB
 
 
