@@ -82,13 +82,17 @@ def _read(path: str) -> str | None:
 
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile and link libhs.so and the torch binding if any source or header changed, the
-    binding also for another torch or Python; returns the path of libhs.so."""
+    binding also for another torch or Python (and not at all where torch is not installed);
+    returns the path of libhs.so."""
     os.makedirs(OBJDIR, exist_ok=True)
     objs, procs = [], []
     tobj = os.path.join(OBJDIR, "hs_torch.o")
-    tcmd, tstamp = _torch_command(tobj), tobj + ".stamp"
-    stamp = _torch_stamp(tcmd)
-    compile_torch = force or _stale(tobj, [TORCH_SOURCE] + HEADERS) or _read(tstamp) != stamp
+    with_torch = importlib.util.find_spec("torch") is not None  # else the library alone: the page calls from Python need it
+    compile_torch = False
+    if with_torch:
+        tcmd, tstamp = _torch_command(tobj), tobj + ".stamp"
+        stamp = _torch_stamp(tcmd)
+        compile_torch = force or _stale(tobj, [TORCH_SOURCE] + HEADERS) or _read(tstamp) != stamp
     if compile_torch:
         import torch
         cmd, log = tcmd + [f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"], tobj + ".log"
@@ -112,7 +116,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         tmp = LIB + f".tmp{os.getpid()}"
         subprocess.check_call([nvcc()] + ARCH + ["-shared", "-o", tmp] + objs)
         os.replace(tmp, LIB)
-    if compile_torch or _stale(TORCH_LIB, [tobj]):
+    if with_torch and (compile_torch or _stale(TORCH_LIB, [tobj])):
         _link_torch(tobj)
         with open(tstamp, "w") as f:
             f.write(stamp)

@@ -1,5 +1,7 @@
 """When the torch binding is compiled again."""
 import os
+import subprocess
+import sys
 
 import pytest
 
@@ -59,3 +61,29 @@ def test_the_binding_follows_the_torch_and_python_it_is_compiled_against(compile
     assert compilers.sources == ["hs_torch.cpp"]
     hs.build()
     assert compilers.sources == ["hs_torch.cpp"]  # and once
+
+
+def test_the_library_builds_where_torch_is_not_installed(compilers, monkeypatch):
+    find = _nvcc.importlib.util.find_spec
+    monkeypatch.setattr(_nvcc.importlib.util, "find_spec", lambda name, *a: None if name == "torch" else find(name, *a))
+    assert hs.build(force=True) == _nvcc.LIB
+    assert sorted(compilers.sources) == sorted(_nvcc.SOURCES)
+
+
+WITHOUT_TORCH = """
+import sys
+sys.modules["torch"] = None  # as if it were not installed
+sys.path.insert(0, sys.argv[1])
+import hierarchical_kv_cache_swap_gb300 as hs
+hs.build()
+assert hs.PageShape(16, 8, 128).bytes == 18432
+try:
+    hs.write_tokens((16, 8, 128), None, None, None, None)
+except ImportError as e:
+    print("page calls:", e)
+"""
+
+
+def test_the_library_is_usable_where_torch_is_not_installed():
+    r = subprocess.run([sys.executable, "-c", WITHOUT_TORCH, _nvcc.ROOT], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "page calls: " in r.stdout, r.stdout + r.stderr
