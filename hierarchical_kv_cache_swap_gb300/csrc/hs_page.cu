@@ -16,7 +16,8 @@
 // are bound by memory traffic: 2 + 9/16 bytes a value. Measured over 131072 tokens of 8 heads
 // of 128 (688 MB of traffic each): writing 105 us (6.55 TB/s, 98 % of a copy's rate), reading
 // 103.5 us (6.64 TB/s, 99 %). A decode step's 64 tokens take 1.8 us to write and their pages
-// 2.1 us to read, which is the launches' own pace.
+// 2.1 us to read, which is the launches' own pace. Appended to a context's histories, the
+// 131072 tokens take 836 us: 181 GB/s over the host link, 94 % of a copy of the same bytes.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -122,7 +123,7 @@ __device__ __forceinline__ void load_block(uint32_t (&w)[8], const uint16_t* p) 
     w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
 }
 // The 32 bytes of a block: one store where they are 32-byte aligned (WIDE), else two. Reading
-// 131072 tokens: 103.7 us against 111.3; the pages of a decode step's 64 tokens: 2.2 against 3.1.
+// 131072 tokens: 103.7 us against 111.3; the pages of a decode step's 64 tokens: .9 us less.
 template <bool WIDE>
 __device__ __forceinline__ void store_values(uint16_t* p, const uint4& a, const uint4& b) {
     if (WIDE) {

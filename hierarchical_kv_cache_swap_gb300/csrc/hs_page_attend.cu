@@ -44,8 +44,8 @@
 // only; the sums that normalise them add the unrounded ones in f32.
 //
 // Measured (16-token pages, 8 heads of 128 with 8 queries each, 128 pages a request; us a
-// call in a graph): 256 requests 105 (5.82 TB/s, 87 % of a copy's rate), of which the copies
-// alone take 91.5 and the arithmetic alone about 100; 64 requests 33 (4.65 TB/s: 512 jobs do
+// call in a graph): 256 requests 105 (5.84 TB/s, 87 % of a copy's rate), of which the copies
+// alone take 91.5 and the arithmetic alone 101.5; 64 requests 33 (4.65 TB/s: 512 jobs do
 // not spread evenly over 152 SMs), 1 request 5.2 and one of five tokens 3.7 (the chain of
 // loads, one pair of tiles and the joins). 32 rows (four drafted tokens) over 16 requests take
 // 21.7, where the products alone would take 8.5 on all SMs.
@@ -891,7 +891,7 @@ cudaError_t set_up(Room* room) {
 // at first. With few jobs the chain decides and more, smaller shares win; with many the work
 // does, and shares only cost, but for the jobs that some SMs have more of than others. us a call:
 //   1 request, 8 heads, 128 tiles:    8 CTAs of 8 warps 5.2, of 4 warps 5.5, of 12 warps 6.4
-//   16 jobs of 512 tiles, 16 rows:    6 CTAs of 12 warps 14.9, of 8 warps 15.6, 7 of 12 26.6
+//   16 jobs of 512 tiles, 16 rows:    6 CTAs of 12 warps 15.2, of 8 warps 15.7, 7 of 12 27.0
 //   256 jobs of 128 tiles, 32 rows:   whole 38.2, 152 whole and 104 halved 46.7, all halved 46.8
 //   512 jobs of 128 tiles:            whole 34.5, all halved 35.6, 456 whole and 56 halved 32.9;
 //                                     such mixtures in clusters of 3, 4 or 8: 37.0, 34.1, 35.2
