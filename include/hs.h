@@ -452,17 +452,16 @@ int hs_read_pages(hs_stream_t stream, const hs_page_shape* shape, int dtype, con
  * qpos and, where a document mask is given, p_j >= start[b] or p_j < prefix[b]. A query that
  * sees no key gets o = 0 and lse = -inf. Keys that no query sees are not read into the
  * result, whatever their bytes hold; a page selected twice counts twice.
- * Rows of q and o are contiguous and 16-byte aligned: (b, t, head) starts b * batch_stride +
- * t * token_stride + head * head_stride elements in; rows of o that overlap are
- * refused. A score that
- * is -inf in f32 has a weight of 0, as if unseen (a NaN in its V still shows); a NaN key makes
- * every query that sees it NaN, in o and lse. The products run on the tensor cores
- * with f32 sums; the queries enter them as halves (bf16 ones scaled by a power of two per
- * row) and the softmax weights are rounded to half for the product with V. A capped score
- * is within 2^-20 of itself, whatever the cap; biases are f32 numbers that count from the
- * nearest key of the selected pages, or from the farthest where the slope is negative, so that
- * the keys with the largest scores keep their differences; the exponentials, and lse, are
- * formed in base 2 by the GPU's approximate instructions (about 2^-22 each).
+ * Rows of q and o are contiguous and 16-byte aligned: (b, t, head) starts
+ * b * batch_stride + t * token_stride + head * head_stride elements in; rows of o that overlap
+ * are refused. A score that is -inf in f32 has a weight of 0, as if unseen (a NaN in its V still shows); a NaN key
+ * makes every query that sees it NaN, in o and lse. The products run on the tensor cores with
+ * f32 sums; the queries enter them as halves (bf16 ones scaled by a power of two per row) and
+ * the softmax weights are rounded to half for the product with V. A capped score is within
+ * 2^-20 of itself, whatever the cap; biases are f32 numbers that count from the nearest key of
+ * the selected pages, or from the farthest where the slope is negative, so that the keys with
+ * the largest scores keep their differences; the exponentials, and lse, are formed in base 2
+ * by the GPU's approximate instructions (about 2^-22 each).
  */
 typedef struct {
     hs_page_shape shape;
