@@ -5,7 +5,7 @@ small fixed-size cache of slots on the GPU; per layer and decode step one fused
 resolution does hit detection, LRU replacement, the page-table update and the
 host-to-device fetch of the misses. All of that runs in the library's CUDA kernels
 (sm_103a) behind the C ABI of ``include/hs.h``; this module only marshals arguments
-(torch tensors or raw addresses, streams, events) to those calls, the page calls through a
+(torch tensors or raw addresses, streams, events) to those calls, the page and latent calls through a
 compiled part of it (``_hs_torch.so``). There is no
 fallback: if the compiled library is missing, loading fails with an error.
 """
@@ -75,6 +75,31 @@ class _PageAttention(ctypes.Structure):
                 ("start", _VP), ("prefix", _VP), ("status", _VP)]
 
 
+class _Rotation(ctypes.Structure):
+    """hs_rotation (include/hs.h)."""
+    _fields_ = [("table", _VP), ("rows", _I64), ("positions", _VP), ("halves", _I)]
+
+
+class _LatentRows(ctypes.Structure):
+    """hs_latent_rows (include/hs.h)."""
+    _fields_ = [("latent", _VP), ("rope", _VP), ("latent_stride", _I64), ("rope_stride", _I64)]
+
+
+class _HeadProduct(ctypes.Structure):
+    """hs_head_product (include/hs.h)."""
+    _fields_ = [("x", _VP), ("x_token_stride", _I64), ("x_head_stride", _I64), ("w", _VP), ("w_head_stride", _I64),
+                ("w_row_stride", _I64), ("out", _VP), ("n", _I64), ("heads", _I)]
+
+
+class _PromptAttention(ctypes.Structure):
+    """hs_prompt_attention (include/hs.h)."""
+    _fields_ = [("dtype", _I), ("B", _I), ("heads", _I), ("causal", _I), ("q_rows", _I64), ("k_rows", _I64),
+                ("q", _VP), ("q_token_stride", _I64), ("q_head_stride", _I64), ("k", _VP), ("k_token_stride", _I64),
+                ("k_head_stride", _I64), ("k_rope", _VP), ("k_rope_stride", _I64), ("v", _VP), ("v_token_stride", _I64),
+                ("v_head_stride", _I64), ("o", _VP), ("o_token_stride", _I64), ("o_head_stride", _I64), ("lse", _VP),
+                ("q_starts", _VP), ("k_starts", _VP), ("sm_scale", ctypes.c_float), ("status", _VP)]
+
+
 SIGNATURES = {
     "hs_create": (_VP, [_I, _I, _I, _I]),
     "hs_create_with_host": (_VP, [_I, _I, _I, _I, _VP, _SZ]),
@@ -104,6 +129,12 @@ SIGNATURES = {
     "hs_append_tokens": (_I, [_VP, _VP, _VP, _I, _VP, _I64, _VP, _VP]),
     "hs_read_pages": (_I, [_VP, _VP, _I, _VP, _I, _I, _VP, _I, _VP, _VP, _VP]),
     "hs_attend_pages": (_I, [_VP, _VP]),
+    "hs_write_latents": (_I, [_VP, _I, _VP, _I64, _VP, _VP, _VP, _I64, _VP]),
+    "hs_append_latents": (_I, [_VP, _VP, _I, _VP, _I64, _VP, _VP, _VP]),
+    "hs_read_latents": (_I, [_VP, _I, _VP, _I, _I, _VP, _I, _VP, _VP, _VP]),
+    "hs_absorb_queries": (_I, [_VP, _VP, _VP, _VP]),
+    "hs_expand_outputs": (_I, [_VP, _VP]),
+    "hs_attend_prompts": (_I, [_VP, _VP]),
     "hs_status_word": (_VP, [_VP]),
     "hs_device": (_I, [_VP]),
     "hs_kernels_per_call": (_I, [_VP]),
@@ -260,6 +291,46 @@ def attend_pages(shape, q, pages, slots, selections, lengths, o, lse, sm_scale: 
     prefix; status: a device int32 word [1]."""
     (_torch_binding or _native()).attend_pages(shape, q, pages, slots, selections, lengths, o, lse, sm_scale, softcap,
                                                slopes, start, prefix, status, stream)
+
+
+LATENT_ENTRY_BYTES = 656  # the entry_bytes of a context that holds latent entries
+
+
+def write_latents(latent, rope, dest, entries, rotation=None, positions=None, halves: bool = False, status=None,
+                  stream=None) -> None:
+    """hs_write_latents: latent [n, 512] and rope [n, 64], bf16 or fp16 (rows contiguous), into
+    uint8 entries [N, 656] (device, or pinned) at dest int64 [n] (negative: padding). rotation:
+    None, or float32 [rows, 64], the cosines and sines of each position, by which the rotary keys
+    are rotated: positions int32 [n], pairs of neighbours or (halves) of dimensions i and i + 32.
+    status: a device int32 word [1], or None."""
+    (_torch_binding or _native()).write_latents(latent, rope, dest, entries, rotation, positions, halves, status, stream)
+
+
+def read_latents(entries, slots, latent, rope, status=None, stream=None) -> None:
+    """hs_read_latents: the entries [B, S, 656] in slots int32 [B, n] decoded into latent [B, n,
+    512] and rope [B, n, 64], bf16 or fp16 (zeros where a slot is negative)."""
+    (_torch_binding or _native()).read_latents(entries, slots, latent, rope, status, stream)
+
+
+def absorb_queries(q, up_k, out, rotation=None, positions=None, halves: bool = False, status=None, stream=None) -> None:
+    """hs_absorb_queries: q bf16 [n, heads, 128 + 64] through the heads' key matrices up_k bf16
+    [heads, 128, 512], and rotated, into out bf16 [n, heads, 576], as Context.attend takes it."""
+    (_torch_binding or _native()).absorb_queries(q, up_k, out, rotation, positions, halves, status, stream)
+
+
+def expand_outputs(o, up_v, out, stream=None) -> None:
+    """hs_expand_outputs: o float32 [n, heads, 512], as Context.attend gives it, through the heads'
+    value matrices up_v bf16 [heads, 128, 512] into out bf16 [n, heads, 128]."""
+    (_torch_binding or _native()).expand_outputs(o, up_v, out, stream)
+
+
+def attend_prompts(q, k, k_rope, v, q_starts, k_starts, o, lse, sm_scale: float, causal: bool = True, status=None,
+                   stream=None) -> None:
+    """hs_attend_prompts: prompts whose rows q_starts int32 [B + 1] bound in q [rows, heads, 128 +
+    64] (the last 64 rotated), o [rows, heads, 128] and lse float32 [rows, heads], and whose keys
+    k_starts int32 [B + 1] bound in k and v [keys, heads, 128] and k_rope [keys, 64] (rotated);
+    bf16 or fp16, rows contiguous. status: a device int32 word [1], or None."""
+    (_torch_binding or _native()).attend_prompts(q, k, k_rope, v, q_starts, k_starts, o, lse, sm_scale, causal, status, stream)
 
 
 class Pool:
@@ -427,6 +498,22 @@ class Context:
         """attend_pages() over this context's device buffer and status word."""
         _native().attend_pages(shape, q, self._pages(shape), out_slots, selections, lengths, o, lse, sm_scale, softcap,
                                slopes, start, prefix, self._lib.hs_status_word(self._h), stream)
+
+    # ------------------------------------------------------------------ latent entries
+    def append_latents(self, latent, rope, positions, requests=None, rotation=None, halves: bool = False,
+                       rotation_positions=None, stream=None) -> None:
+        """hs_append_latents: latent [n, 512] and rope [n, 64], bf16 or fp16, join the histories at
+        positions int32 [n] (negative: skipped) of the requests int32 [n] (None: token i of request
+        i), in the host store and the resident slots; rotated (see write_latents) by their
+        positions, or by rotation_positions int32 [n]."""
+        _native().append_latents(self._h, latent, rope, positions, requests, rotation, rotation_positions, halves, stream)
+
+    def read_latents(self, out_slots, latent, rope, stream=None) -> None:
+        """read_latents() over this context's device buffer and status word."""
+        if self.E != LATENT_ENTRY_BYTES:
+            raise ValueError(f"latent entries have {LATENT_ENTRY_BYTES} bytes, but the context's entries {self.E}")
+        _native().read_latents((self._lib.hs_device_kv(self._h), self.R, self.S, self._lib.hs_device(self._h)), out_slots,
+                               latent, rope, self._lib.hs_status_word(self._h), stream)
 
     def reset(self, stream=None) -> None:
         self._check(self._lib.hs_reset(self._h, _stream(stream)), "hs_reset")

@@ -20,8 +20,9 @@ LIB = os.path.join(HERE, "libhs.so")
 TORCH_LIB = os.path.join(HERE, "_hs_torch.so")  # the compiled part of the Python binding
 TORCH_SOURCE = os.path.join(CSRC, "hs_torch.cpp")
 SOURCES = ["hs_api.cu", "hs_kernels.cu", "hs_noalloc.cu", "hs_consume.cu", "hs_attend.cu", "hs_pool.cu",
-           "hs_page.cu", "hs_page_attend.cu"]
+           "hs_page.cu", "hs_page_attend.cu", "hs_latent.cu", "hs_absorb.cu", "hs_prompt.cu"]
 HEADERS = [os.path.join(CSRC, "hs_internal.h"), os.path.join(CSRC, "hs_page.h"), os.path.join(CSRC, "hs_once.h"),
+           os.path.join(CSRC, "hs_latent.h"), os.path.join(CSRC, "hs_tc.h"), os.path.join(CSRC, "hs_launch.h"),
            os.path.join(ROOT, "include", "hs.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-Xptxas", "-v",

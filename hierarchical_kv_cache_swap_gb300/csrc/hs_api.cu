@@ -19,6 +19,7 @@
 
 #include "hs.h"
 #include "hs_internal.h"
+#include "hs_latent.h"
 #include "hs_page.h"
 
 struct hs_ctx {
@@ -672,6 +673,179 @@ int hs_attend_pages(hs_stream_t stream, const hs_page_attention* a) {
     p.cap = a->softcap;
     cudaError_t e = hs::launch_attend_pages((cudaStream_t)stream, ps, a->dtype == HS_BF16, p, sms);
     if (e != cudaSuccess) return cuda_fail(e, "page attention kernel launch");
+    g_err[0] = 0;
+    return HS_OK;
+}
+
+static int latent_rows_check(int dtype, const hs_latent_rows* r, int64_t n, hs::LatentRows* out) {
+    if (dtype != HS_BF16 && dtype != HS_F16) return fail(HS_ERR_INVALID, "unknown dtype %d", dtype);
+    if (!r) return fail(HS_ERR_INVALID, "null latent rows");
+    if (n < 0) return fail(HS_ERR_INVALID, "n=%lld must not be negative", (long long)n);
+    if (n > 0 && (!r->latent || !r->rope)) return fail(HS_ERR_INVALID, "null latent/rope");
+    if (!aligned16(r->latent) || !aligned16(r->rope) || ((r->latent_stride | r->rope_stride) & 7))
+        return fail(HS_ERR_INVALID, "rows of latent and rope must be 16-byte aligned");
+    *out = hs::LatentRows{(const uint16_t*)r->latent, (const uint16_t*)r->rope, r->latent_stride, r->rope_stride};
+    return HS_OK;
+}
+
+// `positions`: what stands in for the rotation's own where it has none.
+static int rotation_check(const hs_rotation* r, int64_t n, const int32_t* positions, hs::Rotation* out) {
+    *out = hs::Rotation{nullptr, 0, nullptr, 0};
+    if (!r) return HS_OK;
+    if (r->rows < 0 || (r->rows > 0 && !r->table)) return fail(HS_ERR_INVALID, "rotation of %lld rows without a table", (long long)r->rows);
+    if (n > 0 && !r->positions && !positions) return fail(HS_ERR_INVALID, "rotation without positions");
+    if ((uintptr_t)r->table & 3) return fail(HS_ERR_INVALID, "the rotation's table must be 4-byte aligned");
+    static const float none[1] = {0.f};  // no row of it is read
+    *out = hs::Rotation{r->table ? r->table : none, r->rows, r->positions ? r->positions : positions, r->halves != 0};
+    return HS_OK;
+}
+
+int hs_write_latents(hs_stream_t stream, int dtype, const hs_latent_rows* rows, int64_t n, const hs_rotation* rotation,
+                     const int64_t* dest, uint8_t* entries, int64_t num_entries, uint32_t* status) {
+    hs::LatentRows lr;
+    hs::Rotation rot;
+    int rc = latent_rows_check(dtype, rows, n, &lr), sms = 0;
+    if (rc != HS_OK || (rc = rotation_check(rotation, n, nullptr, &rot)) != HS_OK) return rc;
+    if (num_entries < 0 || num_entries > INT64_MAX / (2 * hs::kLatentEntry))
+        return fail(HS_ERR_INVALID, "num_entries=%lld out of range", (long long)num_entries);
+    if (n > 0 && (!dest || (!entries && num_entries > 0))) return fail(HS_ERR_INVALID, "null dest/entries");
+    if (!aligned16(entries)) return fail(HS_ERR_INVALID, "entries must be 16-byte aligned");
+    if ((rc = sm_count(&sms)) != HS_OK) return rc;
+    cudaError_t e = hs::launch_write_latents((cudaStream_t)stream, dtype == HS_BF16, lr, n, rot, dest, entries, num_entries, status, sms);
+    if (e != cudaSuccess) return cuda_fail(e, "latent write kernel launch");
+    g_err[0] = 0;
+    return HS_OK;
+}
+
+int hs_append_latents(hs_ctx* h, hs_stream_t stream, int dtype, const hs_latent_rows* rows, int64_t n,
+                      const hs_rotation* rotation, const int32_t* requests, const int32_t* positions) {
+    hs::LatentRows lr;
+    hs::Rotation rot;
+    if (!h) return fail(HS_ERR_INVALID, "null context");
+    int rc = latent_rows_check(dtype, rows, n, &lr), dev = -1;
+    if (rc != HS_OK) return rc;
+    if (h->L.E != hs::kLatentEntry)
+        return fail(HS_ERR_INVALID, "latent entries have %d bytes, but the context's entries %d", hs::kLatentEntry, h->L.E);
+    if (n > 0 && !positions) return fail(HS_ERR_INVALID, "null positions");
+    if (!requests && n != h->L.R)
+        return fail(HS_ERR_INVALID, "n=%lld without requests, but the context has %d", (long long)n, h->L.R);
+    if ((rc = rotation_check(rotation, n, positions, &rot)) != HS_OK) return rc;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    if (dev != h->device)
+        return fail(HS_ERR_INVALID, "current device %d is not the context's device %d", dev, h->device);
+    e = hs::launch_append_latents(h->L, (cudaStream_t)stream, dtype == HS_BF16, lr, n, rot, requests, positions, h->num_sms);
+    if (e != cudaSuccess) return cuda_fail(e, "latent append kernel launch");
+    g_err[0] = 0;
+    return HS_OK;
+}
+
+int hs_read_latents(hs_stream_t stream, int dtype, const uint8_t* entries, int B, int S, const int32_t* slots, int n,
+                    void* latent, void* rope, uint32_t* status) {
+    int rc, sms = 0;
+    if (dtype != HS_BF16 && dtype != HS_F16) return fail(HS_ERR_INVALID, "unknown dtype %d", dtype);
+    if (B < 0 || S < 0 || n < 0) return fail(HS_ERR_INVALID, "B=%d, S=%d and n=%d must not be negative", B, S, n);
+    if (B > 0 && n > 0 && (!slots || !latent || !rope || (!entries && S > 0)))
+        return fail(HS_ERR_INVALID, "null entries/slots/latent/rope");
+    if (!aligned16(entries) || !aligned16(latent) || !aligned16(rope))
+        return fail(HS_ERR_INVALID, "entries, latent and rope must be 16-byte aligned");
+    if ((rc = sm_count(&sms)) != HS_OK) return rc;
+    cudaError_t e = hs::launch_read_latents((cudaStream_t)stream, dtype == HS_BF16, entries, S, slots, n, (int64_t)B * n, latent,
+                                            rope, status, sms);
+    if (e != cudaSuccess) return cuda_fail(e, "latent read kernel launch");
+    g_err[0] = 0;
+    return HS_OK;
+}
+
+// `align`: elements of x in 16 bytes.
+static int product_check(const hs_head_product* p, int align, hs::HeadProduct* out) {
+    if (!p) return fail(HS_ERR_INVALID, "null product");
+    if (p->n < 0) return fail(HS_ERR_INVALID, "n=%lld must not be negative", (long long)p->n);
+    if (p->heads < 1 || p->heads > 65535) return fail(HS_ERR_INVALID, "heads=%d must be in [1, 65535]", p->heads);
+    if (p->n > 0 && (!p->x || !p->w || !p->out)) return fail(HS_ERR_INVALID, "null x/w/out");
+    if (!aligned16(p->x) || !aligned16(p->w) || !aligned16(p->out) || ((p->x_token_stride | p->x_head_stride) & (align - 1)) ||
+        ((p->w_head_stride | p->w_row_stride) & 7))
+        return fail(HS_ERR_INVALID, "rows of x, w and out must be 16-byte aligned");
+    *out = hs::HeadProduct{p->x, p->x_token_stride, p->x_head_stride, (const uint16_t*)p->w, p->w_head_stride, p->w_row_stride,
+                           (uint16_t*)p->out, p->n, p->heads};
+    return HS_OK;
+}
+
+int hs_absorb_queries(hs_stream_t stream, const hs_head_product* product, const hs_rotation* rotation, uint32_t* status) {
+    hs::HeadProduct p;
+    hs::Rotation rot;
+    int rc = product_check(product, 8, &p), sms = 0;
+    if (rc != HS_OK || (rc = rotation_check(rotation, p.n, nullptr, &rot)) != HS_OK || (rc = sm_count(&sms)) != HS_OK) return rc;
+    cudaError_t e = hs::launch_absorb_queries((cudaStream_t)stream, p, rot, status, sms);
+    if (e != cudaSuccess) return cuda_fail(e, "query absorption kernel launch");
+    g_err[0] = 0;
+    return HS_OK;
+}
+
+int hs_expand_outputs(hs_stream_t stream, const hs_head_product* product) {
+    hs::HeadProduct p;
+    int rc = product_check(product, 4, &p), sms = 0;
+    if (rc != HS_OK || (rc = sm_count(&sms)) != HS_OK) return rc;
+    cudaError_t e = hs::launch_expand_outputs((cudaStream_t)stream, p, sms);
+    if (e != cudaSuccess) return cuda_fail(e, "output expansion kernel launch");
+    g_err[0] = 0;
+    return HS_OK;
+}
+
+int hs_attend_prompts(hs_stream_t stream, const hs_prompt_attention* a) {
+    if (!a) return fail(HS_ERR_INVALID, "null arguments");
+    if (a->dtype != HS_BF16 && a->dtype != HS_F16) return fail(HS_ERR_INVALID, "unknown dtype %d", a->dtype);
+    if (a->B < 0) return fail(HS_ERR_INVALID, "B=%d must not be negative", a->B);
+    if (a->heads < 1 || a->heads > 65535) return fail(HS_ERR_INVALID, "heads=%d must be in [1, 65535]", a->heads);
+    if (a->q_rows < 0 || a->q_rows > 0x7fffff00 || a->k_rows < 0 || a->k_rows > 0x7fffff00)
+        return fail(HS_ERR_INVALID, "q_rows=%lld and k_rows=%lld must be in [0, 2^31 - 256]", (long long)a->q_rows, (long long)a->k_rows);
+    if (!(a->sm_scale > 0.f && a->sm_scale < 1e30f)) return fail(HS_ERR_INVALID, "sm_scale must be positive, below 1e30");
+    if (a->B > 0 && (!a->q_starts || !a->k_starts)) return fail(HS_ERR_INVALID, "null q_starts/k_starts");
+    if (a->B > 0 && a->q_rows > 0 && (!a->q || !a->o || !a->lse)) return fail(HS_ERR_INVALID, "null q/o/lse");
+    if (a->B > 0 && a->k_rows > 0 && (!a->k || !a->k_rope || !a->v)) return fail(HS_ERR_INVALID, "null k/k_rope/v");
+    if (!aligned16(a->q) || !aligned16(a->k) || !aligned16(a->k_rope) || !aligned16(a->v) || !aligned16(a->o) ||
+        ((a->q_token_stride | a->q_head_stride | a->k_token_stride | a->k_head_stride | a->k_rope_stride | a->v_token_stride |
+          a->v_head_stride | a->o_token_stride | a->o_head_stride) & 7))
+        return fail(HS_ERR_INVALID, "rows of q, k, k_rope, v and o must be 16-byte aligned");
+    // the copies' strides: positive, below 2^40 bytes
+    const struct {
+        const char* name;
+        int64_t n, stride;
+    } steps[] = {{"q_token", a->q_rows, a->q_token_stride}, {"q_head", a->heads, a->q_head_stride}, {"k_token", a->k_rows, a->k_token_stride},
+                 {"k_head", a->heads, a->k_head_stride}, {"k_rope", a->k_rows, a->k_rope_stride}, {"v_token", a->k_rows, a->v_token_stride},
+                 {"v_head", a->heads, a->v_head_stride}};
+    for (const auto& s : steps)
+        if (s.n > 1 && (s.stride <= 0 || s.stride >= (int64_t)1 << 39))
+            return fail(HS_ERR_INVALID, "%s_stride=%lld must be positive, below 2^39", s.name, (long long)s.stride);
+    if (rows_overlap(hs::kHeadDim, {Axis{a->q_rows, a->o_token_stride}, Axis{a->heads, a->o_head_stride}, Axis{1, 0}}))
+        return fail(HS_ERR_INVALID, "rows of o overlap");
+    hs::PromptAttention p;
+    p.q = (const uint16_t*)a->q;
+    p.k = (const uint16_t*)a->k;
+    p.k_rope = (const uint16_t*)a->k_rope;
+    p.v = (const uint16_t*)a->v;
+    p.q_token = a->q_token_stride;
+    p.q_head = a->q_head_stride;
+    p.k_token = a->k_token_stride;
+    p.k_head = a->k_head_stride;
+    p.r_token = a->k_rope_stride;
+    p.v_token = a->v_token_stride;
+    p.v_head = a->v_head_stride;
+    p.o = (uint16_t*)a->o;
+    p.o_token = a->o_token_stride;
+    p.o_head = a->o_head_stride;
+    p.lse = a->lse;
+    p.q_starts = a->q_starts;
+    p.k_starts = a->k_starts;
+    p.status = a->status;
+    p.q_rows = a->q_rows;
+    p.k_rows = a->k_rows;
+    p.B = a->B;
+    p.H = a->heads;
+    p.causal = a->causal != 0;
+    p.scale = a->sm_scale;
+    cudaError_t e = hs::launch_attend_prompts((cudaStream_t)stream, a->dtype == HS_BF16, p);
+    if (e != cudaSuccess) return cuda_fail(e, "prompt attention kernel launch");
     g_err[0] = 0;
     return HS_OK;
 }

@@ -1,0 +1,437 @@
+// hs_prompt.cu -- attention of prompts, latent attention's expanded form: every head has keys of its
+// own, 128 values expanded from the latent and the token's 64 rotary ones, which all heads share, and
+// values of 128. For query row i of a prompt of Lq rows and Lk keys,
+//   s_j = scale (<q_i[:128], k_j> + <q_i[128:], k_rope_j>),  o_i = sum_j softmax_j(s) v_j,  lse_i = ln sum_j exp(s_j)
+// over j < Lk, or j <= i + Lk - Lq (causal): 640 operations a (query, key, head) against a few bytes,
+// so the tensor cores bound it (tcgen05, bf16 or fp16 operands, f32 sums).
+//
+// A CTA takes 256 rows of one head, as two tiles of 128 that share every key tile, and walks the key
+// tiles of 128 once, with a running maximum and sum for each row:
+//   * one thread copies keys, rotary keys and values through tensor maps into a ring of eight 16 KB
+//     chunks (a key tile is three chunks of 64 dimensions, the rotary one read straight from the shared
+//     tensor; its values are two chunks of 64 keys);
+//   * one thread issues the products: S = Q K^T (128 x 128 in tensor memory, 12 instructions of 16
+//     dimensions) and O += P V (P from tensor memory, where it lies over the scores it came from), one
+//     row tile's after the other's, so that while one tile's softmax runs the other's products do;
+//   * four warps a row tile hold a row a thread: no value crosses lanes. The maximum m of a row moves
+//     only when a tile's exceeds it by more than 8 (log2), and O is then rescaled in tensor memory; P =
+//     2^(x - m) stays below 2^8 and is rounded to the operands' type for the product (a relative
+//     2^-9 or 2^-12 of each weight, as the queries and keys have themselves), the sum is of the
+//     unrounded f32 values.
+// Keys past a prompt's end that a tile reads (the next prompt's, or zeros behind the tensor) are masked
+// in S, and their values zeroed in shared memory, whatever they hold.
+//
+// Every wait is bounded (hs_tc.h): on expiry the CTA records HS_STATUS_TIMEOUT, writes NaN rows, waits
+// for its copies and products in flight and frees its tensor memory.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "hs_latent.h"
+#include "hs_launch.h"
+#include "hs_once.h"
+#include "hs_tc.h"
+
+namespace hs {
+namespace {
+
+constexpr int kRows = 128;                      // of a row tile (the MMAs' M)
+constexpr int kTileRows = 2 * kRows;            // of a CTA
+constexpr int kKeys = 128;                      // of a key tile
+constexpr int kQDims = kHeadDim + kRope;        // 192
+constexpr uint32_t kChunk = 16384;              // 128 rows x 64 dimensions, or (V) 64 keys x 128
+constexpr int kSlots = 8;                       // of the ring
+constexpr int kKChunks = kQDims / 64, kVChunks = kKeys / 64, kTileChunks = kKChunks + kVChunks;
+constexpr uint32_t kQBytes = 2 * kKChunks * kChunk;
+constexpr int kSoftWarps = 8, kMmaWarp = kSoftWarps, kCopyWarp = kMmaWarp + 1, kThreads = (kCopyWarp + 1) * 32;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColS = 0, kColO = 256;      // row tile w: scores (P over their first half) at + 128 w
+constexpr float kRescaleLog2 = 8.f;
+
+struct Smem {  // beyond Q and the ring
+    uint64_t full[kSlots], free[kSlots];
+    uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drain;
+    uint32_t tmem;
+    volatile int abort;
+    int seq, tile;  // this CTA's prompt and 256-row tile of it (seq < 0: none)
+    int64_t q0, k0;
+    int lq, lk;
+};
+constexpr uint32_t kSmemBytes = 1024 + kQBytes + kSlots * kChunk + sizeof(Smem);
+
+struct Maps {
+    CUtensorMap q, k, r, v;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    if (BF16) {
+        const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&r);
+    }
+    const __half2 r = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// Finds the prompt and the tile of it that CTA `at` of the prompts' tiles takes, by one warp: 32
+// prompts at a time, their tiles counted and added up over the lanes. A prompt whose bounds are not in
+// order, or not within the rows there are, has no tiles.
+__device__ void find_tile(const PromptAttention& A, int at, Smem* sm) {
+    const int lane = threadIdx.x & 31;
+    int64_t before = 0;
+    for (int b0 = 0; b0 < A.B; b0 += 32) {
+        const int b = b0 + lane;
+        int64_t q0 = 0, q1 = 0, k0 = 0, k1 = 0;
+        if (b < A.B) {
+            q0 = A.q_starts[b], q1 = A.q_starts[b + 1];
+            k0 = A.k_starts[b], k1 = A.k_starts[b + 1];
+            if (q0 < 0 || q1 < q0 || q1 > A.q_rows || k0 < 0 || k1 < k0 || k1 > A.k_rows) {
+                if (A.status) atomicOr(A.status, 1u /* HS_STATUS_RANGE */);
+                q1 = q0 = k1 = k0 = 0;
+            }
+        }
+        const int tiles = (int)((q1 - q0 + kTileRows - 1) / kTileRows);
+        int upto = tiles;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int x = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d) upto += x;
+        }
+        const bool mine = at >= before + upto - tiles && at < before + upto;
+        if (mine) {
+            sm->seq = b;
+            sm->tile = (int)(before + upto - 1 - at);  // the last rows, which see the most keys, first
+            sm->q0 = q0;
+            sm->k0 = k0;
+            sm->lq = (int)(q1 - q0);
+            sm->lk = (int)(k1 - k0);
+        }
+        if (__any_sync(0xffffffffu, mine)) return;
+        before += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    if (lane == 0) sm->seq = -1;
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttention A, const __grid_constant__ Maps maps) {
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* ring = base + kQBytes;
+    Smem* sm = reinterpret_cast<Smem*>(ring + kSlots * kChunk);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, h = blockIdx.y;
+
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (warp == 0) {
+        find_tile(A, blockIdx.x, sm);
+    } else if (tid == 32) {
+        for (int i = 0; i < kSlots; ++i) {
+            bar_init(&sm->full[i], 1);
+            bar_init(&sm->free[i], 1);
+        }
+        for (int w = 0; w < 2; ++w) {
+            bar_init(&sm->q_full[w], 1);
+            bar_init(&sm->s_full[w], 1);
+            bar_init(&sm->p_full[w], kRows);
+            bar_init(&sm->o_full[w], 1);
+        }
+        bar_init(&sm->drain, 1);
+        sm->abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kMmaWarp) tmem_alloc<kTmemCols>(&sm->tmem);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = sm->tmem;
+    const int lq = sm->lq, lk = sm->lk, row0 = sm->tile * kTileRows;
+    const bool some = sm->seq >= 0;
+    // Row i sees the keys below i + 1 + past (causal), or all of them.
+    const int past = lk - lq;
+    auto keys_of = [&](int w) {  // the key tiles of row tile w
+        const int first = row0 + w * kRows;
+        if (!some || first >= lq) return 0;
+        const int last = min(first + kRows, lq);  // rows before it
+        const int seen = A.causal ? min(max(last + past, 0), lk) : lk;
+        return (seen + kKeys - 1) / kKeys;
+    };
+    const int nt0 = keys_of(0), nt1 = keys_of(1), nt = max(nt0, nt1);
+
+    if (warp == kCopyWarp) {
+        // ------------------------------------------------------------ copies (one thread)
+        if (lane == 0 && nt > 0) {
+            const int64_t q_row = sm->q0 + row0;
+            for (int w = 0; w < 2; ++w)
+                if ((w ? nt1 : nt0) > 0) {
+                    bar_expect_tx(&sm->q_full[w], kKChunks * kChunk);
+                    for (int c = 0; c < kKChunks; ++c)
+                        tma_load_3d(su32(base) + (w * kKChunks + c) * kChunk, &maps.q, 64 * c, h, (int)(q_row + w * kRows), &sm->q_full[w]);
+                }
+            int g = 0;
+            bool ok = true;
+            for (int i = 0; ok && i < nt; ++i) {
+                const int key = (int)sm->k0 + i * kKeys;
+                for (int c = 0; c < kTileChunks; ++c, ++g) {
+                    const int slot = g % kSlots;
+                    if (g >= kSlots && !bar_wait(&sm->free[slot], (g / kSlots - 1) & 1, &sm->abort)) { ok = false; break; }
+                    bar_expect_tx(&sm->full[slot], kChunk);
+                    const uint32_t to = su32(ring) + slot * kChunk;
+                    if (c < kHeadDim / 64) {
+                        tma_load_3d(to, &maps.k, 64 * c, h, key, &sm->full[slot]);
+                    } else if (c < kKChunks) {
+                        tma_load_2d(to, &maps.r, 0, key, &sm->full[slot]);
+                    } else {
+                        const int at = key + 64 * (c - kKChunks);
+                        tma_load_3d(to, &maps.v, 0, h, at, &sm->full[slot]);
+                        tma_load_3d(to + kChunk / 2, &maps.v, 64, h, at, &sm->full[slot]);
+                    }
+                }
+            }
+            // no copy may land after the CTA's end: the last one into each slot, and the queries
+            for (int s = max(g - kSlots, 0); s < g; ++s) bar_drain(&sm->full[s % kSlots], (s / kSlots) & 1);
+            for (int w = 0; w < 2; ++w)
+                if ((w ? nt1 : nt0) > 0) bar_drain(&sm->q_full[w], 0);
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp) {
+        // ------------------------------------------------------------ products (one thread)
+        if (lane == 0 && nt > 0) {
+            constexpr uint32_t id_s = mma_idesc(BF16, kRows, kKeys, 0), id_o = mma_idesc(BF16, kRows, kHeadDim, 1);
+            const uint32_t q_at = su32(base), ring_at = su32(ring);
+            int ready = 0;
+            bool ok = true;
+            auto upto = [&](int g) {  // chunks up to the g-th have landed
+                for (; ok && ready <= g; ++ready) ok = bar_wait(&sm->full[ready % kSlots], (ready / kSlots) & 1, &sm->abort);
+                return ok;
+            };
+            auto scores = [&](int w, int i) {
+                if (!upto(i * kTileChunks + kKChunks - 1)) return;
+                fence_after();
+#pragma unroll
+                for (int c = 0; c < kKChunks; ++c) {
+                    const uint32_t a = q_at + (w * kKChunks + c) * kChunk, b = ring_at + (i * kTileChunks + c) % kSlots * kChunk;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_ss(tmem + kColS + 128 * w, smem_desc(a + 32 * k, 16, 1024), smem_desc(b + 32 * k, 16, 1024), id_s, (c | k) ? 1u : 0u);
+                }
+                mma_commit(&sm->s_full[w]);
+            };
+            auto values = [&](int w, int i) {
+                if (!upto(i * kTileChunks + kTileChunks - 1)) return;
+                ok = bar_wait(&sm->p_full[w], i & 1, &sm->abort);
+                if (!ok) return;
+                fence_after();
+#pragma unroll
+                for (int c = 0; c < kVChunks; ++c) {
+                    const uint32_t b = ring_at + (i * kTileChunks + kKChunks + c) % kSlots * kChunk;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_ts(tmem + kColO + 128 * w, tmem + kColS + 128 * w + 32 * c + 8 * k, smem_desc(b + 2048 * k, kChunk / 2, 1024), id_o,
+                               (i | c | k) ? 1u : 0u);
+                }
+                if (i == (w ? nt1 : nt0) - 1) mma_commit(&sm->o_full[w]);
+            };
+            auto release = [&](int i, int first, int count) {  // once the products so far are done
+                for (int c = first; c < first + count; ++c) mma_commit(&sm->free[(i * kTileChunks + c) % kSlots]);
+            };
+            for (int w = 0; w < 2; ++w)
+                if (ok && (w ? nt1 : nt0) > 0) {
+                    ok = bar_wait(&sm->q_full[w], 0, &sm->abort);
+                    if (ok) scores(w, 0);
+                }
+            if (ok) release(0, 0, kKChunks);
+            for (int i = 0; ok && i < nt; ++i) {
+                for (int w = 0; ok && w < 2; ++w) {
+                    const int n = w ? nt1 : nt0;
+                    if (i < n) values(w, i);
+                    if (w == 1 && ok) release(i, kKChunks, kVChunks);
+                    if (ok && i + 1 < n) scores(w, i + 1);
+                }
+                if (ok && i + 1 < nt) release(i + 1, 0, kKChunks);
+            }
+            // whatever happened, every product issued here is done before the columns are freed
+            mma_commit(&sm->drain);
+            bar_drain(&sm->drain, 0);
+        }
+        __syncwarp();
+    } else if (some) {
+        // ------------------------------------------------------------ softmax, a row a thread
+        const int w = warp >> 2, row = row0 + w * kRows + (tid & (kRows - 1));  // of the prompt
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16, s_at = tmem + lanes + kColS + 128 * w, o_at = tmem + lanes + kColO + 128 * w;
+        const int n = w ? nt1 : nt0;
+        const float scale = A.scale * 1.4426950408889634f;
+        const int seen = row < lq ? (A.causal ? min(max(row + 1 + past, 0), lk) : lk) : 0;
+        float m = -INFINITY, l = 0.f;
+        bool ok = true;
+        for (int i = 0; i < n; ++i) {
+            const int here = seen - i * kKeys;  // keys of this tile that the row sees
+            if ((i + 1) * kKeys > lk) {         // values behind the prompt's end become zeros
+                const int live = lk - i * kKeys;
+                for (int c = 0; c < kVChunks && ok; ++c) {
+                    const int g = i * kTileChunks + kKChunks + c;
+                    ok = bar_wait(&sm->full[g % kSlots], (g / kSlots) & 1, &sm->abort);
+                    uint8_t* at = ring + g % kSlots * kChunk;
+                    for (int u = tid & (kRows - 1); ok && u < (int)kChunk / 16; u += kRows)
+                        if (64 * c + ((u >> 3) & 63) >= live) reinterpret_cast<uint4*>(at)[u] = make_uint4(0, 0, 0, 0);
+                }
+                fence_async_smem();
+            }
+            ok = ok && bar_wait(&sm->s_full[w], i & 1, &sm->abort);
+            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+            fence_after();
+            uint32_t s[128];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_load32(s + 32 * c, s_at + 32 * c);
+            tmem_wait_ld();
+            if (__any_sync(0xffffffffu, here < kKeys)) {
+#pragma unroll
+                for (int j = 0; j < 128; ++j)
+                    if (j >= here) s[j] = __float_as_uint(-INFINITY);
+            }
+            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int j = 0; j < 128; j += 8)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    top[k] = fmaxf(fmaxf(top[k], __uint_as_float(s[j + 2 * k])), __uint_as_float(s[j + 2 * k + 1]));
+            const float best = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
+            const bool move = best > m + kRescaleLog2 || (m == -INFINITY && best > -INFINITY);
+            if (i > 0 && __any_sync(0xffffffffu, move)) {
+                // O holds tiles 0 .. i - 1: their products ended before these scores did
+                const float f = move ? ex2(m - best) : 1.f;  // m = -inf: O is zero so far
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t o[32];
+                    tmem_load32(o, o_at + 32 * c);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                    tmem_store32(o_at + 32 * c, o);
+                }
+                l *= f;
+            }
+            if (move) m = best;
+            const float from = m == -INFINITY ? 0.f : m;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t p[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    const float x = ex2(fmaf(__uint_as_float(s[64 * c + 2 * j]), scale, -from));
+                    const float y = ex2(fmaf(__uint_as_float(s[64 * c + 2 * j + 1]), scale, -from));
+                    sum[2 * (j & 1)] += x;
+                    sum[2 * (j & 1) + 1] += y;
+                    p[j] = pack<BF16>(x, y);
+                }
+                tmem_store32(s_at + 32 * c, p);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            tmem_wait_st();
+            fence_before();
+            bar_arrive(&sm->p_full[w]);
+        }
+        if (ok && n > 0) ok = bar_wait(&sm->o_full[w], 0, &sm->abort);
+        ok = __all_sync(0xffffffffu, ok);
+        fence_after();
+        if (!ok && lane == 0 && A.status) atomicOr(A.status, 8u /* HS_STATUS_TIMEOUT */);
+        const float inv = l != 0.f ? 1.f / l : 0.f, none = __uint_as_float(0x7FC00000u);
+        const int64_t to = sm->q0 + row;
+        uint16_t* out = A.o + to * A.o_token + h * A.o_head;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+            uint32_t o[32];
+            if (n > 0) {
+                tmem_load32(o, o_at + 32 * c);
+                tmem_wait_ld();
+            }
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(!ok ? none : l == 0.f ? 0.f : __uint_as_float(o[j]) * inv);
+            if (row < lq) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    reinterpret_cast<uint4*>(out + 32 * c)[j] =
+                        make_uint4(pack<BF16>(__uint_as_float(o[8 * j]), __uint_as_float(o[8 * j + 1])),
+                                   pack<BF16>(__uint_as_float(o[8 * j + 2]), __uint_as_float(o[8 * j + 3])),
+                                   pack<BF16>(__uint_as_float(o[8 * j + 4]), __uint_as_float(o[8 * j + 5])),
+                                   pack<BF16>(__uint_as_float(o[8 * j + 6]), __uint_as_float(o[8 * j + 7])));
+            }
+        }
+        if (row < lq) A.lse[to * A.H + h] = !ok ? none : l == 0.f ? -INFINITY : (m + lg2(l)) * 0.69314718055994531f;
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        fence_after();
+        tmem_free<kTmemCols>(tmem);
+    }
+}
+
+// A tensor [tokens][heads][dims] of 16-bit floats (token and head strides in elements) read in boxes of
+// 64 dimensions of `rows` tokens of one head, 128-byte swizzled.
+bool encode(CUtensorMap* map, bool bf16, const uint16_t* x, int dims, int64_t heads, int64_t tokens, int64_t head, int64_t token, int rows) {
+    const EncodeTiled enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t size[3] = {(cuuint64_t)dims, (cuuint64_t)heads, (cuuint64_t)tokens};
+    const cuuint64_t stride[2] = {(cuuint64_t)head * 2, (cuuint64_t)token * 2};
+    const cuuint32_t box[3] = {64, 1, (cuuint32_t)rows}, step[3] = {1, 1, 1};
+    return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<uint16_t*>(x), size, stride, box,
+               step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool encode_rope(CUtensorMap* map, bool bf16, const uint16_t* x, int64_t tokens, int64_t token) {
+    const EncodeTiled enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t size[2] = {(cuuint64_t)kRope, (cuuint64_t)tokens}, stride[1] = {(cuuint64_t)token * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)kKeys}, step[2] = {1, 1};
+    return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<uint16_t*>(x), size, stride, box,
+               step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Ready {};
+
+}  // namespace
+
+cudaError_t launch_attend_prompts(cudaStream_t stream, bool bf16, const PromptAttention& a) {
+    if (a.q_rows == 0 || a.B == 0) return cudaSuccess;
+    static PerDevice<Ready> devices;
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    if (device >= PerDevice<Ready>::kDevices) return cudaErrorInvalidDevice;
+    const Ready* ready;
+    e = (cudaError_t)devices.get(device, [](Ready*) {
+        const cudaError_t x = cudaFuncSetAttribute(prompt_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+        return (int)(x != cudaSuccess ? x : cudaFuncSetAttribute(prompt_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes));
+    }, &ready);
+    if (e != cudaSuccess) return e;
+    Maps maps;
+    // without keys no copy is made of them: the maps then stand on the queries
+    const bool keys = a.k_rows > 0;
+    const int64_t n = keys ? a.k_rows : a.q_rows, q_head = a.H > 1 ? a.q_head : kQDims, q_token = a.q_rows > 1 ? a.q_token : kQDims;
+    const int64_t k_head = keys && a.H > 1 ? a.k_head : kHeadDim, v_head = keys && a.H > 1 ? a.v_head : kHeadDim;
+    const int64_t k_token = keys && n > 1 ? a.k_token : kHeadDim, v_token = keys && n > 1 ? a.v_token : kHeadDim;
+    const int64_t r_token = keys && n > 1 ? a.r_token : kRope;
+    if (!encode(&maps.q, bf16, a.q, kQDims, a.H, a.q_rows, q_head, q_token, kRows) ||
+        !encode(&maps.k, bf16, keys ? a.k : a.q, kHeadDim, a.H, n, k_head, k_token, kKeys) ||
+        !encode(&maps.v, bf16, keys ? a.v : a.q, kHeadDim, a.H, n, v_head, v_token, 64) ||
+        !encode_rope(&maps.r, bf16, keys ? a.k_rope : a.q, n, r_token))
+        return cudaErrorInvalidValue;
+    // a CTA for every 256 rows of a prompt, at most one more than full ones for each prompt
+    const int64_t tiles = a.q_rows / kTileRows + a.B;
+    return launch_dependent(stream, dim3((unsigned)tiles, (unsigned)a.H), kThreads, kSmemBytes, bf16 ? prompt_kernel<true> : prompt_kernel<false>, a, maps);
+}
+
+}  // namespace hs

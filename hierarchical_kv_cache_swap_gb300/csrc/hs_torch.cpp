@@ -1,4 +1,4 @@
-// hs_torch.cpp -- the page calls for torch tensors: checks of types, shapes, strides and
+// hs_torch.cpp -- the page and latent calls for torch tensors: checks of types, shapes, strides and
 // devices, then the C call of include/hs.h. The calls take a few microseconds on the GPU at
 // small sizes, less than their arguments would take to check and marshal in Python.
 #include <Python.h>
@@ -222,24 +222,25 @@ PyObject* append_tokens(PyObject*, PyObject* const* a, Py_ssize_t na) {
     });
 }
 
-// Pages [B, S, page bytes]: a tensor, or (address, B, S, device) of a context's device buffer.
+// Pages (or entries) [B, S, bytes]: a tensor, or (address, B, S, device) of a context's device buffer.
 struct Pages {
     const uint8_t* at;
     int64_t B, S;
 };
-Pages pages_of(PyObject* o, const hs_page_shape& s) {
+Pages rows_in_slots(PyObject* o, const char* name, int64_t bytes) {
     if (PyTuple_Check(o)) {
-        if (PyTuple_GET_SIZE(o) != 4) refuse("pages must be a tensor");
+        if (PyTuple_GET_SIZE(o) != 4) refuse("%s must be a tensor", name);
         const int device = c10::cuda::current_device();
         if (integer(PyTuple_GET_ITEM(o, 3)) != device) refuse("the current device %d is not the context's", device);
         return Pages{(const uint8_t*)(uintptr_t)integer(PyTuple_GET_ITEM(o, 0)), integer(PyTuple_GET_ITEM(o, 1)),
                      integer(PyTuple_GET_ITEM(o, 2))};
     }
-    const at::Tensor& x = tensor(o, "pages");
-    vector(x, "pages", at::kByte, {-1, -1, (int64_t)hs_page_bytes(&s)});
-    on_device({{"pages", &x}});
+    const at::Tensor& x = tensor(o, name);
+    vector(x, name, at::kByte, {-1, -1, bytes});
+    on_device({{name, &x}});
     return Pages{(const uint8_t*)x.data_ptr(), x.size(0), x.size(1)};
 }
+Pages pages_of(PyObject* o, const hs_page_shape& s) { return rows_in_slots(o, "pages", (int64_t)hs_page_bytes(&s)); }
 
 // read_pages(shape, pages, slots, k, v, status, stream)
 PyObject* read_pages(PyObject*, PyObject* const* a, Py_ssize_t na) {
@@ -322,6 +323,207 @@ PyObject* attend_pages(PyObject*, PyObject* const* a, Py_ssize_t na) {
     });
 }
 
+// A rotation as (table, positions, halves), table None for none; `own`: the call has positions of its
+// own, which stand in where these are None. nullptr where nothing is rotated.
+const hs_rotation* rotation_of(PyObject* table, PyObject* positions, PyObject* halves, int64_t n, bool own, hs_rotation* r) {
+    if (!has(table)) {
+        if (!own && has(positions)) refuse("positions without a rotation");
+        return nullptr;
+    }
+    const at::Tensor& t = tensor(table, "rotation");
+    vector(t, "rotation", at::kFloat, {-1, 64});
+    on_device({{"rotation", &t}});
+    const int32_t* p = nullptr;
+    if (has(positions)) {
+        const at::Tensor& x = tensor(positions, "positions");
+        vector(x, "positions", at::kInt, {n});
+        on_device({{"positions", &x}});
+        p = (const int32_t*)x.data_ptr();
+    } else if (!own) {
+        refuse("a rotation wants positions");
+    }
+    const int h = PyObject_IsTrue(halves);
+    if (h < 0) throw Refused();
+    *r = hs_rotation{(const float*)t.data_ptr(), t.size(0), p, h};
+    return r;
+}
+
+// latent [n, 512] and rope [n, 64] with contiguous rows.
+hs_latent_rows latents_of(const at::Tensor& latent, const at::Tensor& rope) {
+    const int64_t n = latent.dim() == 2 ? latent.size(0) : 0;
+    const struct {
+        const char* name;
+        const at::Tensor* x;
+        int width;
+    } both[] = {{"latent", &latent, 512}, {"rope", &rope, 64}};
+    for (const auto& t : both)
+        if (t.x->dim() != 2 || t.x->size(0) != n || t.x->size(1) != t.width || (t.x->stride(1) != 1 && n > 0))
+            refuse("%s must have shape [%lld, %d] with contiguous rows", t.name, (long long)n, t.width);
+    if (rope.scalar_type() != latent.scalar_type()) refuse("latent and rope must have one dtype");
+    return hs_latent_rows{latent.data_ptr(), rope.data_ptr(), stride(latent, 0), stride(rope, 0)};
+}
+
+// write_latents(latent, rope, dest, entries, rotation, positions, halves, status, stream)
+PyObject* write_latents(PyObject*, PyObject* const* a, Py_ssize_t na) {
+    if (!arity(na, 9)) return nullptr;
+    return guarded([&] {
+        const at::Tensor &latent = tensor(a[0], "latent"), &rope = tensor(a[1], "rope"), &dest = tensor(a[2], "dest"),
+                         &entries = tensor(a[3], "entries");
+        const int type = dtype_code(latent, "latent");
+        const hs_latent_rows rows = latents_of(latent, rope);
+        const int64_t n = latent.size(0);
+        vector(dest, "dest", at::kLong, {n});
+        vector(entries, "entries", at::kByte, {-1, HS_LATENT_ENTRY_BYTES});
+        on_device({{"latent", &latent}, {"rope", &rope}, {"dest", &dest},
+                   {"entries", entries.is_cpu() && entries.is_pinned() ? nullptr : &entries}});
+        hs_rotation r;
+        const hs_rotation* const rot = rotation_of(a[4], a[5], a[6], n, false, &r);
+        uint32_t* const status = status_of(a[7]);
+        const hs_stream_t stream = stream_of(a[8]);
+        const int64_t num = entries.size(0), *const to = (const int64_t*)dest.data_ptr();
+        uint8_t* const at = (uint8_t*)entries.data_ptr();
+        return done("hs_write_latents", [&] { return hs_write_latents(stream, type, &rows, n, rot, to, at, num, status); });
+    });
+}
+
+// append_latents(context, latent, rope, positions, requests, rotation, rotation positions, halves, stream)
+PyObject* append_latents(PyObject*, PyObject* const* a, Py_ssize_t na) {
+    if (!arity(na, 9)) return nullptr;
+    return guarded([&] {
+        const at::Tensor &latent = tensor(a[1], "latent"), &rope = tensor(a[2], "rope"), &pos = tensor(a[3], "positions");
+        const at::Tensor* req = has(a[4]) ? &tensor(a[4], "requests") : nullptr;
+        const int type = dtype_code(latent, "latent");
+        const hs_latent_rows rows = latents_of(latent, rope);
+        const int64_t n = latent.size(0);
+        vector(pos, "positions", at::kInt, {n});
+        if (req) vector(*req, "requests", at::kInt, {n});
+        on_device({{"latent", &latent}, {"rope", &rope}, {"positions", &pos}, {"requests", req}});
+        hs_rotation r;
+        const hs_rotation* const rot = rotation_of(a[5], a[6], a[7], n, true, &r);
+        hs_ctx* const ctx = (hs_ctx*)(uintptr_t)integer(a[0]);
+        const hs_stream_t stream = stream_of(a[8]);
+        const int32_t *const requests = req ? (const int32_t*)req->data_ptr() : nullptr, *const positions = (const int32_t*)pos.data_ptr();
+        return done("hs_append_latents", [&] { return hs_append_latents(ctx, stream, type, &rows, n, rot, requests, positions); });
+    });
+}
+
+// read_latents(entries, slots, latent, rope, status, stream)
+PyObject* read_latents(PyObject*, PyObject* const* a, Py_ssize_t na) {
+    if (!arity(na, 6)) return nullptr;
+    return guarded([&] {
+        const at::Tensor &slots = tensor(a[1], "slots"), &latent = tensor(a[2], "latent"), &rope = tensor(a[3], "rope");
+        const int type = dtype_code(latent, "latent");
+        vector(slots, "slots", at::kInt, {-1, -1});
+        const int64_t B = slots.size(0), n = slots.size(1);
+        vector(latent, "latent", latent.scalar_type(), {B, n, 512});
+        vector(rope, "rope", latent.scalar_type(), {B, n, 64});
+        const Pages p = rows_in_slots(a[0], "entries", HS_LATENT_ENTRY_BYTES);
+        if (p.B != B) refuse("entries of %lld requests, slots of %lld", (long long)p.B, (long long)B);
+        on_device({{"slots", &slots}, {"latent", &latent}, {"rope", &rope}});
+        const int requests = int_of(B, "B"), S = int_of(p.S, "S"), count = int_of(n, "n");
+        uint32_t* const status = status_of(a[4]);
+        const hs_stream_t stream = stream_of(a[5]);
+        const int32_t* const from = (const int32_t*)slots.data_ptr();
+        void *const lo = latent.data_ptr(), *const ro = rope.data_ptr();
+        return done("hs_read_latents", [&] { return hs_read_latents(stream, type, p.at, requests, S, from, count, lo, ro, status); });
+    });
+}
+
+// x [n, heads, x_width], w [heads, 128, 512] with contiguous rows, out [n, heads, out_width] contiguous.
+hs_head_product product_of(const at::Tensor& x, const char* name, at::ScalarType type, int x_width, const at::Tensor& w, const at::Tensor& out,
+                           int out_width) {
+    if (x.dim() != 3 || x.size(2) != x_width || x.scalar_type() != type || (x.stride(2) != 1 && x.numel() > 0))
+        refuse("%s must be a %s tensor of shape [*, *, %d] with contiguous rows", name, c10::toString(type), x_width);
+    const int64_t n = x.size(0), H = x.size(1);
+    if (w.dim() != 3 || w.size(0) != H || w.size(1) != 128 || w.size(2) != 512 || w.scalar_type() != at::kBFloat16 ||
+        (w.stride(2) != 1 && w.numel() > 0))
+        refuse("the matrices must be a bfloat16 tensor of shape [%lld, 128, 512] with contiguous rows", (long long)H);
+    vector(out, "out", at::kBFloat16, {n, H, out_width});
+    on_device({{name, &x}, {"the matrices", &w}, {"out", &out}});
+    return hs_head_product{x.data_ptr(), stride(x, 0), stride(x, 1), w.data_ptr(), stride(w, 0), stride(w, 1), out.data_ptr(), n,
+                           int_of(H, "heads")};
+}
+
+// absorb_queries(q, up_k, out, rotation, positions, halves, status, stream)
+PyObject* absorb_queries(PyObject*, PyObject* const* a, Py_ssize_t na) {
+    if (!arity(na, 8)) return nullptr;
+    return guarded([&] {
+        const at::Tensor& q = tensor(a[0], "q");
+        const hs_head_product p = product_of(q, "q", at::kBFloat16, 192, tensor(a[1], "up_k"), tensor(a[2], "out"), 576);
+        hs_rotation r;
+        const hs_rotation* const rot = rotation_of(a[3], a[4], a[5], p.n, false, &r);
+        uint32_t* const status = status_of(a[6]);
+        const hs_stream_t stream = stream_of(a[7]);
+        return done("hs_absorb_queries", [&] { return hs_absorb_queries(stream, &p, rot, status); });
+    });
+}
+
+// expand_outputs(o, up_v, out, stream)
+PyObject* expand_outputs(PyObject*, PyObject* const* a, Py_ssize_t na) {
+    if (!arity(na, 4)) return nullptr;
+    return guarded([&] {
+        const hs_head_product p = product_of(tensor(a[0], "o"), "o", at::kFloat, 512, tensor(a[1], "up_v"), tensor(a[2], "out"), 128);
+        const hs_stream_t stream = stream_of(a[3]);
+        return done("hs_expand_outputs", [&] { return hs_expand_outputs(stream, &p); });
+    });
+}
+
+// attend_prompts(q, k, k_rope, v, q_starts, k_starts, o, lse, sm_scale, causal, status, stream)
+PyObject* attend_prompts(PyObject*, PyObject* const* a, Py_ssize_t na) {
+    if (!arity(na, 12)) return nullptr;
+    return guarded([&] {
+        hs_prompt_attention p{};
+        const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &r = tensor(a[2], "k_rope"), &v = tensor(a[3], "v"),
+                         &qs = tensor(a[4], "q_starts"), &ks = tensor(a[5], "k_starts"), &o = tensor(a[6], "o"), &lse = tensor(a[7], "lse");
+        p.dtype = dtype_code(q, "q");
+        const int64_t H = q.dim() == 3 ? q.size(1) : 0, n = k.dim() == 3 ? k.size(0) : 0, m = q.dim() == 3 ? q.size(0) : 0;
+        const struct {
+            const char* name;
+            const at::Tensor* x;
+            int64_t rows, width;
+        } rows[] = {{"q", &q, m, 192}, {"o", &o, m, 128}, {"k", &k, n, 128}, {"v", &v, n, 128}};
+        for (const auto& t : rows)
+            if (t.x->dim() != 3 || t.x->size(0) != t.rows || t.x->size(1) != H || t.x->size(2) != t.width || t.x->scalar_type() != q.scalar_type() ||
+                (t.x->stride(2) != 1 && t.x->numel() > 0))
+                refuse("%s must have shape [%lld, %lld, %lld] with contiguous rows, and q's dtype", t.name, (long long)t.rows, (long long)H,
+                       (long long)t.width);
+        if (r.dim() != 2 || r.size(0) != n || r.size(1) != 64 || r.scalar_type() != q.scalar_type() || (r.stride(1) != 1 && n > 0))
+            refuse("k_rope must have shape [%lld, 64] with contiguous rows, and q's dtype", (long long)n);
+        vector(qs, "q_starts", at::kInt, {-1});
+        vector(ks, "k_starts", at::kInt, {qs.size(0)});
+        if (qs.size(0) < 1) refuse("q_starts and k_starts must have an element more than there are prompts");
+        vector(lse, "lse", at::kFloat, {m, H});
+        on_device({{"q", &q}, {"k", &k}, {"k_rope", &r}, {"v", &v}, {"q_starts", &qs}, {"k_starts", &ks}, {"o", &o}, {"lse", &lse}});
+        p.B = int_of(qs.size(0) - 1, "B");
+        p.heads = int_of(H, "heads");
+        p.causal = PyObject_IsTrue(a[9]);
+        if (p.causal < 0) throw Refused();
+        p.q_rows = m;
+        p.k_rows = n;
+        p.q = q.data_ptr();
+        p.q_token_stride = stride(q, 0);
+        p.q_head_stride = stride(q, 1);
+        p.k = k.data_ptr();
+        p.k_token_stride = stride(k, 0);
+        p.k_head_stride = stride(k, 1);
+        p.k_rope = r.data_ptr();
+        p.k_rope_stride = stride(r, 0);
+        p.v = v.data_ptr();
+        p.v_token_stride = stride(v, 0);
+        p.v_head_stride = stride(v, 1);
+        p.o = o.data_ptr();
+        p.o_token_stride = stride(o, 0);
+        p.o_head_stride = stride(o, 1);
+        p.lse = (float*)lse.data_ptr();
+        p.q_starts = (const int32_t*)qs.data_ptr();
+        p.k_starts = (const int32_t*)ks.data_ptr();
+        p.sm_scale = (float)number(a[8]);
+        p.status = status_of(a[10]);
+        const hs_stream_t stream = stream_of(a[11]);
+        return done("hs_attend_prompts", [&] { return hs_attend_prompts(stream, &p); });
+    });
+}
+
 PyObject* set_error(PyObject*, PyObject* e) {
     Py_XDECREF(g_error);
     Py_INCREF(e);
@@ -334,6 +536,12 @@ PyMethodDef kMethods[] = {
     {"append_tokens", (PyCFunction)(void (*)(void))append_tokens, METH_FASTCALL, nullptr},
     {"read_pages", (PyCFunction)(void (*)(void))read_pages, METH_FASTCALL, nullptr},
     {"attend_pages", (PyCFunction)(void (*)(void))attend_pages, METH_FASTCALL, nullptr},
+    {"write_latents", (PyCFunction)(void (*)(void))write_latents, METH_FASTCALL, nullptr},
+    {"append_latents", (PyCFunction)(void (*)(void))append_latents, METH_FASTCALL, nullptr},
+    {"read_latents", (PyCFunction)(void (*)(void))read_latents, METH_FASTCALL, nullptr},
+    {"absorb_queries", (PyCFunction)(void (*)(void))absorb_queries, METH_FASTCALL, nullptr},
+    {"expand_outputs", (PyCFunction)(void (*)(void))expand_outputs, METH_FASTCALL, nullptr},
+    {"attend_prompts", (PyCFunction)(void (*)(void))attend_prompts, METH_FASTCALL, nullptr},
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

@@ -487,6 +487,144 @@ typedef struct {
 } hs_page_attention;
 int hs_attend_pages(hs_stream_t stream, const hs_page_attention* args);
 
+/*
+ * ---------------------------------------------------------------------------------
+ * Latent entries. The calls below make the 656-byte entries that hs_attend reads and what goes
+ * before and after it: tokens written into entries with their rotary keys rotated on the way,
+ * entries read back, the two products of latent attention's absorbed form, and, for prompts, the
+ * attention of its expanded form. All of them are enqueue-only and graph-capturable, allocate
+ * nothing and need no workspace; their device pointers belong to the calling thread's current
+ * device. Their kernels are programmatic dependents of the kernel before them on the stream: they
+ * may be launched while it runs, and wait for it to end before they read or write anything.
+ *
+ * An entry is written from a latent of 512 values and a rotary key of 64. Each 128 latent values
+ * share a scale, the smallest power of two s >= 2^-126 with 448 s >= max |x|; a code is the E4M3
+ * number nearest to x / s (ties to even). A block with an infinity or a NaN gets a NaN for its
+ * scale and reads back as NaNs. The rotary values are rotated in f32 and rounded once to bf16.
+ */
+#define HS_LATENT_ENTRY_BYTES 656
+
+/* Rotation by position p: with c_i and s_i from row p of the table the pair (a, b) becomes
+ * (a c_i - b s_i, a s_i + b c_i), 0 <= i < 32. */
+typedef struct {
+    const float* table;       /* device [rows][64]: 32 cosines, then 32 sines, of each position */
+    int64_t rows;
+    const int32_t* positions; /* device [n]: the tokens' positions */
+    int halves;               /* pair i is dimensions i and i + 32; 0: 2 i and 2 i + 1 */
+} hs_rotation;
+
+/* Latents and rotary keys of tokens: token i's start i * stride elements into the tensor; each is
+ * contiguous and 16-byte aligned (strides multiples of 8). */
+typedef struct {
+    const void* latent;
+    const void* rope;
+    int64_t latent_stride, rope_stride;
+} hs_latent_rows;
+
+/*
+ * hs_write_latents -- n tokens (dtype HS_BF16 or HS_F16) into entries (device memory, or pinned
+ * memory mapped on the device; 16-byte aligned): token i into entry dest[i] (device int64 [n];
+ * negative: the token is padding and is skipped). rotation: NULL for rotary keys that are stored
+ * as they are. An entry >= num_entries, or a position that the table has no row for, is skipped
+ * and sets HS_STATUS_RANGE in *status (device word, or NULL). The entries of one call are distinct.
+ * Returns HS_OK, HS_ERR_INVALID or HS_ERR_CUDA.
+ */
+int hs_write_latents(hs_stream_t stream, int dtype, const hs_latent_rows* rows, int64_t n, const hs_rotation* rotation,
+                     const int64_t* dest, uint8_t* entries, int64_t num_entries, uint32_t* status);
+
+/*
+ * hs_append_latents -- hs_append for tokens: token i joins request requests[i] (device int32 [n];
+ * NULL: request i, and n must be num_requests) at position positions[i] (device int32 [n];
+ * negative: skipped), in the host store and, when that position is resident, in its slot as well,
+ * so the cache stays exact; the replacement state does not change. The context's entry_bytes must
+ * be 656. rotation->positions may be NULL: the tokens are then rotated by `positions`. A position
+ * >= context_len (or the request's extent), a request >= num_requests, or a position that the
+ * table has no row for is skipped and sets HS_STATUS_RANGE; a negative request is skipped like a
+ * negative position. Distinct (request, position) pairs only. Stream ordered with the context's
+ * other calls.
+ */
+int hs_append_latents(hs_ctx* ctx, hs_stream_t stream, int dtype, const hs_latent_rows* rows, int64_t n,
+                      const hs_rotation* rotation, const int32_t* requests, const int32_t* positions);
+
+/*
+ * hs_read_latents -- decodes entries: for each request b < B and j < n the entry in slot
+ * slots[b][j] (device int32 [B][n]) of entries [B][S] (16-byte aligned, e.g. hs_device_kv())
+ * becomes latent[b][j] and rope[b][j] (device [B][n][512] and [B][n][64] of `dtype`, contiguous,
+ * 16-byte aligned, overwritten). A negative slot reads as zeros, one >= S too, setting
+ * HS_STATUS_RANGE in *status (or NULL). A value is code * scale rounded to `dtype`, which is exact
+ * in bf16 but below 2^-126; what is too large for fp16 becomes infinite.
+ */
+int hs_read_latents(hs_stream_t stream, int dtype, const uint8_t* entries, int B, int S, const int32_t* slots, int n,
+                    void* latent, void* rope, uint32_t* status);
+
+/* Rows of n tokens and `heads` heads, each times its head's matrix: row (token, head) of x starts
+ * token * x_token_stride + head * x_head_stride elements in; w, bf16, holds a matrix of 128 rows of
+ * 512 for each head, w_head_stride apart, its rows w_row_stride apart (a part of one projection's
+ * weights, say). Rows are contiguous and 16-byte aligned; out is contiguous and 16-byte aligned. */
+typedef struct {
+    const void* x;
+    int64_t x_token_stride, x_head_stride;
+    const void* w;
+    int64_t w_head_stride, w_row_stride;
+    void* out;
+    int64_t n;
+    int heads; /* 1 .. 65535 */
+} hs_head_product;
+
+/*
+ * hs_absorb_queries -- the queries of the absorbed form, as hs_attend takes them: of x (bf16
+ * [n][heads][128 + 64]) the first 128 values become out[..][c] = sum_d x[..][d] w[head][d][c], c <
+ * 512, and the last 64, rotated (rotation: NULL if they are already), out[..][512 ..] (out: bf16
+ * [n][heads][576], not x). bf16 products, f32 sums, one rounding. A token whose position is
+ * negative gets zeros for its rotary values; so does one that the table has no row for, which
+ * sets HS_STATUS_RANGE in *status (or NULL). Returns HS_OK, HS_ERR_INVALID or HS_ERR_CUDA.
+ */
+int hs_absorb_queries(hs_stream_t stream, const hs_head_product* product, const hs_rotation* rotation, uint32_t* status);
+
+/*
+ * hs_expand_outputs -- what hs_attend gives (x: f32 [n][heads][512], strides multiples of 4)
+ * through the heads' value matrices: out[..][e] = sum_c x[..][c] w[head][e][c], e < 128 (out: bf16
+ * [n][heads][128]). x is rounded to bf16 for the products, the sums are f32.
+ */
+int hs_expand_outputs(hs_stream_t stream, const hs_head_product* product);
+
+/*
+ * hs_attend_prompts -- attention of B prompts in the expanded form. The rows of prompt b are
+ * q_starts[b] .. q_starts[b + 1] - 1 of q, o and lse, its keys k_starts[b] .. k_starts[b + 1] - 1
+ * of k, k_rope and v; there may be more keys than rows (a chunk behind earlier ones) or fewer. For
+ * row i of Lq and key j of Lk, s_j = sm_scale (<q[:128], k_j> + <q[128:], k_rope_j>), over j < Lk,
+ * or with `causal` j <= i + Lk - Lq: o = sum_j softmax_j(s) v_j, lse = ln sum_j exp(s_j). A row
+ * that sees no key gets o = 0 and lse = -inf. Keys behind a prompt's last are not read into its
+ * result, whatever they hold, and rows of q outside every prompt leave o and lse as they were. A prompt whose starts descend, or lie outside the rows there are, is left out and sets
+ * HS_STATUS_RANGE. The products run on the tensor cores in `dtype` with f32 sums; the softmax
+ * weights are rounded to it, relative to a maximum that is at most 2^8 times too small. Rows of every tensor
+ * are contiguous and 16-byte aligned (strides multiples of 8, positive where there is more than
+ * one row); rows of o that overlap are refused. HS_STATUS_TIMEOUT: a lost hand-off within the
+ * kernel (a defect); its rows are then NaN.
+ */
+typedef struct {
+    int dtype;                 /* of q, k, k_rope, v and o: HS_BF16 or HS_F16 */
+    int B, heads;              /* prompts; heads 1 .. 65535 */
+    int causal;
+    int64_t q_rows, k_rows;    /* of the tensors */
+    const void* q;             /* [q_rows][heads][128 + 64], the last 64 rotated */
+    int64_t q_token_stride, q_head_stride;
+    const void* k;             /* [k_rows][heads][128] */
+    int64_t k_token_stride, k_head_stride;
+    const void* k_rope;        /* [k_rows][64], rotated; the heads share it */
+    int64_t k_rope_stride;
+    const void* v;             /* [k_rows][heads][128] */
+    int64_t v_token_stride, v_head_stride;
+    void* o;                   /* [q_rows][heads][128] */
+    int64_t o_token_stride, o_head_stride;
+    float* lse;                /* device [q_rows][heads], contiguous */
+    const int32_t* q_starts;   /* device [B + 1] */
+    const int32_t* k_starts;   /* device [B + 1] */
+    float sm_scale;            /* > 0, finite */
+    uint32_t* status;          /* device word, or NULL */
+} hs_prompt_attention;
+int hs_attend_prompts(hs_stream_t stream, const hs_prompt_attention* args);
+
 /* hs_status_word -- the context's device status word, for the calls above. */
 uint32_t* hs_status_word(hs_ctx* ctx);
 
