@@ -44,14 +44,19 @@ constexpr uint32_t kChunk = 16384;              // 128 rows x 64 dimensions, or 
 constexpr int kSlots = 8;                       // of the ring
 constexpr int kKChunks = kQDims / 64, kVChunks = kKeys / 64, kTileChunks = kKChunks + kVChunks;
 constexpr uint32_t kQBytes = 2 * kKChunks * kChunk;
-constexpr int kSoftWarps = 8, kMmaWarp = kSoftWarps, kCopyWarp = kMmaWarp + 1, kThreads = (kCopyWarp + 1) * 32;
+constexpr int kSoftWarps = 8, kMmaWarp = kSoftWarps, kCopyWarp = kMmaWarp + 1;
+// Three warpgroups, launched with kLaunchRegs registers a thread; the two softmax ones take what the
+// third, of the issuing threads, gives up: a row of scores stays in registers.
+constexpr int kThreads = 384, kLaunchRegs = 168, kSoftRegs = 216, kIssueRegs = 72;
+static_assert(2 * kSoftRegs + kIssueRegs <= 3 * kLaunchRegs, "the split stays within what the block has");
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;      // row tile w: scores (P over their first half) at + 128 w
 constexpr float kRescaleLog2 = 8.f;
 
 struct Smem {  // beyond Q and the ring
-    uint64_t full[kSlots], free[kSlots];
-    uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drain;
+    uint64_t k_full[2], v_full[2];  // a key tile's keys and values, by its parity
+    uint64_t free[kSlots];
+    uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2], drain;  // by row tile; P by halves of the keys
     uint32_t tmem;
     volatile int abort;
     int seq, tile;  // this CTA's prompt and 256-row tile of it (seq < 0: none)
@@ -73,6 +78,24 @@ __device__ __forceinline__ float lg2(float x) {
     float y;
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+// Two values at a time: x * a + b, x + y.
+__device__ __forceinline__ float2 fma2(float2 x, float a, float b) {
+    float2 y;
+    asm("{ .reg .b64 x, a, b, d; mov.b64 x, {%2, %3}; mov.b64 a, {%4, %4}; mov.b64 b, {%5, %5}; fma.rn.f32x2 d, x, a, b; mov.b64 {%0, %1}, d; }"
+        : "=f"(y.x), "=f"(y.y) : "f"(x.x), "f"(x.y), "f"(a), "f"(b));
+    return y;
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+    float2 r;
+    asm("{ .reg .b64 x, y, d; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; add.rn.f32x2 d, x, y; mov.b64 {%0, %1}, d; }"
+        : "=f"(r.x), "=f"(r.y) : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+    return r;
 }
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack(float lo, float hi) {
@@ -120,7 +143,11 @@ __device__ void find_tile(const PromptAttention& A, int at, Smem* sm) {
         if (__any_sync(0xffffffffu, mine)) return;
         before += __shfl_sync(0xffffffffu, upto, 31);
     }
-    if (lane == 0) sm->seq = -1;
+    if (lane == 0) {
+        sm->seq = -1;
+        sm->tile = sm->lq = sm->lk = 0;
+        sm->q0 = sm->k0 = 0;
+    }
 }
 
 template <bool BF16>
@@ -129,20 +156,20 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* ring = base + kQBytes;
     Smem* sm = reinterpret_cast<Smem*>(ring + kSlots * kChunk);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, h = blockIdx.y;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, h = blockIdx.y;
 
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (warp == 0) {
         find_tile(A, blockIdx.x, sm);
     } else if (tid == 32) {
-        for (int i = 0; i < kSlots; ++i) {
-            bar_init(&sm->full[i], 1);
-            bar_init(&sm->free[i], 1);
-        }
+        for (int i = 0; i < kSlots; ++i) bar_init(&sm->free[i], 1);
         for (int w = 0; w < 2; ++w) {
+            bar_init(&sm->k_full[w], 1);
+            bar_init(&sm->v_full[w], 1);
             bar_init(&sm->q_full[w], 1);
             bar_init(&sm->s_full[w], 1);
-            bar_init(&sm->p_full[w], kRows);
+            bar_init(&sm->p_full[w][0], kRows);
+            bar_init(&sm->p_full[w][1], kRows);
             bar_init(&sm->o_full[w], 1);
         }
         bar_init(&sm->drain, 1);
@@ -153,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
     fence_before();
     __syncthreads();
     fence_after();
-    const uint32_t tmem = sm->tmem;
+    constexpr uint32_t tmem = 0;  // all the columns there are: the allocation can only begin at the first
     const int lq = sm->lq, lk = sm->lk, row0 = sm->tile * kTileRows;
     const bool some = sm->seq >= 0;
     // Row i sees the keys below i + 1 + past (causal), or all of them.
@@ -167,104 +194,117 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
     };
     const int nt0 = keys_of(0), nt1 = keys_of(1), nt = max(nt0, nt1);
 
-    if (warp == kCopyWarp) {
-        // ------------------------------------------------------------ copies (one thread)
-        if (lane == 0 && nt > 0) {
-            const int64_t q_row = sm->q0 + row0;
-            for (int w = 0; w < 2; ++w)
-                if ((w ? nt1 : nt0) > 0) {
-                    bar_expect_tx(&sm->q_full[w], kKChunks * kChunk);
-                    for (int c = 0; c < kKChunks; ++c)
-                        tma_load_3d(su32(base) + (w * kKChunks + c) * kChunk, &maps.q, 64 * c, h, (int)(q_row + w * kRows), &sm->q_full[w]);
-                }
-            int g = 0;
-            bool ok = true;
-            for (int i = 0; ok && i < nt; ++i) {
-                const int key = (int)sm->k0 + i * kKeys;
-                for (int c = 0; c < kTileChunks; ++c, ++g) {
-                    const int slot = g % kSlots;
-                    if (g >= kSlots && !bar_wait(&sm->free[slot], (g / kSlots - 1) & 1, &sm->abort)) { ok = false; break; }
-                    bar_expect_tx(&sm->full[slot], kChunk);
-                    const uint32_t to = su32(ring) + slot * kChunk;
-                    if (c < kHeadDim / 64) {
-                        tma_load_3d(to, &maps.k, 64 * c, h, key, &sm->full[slot]);
-                    } else if (c < kKChunks) {
-                        tma_load_2d(to, &maps.r, 0, key, &sm->full[slot]);
-                    } else {
-                        const int at = key + 64 * (c - kKChunks);
-                        tma_load_3d(to, &maps.v, 0, h, at, &sm->full[slot]);
-                        tma_load_3d(to + kChunk / 2, &maps.v, 64, h, at, &sm->full[slot]);
+    if (warp >= kSoftWarps) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+        if (warp == kCopyWarp) {
+            // ------------------------------------------------------------ copies (one thread)
+            if (lane == 0 && nt > 0) {
+                const int64_t q_row = sm->q0 + row0;
+                for (int w = 0; w < 2; ++w)
+                    if ((w ? nt1 : nt0) > 0) {
+                        bar_expect_tx(&sm->q_full[w], kKChunks * kChunk);
+                        for (int c = 0; c < kKChunks; ++c)
+                            tma_load_3d(su32(base) + (w * kKChunks + c) * kChunk, &maps.q, 64 * c, h, (int)(q_row + w * kRows), &sm->q_full[w]);
+                    }
+                int g = 0, tiles = 0;
+                bool ok = true;
+                auto open = [&] {  // the next slot, once it is free
+                    ok = ok && (g < kSlots || bar_wait(&sm->free[g % kSlots], (g / kSlots - 1) & 1, &sm->abort));
+                    return su32(ring) + g++ % kSlots * kChunk;
+                };
+                for (; ok && tiles < nt; ++tiles) {
+                    const int key = (int)sm->k0 + tiles * kKeys;
+                    uint64_t *const k_full = &sm->k_full[tiles & 1], *const v_full = &sm->v_full[tiles & 1];
+                    uint32_t to = open();
+                    if (!ok) break;
+                    bar_expect_tx(k_full, kKChunks * kChunk);
+                    tma_load_3d(to, &maps.k, 0, h, key, k_full);
+                    if (to = open(); ok) tma_load_3d(to, &maps.k, 64, h, key, k_full);
+                    if (to = open(); ok) tma_load_2d(to, &maps.r, 0, key, k_full);
+                    to = open();
+                    if (!ok) break;
+                    bar_expect_tx(v_full, kVChunks * kChunk);
+                    tma_load_3d(to, &maps.v, 0, h, key, v_full);
+                    tma_load_3d(to + kChunk / 2, &maps.v, 64, h, key, v_full);
+                    if (to = open(); ok) {
+                        tma_load_3d(to, &maps.v, 0, h, key + 64, v_full);
+                        tma_load_3d(to + kChunk / 2, &maps.v, 64, h, key + 64, v_full);
                     }
                 }
-            }
-            // no copy may land after the CTA's end: the last one into each slot, and the queries
-            for (int s = max(g - kSlots, 0); s < g; ++s) bar_drain(&sm->full[s % kSlots], (s / kSlots) & 1);
-            for (int w = 0; w < 2; ++w)
-                if ((w ? nt1 : nt0) > 0) bar_drain(&sm->q_full[w], 0);
-        }
-        __syncwarp();
-    } else if (warp == kMmaWarp) {
-        // ------------------------------------------------------------ products (one thread)
-        if (lane == 0 && nt > 0) {
-            constexpr uint32_t id_s = mma_idesc(BF16, kRows, kKeys, 0), id_o = mma_idesc(BF16, kRows, kHeadDim, 1);
-            const uint32_t q_at = su32(base), ring_at = su32(ring);
-            int ready = 0;
-            bool ok = true;
-            auto upto = [&](int g) {  // chunks up to the g-th have landed
-                for (; ok && ready <= g; ++ready) ok = bar_wait(&sm->full[ready % kSlots], (ready / kSlots) & 1, &sm->abort);
-                return ok;
-            };
-            auto scores = [&](int w, int i) {
-                if (!upto(i * kTileChunks + kKChunks - 1)) return;
-                fence_after();
-#pragma unroll
-                for (int c = 0; c < kKChunks; ++c) {
-                    const uint32_t a = q_at + (w * kKChunks + c) * kChunk, b = ring_at + (i * kTileChunks + c) % kSlots * kChunk;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_ss(tmem + kColS + 128 * w, smem_desc(a + 32 * k, 16, 1024), smem_desc(b + 32 * k, 16, 1024), id_s, (c | k) ? 1u : 0u);
+                // no copy may land after the CTA's end: the last tiles', and the queries
+                for (int i = max(tiles - 2, 0); i < tiles; ++i) {
+                    bar_drain(&sm->k_full[i & 1], (i >> 1) & 1);
+                    bar_drain(&sm->v_full[i & 1], (i >> 1) & 1);
                 }
-                mma_commit(&sm->s_full[w]);
+                for (int w = 0; w < 2; ++w)
+                    if ((w ? nt1 : nt0) > 0) bar_drain(&sm->q_full[w], 0);
+            }
+            __syncwarp();
+        } else if (warp == kMmaWarp) {
+            // ------------------------------------------------------------ products (issued by one lane)
+            constexpr uint32_t id_s = mma_idesc(BF16, kRows, kKeys, 0), id_o = mma_idesc(BF16, kRows, kHeadDim, 1);
+            const uint32_t q_at = smem_desc(su32(base), 16), k_at = smem_desc(su32(ring), 16), v_at = smem_desc(su32(ring), kChunk / 2);
+            const bool leader = elect_one();
+            bool ok = true;
+            auto wait = [&](uint64_t* b, int parity) { ok = __all_sync(0xffffffffu, ok && bar_wait(b, parity & 1, &sm->abort)); };
+            // A chunk's slot is free once the products issued so far, the last that read it among them, are done.
+            auto scores = [&](int w, int i) {
+                fence_after();
+                if (leader) {
+                    const int first = i * kTileChunks;
+                    const bool last = w == 1 || i >= nt1;
+#pragma unroll
+                    for (int c = 0; c < kKChunks; ++c) {
+                        const uint32_t a = q_at + (w * kKChunks + c) * (kChunk / 16), b = k_at + (first + c) % kSlots * (kChunk / 16);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) mma_ss(tmem + kColS + 128 * w, a + 2 * k, b + 2 * k, id_s, (c | k) ? 1u : 0u);
+                        if (last) mma_commit(&sm->free[(first + c) % kSlots]);
+                    }
+                    mma_commit(&sm->s_full[w]);
+                }
+                __syncwarp();
             };
             auto values = [&](int w, int i) {
-                if (!upto(i * kTileChunks + kTileChunks - 1)) return;
-                ok = bar_wait(&sm->p_full[w], i & 1, &sm->abort);
-                if (!ok) return;
-                fence_after();
+                const int first = i * kTileChunks + kKChunks;
+                const bool last = w == 1 || i >= nt1;
 #pragma unroll
                 for (int c = 0; c < kVChunks; ++c) {
-                    const uint32_t b = ring_at + (i * kTileChunks + kKChunks + c) % kSlots * kChunk;
+                    wait(&sm->p_full[w][c], i);
+                    if (!ok) return;
+                    fence_after();
+                    if (leader) {
+                        const uint32_t b = v_at + (first + c) % kSlots * (kChunk / 16);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_ts(tmem + kColO + 128 * w, tmem + kColS + 128 * w + 32 * c + 8 * k, smem_desc(b + 2048 * k, kChunk / 2, 1024), id_o,
-                               (i | c | k) ? 1u : 0u);
+                        for (int k = 0; k < 4; ++k)
+                            mma_ts(tmem + kColO + 128 * w, tmem + kColS + 128 * w + 32 * c + 8 * k, b + 128 * k, id_o, (c | k) ? 1u : i);
+                        if (last) mma_commit(&sm->free[(first + c) % kSlots]);
+                        if (c == kVChunks - 1 && i == (w ? nt1 : nt0) - 1) mma_commit(&sm->o_full[w]);
+                    }
+                    __syncwarp();
                 }
-                if (i == (w ? nt1 : nt0) - 1) mma_commit(&sm->o_full[w]);
             };
-            auto release = [&](int i, int first, int count) {  // once the products so far are done
-                for (int c = first; c < first + count; ++c) mma_commit(&sm->free[(i * kTileChunks + c) % kSlots]);
-            };
+            if (nt > 0) wait(&sm->k_full[0], 0);
             for (int w = 0; w < 2; ++w)
                 if (ok && (w ? nt1 : nt0) > 0) {
-                    ok = bar_wait(&sm->q_full[w], 0, &sm->abort);
+                    wait(&sm->q_full[w], 0);
                     if (ok) scores(w, 0);
                 }
-            if (ok) release(0, 0, kKChunks);
+            // The waits for copies come while the products ahead of them run.
             for (int i = 0; ok && i < nt; ++i) {
+                wait(&sm->v_full[i & 1], i >> 1);
+                if (i + 1 < nt) wait(&sm->k_full[(i + 1) & 1], (i + 1) >> 1);
                 for (int w = 0; ok && w < 2; ++w) {
                     const int n = w ? nt1 : nt0;
                     if (i < n) values(w, i);
-                    if (w == 1 && ok) release(i, kKChunks, kVChunks);
                     if (ok && i + 1 < n) scores(w, i + 1);
                 }
-                if (ok && i + 1 < nt) release(i + 1, 0, kKChunks);
             }
             // whatever happened, every product issued here is done before the columns are freed
-            mma_commit(&sm->drain);
+            if (leader) mma_commit(&sm->drain);
             bar_drain(&sm->drain, 0);
         }
-        __syncwarp();
-    } else if (some) {
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
         // ------------------------------------------------------------ softmax, a row a thread
         const int w = warp >> 2, row = row0 + w * kRows + (tid & (kRows - 1));  // of the prompt
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16, s_at = tmem + lanes + kColS + 128 * w, o_at = tmem + lanes + kColO + 128 * w;
@@ -277,11 +317,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
             const int here = seen - i * kKeys;  // keys of this tile that the row sees
             if ((i + 1) * kKeys > lk) {         // values behind the prompt's end become zeros
                 const int live = lk - i * kKeys;
+                ok = bar_wait(&sm->v_full[i & 1], (i >> 1) & 1, &sm->abort);
                 for (int c = 0; c < kVChunks && ok; ++c) {
-                    const int g = i * kTileChunks + kKChunks + c;
-                    ok = bar_wait(&sm->full[g % kSlots], (g / kSlots) & 1, &sm->abort);
-                    uint8_t* at = ring + g % kSlots * kChunk;
-                    for (int u = tid & (kRows - 1); ok && u < (int)kChunk / 16; u += kRows)
+                    uint8_t* at = ring + (i * kTileChunks + kKChunks + c) % kSlots * kChunk;
+                    for (int u = tid & (kRows - 1); u < (int)kChunk / 16; u += kRows)
                         if (64 * c + ((u >> 3) & 63) >= live) reinterpret_cast<uint4*>(at)[u] = make_uint4(0, 0, 0, 0);
                 }
                 fence_async_smem();
@@ -290,21 +329,28 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
             if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
             fence_after();
             uint32_t s[128];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_load32(s + 32 * c, s_at + 32 * c);
-            tmem_wait_ld();
-            if (__any_sync(0xffffffffu, here < kKeys)) {
-#pragma unroll
-                for (int j = 0; j < 128; ++j)
-                    if (j >= here) s[j] = __float_as_uint(-INFINITY);
-            }
             float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            const bool masked = __any_sync(0xffffffffu, here < kKeys);
 #pragma unroll
-            for (int j = 0; j < 128; j += 8)
+            for (int c = 0; c < 2; ++c) tmem_load32(s + 32 * c, s_at + 32 * c);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    top[k] = fmaxf(fmaxf(top[k], __uint_as_float(s[j + 2 * k])), __uint_as_float(s[j + 2 * k + 1]));
-            const float best = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
+            for (int half = 0; half < 2; ++half) {  // the second half is on its way while the first is looked through
+                tmem_wait_ld();
+                if (half == 0) {
+#pragma unroll
+                    for (int c = 2; c < 4; ++c) tmem_load32(s + 32 * c, s_at + 32 * c);
+                }
+                if (masked) {
+#pragma unroll
+                    for (int j = 64 * half; j < 64 * half + 64; ++j)
+                        if (j >= here) s[j] = __float_as_uint(-INFINITY);
+                }
+#pragma unroll
+                for (int j = 64 * half; j < 64 * half + 64; j += 8)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) top[k] = max3(top[k], __uint_as_float(s[j + 2 * k]), __uint_as_float(s[j + 2 * k + 1]));
+            }
+            const float best = max3(fmaxf(top[0], top[1]), top[2], top[3]) * scale;
             const bool move = best > m + kRescaleLog2 || (m == -INFINITY && best > -INFINITY);
             if (i > 0 && __any_sync(0xffffffffu, move)) {
                 // O holds tiles 0 .. i - 1: their products ended before these scores did
@@ -321,25 +367,24 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
                 l *= f;
             }
             if (move) m = best;
-            const float from = m == -INFINITY ? 0.f : m;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            const float from = m == -INFINITY ? 0.f : -m;
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 uint32_t p[32];
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
-                    const float x = ex2(fmaf(__uint_as_float(s[64 * c + 2 * j]), scale, -from));
-                    const float y = ex2(fmaf(__uint_as_float(s[64 * c + 2 * j + 1]), scale, -from));
-                    sum[2 * (j & 1)] += x;
-                    sum[2 * (j & 1) + 1] += y;
-                    p[j] = pack<BF16>(x, y);
+                    float2 x = fma2(make_float2(__uint_as_float(s[64 * c + 2 * j]), __uint_as_float(s[64 * c + 2 * j + 1])), scale, from);
+                    x = make_float2(ex2(x.x), ex2(x.y));
+                    sum[j & 1] = add2(sum[j & 1], x);
+                    p[j] = pack<BF16>(x.x, x.y);
                 }
                 tmem_store32(s_at + 32 * c, p);
+                tmem_wait_st();
+                fence_before();
+                bar_arrive(&sm->p_full[w][c]);
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            tmem_wait_st();
-            fence_before();
-            bar_arrive(&sm->p_full[w]);
+            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         }
         if (ok && n > 0) ok = bar_wait(&sm->o_full[w], 0, &sm->abort);
         ok = __all_sync(0xffffffffu, ok);
@@ -374,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
     __syncthreads();
     if (warp == kMmaWarp) {
         fence_after();
-        tmem_free<kTmemCols>(tmem);
+        tmem_free<kTmemCols>(sm->tmem);
     }
 }
 
@@ -413,8 +458,14 @@ cudaError_t launch_attend_prompts(cudaStream_t stream, bool bf16, const PromptAt
     if (device >= PerDevice<Ready>::kDevices) return cudaErrorInvalidDevice;
     const Ready* ready;
     e = (cudaError_t)devices.get(device, [](Ready*) {
-        const cudaError_t x = cudaFuncSetAttribute(prompt_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
-        return (int)(x != cudaSuccess ? x : cudaFuncSetAttribute(prompt_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes));
+        for (auto kernel : {prompt_kernel<true>, prompt_kernel<false>}) {
+            cudaFuncAttributes at;
+            cudaError_t x = cudaFuncGetAttributes(&at, kernel);
+            if (x == cudaSuccess && at.numRegs < kLaunchRegs) x = cudaErrorInvalidKernelImage;  // the warps' split of them would not add up
+            if (x == cudaSuccess) x = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+            if (x != cudaSuccess) return (int)x;
+        }
+        return 0;
     }, &ready);
     if (e != cudaSuccess) return e;
     Maps maps;

@@ -13,6 +13,14 @@ namespace hs {
 #ifdef __CUDACC__
 __device__ __forceinline__ uint32_t su32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
+// One lane of a converged warp, the same one each time. A warp that issues tensor instructions runs its
+// loops as a whole and only issues from one lane: the operands then stay in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(one));
+    return one != 0;
+}
+
 // ---------------------------------------------------------------- mbarriers
 __device__ __forceinline__ void bar_init(uint64_t* b, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(su32(b)), "r"(count) : "memory");
@@ -62,24 +70,25 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
 }
 
 // ---------------------------------------------------------------- tcgen05
-// A shared-memory operand of rows of 128 swizzled bytes.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-    return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
-           ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) /* descriptor version */ |
-           (2ull << 61) /* 128-byte swizzle */;
-}
+// A shared-memory operand of rows of 128 swizzled bytes: the low word of its descriptor (where it is,
+// and `lbo`, the bytes between its 64-element columns if it is read across its rows), to which bytes / 16
+// may be added, and the high word (1024 bytes from eight rows to the next eight).
+__device__ __forceinline__ uint32_t smem_desc(uint32_t addr, uint32_t lbo) { return (addr >> 4 & 0x3FFFu) | lbo >> 4 << 16; }
+constexpr uint32_t kDescHigh = 1024u >> 4 | 1u << 14 /* descriptor version */ | 2u << 29 /* 128-byte swizzle */;
 // kind::f16: D f32, A and B of one 16-bit type, A K-major, B K- or MN-major.
 __host__ __device__ constexpr uint32_t mma_idesc(bool bf16, int m, int n, int b_mn) {
     return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | ((uint32_t)b_mn << 16) | ((uint32_t)(n >> 3) << 17) |
            ((uint32_t)(m >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
-    asm volatile("{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }"
-                 ::"r"(d), "l"(a), "l"(b), "r"(id), "r"(acc) : "memory");
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc) {
+    asm volatile("{ .reg .pred p; .reg .b64 x, y; setp.ne.b32 p, %4, 0; mov.b64 x, {%1, %5}; mov.b64 y, {%2, %5};"
+                 " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p; }"
+                 ::"r"(d), "r"(a), "r"(b), "r"(id), "r"(acc), "r"(kDescHigh) : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t id, uint32_t acc) {
-    asm volatile("{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }"
-                 ::"r"(d), "r"(a_tmem), "l"(b), "r"(id), "r"(acc) : "memory");
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b, uint32_t id, uint32_t acc) {
+    asm volatile("{ .reg .pred p; .reg .b64 y; setp.ne.b32 p, %4, 0; mov.b64 y, {%2, %5};"
+                 " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p; }"
+                 ::"r"(d), "r"(a_tmem), "r"(b), "r"(id), "r"(acc), "r"(kDescHigh) : "memory");
 }
 __device__ __forceinline__ void mma_commit(uint64_t* b) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(su32(b)) : "memory");
