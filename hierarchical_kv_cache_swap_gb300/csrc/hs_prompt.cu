@@ -65,6 +65,14 @@ struct Smem {  // beyond Q and the ring
 };
 constexpr uint32_t kSmemBytes = 1024 + kQBytes + kSlots * kChunk + sizeof(Smem);
 
+// The CTAs' order: groups of `heads` heads; within one the prompts' tiles, those with the most keys
+// first, and for each tile the heads. The long tiles of all heads of a group so start before its short
+// ones, which then fill the SMs that finish early, while the CTAs that run at the same time share the
+// keys and values of a few heads in L2.
+struct Order {
+    uint32_t heads, per_group;  // per_group: heads * tiles
+};
+
 struct Maps {
     CUtensorMap q, k, r, v;
 };
@@ -151,16 +159,19 @@ __device__ void find_tile(const PromptAttention& A, int at, Smem* sm) {
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttention A, const __grid_constant__ Maps maps) {
+__global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttention A, const Order order, const __grid_constant__ Maps maps) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* ring = base + kQBytes;
     Smem* sm = reinterpret_cast<Smem*>(ring + kSlots * kChunk);
-    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, h = blockIdx.y;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    const uint32_t group = blockIdx.x / order.per_group, in = blockIdx.x - group * order.per_group;
+    const uint32_t heads = min(order.heads, A.H - group * order.heads);
+    const int h = (int)(group * order.heads + in % heads);
 
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (warp == 0) {
-        find_tile(A, blockIdx.x, sm);
+        find_tile(A, (int)(in / heads), sm);
     } else if (tid == 32) {
         for (int i = 0; i < kSlots; ++i) bar_init(&sm->free[i], 1);
         for (int w = 0; w < 2; ++w) {
@@ -482,7 +493,15 @@ cudaError_t launch_attend_prompts(cudaStream_t stream, bool bf16, const PromptAt
         return cudaErrorInvalidValue;
     // a CTA for every 256 rows of a prompt, at most one more than full ones for each prompt
     const int64_t tiles = a.q_rows / kTileRows + a.B;
-    return launch_dependent(stream, dim3((unsigned)tiles, (unsigned)a.H), kThreads, kSmemBytes, bf16 ? prompt_kernel<true> : prompt_kernel<false>, a, maps);
+    // as many heads to a group as keep their keys and values in 64 MB, half of L2, and at most 16
+    constexpr int64_t kShared = 64 << 20;
+    const int64_t fit = kShared / ((a.k_rows > 0 ? a.k_rows : 1) * 4 * kHeadDim), heads = fit < 1 ? 1 : fit < 16 ? fit : 16;
+    Order order;
+    order.heads = (uint32_t)(heads < a.H ? heads : a.H);
+    if (tiles * a.H > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    order.per_group = (uint32_t)(order.heads * tiles);
+    return launch_dependent(stream, dim3((unsigned)(tiles * a.H)), kThreads, kSmemBytes, bf16 ? prompt_kernel<true> : prompt_kernel<false>, a, order,
+                            maps);
 }
 
 }  // namespace hs
