@@ -43,8 +43,10 @@ constexpr int kQDims = kHeadDim + kRope;        // 192
 constexpr uint32_t kChunk = 16384;              // 128 rows x 64 dimensions, or (V) 64 keys x 128
 constexpr int kSlots = 8;                       // of the ring
 constexpr int kKChunks = kQDims / 64, kVChunks = kKeys / 64, kTileChunks = kKChunks + kVChunks;
+// What of a key tile lands together: the first chunk of keys, the two others, each chunk of values.
+enum { kKeys0, kKeys12, kValues0, kValues1, kParts };
 constexpr uint32_t kQBytes = 2 * kKChunks * kChunk;
-constexpr int kSoftWarps = 8, kMmaWarp = kSoftWarps, kCopyWarp = kMmaWarp + 1;
+constexpr int kSoftWarps = 8, kMmaWarp = kSoftWarps /* and the next, one for each row tile */, kCopyWarp = kMmaWarp + 2;
 // Three warpgroups, launched with kLaunchRegs registers a thread; the two softmax ones take what the
 // third, of the issuing threads, gives up: a row of scores stays in registers.
 constexpr int kThreads = 384, kLaunchRegs = 168, kSoftRegs = 216, kIssueRegs = 72;
@@ -54,9 +56,8 @@ constexpr uint32_t kColS = 0, kColO = 256;      // row tile w: scores (P over th
 constexpr float kRescaleLog2 = 8.f;
 
 struct Smem {  // beyond Q and the ring
-    uint64_t k_full[2], v_full[2];  // a key tile's keys and values, by its parity
-    uint64_t free[kSlots];
-    uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2], drain;  // by row tile; P by halves of the keys
+    uint64_t full[2][kParts], free[kSlots];  // full: by the parity of the key tile
+    uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2], turn[2], drain[2];  // by row tile; P by halves of the keys
     uint32_t tmem;
     volatile int abort;
     int seq, tile;  // this CTA's prompt and 256-row tile of it (seq < 0: none)
@@ -173,17 +174,17 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
     if (warp == 0) {
         find_tile(A, (int)(in / heads), sm);
     } else if (tid == 32) {
-        for (int i = 0; i < kSlots; ++i) bar_init(&sm->free[i], 1);
+        for (int i = 0; i < kSlots; ++i) bar_init(&sm->free[i], 2);
+        for (int i = 0; i < 2 * kParts; ++i) bar_init(&sm->full[0][i], 1);
         for (int w = 0; w < 2; ++w) {
-            bar_init(&sm->k_full[w], 1);
-            bar_init(&sm->v_full[w], 1);
             bar_init(&sm->q_full[w], 1);
             bar_init(&sm->s_full[w], 1);
             bar_init(&sm->p_full[w][0], kRows);
             bar_init(&sm->p_full[w][1], kRows);
             bar_init(&sm->o_full[w], 1);
+            bar_init(&sm->turn[w], 1);
+            bar_init(&sm->drain[w], 1);
         }
-        bar_init(&sm->drain, 1);
         sm->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -217,102 +218,129 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
                         for (int c = 0; c < kKChunks; ++c)
                             tma_load_3d(su32(base) + (w * kKChunks + c) * kChunk, &maps.q, 64 * c, h, (int)(q_row + w * kRows), &sm->q_full[w]);
                     }
-                int g = 0, tiles = 0;
+                int g = 0;
                 bool ok = true;
-                auto open = [&] {  // the next slot, once it is free
-                    ok = ok && (g < kSlots || bar_wait(&sm->free[g % kSlots], (g / kSlots - 1) & 1, &sm->abort));
-                    return su32(ring) + g++ % kSlots * kChunk;
-                };
-                for (; ok && tiles < nt; ++tiles) {
-                    const int key = (int)sm->k0 + tiles * kKeys;
-                    uint64_t *const k_full = &sm->k_full[tiles & 1], *const v_full = &sm->v_full[tiles & 1];
-                    uint32_t to = open();
-                    if (!ok) break;
-                    bar_expect_tx(k_full, kKChunks * kChunk);
-                    tma_load_3d(to, &maps.k, 0, h, key, k_full);
-                    if (to = open(); ok) tma_load_3d(to, &maps.k, 64, h, key, k_full);
-                    if (to = open(); ok) tma_load_2d(to, &maps.r, 0, key, k_full);
-                    to = open();
-                    if (!ok) break;
-                    bar_expect_tx(v_full, kVChunks * kChunk);
-                    tma_load_3d(to, &maps.v, 0, h, key, v_full);
-                    tma_load_3d(to + kChunk / 2, &maps.v, 64, h, key, v_full);
-                    if (to = open(); ok) {
-                        tma_load_3d(to, &maps.v, 0, h, key + 64, v_full);
-                        tma_load_3d(to + kChunk / 2, &maps.v, 64, h, key + 64, v_full);
+                for (int i = 0; ok && i < nt; ++i) {
+                    const int key = (int)sm->k0 + i * kKeys;
+#pragma unroll
+                    for (int c = 0; c < kTileChunks; ++c) {
+                        const int slot = g % kSlots, part = c < 2 ? c : c - 1;
+                        uint64_t* const full = &sm->full[i & 1][part];
+                        if (g >= kSlots && !bar_wait(&sm->free[slot], (g / kSlots - 1) & 1, &sm->abort)) { ok = false; break; }
+                        ++g;
+                        if (c != 2) bar_expect_tx(full, part == kKeys12 ? 2 * kChunk : kChunk);
+                        const uint32_t to = su32(ring) + slot * kChunk;
+                        if (c < kHeadDim / 64) {
+                            tma_load_3d(to, &maps.k, 64 * c, h, key, full);
+                        } else if (c < kKChunks) {
+                            tma_load_2d(to, &maps.r, 0, key, full);
+                        } else {
+                            tma_load_3d(to, &maps.v, 0, h, key + 64 * (c - kKChunks), full);
+                            tma_load_3d(to + kChunk / 2, &maps.v, 64, h, key + 64 * (c - kKChunks), full);
+                        }
                     }
                 }
                 // no copy may land after the CTA's end: the last tiles', and the queries
-                for (int i = max(tiles - 2, 0); i < tiles; ++i) {
-                    bar_drain(&sm->k_full[i & 1], (i >> 1) & 1);
-                    bar_drain(&sm->v_full[i & 1], (i >> 1) & 1);
-                }
+                for (int i = max(g / kTileChunks - 2, 0); i * kTileChunks < g; ++i)
+                    for (int part = 0; part < kParts; ++part)
+                        if (g > i * kTileChunks + (part < 2 ? part : part + 1)) bar_drain(&sm->full[i & 1][part], (i >> 1) & 1);
                 for (int w = 0; w < 2; ++w)
                     if ((w ? nt1 : nt0) > 0) bar_drain(&sm->q_full[w], 0);
             }
             __syncwarp();
-        } else if (warp == kMmaWarp) {
-            // ------------------------------------------------------------ products (issued by one lane)
+        } else if (warp < kCopyWarp) {
+            // ------------------------------------------------------------ a row tile's products (issued by one lane)
             constexpr uint32_t id_s = mma_idesc(BF16, kRows, kKeys, 0), id_o = mma_idesc(BF16, kRows, kHeadDim, 1);
-            const uint32_t q_at = smem_desc(su32(base), 16), k_at = smem_desc(su32(ring), 16), v_at = smem_desc(su32(ring), kChunk / 2);
+            const int w = warp - kMmaWarp, n = w ? nt1 : nt0;
+            const uint32_t q_at = smem_desc(su32(base), 16) + w * kKChunks * (kChunk / 16), k_at = smem_desc(su32(ring), 16),
+                           v_at = smem_desc(su32(ring), kChunk / 2), s_col = tmem + kColS + 128 * w, o_col = tmem + kColO + 128 * w;
             const bool leader = elect_one();
             bool ok = true;
             auto wait = [&](uint64_t* b, int parity) { ok = __all_sync(0xffffffffu, ok && bar_wait(b, parity & 1, &sm->abort)); };
-            // A chunk's slot is free once the products issued so far, the last that read it among them, are done.
-            auto scores = [&](int w, int i) {
-                fence_after();
-                if (leader) {
-                    const int first = i * kTileChunks;
-                    const bool last = w == 1 || i >= nt1;
+            auto landed = [&](int i, int part) { wait(&sm->full[i & 1][part], i >> 1); };
+            // The products of one lane; a chunk's slot is free once both tiles' that read it are done.
+            auto scores = [&](int i, int from, int to) {
 #pragma unroll
-                    for (int c = 0; c < kKChunks; ++c) {
-                        const uint32_t a = q_at + (w * kKChunks + c) * (kChunk / 16), b = k_at + (first + c) % kSlots * (kChunk / 16);
+                for (int c = from; c < to; ++c) {
+                    const int slot = (i * kTileChunks + c) % kSlots;
+                    const uint32_t a = q_at + c * (kChunk / 16), b = k_at + slot * (kChunk / 16);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) mma_ss(tmem + kColS + 128 * w, a + 2 * k, b + 2 * k, id_s, (c | k) ? 1u : 0u);
-                        if (last) mma_commit(&sm->free[(first + c) % kSlots]);
-                    }
-                    mma_commit(&sm->s_full[w]);
+                    for (int k = 0; k < 4; ++k) mma_ss(s_col, a + 2 * k, b + 2 * k, id_s, (c | k) ? 1u : 0u);
+                    mma_commit(&sm->free[slot]);
                 }
-                __syncwarp();
+                if (to == kKChunks) mma_commit(&sm->s_full[w]);
             };
-            auto values = [&](int w, int i) {
-                const int first = i * kTileChunks + kKChunks;
-                const bool last = w == 1 || i >= nt1;
+            auto values = [&](int i, int c) {
+                const int slot = (i * kTileChunks + kKChunks + c) % kSlots;
+                const uint32_t b = v_at + slot * (kChunk / 16);
 #pragma unroll
-                for (int c = 0; c < kVChunks; ++c) {
-                    wait(&sm->p_full[w][c], i);
-                    if (!ok) return;
+                for (int k = 0; k < 4; ++k) mma_ts(o_col, s_col + 32 * c + 8 * k, b + 128 * k, id_o, (c | k) ? 1u : i);
+                mma_commit(&sm->free[slot]);
+            };
+            auto skip = [&](int i, int part) {  // a part that only the other tile reads
+                landed(i, part);
+                if (!ok || !leader) return;
+                const int g = i * kTileChunks + (part < 2 ? part : part + 1);
+                bar_arrive(&sm->free[g % kSlots]);
+                if (part == kKeys12) bar_arrive(&sm->free[(g + 1) % kSlots]);
+            };
+            // The tiles take turns, each with the products of one key tile's values and of the next one's
+            // scores: interleaved, both tiles' would end together and leave the tensor core idle while
+            // both softmaxes run (4050 cycles a key tile instead of 2900).
+            int turns = 0;
+            auto take = [&] {
+                if (w == 1 || turns > 0) wait(&sm->turn[w], turns - (w == 0));
+                ++turns;
+            };
+            auto give = [&] { if (ok && leader) bar_arrive(&sm->turn[1 - w]); };
+            if (n > 0) {
+                wait(&sm->q_full[w], 0);
+                landed(0, kKeys0);
+                landed(0, kKeys12);
+            }
+            if (nt > 0) {
+                take();
+                fence_after();
+                if (ok && n > 0 && leader) scores(0, 0, kKChunks);
+                __syncwarp();
+                give();
+                if (n == 0) skip(0, kKeys0), skip(0, kKeys12);
+            }
+            for (int i = 0; ok && i < nt; ++i) {
+                const bool next = i + 1 < n;
+                if (i < n) {  // what has had the time to land is waited for before the turn
+                    landed(i, kValues0);
+                    landed(i, kValues1);
+                    if (next) landed(i + 1, kKeys0);
+                    wait(&sm->p_full[w][0], i);
+                }
+                take();
+                if (ok && i < n) {
                     fence_after();
-                    if (leader) {
-                        const uint32_t b = v_at + (first + c) % kSlots * (kChunk / 16);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_ts(tmem + kColO + 128 * w, tmem + kColS + 128 * w + 32 * c + 8 * k, b + 128 * k, id_o, (c | k) ? 1u : i);
-                        if (last) mma_commit(&sm->free[(first + c) % kSlots]);
-                        if (c == kVChunks - 1 && i == (w ? nt1 : nt0) - 1) mma_commit(&sm->o_full[w]);
+                    if (leader) values(i, 0);
+                    __syncwarp();
+                    wait(&sm->p_full[w][1], i);
+                    fence_after();
+                    if (ok && leader) {
+                        values(i, 1);
+                        if (next) scores(i + 1, 0, 1);
+                        else mma_commit(&sm->o_full[w]);
                     }
                     __syncwarp();
+                    if (next) {
+                        landed(i + 1, kKeys12);
+                        fence_after();
+                        if (ok && leader) scores(i + 1, 1, kKChunks);
+                        __syncwarp();
+                    }
                 }
-            };
-            if (nt > 0) wait(&sm->k_full[0], 0);
-            for (int w = 0; w < 2; ++w)
-                if (ok && (w ? nt1 : nt0) > 0) {
-                    wait(&sm->q_full[w], 0);
-                    if (ok) scores(w, 0);
-                }
-            // The waits for copies come while the products ahead of them run.
-            for (int i = 0; ok && i < nt; ++i) {
-                wait(&sm->v_full[i & 1], i >> 1);
-                if (i + 1 < nt) wait(&sm->k_full[(i + 1) & 1], (i + 1) >> 1);
-                for (int w = 0; ok && w < 2; ++w) {
-                    const int n = w ? nt1 : nt0;
-                    if (i < n) values(w, i);
-                    if (ok && i + 1 < n) scores(w, i + 1);
-                }
+                give();
+                if (i >= n) skip(i, kValues0), skip(i, kValues1);
+                if (!next && i + 1 < nt) skip(i + 1, kKeys0), skip(i + 1, kKeys12);
             }
             // whatever happened, every product issued here is done before the columns are freed
-            if (leader) mma_commit(&sm->drain);
-            bar_drain(&sm->drain, 0);
+            if (leader) mma_commit(&sm->drain[w]);
+            bar_drain(&sm->drain[w], 0);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
@@ -328,9 +356,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
             const int here = seen - i * kKeys;  // keys of this tile that the row sees
             if ((i + 1) * kKeys > lk) {         // values behind the prompt's end become zeros
                 const int live = lk - i * kKeys;
-                ok = bar_wait(&sm->v_full[i & 1], (i >> 1) & 1, &sm->abort);
                 for (int c = 0; c < kVChunks && ok; ++c) {
-                    uint8_t* at = ring + (i * kTileChunks + kKChunks + c) % kSlots * kChunk;
+                    const int g = i * kTileChunks + kKChunks + c;
+                    ok = bar_wait(&sm->full[i & 1][kValues0 + c], (i >> 1) & 1, &sm->abort);
+                    if (!ok) break;
+                    uint8_t* at = ring + g % kSlots * kChunk;
                     for (int u = tid & (kRows - 1); u < (int)kChunk / 16; u += kRows)
                         if (64 * c + ((u >> 3) & 63) >= live) reinterpret_cast<uint4*>(at)[u] = make_uint4(0, 0, 0, 0);
                 }

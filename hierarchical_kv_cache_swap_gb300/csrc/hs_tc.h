@@ -31,10 +31,13 @@ __device__ __forceinline__ void bar_arrive(uint64_t* b) {
 __device__ __forceinline__ void bar_expect_tx(uint64_t* b, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(su32(b)), "r"(bytes) : "memory");
 }
+// Whether the phase of `parity` is complete, now or within about kNapNs: the thread sleeps meanwhile.
+// Short naps, and polls, take issue slots from the thread that feeds the tensor core.
+constexpr uint32_t kNapNs = 1000000;
 __device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t parity) {
     uint32_t ok;
-    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-                 : "=r"(ok) : "r"(su32(b)), "r"(parity) : "memory");
+    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(ok) : "r"(su32(b)), "r"(parity), "r"(kNapNs) : "memory");
     return ok != 0;
 }
 // Waits for the phase of `parity` to complete. False, with *abort set, once this wait has lasted
@@ -54,9 +57,8 @@ __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, volatile 
 }
 // The same wait whatever *abort says: for what must land before the CTA ends.
 __device__ __forceinline__ void bar_drain(uint64_t* b, uint32_t parity) {
-    const uint64_t by = global_ns() + kWaitNs;
-    while (!bar_try(b, parity) && global_ns() <= by) {
-    }
+    int ignored = 0;
+    bar_wait(b, parity, &ignored);
 }
 
 // ---------------------------------------------------------------- copies by tensor maps
@@ -67,6 +69,12 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
     asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
                  ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(su32(bar)) : "memory");
+}
+
+// The boxes of such copies brought into L2.
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int x, int y, int z) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];"
+                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z) : "memory");
 }
 
 // ---------------------------------------------------------------- tcgen05
