@@ -46,7 +46,8 @@ constexpr int kKChunks = kQDims / 64, kVChunks = kKeys / 64, kTileChunks = kKChu
 // What of a key tile lands together: the first chunk of keys, the two others, each chunk of values.
 enum { kKeys0, kKeys12, kValues0, kValues1, kParts };
 constexpr uint32_t kQBytes = 2 * kKChunks * kChunk;
-constexpr int kSoftWarps = 8, kMmaWarp = kSoftWarps /* and the next, one for each row tile */, kCopyWarp = kMmaWarp + 2;
+constexpr int kSoftWarps = 8, kMmaWarp = kSoftWarps /* and the next, one for each row tile */, kCopyWarp = kMmaWarp + 2,
+              kItemWarp = kCopyWarp + 1;
 // Three warpgroups, launched with kLaunchRegs registers a thread; the two softmax ones take what the
 // third, of the issuing threads, gives up: a row of scores stays in registers.
 constexpr int kThreads = 384, kLaunchRegs = 168, kSoftRegs = 216, kIssueRegs = 72;
@@ -55,14 +56,22 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;      // row tile w: scores (P over their first half) at + 128 w
 constexpr float kRescaleLog2 = 8.f;
 
+// What a CTA works on: 256 rows of a prompt for one head.
+struct Item {
+    int64_t q0, k0;  // the prompt's first row and first key
+    int lq, lk;      // its rows and keys; lq = 0: there is no further item
+    int row0, h;
+};
+
 struct Smem {  // beyond Q and the ring
-    uint64_t full[2][kParts], free[kSlots];  // full: by the parity of the key tile
-    uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2], turn[2], drain[2];  // by row tile; P by halves of the keys
+    __align__(16) uint32_t answer[4];                    // of the launch control
+    uint64_t answered, wanted;                           // an answer is there; the next item is wanted
+    uint64_t item_full[2], item_free[2];
+    uint64_t full[2][kParts], free[kSlots];              // full: by the parity of the key tile
+    uint64_t q_full[2], q_free[2], s_full[2], p_full[2][2], o_full[2], turn[2], drain[2];  // by row tile; P by halves of the keys
+    Item item[2];
     uint32_t tmem;
     volatile int abort;
-    int seq, tile;  // this CTA's prompt and 256-row tile of it (seq < 0: none)
-    int64_t q0, k0;
-    int lq, lk;
 };
 constexpr uint32_t kSmemBytes = 1024 + kQBytes + kSlots * kChunk + sizeof(Smem);
 
@@ -72,6 +81,7 @@ constexpr uint32_t kSmemBytes = 1024 + kQBytes + kSlots * kChunk + sizeof(Smem);
 // keys and values of a few heads in L2.
 struct Order {
     uint32_t heads, per_group;  // per_group: heads * tiles
+    bool wide;                  // rows of o are 32-byte aligned
 };
 
 struct Maps {
@@ -116,10 +126,10 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// Finds the prompt and the tile of it that CTA `at` of the prompts' tiles takes, by one warp: 32
+// Finds the prompt and the tile of it that the `at`-th of the prompts' tiles is, by one warp: 32
 // prompts at a time, their tiles counted and added up over the lanes. A prompt whose bounds are not in
-// order, or not within the rows there are, has no tiles.
-__device__ void find_tile(const PromptAttention& A, int at, Smem* sm) {
+// order, or not within the rows there are, has no tiles. False: there are not so many.
+__device__ bool find_tile(const PromptAttention& A, int at, Item* item) {
     const int lane = threadIdx.x & 31;
     int64_t before = 0;
     for (int b0 = 0; b0 < A.B; b0 += 32) {
@@ -142,21 +152,41 @@ __device__ void find_tile(const PromptAttention& A, int at, Smem* sm) {
         }
         const bool mine = at >= before + upto - tiles && at < before + upto;
         if (mine) {
-            sm->seq = b;
-            sm->tile = (int)(before + upto - 1 - at);  // the last rows, which see the most keys, first
-            sm->q0 = q0;
-            sm->k0 = k0;
-            sm->lq = (int)(q1 - q0);
-            sm->lk = (int)(k1 - k0);
+            item->q0 = q0;
+            item->k0 = k0;
+            item->lq = (int)(q1 - q0);
+            item->lk = (int)(k1 - k0);
+            item->row0 = (int)(before + upto - 1 - at) * kTileRows;  // the last rows, which see the most keys, first
         }
-        if (__any_sync(0xffffffffu, mine)) return;
+        if (__any_sync(0xffffffffu, mine)) return true;
         before += __shfl_sync(0xffffffffu, upto, 31);
     }
-    if (lane == 0) {
-        sm->seq = -1;
-        sm->tile = sm->lq = sm->lk = 0;
-        sm->q0 = sm->k0 = 0;
-    }
+    return false;
+}
+
+// The key tiles that row tile w of an item sees: row i sees the keys below i + 1 + lk - lq (causal), or all.
+__device__ __forceinline__ int key_tiles(const Item& it, int w, int causal) {
+    const int first = it.row0 + w * kRows;
+    if (first >= it.lq) return 0;
+    const int last = min(first + kRows, it.lq);
+    const int seen = causal ? min(max(last + it.lk - it.lq, 0), it.lk) : it.lk;
+    return (seen + kKeys - 1) / kKeys;
+}
+
+// Asks for the index of a CTA of this grid that has not begun, which then never will: its work is this
+// CTA's. The answer lands at `to`, counted on `bar`.
+__device__ __forceinline__ void ask_for_block(uint32_t* to, uint64_t* bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+                 ::"r"(su32(to)), "r"(su32(bar)) : "memory");
+}
+// Whether there was one, and its index.
+__device__ __forceinline__ bool block_given(const uint32_t* from, uint32_t* index) {
+    uint32_t ok, x;
+    asm volatile("{ .reg .pred p; .reg .b128 r; ld.shared.b128 r, [%2]; clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;"
+                 " selp.u32 %0, 1, 0, p; mov.u32 %1, 0; @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r; }"
+                 : "=r"(ok), "=r"(x) : "r"(su32(from)) : "memory");
+    *index = x;
+    return ok != 0;
 }
 
 template <bool BF16>
@@ -166,18 +196,18 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
     uint8_t* ring = base + kQBytes;
     Smem* sm = reinterpret_cast<Smem*>(ring + kSlots * kChunk);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-    const uint32_t group = blockIdx.x / order.per_group, in = blockIdx.x - group * order.per_group;
-    const uint32_t heads = min(order.heads, A.H - group * order.heads);
-    const int h = (int)(group * order.heads + in % heads);
 
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (warp == 0) {
-        find_tile(A, (int)(in / heads), sm);
-    } else if (tid == 32) {
+    if (tid == 0) {
+        bar_init(&sm->answered, 1);
+        bar_init(&sm->wanted, 1);
         for (int i = 0; i < kSlots; ++i) bar_init(&sm->free[i], 2);
         for (int i = 0; i < 2 * kParts; ++i) bar_init(&sm->full[0][i], 1);
         for (int w = 0; w < 2; ++w) {
+            bar_init(&sm->item_full[w], 1);
+            bar_init(&sm->item_free[w], 3 + kSoftWarps);
             bar_init(&sm->q_full[w], 1);
+            bar_init(&sm->q_free[w], 1);
             bar_init(&sm->s_full[w], 1);
             bar_init(&sm->p_full[w][0], kRows);
             bar_init(&sm->p_full[w][1], kRows);
@@ -193,76 +223,123 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
     __syncthreads();
     fence_after();
     constexpr uint32_t tmem = 0;  // all the columns there are: the allocation can only begin at the first
-    const int lq = sm->lq, lk = sm->lk, row0 = sm->tile * kTileRows;
-    const bool some = sm->seq >= 0;
-    // Row i sees the keys below i + 1 + past (causal), or all of them.
-    const int past = lk - lq;
-    auto keys_of = [&](int w) {  // the key tiles of row tile w
-        const int first = row0 + w * kRows;
-        if (!some || first >= lq) return 0;
-        const int last = min(first + kRows, lq);  // rows before it
-        const int seen = A.causal ? min(max(last + past, 0), lk) : lk;
-        return (seen + kKeys - 1) / kKeys;
-    };
-    const int nt0 = keys_of(0), nt1 = keys_of(1), nt = max(nt0, nt1);
 
+    // Every role walks the same items and counts them (k), the key tiles of those before (t0) and, where it
+    // needs them, a row tile's own (c0): the barriers' phases go on from item to item.
     if (warp >= kSoftWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
-        if (warp == kCopyWarp) {
+        bool ok = true;
+        auto wait = [&](uint64_t* b, int parity) { ok = __all_sync(0xffffffffu, ok && bar_wait(b, parity & 1, &sm->abort)); };
+        auto next_item = [&](int k) {  // the k-th item
+            wait(&sm->item_full[k & 1], k >> 1);
+            const Item it = sm->item[k & 1];
+            __syncwarp();
+            if (lane == 0) bar_arrive(&sm->item_free[k & 1]);
+            return it;
+        };
+        if (warp == kItemWarp) {
+            // ------------------------------------------------------------ items
+            uint32_t index = blockIdx.x;
+            for (int k = 0, asked = 0;;) {
+                const uint32_t group = index / order.per_group, in = index - group * order.per_group;
+                const uint32_t heads = min(order.heads, A.H - group * order.heads);
+                if (k >= 2) wait(&sm->item_free[k & 1], (k >> 1) - 1);
+                if (!ok) break;
+                if (find_tile(A, (int)(in / heads), &sm->item[k & 1])) {
+                    if (lane == 0) sm->item[k & 1].h = (int)(group * order.heads + in % heads);
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(&sm->item_full[k & 1]);
+                    wait(&sm->wanted, k);
+                    ++k;
+                }
+                if (lane == 0) {
+                    fence_async_smem();
+                    bar_expect_tx(&sm->answered, sizeof sm->answer);
+                    ask_for_block(sm->answer, &sm->answered);
+                }
+                __syncwarp();
+                wait(&sm->answered, asked++);
+                if (!ok) break;
+                const bool more = block_given(sm->answer, &index);
+                __syncwarp();
+                if (!more) {
+                    if (k >= 2) wait(&sm->item_free[k & 1], (k >> 1) - 1);
+                    if (lane == 0) {
+                        sm->item[k & 1].lq = 0;
+                        bar_arrive(&sm->item_full[k & 1]);
+                    }
+                    break;
+                }
+            }
+        } else if (warp == kCopyWarp) {
             // ------------------------------------------------------------ copies (one thread)
-            if (lane == 0 && nt > 0) {
-                const int64_t q_row = sm->q0 + row0;
-                for (int w = 0; w < 2; ++w)
-                    if ((w ? nt1 : nt0) > 0) {
+            const bool leader = elect_one();
+            int t0 = 0, issued = 0, asked = -1;  // chunks; the last item whose queries are on their way
+            for (int k = 0;; ++k) {
+                const Item it = next_item(k);
+                if (!ok || it.lq == 0) break;
+                const int n[2] = {key_tiles(it, 0, A.causal), key_tiles(it, 1, A.causal)}, nt = max(n[0], n[1]);
+                if (leader) {
+                    const int64_t q_row = it.q0 + it.row0;
+                    for (int w = 0; w < 2; ++w) {
+                        if (k > 0) ok = ok && bar_wait(&sm->q_free[w], (k - 1) & 1, &sm->abort);
+                        if (!ok) break;
+                        if (w == 1) asked = k;
+                        if (n[w] == 0) {
+                            bar_arrive(&sm->q_full[w]);
+                            continue;
+                        }
                         bar_expect_tx(&sm->q_full[w], kKChunks * kChunk);
                         for (int c = 0; c < kKChunks; ++c)
-                            tma_load_3d(su32(base) + (w * kKChunks + c) * kChunk, &maps.q, 64 * c, h, (int)(q_row + w * kRows), &sm->q_full[w]);
+                            tma_load_3d(su32(base) + (w * kKChunks + c) * kChunk, &maps.q, 64 * c, it.h, (int)(q_row + w * kRows), &sm->q_full[w]);
                     }
-                int g = 0;
-                bool ok = true;
-                for (int i = 0; ok && i < nt; ++i) {
-                    const int key = (int)sm->k0 + i * kKeys;
+                    for (int i = 0; ok && i < nt; ++i) {
+                        const int key = (int)it.k0 + i * kKeys, t = t0 + i;
 #pragma unroll
-                    for (int c = 0; c < kTileChunks; ++c) {
-                        const int slot = g % kSlots, part = c < 2 ? c : c - 1;
-                        uint64_t* const full = &sm->full[i & 1][part];
-                        if (g >= kSlots && !bar_wait(&sm->free[slot], (g / kSlots - 1) & 1, &sm->abort)) { ok = false; break; }
-                        ++g;
-                        if (c != 2) bar_expect_tx(full, part == kKeys12 ? 2 * kChunk : kChunk);
-                        const uint32_t to = su32(ring) + slot * kChunk;
-                        if (c < kHeadDim / 64) {
-                            tma_load_3d(to, &maps.k, 64 * c, h, key, full);
-                        } else if (c < kKChunks) {
-                            tma_load_2d(to, &maps.r, 0, key, full);
-                        } else {
-                            tma_load_3d(to, &maps.v, 0, h, key + 64 * (c - kKChunks), full);
-                            tma_load_3d(to + kChunk / 2, &maps.v, 64, h, key + 64 * (c - kKChunks), full);
+                        for (int c = 0; c < kTileChunks; ++c) {
+                            const int g = t * kTileChunks + c, slot = g % kSlots, part = c < 2 ? c : c - 1;
+                            uint64_t* const full = &sm->full[t & 1][part];
+                            if (g >= kSlots && !bar_wait(&sm->free[slot], (g / kSlots - 1) & 1, &sm->abort)) { ok = false; break; }
+                            issued = g + 1;
+                            if (c != 2) bar_expect_tx(full, part == kKeys12 ? 2 * kChunk : kChunk);
+                            const uint32_t to = su32(ring) + slot * kChunk;
+                            if (c < kHeadDim / 64) {
+                                tma_load_3d(to, &maps.k, 64 * c, it.h, key, full);
+                            } else if (c < kKChunks) {
+                                tma_load_2d(to, &maps.r, 0, key, full);
+                            } else {
+                                tma_load_3d(to, &maps.v, 0, it.h, key + 64 * (c - kKChunks), full);
+                                tma_load_3d(to + kChunk / 2, &maps.v, 64, it.h, key + 64 * (c - kKChunks), full);
+                            }
                         }
                     }
+                    bar_arrive(&sm->wanted);  // the next item: what is left of this one covers the search for it
                 }
-                // no copy may land after the CTA's end: the last tiles', and the queries
-                for (int i = max(g / kTileChunks - 2, 0); i * kTileChunks < g; ++i)
+                ok = __all_sync(0xffffffffu, ok);
+                t0 += nt;
+                if (!ok) break;
+            }
+            // no copy may land after the CTA's end: the last key tiles', and the queries
+            if (leader) {
+                for (int t = max(issued / kTileChunks - 2, 0); t * kTileChunks < issued; ++t)
                     for (int part = 0; part < kParts; ++part)
-                        if (g > i * kTileChunks + (part < 2 ? part : part + 1)) bar_drain(&sm->full[i & 1][part], (i >> 1) & 1);
-                for (int w = 0; w < 2; ++w)
-                    if ((w ? nt1 : nt0) > 0) bar_drain(&sm->q_full[w], 0);
+                        if (issued > t * kTileChunks + (part < 2 ? part : part + 1)) bar_drain(&sm->full[t & 1][part], (t >> 1) & 1);
+                for (int w = 0; w < 2 && asked >= 0; ++w) bar_drain(&sm->q_full[w], asked & 1);
             }
             __syncwarp();
-        } else if (warp < kCopyWarp) {
+        } else {
             // ------------------------------------------------------------ a row tile's products (issued by one lane)
             constexpr uint32_t id_s = mma_idesc(BF16, kRows, kKeys, 0), id_o = mma_idesc(BF16, kRows, kHeadDim, 1);
-            const int w = warp - kMmaWarp, n = w ? nt1 : nt0;
+            const int w = warp - kMmaWarp;
             const uint32_t q_at = smem_desc(su32(base), 16) + w * kKChunks * (kChunk / 16), k_at = smem_desc(su32(ring), 16),
                            v_at = smem_desc(su32(ring), kChunk / 2), s_col = tmem + kColS + 128 * w, o_col = tmem + kColO + 128 * w;
             const bool leader = elect_one();
-            bool ok = true;
-            auto wait = [&](uint64_t* b, int parity) { ok = __all_sync(0xffffffffu, ok && bar_wait(b, parity & 1, &sm->abort)); };
-            auto landed = [&](int i, int part) { wait(&sm->full[i & 1][part], i >> 1); };
+            auto landed = [&](int t, int part) { wait(&sm->full[t & 1][part], t >> 1); };
             // The products of one lane; a chunk's slot is free once both tiles' that read it are done.
-            auto scores = [&](int i, int from, int to) {
+            auto scores = [&](int t, int from, int to) {
 #pragma unroll
                 for (int c = from; c < to; ++c) {
-                    const int slot = (i * kTileChunks + c) % kSlots;
+                    const int slot = (t * kTileChunks + c) % kSlots;
                     const uint32_t a = q_at + c * (kChunk / 16), b = k_at + slot * (kChunk / 16);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) mma_ss(s_col, a + 2 * k, b + 2 * k, id_s, (c | k) ? 1u : 0u);
@@ -270,190 +347,239 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
                 }
                 if (to == kKChunks) mma_commit(&sm->s_full[w]);
             };
-            auto values = [&](int i, int c) {
-                const int slot = (i * kTileChunks + kKChunks + c) % kSlots;
+            auto values = [&](int t, int c, int add) {
+                const int slot = (t * kTileChunks + kKChunks + c) % kSlots;
                 const uint32_t b = v_at + slot * (kChunk / 16);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) mma_ts(o_col, s_col + 32 * c + 8 * k, b + 128 * k, id_o, (c | k) ? 1u : i);
+                for (int k = 0; k < 4; ++k) mma_ts(o_col, s_col + 32 * c + 8 * k, b + 128 * k, id_o, (c | k) ? 1u : add);
                 mma_commit(&sm->free[slot]);
             };
-            auto skip = [&](int i, int part) {  // a part that only the other tile reads
-                landed(i, part);
+            auto skip = [&](int t, int part) {  // a part that only the other tile reads
+                landed(t, part);
                 if (!ok || !leader) return;
-                const int g = i * kTileChunks + (part < 2 ? part : part + 1);
+                const int g = t * kTileChunks + (part < 2 ? part : part + 1);
                 bar_arrive(&sm->free[g % kSlots]);
                 if (part == kKeys12) bar_arrive(&sm->free[(g + 1) % kSlots]);
             };
             // The tiles take turns, each with the products of one key tile's values and of the next one's
             // scores: interleaved, both tiles' would end together and leave the tensor core idle while
-            // both softmaxes run (4050 cycles a key tile instead of 2900).
+            // both softmaxes run (4050 cycles a key tile instead of 3500).
             int turns = 0;
             auto take = [&] {
                 if (w == 1 || turns > 0) wait(&sm->turn[w], turns - (w == 0));
                 ++turns;
             };
             auto give = [&] { if (ok && leader) bar_arrive(&sm->turn[1 - w]); };
-            if (n > 0) {
-                wait(&sm->q_full[w], 0);
-                landed(0, kKeys0);
-                landed(0, kKeys12);
-            }
-            if (nt > 0) {
-                take();
-                fence_after();
-                if (ok && n > 0 && leader) scores(0, 0, kKChunks);
+            int t0 = 0, c0 = 0;
+            for (int k = 0;; ++k) {
+                const Item it = next_item(k);
+                if (!ok || it.lq == 0) break;
+                const int n = key_tiles(it, w, A.causal), nt = max(n, key_tiles(it, 1 - w, A.causal));
+                if (n > 0) {
+                    wait(&sm->q_full[w], k);
+                    landed(t0, kKeys0);
+                    landed(t0, kKeys12);
+                }
+                if (nt > 0) {
+                    take();
+                    fence_after();
+                    if (ok && n > 0 && leader) scores(t0, 0, kKChunks);
+                    __syncwarp();
+                    give();
+                    if (n == 0) skip(t0, kKeys0), skip(t0, kKeys12);
+                }
+                if (leader && ok) {
+                    if (n == 0) bar_arrive(&sm->q_free[w]), bar_arrive(&sm->o_full[w]);
+                    if (n == 1) mma_commit(&sm->q_free[w]);
+                }
                 __syncwarp();
-                give();
-                if (n == 0) skip(0, kKeys0), skip(0, kKeys12);
-            }
-            for (int i = 0; ok && i < nt; ++i) {
-                const bool next = i + 1 < n;
-                if (i < n) {  // what has had the time to land is waited for before the turn
-                    landed(i, kValues0);
-                    landed(i, kValues1);
-                    if (next) landed(i + 1, kKeys0);
-                    wait(&sm->p_full[w][0], i);
-                }
-                take();
-                if (ok && i < n) {
-                    fence_after();
-                    if (leader) values(i, 0);
-                    __syncwarp();
-                    wait(&sm->p_full[w][1], i);
-                    fence_after();
-                    if (ok && leader) {
-                        values(i, 1);
-                        if (next) scores(i + 1, 0, 1);
-                        else mma_commit(&sm->o_full[w]);
+                for (int i = 0; ok && i < nt; ++i) {
+                    const bool next = i + 1 < n;
+                    const int t = t0 + i;
+                    if (i < n) {  // what has had the time to land is waited for before the turn
+                        landed(t, kValues0);
+                        landed(t, kValues1);
+                        if (next) landed(t + 1, kKeys0);
+                        wait(&sm->p_full[w][0], c0 + i);
                     }
-                    __syncwarp();
-                    if (next) {
-                        landed(i + 1, kKeys12);
+                    take();
+                    if (ok && i < n) {
                         fence_after();
-                        if (ok && leader) scores(i + 1, 1, kKChunks);
+                        if (leader) values(t, 0, i);
                         __syncwarp();
+                        wait(&sm->p_full[w][1], c0 + i);
+                        fence_after();
+                        if (ok && leader) {
+                            values(t, 1, i);
+                            if (next) scores(t + 1, 0, 1);
+                            else mma_commit(&sm->o_full[w]);
+                        }
+                        __syncwarp();
+                        if (next) {
+                            landed(t + 1, kKeys12);
+                            fence_after();
+                            if (ok && leader) {
+                                scores(t + 1, 1, kKChunks);
+                                if (i + 2 == n) mma_commit(&sm->q_free[w]);
+                            }
+                            __syncwarp();
+                        }
                     }
+                    give();
+                    if (i >= n) skip(t, kValues0), skip(t, kValues1);
+                    if (!next && i + 1 < nt) skip(t + 1, kKeys0), skip(t + 1, kKeys12);
                 }
-                give();
-                if (i >= n) skip(i, kValues0), skip(i, kValues1);
-                if (!next && i + 1 < nt) skip(i + 1, kKeys0), skip(i + 1, kKeys12);
+                t0 += nt;
+                c0 += n;
+                if (!ok) break;
             }
-            // whatever happened, every product issued here is done before the columns are freed
+            // whatever happened, every product issued here is done before the columns are freed. (O is free for
+            // an item's first values as soon as its first P is there: the same threads had read O before.)
             if (leader) mma_commit(&sm->drain[w]);
             bar_drain(&sm->drain[w], 0);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
         // ------------------------------------------------------------ softmax, a row a thread
-        const int w = warp >> 2, row = row0 + w * kRows + (tid & (kRows - 1));  // of the prompt
+        const int w = warp >> 2;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16, s_at = tmem + lanes + kColS + 128 * w, o_at = tmem + lanes + kColO + 128 * w;
-        const int n = w ? nt1 : nt0;
         const float scale = A.scale * 1.4426950408889634f;
-        const int seen = row < lq ? (A.causal ? min(max(row + 1 + past, 0), lk) : lk) : 0;
-        float m = -INFINITY, l = 0.f;
         bool ok = true;
-        for (int i = 0; i < n; ++i) {
-            const int here = seen - i * kKeys;  // keys of this tile that the row sees
-            if ((i + 1) * kKeys > lk) {         // values behind the prompt's end become zeros
-                const int live = lk - i * kKeys;
-                for (int c = 0; c < kVChunks && ok; ++c) {
-                    const int g = i * kTileChunks + kKChunks + c;
-                    ok = bar_wait(&sm->full[i & 1][kValues0 + c], (i >> 1) & 1, &sm->abort);
-                    if (!ok) break;
-                    uint8_t* at = ring + g % kSlots * kChunk;
-                    for (int u = tid & (kRows - 1); u < (int)kChunk / 16; u += kRows)
-                        if (64 * c + ((u >> 3) & 63) >= live) reinterpret_cast<uint4*>(at)[u] = make_uint4(0, 0, 0, 0);
+        int t0 = 0, c0 = 0;
+        for (int k = 0;; ++k) {
+            ok = __all_sync(0xffffffffu, bar_wait(&sm->item_full[k & 1], (k >> 1) & 1, &sm->abort));
+            if (!ok) break;
+            const Item& it = sm->item[k & 1];  // until it is given back
+            if (it.lq == 0) break;
+            const int n = key_tiles(it, w, A.causal), nt = max(n, key_tiles(it, 1 - w, A.causal)), lk = it.lk;
+            const int row = it.row0 + w * kRows + (tid & (kRows - 1));  // of the prompt
+            const int seen = row < it.lq ? (A.causal ? min(max(row + 1 + lk - it.lq, 0), lk) : lk) : 0;
+            float m = -INFINITY, l = 0.f;
+            for (int i = 0; i < n; ++i) {
+                const int here = seen - i * kKeys;  // keys of this tile that the row sees
+                ok = ok && bar_wait(&sm->s_full[w], (c0 + i) & 1, &sm->abort);
+                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                if ((i + 1) * kKeys > lk) {         // values behind the prompt's end become zeros (here, not before the scores: the barriers' phase before is over by now)
+                    const int live = lk - i * kKeys, t = t0 + i;
+                    for (int c = 0; c < kVChunks && ok; ++c) {
+                        ok = bar_wait(&sm->full[t & 1][kValues0 + c], (t >> 1) & 1, &sm->abort);
+                        if (!ok) break;
+                        uint8_t* at = ring + (t * kTileChunks + kKChunks + c) % kSlots * kChunk;
+                        for (int u = tid & (kRows - 1); u < (int)kChunk / 16; u += kRows)
+                            if (64 * c + ((u >> 3) & 63) >= live) reinterpret_cast<uint4*>(at)[u] = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_async_smem();
                 }
-                fence_async_smem();
-            }
-            ok = ok && bar_wait(&sm->s_full[w], i & 1, &sm->abort);
-            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-            fence_after();
-            uint32_t s[128];
-            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            const bool masked = __any_sync(0xffffffffu, here < kKeys);
+                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                fence_after();
+                uint32_t s[128];
+                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                const bool masked = __any_sync(0xffffffffu, here < kKeys);
 #pragma unroll
-            for (int c = 0; c < 2; ++c) tmem_load32(s + 32 * c, s_at + 32 * c);
+                for (int c = 0; c < 2; ++c) tmem_load32(s + 32 * c, s_at + 32 * c);
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {  // the second half is on its way while the first is looked through
-                tmem_wait_ld();
-                if (half == 0) {
-#pragma unroll
-                    for (int c = 2; c < 4; ++c) tmem_load32(s + 32 * c, s_at + 32 * c);
-                }
-                if (masked) {
-#pragma unroll
-                    for (int j = 64 * half; j < 64 * half + 64; ++j)
-                        if (j >= here) s[j] = __float_as_uint(-INFINITY);
-                }
-#pragma unroll
-                for (int j = 64 * half; j < 64 * half + 64; j += 8)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) top[k] = max3(top[k], __uint_as_float(s[j + 2 * k]), __uint_as_float(s[j + 2 * k + 1]));
-            }
-            const float best = max3(fmaxf(top[0], top[1]), top[2], top[3]) * scale;
-            const bool move = best > m + kRescaleLog2 || (m == -INFINITY && best > -INFINITY);
-            if (i > 0 && __any_sync(0xffffffffu, move)) {
-                // O holds tiles 0 .. i - 1: their products ended before these scores did
-                const float f = move ? ex2(m - best) : 1.f;  // m = -inf: O is zero so far
-#pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t o[32];
-                    tmem_load32(o, o_at + 32 * c);
+                for (int half = 0; half < 2; ++half) {  // the second half is on its way while the first is looked through
                     tmem_wait_ld();
+                    if (half == 0) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                    tmem_store32(o_at + 32 * c, o);
+                        for (int c = 2; c < 4; ++c) tmem_load32(s + 32 * c, s_at + 32 * c);
+                    }
+                    if (masked) {
+#pragma unroll
+                        for (int c = 2 * half; c < 2 * half + 2; ++c) {
+                            const int left = here - 32 * c;  // of these 32 keys
+                            const uint32_t keep = left >= 32 ? 0xffffffffu : left > 0 ? (1u << left) - 1u : 0u;
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (!(keep >> j & 1u)) s[32 * c + j] = __float_as_uint(-INFINITY);
+                        }
+                    }
+#pragma unroll
+                    for (int j = 64 * half; j < 64 * half + 64; j += 8)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) top[x] = max3(top[x], __uint_as_float(s[j + 2 * x]), __uint_as_float(s[j + 2 * x + 1]));
                 }
-                l *= f;
-            }
-            if (move) m = best;
-            const float from = m == -INFINITY ? 0.f : -m;
-            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t p[32];
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    float2 x = fma2(make_float2(__uint_as_float(s[64 * c + 2 * j]), __uint_as_float(s[64 * c + 2 * j + 1])), scale, from);
-                    x = make_float2(ex2(x.x), ex2(x.y));
-                    sum[j & 1] = add2(sum[j & 1], x);
-                    p[j] = pack<BF16>(x.x, x.y);
-                }
-                tmem_store32(s_at + 32 * c, p);
-                tmem_wait_st();
-                fence_before();
-                bar_arrive(&sm->p_full[w][c]);
-            }
-            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-        }
-        if (ok && n > 0) ok = bar_wait(&sm->o_full[w], 0, &sm->abort);
-        ok = __all_sync(0xffffffffu, ok);
-        fence_after();
-        if (!ok && lane == 0 && A.status) atomicOr(A.status, 8u /* HS_STATUS_TIMEOUT */);
-        const float inv = l != 0.f ? 1.f / l : 0.f, none = __uint_as_float(0x7FC00000u);
-        const int64_t to = sm->q0 + row;
-        uint16_t* out = A.o + to * A.o_token + h * A.o_head;
+                const float best = max3(fmaxf(top[0], top[1]), top[2], top[3]) * scale;
+                const bool move = best > m + kRescaleLog2 || (m == -INFINITY && best > -INFINITY);
+                if (i > 0 && __any_sync(0xffffffffu, move)) {
+                    // O holds tiles 0 .. i - 1: their products ended before these scores did
+                    const float f = move ? ex2(m - best) : 1.f;  // m = -inf: O is zero so far
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-            uint32_t o[32];
-            if (n > 0) {
-                tmem_load32(o, o_at + 32 * c);
-                tmem_wait_ld();
-            }
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t o[32];
+                        tmem_load32(o, o_at + 32 * c);
+                        tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(!ok ? none : l == 0.f ? 0.f : __uint_as_float(o[j]) * inv);
-            if (row < lq) {
+                        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                        tmem_store32(o_at + 32 * c, o);
+                    }
+                    l *= f;
+                }
+                if (move) m = best;
+                const float from = m == -INFINITY ? 0.f : -m;
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    reinterpret_cast<uint4*>(out + 32 * c)[j] =
-                        make_uint4(pack<BF16>(__uint_as_float(o[8 * j]), __uint_as_float(o[8 * j + 1])),
-                                   pack<BF16>(__uint_as_float(o[8 * j + 2]), __uint_as_float(o[8 * j + 3])),
-                                   pack<BF16>(__uint_as_float(o[8 * j + 4]), __uint_as_float(o[8 * j + 5])),
-                                   pack<BF16>(__uint_as_float(o[8 * j + 6]), __uint_as_float(o[8 * j + 7])));
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t p[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        float2 x = fma2(make_float2(__uint_as_float(s[64 * c + 2 * j]), __uint_as_float(s[64 * c + 2 * j + 1])), scale, from);
+                        x = make_float2(ex2(x.x), ex2(x.y));
+                        sum[j & 1] = add2(sum[j & 1], x);
+                        p[j] = pack<BF16>(x.x, x.y);
+                    }
+                    tmem_store32(s_at + 32 * c, p);
+                    tmem_wait_st();
+                    fence_before();
+                    bar_arrive(&sm->p_full[w][c]);
+                }
+                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             }
+            ok = __all_sync(0xffffffffu, ok && bar_wait(&sm->o_full[w], k & 1, &sm->abort));
+            fence_after();
+            const float inv = l != 0.f ? 1.f / l : 0.f, none = __uint_as_float(0x7FC00000u);
+            const int64_t to = it.q0 + row;
+            const bool there = row < it.lq;
+            const int h = it.h;
+            __syncwarp();
+            if (lane == 0) bar_arrive(&sm->item_free[k & 1]);
+            uint16_t* const out = A.o + to * A.o_token + h * A.o_head;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                uint32_t r[32];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t o[32];
+                    if (n > 0) {
+                        tmem_load32(o, o_at + 64 * half + 32 * c);
+                        tmem_wait_ld();
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const uint32_t both = pack<BF16>(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
+                        r[16 * c + j] = !ok ? 0x7FFF7FFFu : l == 0.f ? 0u : both;
+                    }
+                }
+                if (!there) continue;
+#pragma unroll
+                for (int c = 0; c < 32; c += 8) {
+                    uint16_t* const at = out + 64 * half + 2 * c;
+                    if (order.wide) {
+                        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(r[c]), "r"(r[c + 1]),
+                                     "r"(r[c + 2]), "r"(r[c + 3]), "r"(r[c + 4]), "r"(r[c + 5]), "r"(r[c + 6]), "r"(r[c + 7]) : "memory");
+                    } else {
+                        reinterpret_cast<uint4*>(at)[0] = make_uint4(r[c], r[c + 1], r[c + 2], r[c + 3]);
+                        reinterpret_cast<uint4*>(at)[1] = make_uint4(r[c + 4], r[c + 5], r[c + 6], r[c + 7]);
+                    }
+                }
+            }
+            if (there)
+                A.lse[to * A.H + h] = !ok ? none : l == 0.f ? -INFINITY : (m + lg2(l)) * 0.69314718055994531f;
+            t0 += nt;
+            c0 += n;
+            if (!ok) break;
         }
-        if (row < lq) A.lse[to * A.H + h] = !ok ? none : l == 0.f ? -INFINITY : (m + lg2(l)) * 0.69314718055994531f;
+        if (!ok && lane == 0 && A.status) atomicOr(A.status, 8u /* HS_STATUS_TIMEOUT */);
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     fence_before();
@@ -530,6 +656,7 @@ cudaError_t launch_attend_prompts(cudaStream_t stream, bool bf16, const PromptAt
     order.heads = (uint32_t)(heads < a.H ? heads : a.H);
     if (tiles * a.H > 0x7fffffff) return cudaErrorInvalidConfiguration;
     order.per_group = (uint32_t)(order.heads * tiles);
+    order.wide = (((uintptr_t)a.o | (uintptr_t)(a.o_token * 2) | (uintptr_t)(a.o_head * 2)) & 31) == 0;
     return launch_dependent(stream, dim3((unsigned)(tiles * a.H)), kThreads, kSmemBytes, bf16 ? prompt_kernel<true> : prompt_kernel<false>, a, order,
                             maps);
 }
