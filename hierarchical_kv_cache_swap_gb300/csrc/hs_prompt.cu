@@ -56,6 +56,8 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;      // row tile w: scores (P over their first half) at + 128 w
 constexpr float kRescaleLog2 = 8.f;
 
+constexpr int kItems = 4;  // that may be known ahead
+
 // What a CTA works on: 256 rows of a prompt for one head.
 struct Item {
     int64_t q0, k0;  // the prompt's first row and first key
@@ -66,10 +68,10 @@ struct Item {
 struct Smem {  // beyond Q and the ring
     __align__(16) uint32_t answer[4];                    // of the launch control
     uint64_t answered, wanted;                           // an answer is there; the next item is wanted
-    uint64_t item_full[2], item_free[2];
+    uint64_t item_full[kItems], item_free[kItems];
     uint64_t full[2][kParts], free[kSlots];              // full: by the parity of the key tile
     uint64_t q_full[2], q_free[2], s_full[2], p_full[2][2], o_full[2], turn[2], drain[2];  // by row tile; P by halves of the keys
-    Item item[2];
+    Item item[kItems];
     uint32_t tmem;
     volatile int abort;
 };
@@ -128,8 +130,9 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
 
 // Finds the prompt and the tile of it that the `at`-th of the prompts' tiles is, by one warp: 32
 // prompts at a time, their tiles counted and added up over the lanes. A prompt whose bounds are not in
-// order, or not within the rows there are, has no tiles. False: there are not so many.
-__device__ bool find_tile(const PromptAttention& A, int at, Item* item) {
+// order, or not within the rows there are, has no tiles. False: there are not so many; else *found is
+// true for the lane whose *item is filled in.
+__device__ bool find_tile(const PromptAttention& A, int at, Item* item, bool* found) {
     const int lane = threadIdx.x & 31;
     int64_t before = 0;
     for (int b0 = 0; b0 < A.B; b0 += 32) {
@@ -151,6 +154,7 @@ __device__ bool find_tile(const PromptAttention& A, int at, Item* item) {
             if (lane >= d) upto += x;
         }
         const bool mine = at >= before + upto - tiles && at < before + upto;
+        *found = mine;
         if (mine) {
             item->q0 = q0;
             item->k0 = k0;
@@ -201,11 +205,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
     if (tid == 0) {
         bar_init(&sm->answered, 1);
         bar_init(&sm->wanted, 1);
+        for (int i = 0; i < kItems; ++i) {
+            bar_init(&sm->item_full[i], 1);
+            bar_init(&sm->item_free[i], 3 + kSoftWarps);
+        }
         for (int i = 0; i < kSlots; ++i) bar_init(&sm->free[i], 2);
         for (int i = 0; i < 2 * kParts; ++i) bar_init(&sm->full[0][i], 1);
         for (int w = 0; w < 2; ++w) {
-            bar_init(&sm->item_full[w], 1);
-            bar_init(&sm->item_free[w], 3 + kSoftWarps);
             bar_init(&sm->q_full[w], 1);
             bar_init(&sm->q_free[w], 1);
             bar_init(&sm->s_full[w], 1);
@@ -231,10 +237,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
         bool ok = true;
         auto wait = [&](uint64_t* b, int parity) { ok = __all_sync(0xffffffffu, ok && bar_wait(b, parity & 1, &sm->abort)); };
         auto next_item = [&](int k) {  // the k-th item
-            wait(&sm->item_full[k & 1], k >> 1);
-            const Item it = sm->item[k & 1];
+            wait(&sm->item_full[k % kItems], k / kItems);
+            const Item it = sm->item[k % kItems];
             __syncwarp();
-            if (lane == 0) bar_arrive(&sm->item_free[k & 1]);
+            if (lane == 0) bar_arrive(&sm->item_free[k % kItems]);
             return it;
         };
         if (warp == kItemWarp) {
@@ -243,15 +249,21 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
             for (int k = 0, asked = 0;;) {
                 const uint32_t group = index / order.per_group, in = index - group * order.per_group;
                 const uint32_t heads = min(order.heads, A.H - group * order.heads);
-                if (k >= 2) wait(&sm->item_free[k & 1], (k >> 1) - 1);
-                if (!ok) break;
-                if (find_tile(A, (int)(in / heads), &sm->item[k & 1])) {
-                    if (lane == 0) sm->item[k & 1].h = (int)(group * order.heads + in % heads);
+                Item it;
+                bool found;
+                if (find_tile(A, (int)(in / heads), &it, &found)) {
+                    if (k >= kItems) wait(&sm->item_free[k % kItems], k / kItems - 1);
+                    if (!ok) break;
+                    if (found) {
+                        it.h = (int)(group * order.heads + in % heads);
+                        sm->item[k % kItems] = it;
+                        bar_arrive(&sm->item_full[k % kItems]);
+                    }
                     __syncwarp();
-                    if (lane == 0) bar_arrive(&sm->item_full[k & 1]);
                     wait(&sm->wanted, k);
                     ++k;
                 }
+                if (!ok) break;
                 if (lane == 0) {
                     fence_async_smem();
                     bar_expect_tx(&sm->answered, sizeof sm->answer);
@@ -263,59 +275,74 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
                 const bool more = block_given(sm->answer, &index);
                 __syncwarp();
                 if (!more) {
-                    if (k >= 2) wait(&sm->item_free[k & 1], (k >> 1) - 1);
+                    if (k >= kItems) wait(&sm->item_free[k % kItems], k / kItems - 1);
                     if (lane == 0) {
-                        sm->item[k & 1].lq = 0;
-                        bar_arrive(&sm->item_full[k & 1]);
+                        sm->item[k % kItems].lq = 0;
+                        bar_arrive(&sm->item_full[k % kItems]);
                     }
                     break;
                 }
             }
         } else if (warp == kCopyWarp) {
-            // ------------------------------------------------------------ copies (one thread)
+            // ------------------------------------------------------------ copies (issued by one lane)
             const bool leader = elect_one();
             int t0 = 0, issued = 0, asked = -1;  // chunks; the last item whose queries are on their way
             for (int k = 0;; ++k) {
                 const Item it = next_item(k);
                 if (!ok || it.lq == 0) break;
-                const int n[2] = {key_tiles(it, 0, A.causal), key_tiles(it, 1, A.causal)}, nt = max(n[0], n[1]);
-                if (leader) {
-                    const int64_t q_row = it.q0 + it.row0;
-                    for (int w = 0; w < 2; ++w) {
-                        if (k > 0) ok = ok && bar_wait(&sm->q_free[w], (k - 1) & 1, &sm->abort);
-                        if (!ok) break;
-                        if (w == 1) asked = k;
-                        if (n[w] == 0) {
+                const int n0 = key_tiles(it, 0, A.causal), n1 = key_tiles(it, 1, A.causal), nt = max(n0, n1);
+                const int q_row = (int)it.q0 + it.row0;
+                auto chunk = [&](int t, int key, int c) {  // c: known when compiled
+                    const int g = t * kTileChunks + c, slot = g % kSlots, part = c < 2 ? c : c - 1;
+                    if (g >= kSlots) wait(&sm->free[slot], g / kSlots - 1);
+                    if (!ok) return;
+                    issued = g + 1;
+                    if (leader) {
+                        uint64_t* const full = &sm->full[t & 1][part];
+                        if (c != 2) bar_expect_tx(full, part == kKeys12 ? 2 * kChunk : kChunk);
+                        const uint32_t to = su32(ring) + slot * kChunk;
+                        if (c < kHeadDim / 64) tma_load_4d(to, &maps.k, 0, key, c, it.h, full);
+                        else if (c < kKChunks) tma_load_2d(to, &maps.r, 0, key, full);
+                        else tma_load_4d(to, &maps.v, 0, key + 64 * (c - kKChunks), 0, it.h, full);
+                    }
+                    __syncwarp();
+                };
+                auto queries = [&](int w, int n) {
+                    if (k > 0) wait(&sm->q_free[w], k - 1);
+                    if (!ok) return;
+                    if (w == 1) asked = k;
+                    if (leader) {
+                        if (n > 0) {
+                            bar_expect_tx(&sm->q_full[w], kKChunks * kChunk);
+                            tma_load_4d(su32(base) + w * kKChunks * kChunk, &maps.q, 0, q_row + w * kRows, 0, it.h, &sm->q_full[w]);
+                        } else {
                             bar_arrive(&sm->q_full[w]);
-                            continue;
                         }
-                        bar_expect_tx(&sm->q_full[w], kKChunks * kChunk);
-                        for (int c = 0; c < kKChunks; ++c)
-                            tma_load_3d(su32(base) + (w * kKChunks + c) * kChunk, &maps.q, 64 * c, it.h, (int)(q_row + w * kRows), &sm->q_full[w]);
                     }
-                    for (int i = 0; ok && i < nt; ++i) {
-                        const int key = (int)it.k0 + i * kKeys, t = t0 + i;
+                    __syncwarp();
+                };
+                auto want = [&] {  // the next item: what is left of this one covers the search for it
+                    if (leader) bar_arrive(&sm->wanted);
+                    __syncwarp();
+                };
+                if (nt <= 2) want();
+                // the first keys have room before the queries do, whose place the item before still reads
+                if (nt > 0) {
 #pragma unroll
-                        for (int c = 0; c < kTileChunks; ++c) {
-                            const int g = t * kTileChunks + c, slot = g % kSlots, part = c < 2 ? c : c - 1;
-                            uint64_t* const full = &sm->full[t & 1][part];
-                            if (g >= kSlots && !bar_wait(&sm->free[slot], (g / kSlots - 1) & 1, &sm->abort)) { ok = false; break; }
-                            issued = g + 1;
-                            if (c != 2) bar_expect_tx(full, part == kKeys12 ? 2 * kChunk : kChunk);
-                            const uint32_t to = su32(ring) + slot * kChunk;
-                            if (c < kHeadDim / 64) {
-                                tma_load_3d(to, &maps.k, 64 * c, it.h, key, full);
-                            } else if (c < kKChunks) {
-                                tma_load_2d(to, &maps.r, 0, key, full);
-                            } else {
-                                tma_load_3d(to, &maps.v, 0, it.h, key + 64 * (c - kKChunks), full);
-                                tma_load_3d(to + kChunk / 2, &maps.v, 64, it.h, key + 64 * (c - kKChunks), full);
-                            }
-                        }
-                    }
-                    bar_arrive(&sm->wanted);  // the next item: what is left of this one covers the search for it
+                    for (int c = 0; c < kKChunks; ++c) chunk(t0, (int)it.k0, c);
                 }
-                ok = __all_sync(0xffffffffu, ok);
+                queries(0, n0);
+                queries(1, n1);
+                for (int i = 0; ok && i < nt; ++i) {
+                    const int key = (int)it.k0 + i * kKeys;
+                    if (i > 0 && i == nt - 2) want();
+                    if (i > 0) {
+#pragma unroll
+                        for (int c = 0; c < kKChunks; ++c) chunk(t0 + i, key, c);
+                    }
+#pragma unroll
+                    for (int c = kKChunks; c < kTileChunks; ++c) chunk(t0 + i, key, c);
+                }
                 t0 += nt;
                 if (!ok) break;
             }
@@ -447,9 +474,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
         bool ok = true;
         int t0 = 0, c0 = 0;
         for (int k = 0;; ++k) {
-            ok = __all_sync(0xffffffffu, bar_wait(&sm->item_full[k & 1], (k >> 1) & 1, &sm->abort));
+            ok = __all_sync(0xffffffffu, bar_wait(&sm->item_full[k % kItems], (k / kItems) & 1, &sm->abort));
             if (!ok) break;
-            const Item& it = sm->item[k & 1];  // until it is given back
+            const Item& it = sm->item[k % kItems];  // until it is given back
             if (it.lq == 0) break;
             const int n = key_tiles(it, w, A.causal), nt = max(n, key_tiles(it, 1 - w, A.causal)), lk = it.lk;
             const int row = it.row0 + w * kRows + (tid & (kRows - 1));  // of the prompt
@@ -458,18 +485,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
             for (int i = 0; i < n; ++i) {
                 const int here = seen - i * kKeys;  // keys of this tile that the row sees
                 ok = ok && bar_wait(&sm->s_full[w], (c0 + i) & 1, &sm->abort);
-                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-                if ((i + 1) * kKeys > lk) {         // values behind the prompt's end become zeros (here, not before the scores: the barriers' phase before is over by now)
-                    const int live = lk - i * kKeys, t = t0 + i;
-                    for (int c = 0; c < kVChunks && ok; ++c) {
-                        ok = bar_wait(&sm->full[t & 1][kValues0 + c], (t >> 1) & 1, &sm->abort);
-                        if (!ok) break;
-                        uint8_t* at = ring + (t * kTileChunks + kKChunks + c) % kSlots * kChunk;
-                        for (int u = tid & (kRows - 1); u < (int)kChunk / 16; u += kRows)
-                            if (64 * c + ((u >> 3) & 63) >= live) reinterpret_cast<uint4*>(at)[u] = make_uint4(0, 0, 0, 0);
-                    }
-                    fence_async_smem();
-                }
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                 fence_after();
                 uint32_t s[128];
@@ -529,6 +544,16 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
                         p[j] = pack<BF16>(x.x, x.y);
                     }
                     tmem_store32(s_at + 32 * c, p);
+                    const int live = lk - i * kKeys - 64 * c;
+                    if (live < 64) {  // values behind the prompt's end become zeros
+                        // (the scores are there, so the fill before this one of the barrier is over)
+                        const int t = t0 + i, first = max(live, 0);
+                        ok = ok && bar_wait(&sm->full[t & 1][kValues0 + c], (t >> 1) & 1, &sm->abort);
+                        uint4* at = reinterpret_cast<uint4*>(ring + (t * kTileChunks + kKChunks + c) % kSlots * kChunk);
+                        for (int u = tid & (kRows - 1); ok && u < (64 - first) * 16; u += kRows)
+                            at[(u & 8 ? 512 : 0) + (first + (u >> 4)) * 8 + (u & 7)] = make_uint4(0, 0, 0, 0);
+                        fence_async_smem();
+                    }
                     tmem_wait_st();
                     fence_before();
                     bar_arrive(&sm->p_full[w][c]);
@@ -542,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
             const bool there = row < it.lq;
             const int h = it.h;
             __syncwarp();
-            if (lane == 0) bar_arrive(&sm->item_free[k & 1]);
+            if (lane == 0) bar_arrive(&sm->item_free[k % kItems]);
             uint16_t* const out = A.o + to * A.o_token + h * A.o_head;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
@@ -591,14 +616,16 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
 }
 
 // A tensor [tokens][heads][dims] of 16-bit floats (token and head strides in elements) read in boxes of
-// 64 dimensions of `rows` tokens of one head, 128-byte swizzled.
-bool encode(CUtensorMap* map, bool bf16, const uint16_t* x, int dims, int64_t heads, int64_t tokens, int64_t head, int64_t token, int rows) {
+// all dimensions, or the first `columns` times 64, of `rows` tokens of one head: a column of 64 after
+// the other, rows of 128 swizzled bytes.
+bool encode(CUtensorMap* map, bool bf16, const uint16_t* x, int dims, int64_t heads, int64_t tokens, int64_t head, int64_t token, int rows,
+            int columns) {
     const EncodeTiled enc = tensor_map_encoder();
     if (!enc) return false;
-    const cuuint64_t size[3] = {(cuuint64_t)dims, (cuuint64_t)heads, (cuuint64_t)tokens};
-    const cuuint64_t stride[2] = {(cuuint64_t)head * 2, (cuuint64_t)token * 2};
-    const cuuint32_t box[3] = {64, 1, (cuuint32_t)rows}, step[3] = {1, 1, 1};
-    return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<uint16_t*>(x), size, stride, box,
+    const cuuint64_t size[4] = {64, (cuuint64_t)tokens, (cuuint64_t)dims / 64, (cuuint64_t)heads};
+    const cuuint64_t stride[3] = {(cuuint64_t)token * 2, 128, (cuuint64_t)head * 2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)rows, (cuuint32_t)columns, 1}, step[4] = {1, 1, 1, 1};
+    return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<uint16_t*>(x), size, stride, box,
                step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -642,9 +669,9 @@ cudaError_t launch_attend_prompts(cudaStream_t stream, bool bf16, const PromptAt
     const int64_t k_head = keys && a.H > 1 ? a.k_head : kHeadDim, v_head = keys && a.H > 1 ? a.v_head : kHeadDim;
     const int64_t k_token = keys && n > 1 ? a.k_token : kHeadDim, v_token = keys && n > 1 ? a.v_token : kHeadDim;
     const int64_t r_token = keys && n > 1 ? a.r_token : kRope;
-    if (!encode(&maps.q, bf16, a.q, kQDims, a.H, a.q_rows, q_head, q_token, kRows) ||
-        !encode(&maps.k, bf16, keys ? a.k : a.q, kHeadDim, a.H, n, k_head, k_token, kKeys) ||
-        !encode(&maps.v, bf16, keys ? a.v : a.q, kHeadDim, a.H, n, v_head, v_token, 64) ||
+    if (!encode(&maps.q, bf16, a.q, kQDims, a.H, a.q_rows, q_head, q_token, kRows, kKChunks) ||
+        !encode(&maps.k, bf16, keys ? a.k : a.q, kHeadDim, a.H, n, k_head, k_token, kKeys, 1) ||
+        !encode(&maps.v, bf16, keys ? a.v : a.q, kHeadDim, a.H, n, v_head, v_token, 64, kHeadDim / 64) ||
         !encode_rope(&maps.r, bf16, keys ? a.k_rope : a.q, n, r_token))
         return cudaErrorInvalidValue;
     // a CTA for every 256 rows of a prompt, at most one more than full ones for each prompt
