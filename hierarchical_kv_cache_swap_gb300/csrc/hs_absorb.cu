@@ -16,26 +16,21 @@
 #include "hs_latent.h"
 #include "hs_launch.h"
 #include "hs_once.h"
+#include "hs_tc.h"
 
 namespace hs {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kAbsorbCols = 128;  // latent dimensions of a CTA
 
-__device__ __forceinline__ uint32_t su32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ void copy16(uint32_t to, const void* from, bool there) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16u : 0u) : "memory");
 }
-__device__ __forceinline__ void copies_landed() {
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    asm volatile("cp.async.wait_all;" ::: "memory");
-}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>  // all groups of copies but the last LEFT have landed
+__device__ __forceinline__ void copies_landed() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
 __device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t at) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at));
-}
-__device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t at) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at));
 }
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -50,45 +45,102 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
 template <int UNITS>
 __device__ __forceinline__ uint32_t at(int r, int u) { return (uint32_t)(r * UNITS + (u ^ (r & 7))) * 16; }
 
-// The rows [TM][units of 16 bytes] staged in shared memory to rows of `out`, `pitch` elements apart.
-template <int TM, int UNITS>
-__device__ __forceinline__ void store_rows(const uint8_t* from, uint16_t* out, int64_t pitch, int64_t rows) {
-    for (int i = threadIdx.x; i < TM * UNITS; i += kThreads) {
-        const int r = i / UNITS, u = i % UNITS;
-        if (r < rows) reinterpret_cast<uint4*>(out + r * pitch)[u] = *reinterpret_cast<const uint4*>(from + at<UNITS>(r, u));
-    }
-}
+// ---------------------------------------------------------------- queries
+// A CTA takes 128 latent dimensions (the product's rows, lanes of tensor memory) of a head and NT tokens
+// (its columns): one copy brings the piece of the matrix (read across its rows: they are the product's
+// inner dimension), one the tokens, and eight instructions multiply them. Meanwhile four warps rotate
+// every fourth token's other values. They then bring the columns into rows of tokens in shared memory,
+// neighbouring lanes exchanging a value of two columns, and one copy writes these. Several CTAs of an SM
+// overlap.
+constexpr int kPieces = kLatent / 128, kAbsorbThreads = 160;
 
-// Grid: 4 pieces of 128 latent dimensions and one of the rotary values, the heads, shares of the tokens.
-// A CTA takes tiles of TM tokens; its warps are TM / 32 (at least one) by the rest over the dimensions.
-template <int TM>
-__global__ void __launch_bounds__(kThreads) absorb_kernel(const HeadProduct p, const Rotation rot, uint32_t* status) {
-    constexpr int kM = TM >= 32 ? 2 : 1;                     // m16 tiles of a warp
-    constexpr int kWarpRows = TM / (16 * kM), kWarpCols = kWarps / kWarpRows, kN = kAbsorbCols / 8 / kWarpCols;  // n8 tiles of a warp
-    static_assert(kN % 2 == 0, "two n8 tiles to a load");
-    extern __shared__ __align__(128) uint8_t smem[];
-    uint8_t *const w = smem, *const x = smem + kHeadDim * kAbsorbCols * 2;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, piece = blockIdx.x, h = blockIdx.y;
-    constexpr int kWidth = kHeadDim + kRope;
-    const uint16_t* in = (const uint16_t*)p.x + h * p.x_head;
-    uint16_t* out = p.out + (int64_t)h * (kLatent + kRope);
-    const int64_t pitch = (int64_t)p.heads * (kLatent + kRope);
+struct AbsorbSmem {  // beyond the operands
+    uint64_t landed, done;
+    uint32_t tmem;
+    volatile int abort;
+};
+template <int NT>
+constexpr uint32_t absorb_smem() { return 1024 + 32768 + NT * 256 + sizeof(AbsorbSmem); }
+
+struct AbsorbMaps {
+    CUtensorMap w, x, out;
+};
+
+template <int NT>
+__global__ void __launch_bounds__(kAbsorbThreads) absorb_kernel(const HeadProduct p, const Rotation rot, uint32_t* status,
+                                                                const __grid_constant__ AbsorbMaps maps) {
+    constexpr uint32_t kCols = NT < 32 ? 32 : NT;  // of tensor memory
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    uint8_t* const base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    AbsorbSmem* const sm = reinterpret_cast<AbsorbSmem*>(base + 32768 + NT * 256);
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, piece = blockIdx.x, h = blockIdx.y;
+    const int64_t t0 = (int64_t)blockIdx.z * NT, pitch = (int64_t)p.heads * (kLatent + kRope);
+    uint16_t* const out = p.out + (int64_t)h * (kLatent + kRope);
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (piece == kLatent / kAbsorbCols) {  // a warp a token, a lane a pair
-        const int first = rot.halves ? lane : 2 * lane, second = rot.halves ? lane + 32 : 2 * lane + 1;
-        for (int64_t t = (int64_t)blockIdx.z * kWarps + warp; t < p.n; t += (int64_t)gridDim.z * kWarps) {
-            const uint16_t* r = in + t * p.x_token + kHeadDim;
-            float2 v = make_float2(__uint_as_float((uint32_t)r[first] << 16), __uint_as_float((uint32_t)r[second] << 16));
-            if (rot.table) {
-                const int32_t pos = rot.positions[t];
-                if (pos >= 0 && pos < rot.rows) {
-                    v = turn(v.x, v.y, rot.table[(int64_t)pos * kRope + lane], rot.table[(int64_t)pos * kRope + 32 + lane]);
-                } else {
-                    if (pos >= 0 && lane == 0 && h == 0 && status) atomicOr(status, 1u /* HS_STATUS_RANGE */);
-                    v = make_float2(0.f, 0.f);
-                }
-            }
-            uint16_t* o = out + t * pitch + kLatent;
+    if (warp == 4) {
+        if (lane == 0) {
+            bar_init(&sm->landed, 1);
+            bar_init(&sm->done, 1);
+            sm->abort = 0;
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+            bar_expect_tx(&sm->landed, 32768 + NT * 256);
+            tma_load_4d(su32(base), &maps.w, 0, 0, 2 * piece, h, &sm->landed);
+            tma_load_4d(su32(base) + 32768, &maps.x, 0, (int)t0, 0, h, &sm->landed);
+        }
+        __syncwarp();
+        tmem_alloc<kCols>(&sm->tmem);
+    }
+    // warp w rotates every 16th token: its pairs, and where they are, are loaded while the operands come
+    constexpr int kTurns = NT / (4 * kPieces);
+    const int first = rot.halves ? lane : 2 * lane, second = rot.halves ? lane + 32 : 2 * lane + 1;
+    auto token = [&](int i) { return t0 + (i * 4 + warp) * kPieces + piece; };
+    uint32_t x[kTurns], y[kTurns], mine = 0;
+    int32_t pos[kTurns];
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) {
+        if (warp == 4 || token(i) >= p.n) continue;
+        mine |= 1u << i;
+        const uint16_t* const r = (const uint16_t*)p.x + token(i) * p.x_token + h * p.x_head + kHeadDim;
+        x[i] = r[first];
+        y[i] = r[second];
+        pos[i] = rot.table ? rot.positions[token(i)] : 0;
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    // the cosines and sines of the rotations' positions: none, and zeros, where there is no row
+    float c[kTurns], s[kTurns];
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) {
+        c[i] = s[i] = 0.f;
+        if (!rot.table || !(mine >> i & 1)) continue;
+        if (pos[i] >= 0 && pos[i] < rot.rows) {
+            c[i] = rot.table[(int64_t)pos[i] * kRope + lane];
+            s[i] = rot.table[(int64_t)pos[i] * kRope + 32 + lane];
+        } else {
+            x[i] = y[i] = 0;
+            if (pos[i] >= 0 && lane == 0 && h == 0 && status) atomicOr(status, 1u /* HS_STATUS_RANGE */);
+        }
+    }
+    const uint32_t tmem = sm->tmem;
+    if (warp == 4) {
+        const bool ok = __all_sync(0xffffffffu, bar_wait(&sm->landed, 0, &sm->abort));
+        if (ok && elect_one()) {
+            constexpr uint32_t id = mma_idesc(true, 128, NT, 0) | 1u << 15;  // A across its rows
+            const uint32_t a = smem_desc(su32(base), 16384), b = smem_desc(su32(base) + 32768, 16);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) mma_ss(tmem, a + 128 * k, b + NT * 8 * (k >> 2) + 2 * (k & 3), id, k ? 1u : 0u);
+            mma_commit(&sm->done);
+        }
+        __syncwarp();
+    }
+    if (warp < 4) {  // the rotations: a warp a token, a lane a pair
+#pragma unroll
+        for (int i = 0; i < kTurns; ++i) {
+            if (!(mine >> i & 1)) continue;
+            float2 v = make_float2(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16));
+            if (rot.table) v = turn(v.x, v.y, c[i], s[i]);
+            uint16_t* const o = out + token(i) * pitch + kLatent;
             const uint32_t both = pack(v.x, v.y);
             if (rot.halves) {
                 o[first] = (uint16_t)both;
@@ -97,155 +149,262 @@ __global__ void __launch_bounds__(kThreads) absorb_kernel(const HeadProduct p, c
                 reinterpret_cast<uint32_t*>(o)[lane] = both;
             }
         }
-        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-        return;
     }
-    static_assert(kWidth == 192, "row of a query");
-    for (int i = tid; i < kHeadDim * 16; i += kThreads) {
-        const int d = i >> 4, u = i & 15;
-        copy16(su32(w) + at<16>(d, u), p.w + h * p.w_head + d * p.w_row + piece * kAbsorbCols + 8 * u, true);
-    }
-    const int wr = warp / kWarpCols, wc = warp % kWarpCols;
-    for (int64_t t0 = (int64_t)blockIdx.z * TM; t0 < p.n; t0 += (int64_t)gridDim.z * TM) {
-        for (int i = tid; i < TM * 16; i += kThreads) {
-            const int t = i >> 4, u = i & 15;
-            const bool there = t0 + t < p.n;
-            copy16(su32(x) + at<16>(t, u), in + (there ? t0 + t : 0) * p.x_token + 8 * u, there);
-        }
-        copies_landed();
-        __syncthreads();
-        float acc[kM][kN][4] = {};
+    if (warp < 4) {
+        const bool ok = __all_sync(0xffffffffu, bar_wait(&sm->done, 0, &sm->abort));
+        fence_after();
+        if (!ok && lane == 0 && status) atomicOr(status, 8u /* HS_STATUS_TIMEOUT */);
+        const int odd = lane & 1, unit = (warp & 1) * 4 + (lane >> 3), byte = (lane & 6) * 2;  // of the 128-byte row of 64 dimensions
+        uint8_t* const to = base + (warp >> 1) * NT * 128 + byte;
 #pragma unroll
-        for (int k = 0; k < kHeadDim / 16; ++k) {
-            uint32_t a[kM][4];
+        for (int c = 0; c < NT; c += 32) {
+            uint32_t v[32];
+            tmem_load32(v, tmem + ((uint32_t)(warp * 32) << 16) + c);
+            tmem_wait_ld();
 #pragma unroll
-            for (int m = 0; m < kM; ++m) ldsm(a[m], su32(x) + at<16>((wr * kM + m) * 16 + (lane & 15), 2 * k + (lane >> 4)));
-#pragma unroll
-            for (int n = 0; n < kN; n += 2) {
-                uint32_t b[4];
-                ldsm_t(b, su32(w) + at<16>(16 * k + (lane & 15), wc * kN + n + (lane >> 4)));
-#pragma unroll
-                for (int m = 0; m < kM; ++m) {
-                    mma(acc[m][n], a[m], b[0], b[1]);
-                    mma(acc[m][n + 1], a[m], b[2], b[3]);
-                }
+            for (int j = 0; j < 32 && c + j < NT; j += 2) {
+                const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
+                const float x = __uint_as_float(odd ? other : v[j]), y = __uint_as_float(odd ? v[j + 1] : other);
+                const int t = c + j + odd;
+                *reinterpret_cast<uint32_t*>(to + t * 128 + ((unit ^ (t & 7)) << 4)) = ok ? pack(x, y) : 0x7FFF7FFFu;
             }
         }
-        __syncthreads();  // the tokens' shared memory becomes the staging of the result
-#pragma unroll
-        for (int m = 0; m < kM; ++m)
-#pragma unroll
-            for (int n = 0; n < kN; ++n)
-#pragma unroll
-                for (int r = 0; r < 2; ++r)
-                    *reinterpret_cast<uint32_t*>(x + at<16>((wr * kM + m) * 16 + 8 * r + (lane >> 2), wc * kN + n) + 4 * (lane & 3)) =
-                        pack(acc[m][n][2 * r], acc[m][n][2 * r + 1]);
-        __syncthreads();
-        store_rows<TM, 16>(x, out + t0 * pitch + piece * kAbsorbCols, pitch, p.n - t0);
-        __syncthreads();
+        fence_async_smem();
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        if (tid == 0) tma_store_4d(&maps.out, 0, (int)t0, 2 * piece, h, su32(base));
+        __syncwarp();
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-template <int TM>
-constexpr uint32_t absorb_smem() { return kHeadDim * kAbsorbCols * 2 + TM * kAbsorbCols * 2; }
-
-// Grid: pieces of TE output dimensions, the heads, shares of the tokens. The f32 rows are rounded to
-// bf16 for the product, as the sums behind them have been: a relative 2^-9 of each, under the result's
-// own rounding once 512 of them are summed.
-template <int TM, int TE>
-__global__ void __launch_bounds__(kThreads) expand_kernel(const HeadProduct p) {
-    constexpr int kM = TM >= 32 ? 2 : 1, kWarpRows = TM / (16 * kM), kN = TE >= 128 ? 4 : 2;
-    constexpr int kWarpCols = TE / (8 * kN), kShares = kWarps / (kWarpRows * kWarpCols);  // of the 512 dimensions
-    constexpr int kUnits = kLatent / 8, kSteps = kLatent / 16 / kShares;
-    extern __shared__ __align__(128) uint8_t smem[];
-    uint8_t *const w = smem, *const x = smem + TE * kLatent * 2;
-    float* const sums = reinterpret_cast<float*>(x + TM * kLatent * 2);  // [kShares - 1][TM][TE]
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, e0 = blockIdx.x * TE, h = blockIdx.y;
-    const float* in = (const float*)p.x + h * p.x_head;
-    const int64_t pitch = (int64_t)p.heads * kHeadDim;
-    uint16_t* out = p.out + (int64_t)h * kHeadDim + e0;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    for (int i = tid; i < TE * kUnits; i += kThreads) {
-        const int e = i / kUnits, u = i % kUnits;
-        copy16(su32(w) + at<kUnits>(e, u), p.w + h * p.w_head + (e0 + e) * p.w_row + 8 * u, true);
+    fence_before();
+    __syncthreads();
+    if (warp == 4) {
+        fence_after();
+        tmem_free<kCols>(tmem);
     }
-    const int share = warp / (kWarpRows * kWarpCols), wr = warp / kWarpCols % kWarpRows, wc = warp % kWarpCols;
-    for (int64_t t0 = (int64_t)blockIdx.z * TM; t0 < p.n; t0 += (int64_t)gridDim.z * TM) {
-        for (int i = tid; i < TM * kUnits; i += kThreads) {
-            const int t = i / kUnits, u = i % kUnits;
-            float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-            if (t0 + t < p.n) {
-                const float4* r = reinterpret_cast<const float4*>(in + (t0 + t) * p.x_token) + 2 * u;
-                a = r[0];
-                b = r[1];
+}
+
+// ---------------------------------------------------------------- outputs
+// Grid: pieces of TE output dimensions, the heads, tiles of TM tokens. Steps of 64 latent dimensions of
+// both operands pass through kStages places of shared memory. The f32 rows are rounded to bf16 for the
+// product, as the sums behind them have been: a relative 2^-8 of each at most, about the result's own
+// rounding once 512 of them are summed.
+template <int TM, int TE, int STAGES>
+__global__ void __launch_bounds__(kThreads) expand_kernel(const HeadProduct p) {
+    constexpr int kM = TM >= 32 ? 2 : 1, kWarpRows = TM / (16 * kM), kN = TE / 8 / (kWarps / kWarpRows) >= 2 ? TE / 8 / (kWarps / kWarpRows) : 2;
+    constexpr int kWarpCols = TE / (8 * kN), kShares = kWarps / (kWarpRows * kWarpCols);  // of a step's dimensions
+    static_assert(kShares >= 1 && kShares <= 4, "a share has at least 16 dimensions of a step");
+    constexpr int kSteps = kLatent / 64;
+    constexpr uint32_t kW = TE * 128, kX = TM * 256, kStage = kW + kX;  // W rows of 64 bf16, x rows of 64 f32
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, e0 = blockIdx.x * TE, h = blockIdx.y;
+    const int64_t t0 = (int64_t)blockIdx.z * TM;
+    const float* in = (const float*)p.x + h * p.x_head;
+    const uint16_t* mat = p.w + h * p.w_head + e0 * p.w_row;
+    const int64_t pitch = (int64_t)p.heads * kHeadDim;
+    uint16_t* out = p.out + (int64_t)h * kHeadDim + e0 + t0 * pitch;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // 16-byte unit u of row t of x lies at u ^ 2 (t % 8): the eight rows of a fragment in different banks
+    auto fetch = [&](int s) {
+        if (s < kSteps) {
+            const uint32_t wa = su32(smem) + s % STAGES * kStage, xa = wa + kW;
+            for (int i = tid; i < TE * 8; i += kThreads) copy16(wa + at<8>(i >> 3, i & 7), mat + (i >> 3) * p.w_row + 64 * s + 8 * (i & 7), true);
+            for (int i = tid; i < TM * 16; i += kThreads) {
+                const int t = i >> 4, u = i & 15;
+                const bool there = t0 + t < p.n;
+                copy16(xa + t * 256 + ((u ^ (t & 7) << 1) << 4), in + (there ? t0 + t : 0) * p.x_token + 64 * s + 4 * u, there);
             }
-            *reinterpret_cast<uint4*>(x + at<kUnits>(t, u)) = make_uint4(pack(a.x, a.y), pack(a.z, a.w), pack(b.x, b.y), pack(b.z, b.w));
         }
-        copies_landed();
+        copies_end();
+    };
+    const int share = warp / (kWarpRows * kWarpCols), wr = warp / kWarpCols % kWarpRows, wc = warp % kWarpCols;
+    float acc[kM][kN][4] = {};
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s) fetch(s);
+    for (int s = 0; s < kSteps; ++s) {
+        copies_landed<STAGES - 2>();
         __syncthreads();
-        float acc[kM][kN][4] = {};
-#pragma unroll 4
-        for (int k = share * kSteps; k < (share + 1) * kSteps; ++k) {
+        fetch(s + STAGES - 1);
+        const uint8_t* const w = smem + s % STAGES * kStage;
+        const uint8_t* const x = w + kW;
+#pragma unroll
+        for (int k = share; k < 4; k += kShares) {
             uint32_t a[kM][4];
 #pragma unroll
-            for (int m = 0; m < kM; ++m) ldsm(a[m], su32(x) + at<kUnits>((wr * kM + m) * 16 + (lane & 15), 2 * k + (lane >> 4)));
+            for (int m = 0; m < kM; ++m)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {  // rows g and g + 8, columns 2 c and 2 c + 8
+                    const int t = (wr * kM + m) * 16 + (lane >> 2) + 8 * (r & 1), u = 4 * k + 2 * (r >> 1) + ((lane & 3) >> 1);
+                    const float2 v = *reinterpret_cast<const float2*>(x + t * 256 + ((u ^ (t & 7) << 1) << 4) + 8 * (lane & 1));
+                    a[m][r] = pack(v.x, v.y);
+                }
 #pragma unroll
             for (int n = 0; n < kN; n += 2) {
-                uint32_t b[4];  // 16 output dimensions by 16 latent ones
-                ldsm(b, su32(w) + at<kUnits>((wc * kN + n) * 8 + (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)));
+                uint32_t c[4];  // 16 output dimensions by 16 latent ones
+                ldsm(c, su32(w) + at<8>((wc * kN + n) * 8 + (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)));
 #pragma unroll
                 for (int m = 0; m < kM; ++m) {
-                    mma(acc[m][n], a[m], b[0], b[1]);
-                    mma(acc[m][n + 1], a[m], b[2], b[3]);
+                    mma(acc[m][n], a[m], c[0], c[1]);
+                    mma(acc[m][n + 1], a[m], c[2], c[3]);
                 }
             }
         }
-        auto place = [&](int m, int n, int r) { return ((wr * kM + m) * 16 + 8 * r + (lane >> 2)) * TE + (wc * kN + n) * 8 + 2 * (lane & 3); };
-        if (kShares > 1) {
-            if (share > 0)
-                for (int m = 0; m < kM; ++m)
-                    for (int n = 0; n < kN; ++n)
-                        for (int r = 0; r < 2; ++r)
-                            *reinterpret_cast<float2*>(sums + (share - 1) * TM * TE + place(m, n, r)) = make_float2(acc[m][n][2 * r], acc[m][n][2 * r + 1]);
-            __syncthreads();
-            if (share == 0)
-                for (int s = 0; s < kShares - 1; ++s)
-#pragma unroll
-                    for (int m = 0; m < kM; ++m)
-#pragma unroll
-                        for (int n = 0; n < kN; ++n)
-#pragma unroll
-                            for (int r = 0; r < 2; ++r) {
-                                const float2 v = *reinterpret_cast<const float2*>(sums + s * TM * TE + place(m, n, r));
-                                acc[m][n][2 * r] += v.x;
-                                acc[m][n][2 * r + 1] += v.y;
-                            }
-        } else {
-            __syncthreads();
-        }
-        if (share == 0) {  // the tokens' shared memory becomes the staging of the result
+    }
+    copies_landed<0>();
+    __syncthreads();
+    // the shares are added up in their order, in what held the operands
+    auto place = [&](int m, int n, int r) { return ((wr * kM + m) * 16 + 8 * r + (lane >> 2)) * TE + (wc * kN + n) * 8 + 2 * (lane & 3); };
+    float* const sums = reinterpret_cast<float*>(smem + TM * TE * 2);  // [kShares - 1][TM][TE], behind the staged result
+    static_assert(TM * TE * 2 + (kShares - 1) * TM * TE * 4 <= STAGES * kStage, "room for the shares");
+    if (kShares > 1) {
+        if (share > 0)
 #pragma unroll
             for (int m = 0; m < kM; ++m)
 #pragma unroll
                 for (int n = 0; n < kN; ++n)
 #pragma unroll
                     for (int r = 0; r < 2; ++r)
-                        *reinterpret_cast<uint32_t*>(x + ((wr * kM + m) * 16 + 8 * r + (lane >> 2)) * (TE * 2) + ((wc * kN + n) * 8 + 2 * (lane & 3)) * 2) =
-                            pack(acc[m][n][2 * r], acc[m][n][2 * r + 1]);
-        }
+                        *reinterpret_cast<float2*>(sums + (share - 1) * TM * TE + place(m, n, r)) = make_float2(acc[m][n][2 * r], acc[m][n][2 * r + 1]);
         __syncthreads();
-        constexpr int kOut = TE / 8;
-        for (int i = tid; i < TM * kOut; i += kThreads)
-            if (t0 + i / kOut < p.n)
-                reinterpret_cast<uint4*>(out + (t0 + i / kOut) * pitch)[i % kOut] = reinterpret_cast<const uint4*>(x)[i];
-        __syncthreads();
+    }
+    if (share == 0) {
+#pragma unroll
+        for (int m = 0; m < kM; ++m)
+#pragma unroll
+            for (int n = 0; n < kN; ++n)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    float2 v = make_float2(acc[m][n][2 * r], acc[m][n][2 * r + 1]);
+#pragma unroll
+                    for (int s = 0; s < kShares - 1; ++s) {
+                        const float2 y = *reinterpret_cast<const float2*>(sums + s * TM * TE + place(m, n, r));
+                        v = make_float2(v.x + y.x, v.y + y.y);
+                    }
+                    const int t = (wr * kM + m) * 16 + 8 * r + (lane >> 2), e = wc * kN + n;
+                    *reinterpret_cast<uint32_t*>(smem + (t * (TE / 8) + (e ^ (t & (TE / 8 - 1) & 7))) * 16 + 4 * (lane & 3)) = pack(v.x, v.y);
+                }
+    }
+    __syncthreads();
+    constexpr int kOut = TE / 8;
+    for (int i = tid; i < TM * kOut; i += kThreads) {
+        const int t = i / kOut, u = i % kOut;
+        if (t0 + t < p.n) reinterpret_cast<uint4*>(out + t * pitch)[u] = *reinterpret_cast<const uint4*>(smem + (t * kOut + (u ^ (t & (kOut - 1) & 7))) * 16);
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
-template <int TM, int TE>
-constexpr uint32_t expand_smem() {
-    constexpr int kM = TM >= 32 ? 2 : 1, kN = TE >= 128 ? 4 : 2, shares = kWarps / (TM / (16 * kM) * (TE / (8 * kN)));
-    return TE * kLatent * 2 + TM * kLatent * 2 + (shares - 1) * TM * TE * 4;
+template <int TM, int TE, int STAGES>
+constexpr uint32_t expand_smem() { return STAGES * (TE * 128 + TM * 256); }
+
+// Many tokens: a CTA keeps its head's whole matrix (128 output dimensions: the product's rows) and takes
+// tiles of 32 tokens (its columns), each by one of two groups of eight warps: they load a tile's f32 rows
+// straight into registers, round them into shared memory, and load the next ones while one thread
+// multiplies and all write the columns, two at a time as above. The two groups' tiles keep 128 KB of
+// loads under way, which is what it takes to draw an SM's share of the memory's rate.
+constexpr int kTokens = 32, kGroupThreads = 256, kManyThreads = 2 * kGroupThreads;
+struct ExpandSmem {  // beyond the operands
+    uint64_t landed, done[2];
+    uint32_t tmem;
+    volatile int abort;
+};
+constexpr uint32_t kMatrix = kHeadDim * kLatent * 2, kTokenTile = kTokens * kLatent * 2;
+constexpr uint32_t kManySmem = 1024 + kMatrix + 2 * kTokenTile + sizeof(ExpandSmem);
+
+__global__ void __launch_bounds__(kManyThreads, 1) expand_many_kernel(const HeadProduct p, const __grid_constant__ CUtensorMap map) {
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    uint8_t* const base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    ExpandSmem* const sm = reinterpret_cast<ExpandSmem*>(base + kMatrix + 2 * kTokenTile);
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31, h = blockIdx.x;
+    const int group = warp >> 3, tid = threadIdx.x & (kGroupThreads - 1);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (threadIdx.x == 0) {
+        bar_init(&sm->landed, 1);
+        bar_init(&sm->done[0], 1);
+        bar_init(&sm->done[1], 1);
+        sm->abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        bar_expect_tx(&sm->landed, kMatrix);
+        for (int c = 0; c < 4; ++c) tma_load_4d(su32(base) + c * (kMatrix / 4), &map, 0, 0, 2 * c, h, &sm->landed);
+    }
+    if (warp == 0) tmem_alloc<2 * kTokens>(&sm->tmem);
+    // unit u (8 values) of the group's tile: of token u / 64, dimensions 8 (u % 64) on
+    const float* const in = (const float*)p.x + h * p.x_head;
+    const int64_t step = (int64_t)gridDim.y * 2 * kTokens, pitch = (int64_t)p.heads * kHeadDim;
+    constexpr int kUnits = kTokens * kLatent / 8 / kGroupThreads;  // of a thread
+    uint8_t* const x = base + kMatrix + group * kTokenTile;
+    float4 v[2 * kUnits];
+    auto fetch = [&](int64_t t0) {
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i) {
+            const int u = i * kGroupThreads + tid;
+            const int64_t t = t0 + (u >> 6);
+            if (t < p.n) {
+                const float4* const r = reinterpret_cast<const float4*>(in + t * p.x_token) + 2 * (u & 63);
+                v[2 * i] = r[0];
+                v[2 * i + 1] = r[1];
+            } else {
+                v[2 * i] = v[2 * i + 1] = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+        }
+    };
+    int64_t t0 = ((int64_t)blockIdx.y * 2 + group) * kTokens;
+    fetch(t0);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t cols = sm->tmem + group * kTokens;
+    bool ok = true;
+    for (int k = 0; t0 < p.n; t0 += step, ++k) {
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i) {
+            const int u = i * kGroupThreads + tid, t = u >> 6, c = u & 63;  // a column of 64 dimensions after the other
+            *reinterpret_cast<uint4*>(x + (c >> 3) * (kTokens * 128) + t * 128 + (((c & 7) ^ (t & 7)) << 4)) =
+                make_uint4(pack(v[2 * i].x, v[2 * i].y), pack(v[2 * i].z, v[2 * i].w), pack(v[2 * i + 1].x, v[2 * i + 1].y),
+                           pack(v[2 * i + 1].z, v[2 * i + 1].w));
+        }
+        fence_async_smem();
+        fence_before();
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(kGroupThreads) : "memory");
+        if (t0 + step < p.n) fetch(t0 + step);
+        if ((warp & 7) == 0) {
+            ok = __all_sync(0xffffffffu, ok && bar_wait(&sm->landed, 0, &sm->abort));
+            fence_after();
+            if (ok && elect_one()) {
+                constexpr uint32_t id = mma_idesc(true, kHeadDim, kTokens, 0);
+                const uint32_t a = smem_desc(su32(base), 16), b = smem_desc(su32(x), 16);
+#pragma unroll
+                for (int s = 0; s < kLatent / 16; ++s)
+                    mma_ss(cols, a + (s >> 2) * (kHeadDim * 8) + 2 * (s & 3), b + (s >> 2) * (kTokens * 8) + 2 * (s & 3), id, s ? 1u : 0u);
+                mma_commit(&sm->done[group]);
+            }
+            __syncwarp();
+        }
+        ok = __all_sync(0xffffffffu, ok && bar_wait(&sm->done[group], k & 1, &sm->abort));
+        fence_after();
+        // warps w and w + 4 share 32 output dimensions: half of the columns each
+        uint32_t d[16];
+        const int half = (warp >> 2) & 1, odd = lane & 1;
+        tmem_load16(d, cols + ((uint32_t)((warp & 3) * 32) << 16) + 16 * half);
+        tmem_wait_ld();
+        fence_before();
+        uint16_t* const to = p.out + h * kHeadDim + (warp & 3) * 32 + (lane & ~1);
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? d[j] : d[j + 1], 1);
+            const float lo = __uint_as_float(odd ? other : d[j]), hi = __uint_as_float(odd ? d[j + 1] : other);
+            const int64_t t = t0 + 16 * half + j + odd;
+            if (t < p.n) *reinterpret_cast<uint32_t*>(to + t * pitch) = ok ? pack(lo, hi) : 0x7FFF7FFFu;
+        }
+        if (!ok) break;
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(kGroupThreads) : "memory");  // all have read the columns
+    }
+    // after an abort: no copy and no product may be under way at the CTA's end
+    if (threadIdx.x == 0) bar_drain(&sm->landed, 0);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        fence_after();
+        tmem_free<2 * kTokens>(sm->tmem);
+    }
 }
 
 struct Ready {};
@@ -263,31 +422,58 @@ cudaError_t set_up() {
     return (cudaError_t)devices.get(device, [](Ready*) {
         cudaError_t x = allow(absorb_kernel<16>, absorb_smem<16>());
         if (x == cudaSuccess) x = allow(absorb_kernel<64>, absorb_smem<64>());
-        if (x == cudaSuccess) x = allow(expand_kernel<16, 32>, expand_smem<16, 32>());
-        if (x == cudaSuccess) x = allow(expand_kernel<64, 128>, expand_smem<64, 128>());
+        if (x == cudaSuccess) x = allow(expand_kernel<16, 32, 8>, expand_smem<16, 32, 8>());
+        if (x == cudaSuccess) x = allow(expand_many_kernel, kManySmem);
         return (int)x;
     }, &ready);
 }
 
-unsigned tiles(int64_t n, int of) { return (unsigned)((n + of - 1) / of < 1024 ? (n + of - 1) / of : 1024); }
+int64_t tiles(int64_t n, int of) { return (n + of - 1) / of; }
 
 }  // namespace
+
+// A tensor [heads][rows][columns of 64] of bf16, its strides in elements, in boxes of `box_rows` rows of
+// `box_columns` columns of one head: a column after the other, rows of 128 swizzled bytes.
+static bool encode(CUtensorMap* map, const uint16_t* x, int64_t rows, int columns, int heads, int64_t row, int64_t head, int box_rows, int box_columns) {
+    const EncodeTiled enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t size[4] = {64, (cuuint64_t)rows, (cuuint64_t)columns, (cuuint64_t)heads};
+    const cuuint64_t stride[3] = {(cuuint64_t)row * 2, 128, (cuuint64_t)head * 2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)box_rows, (cuuint32_t)box_columns, 1}, step[4] = {1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t*>(x), size, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 cudaError_t launch_absorb_queries(cudaStream_t stream, const HeadProduct& p, const Rotation& rot, uint32_t* status, int num_sms) {
     if (p.n == 0 || p.heads == 0) return cudaSuccess;
     cudaError_t e = set_up();
     if (e != cudaSuccess) return e;
-    constexpr unsigned pieces = kLatent / kAbsorbCols + 1;
-    if (p.n <= 16) return launch_dependent(stream, dim3(pieces, p.heads, tiles(p.n, 16)), kThreads, absorb_smem<16>(), absorb_kernel<16>, p, rot, status);
-    return launch_dependent(stream, dim3(pieces, p.heads, tiles(p.n, 64)), kThreads, absorb_smem<64>(), absorb_kernel<64>, p, rot, status);
+    // 16 tokens a CTA while all CTAs fit the SMs at once, 64 beyond (37 tokens of 20 heads: 3.0 us against
+    // 3.6; 64 of 128 heads: 10.6 against 6.2)
+    const int nt = 4 * tiles(p.n, 16) * p.heads <= 4 * (int64_t)num_sms ? 16 : 64;
+    AbsorbMaps maps;
+    if (!encode(&maps.w, p.w, kHeadDim, kLatent / 64, p.heads, p.w_row, p.heads > 1 ? p.w_head : kHeadDim * kLatent, kHeadDim, 2) ||
+        !encode(&maps.x, (const uint16_t*)p.x, p.n, kHeadDim / 64, p.heads, p.n > 1 ? p.x_token : kHeadDim, p.heads > 1 ? p.x_head : kHeadDim, nt, 2) ||
+        !encode(&maps.out, p.out, p.n, (kLatent + kRope) / 64, p.heads, (int64_t)p.heads * (kLatent + kRope), kLatent + kRope, nt, 2))
+        return cudaErrorInvalidValue;
+    const dim3 grid(kPieces, p.heads, (unsigned)tiles(p.n, nt));
+    if (nt == 16) return launch_dependent(stream, grid, kAbsorbThreads, absorb_smem<16>(), absorb_kernel<16>, p, rot, status, maps);
+    return launch_dependent(stream, grid, kAbsorbThreads, absorb_smem<64>(), absorb_kernel<64>, p, rot, status, maps);
 }
 
 cudaError_t launch_expand_outputs(cudaStream_t stream, const HeadProduct& p, int num_sms) {
     if (p.n == 0 || p.heads == 0) return cudaSuccess;
     cudaError_t e = set_up();
     if (e != cudaSuccess) return e;
-    if (p.n <= 16) return launch_dependent(stream, dim3(kHeadDim / 32, p.heads, tiles(p.n, 16)), kThreads, expand_smem<16, 32>(), expand_kernel<16, 32>, p);
-    return launch_dependent(stream, dim3(kHeadDim / 128, p.heads, tiles(p.n, 64)), kThreads, expand_smem<64, 128>(), expand_kernel<64, 128>, p);
+    // few tokens of few heads: pieces of 32 output dimensions, while all CTAs run at once, two an SM (64
+    // tokens of 16 heads: 3.0 us against 5.4; 16 of 128 heads: 4.7 against 4.1)
+    const int64_t small = kHeadDim / 32 * p.heads * tiles(p.n, 16);
+    if (small <= 2 * (int64_t)num_sms)
+        return launch_dependent(stream, dim3(kHeadDim / 32, p.heads, (unsigned)tiles(p.n, 16)), kThreads, expand_smem<16, 32, 8>(), expand_kernel<16, 32, 8>, p);
+    CUtensorMap map;
+    if (!encode(&map, p.w, kHeadDim, kLatent / 64, p.heads, p.w_row, p.heads > 1 ? p.w_head : kHeadDim * kLatent, kHeadDim, 2)) return cudaErrorInvalidValue;
+    const int64_t most = (num_sms + p.heads - 1) / p.heads, t = tiles(p.n, 2 * kTokens);
+    return launch_dependent(stream, dim3(p.heads, (unsigned)(t < most ? t : most)), kManyThreads, kManySmem, expand_many_kernel, p, map);
 }
 
 }  // namespace hs
