@@ -472,7 +472,8 @@ cudaError_t launch_expand_outputs(cudaStream_t stream, const HeadProduct& p, int
         return launch_dependent(stream, dim3(kHeadDim / 32, p.heads, (unsigned)tiles(p.n, 16)), kThreads, expand_smem<16, 32, 8>(), expand_kernel<16, 32, 8>, p);
     CUtensorMap map;
     if (!encode(&map, p.w, kHeadDim, kLatent / 64, p.heads, p.w_row, p.heads > 1 ? p.w_head : kHeadDim * kLatent, kHeadDim, 2)) return cudaErrorInvalidValue;
-    const int64_t most = (num_sms + p.heads - 1) / p.heads, t = tiles(p.n, 2 * kTokens);
+    // all CTAs at once: a second round would read the matrices again (256 tokens of 128 heads: 20.5 us, 22.9 in two)
+    const int64_t most = p.heads < num_sms ? num_sms / p.heads : 1, t = tiles(p.n, 2 * kTokens);
     return launch_dependent(stream, dim3(p.heads, (unsigned)(t < most ? t : most)), kManyThreads, kManySmem, expand_many_kernel, p, map);
 }
 
