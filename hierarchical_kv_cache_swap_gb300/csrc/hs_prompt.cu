@@ -292,21 +292,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
                 if (!ok || it.lq == 0) break;
                 const int n0 = key_tiles(it, 0, A.causal), n1 = key_tiles(it, 1, A.causal), nt = max(n0, n1);
                 const int q_row = (int)it.q0 + it.row0;
-                auto chunk = [&](int t, int key, int c) {  // c: known when compiled
-                    const int g = t * kTileChunks + c, slot = g % kSlots, part = c < 2 ? c : c - 1;
-                    if (g >= kSlots) wait(&sm->free[slot], g / kSlots - 1);
-                    if (!ok) return;
-                    issued = g + 1;
-                    if (leader) {
-                        uint64_t* const full = &sm->full[t & 1][part];
-                        if (c != 2) bar_expect_tx(full, part == kKeys12 ? 2 * kChunk : kChunk);
-                        const uint32_t to = su32(ring) + slot * kChunk;
-                        if (c < kHeadDim / 64) tma_load_4d(to, &maps.k, 0, key, c, it.h, full);
-                        else if (c < kKChunks) tma_load_2d(to, &maps.r, 0, key, full);
-                        else tma_load_4d(to, &maps.v, 0, key + 64 * (c - kKChunks), 0, it.h, full);
-                    }
-                    __syncwarp();
-                };
                 auto queries = [&](int w, int n) {
                     if (k > 0) wait(&sm->q_free[w], k - 1);
                     if (!ok) return;
@@ -321,27 +306,33 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
                     }
                     __syncwarp();
                 };
-                auto want = [&] {  // the next item: what is left of this one covers the search for it
-                    if (leader) bar_arrive(&sm->wanted);
-                    __syncwarp();
-                };
-                if (nt <= 2) want();
-                // the first keys have room before the queries do, whose place the item before still reads
-                if (nt > 0) {
-#pragma unroll
-                    for (int c = 0; c < kKChunks; ++c) chunk(t0, (int)it.k0, c);
-                }
-                queries(0, n0);
-                queries(1, n1);
-                for (int i = 0; ok && i < nt; ++i) {
-                    const int key = (int)it.k0 + i * kKeys;
-                    if (i > 0 && i == nt - 2) want();
-                    if (i > 0) {
-#pragma unroll
-                        for (int c = 0; c < kKChunks; ++c) chunk(t0 + i, key, c);
+                const int first = t0 * kTileChunks, end = first + nt * kTileChunks;
+                for (int g = first, i = 0, c = 0;; ++g) {
+                    // the first keys have room before the queries do, whose place the item before still reads
+                    if (g == first + (nt > 0 ? kKChunks : 0)) {
+#pragma unroll 1
+                        for (int w = 0; w < 2; ++w) queries(w, w ? n1 : n0);
                     }
-#pragma unroll
-                    for (int c = kKChunks; c < kTileChunks; ++c) chunk(t0 + i, key, c);
+                    // the next item is wanted: what is left of this one covers the search for it
+                    if (g == max(end - 2 * kTileChunks, first)) {
+                        if (leader) bar_arrive(&sm->wanted);
+                        __syncwarp();
+                    }
+                    if (!ok || g == end) break;
+                    const int slot = g % kSlots, part = c < 2 ? c : c - 1, key = (int)it.k0 + i * kKeys;
+                    if (g >= kSlots) wait(&sm->free[slot], g / kSlots - 1);
+                    if (!ok) break;
+                    issued = g + 1;
+                    if (leader) {
+                        uint64_t* const full = &sm->full[(t0 + i) & 1][part];
+                        if (c != 2) bar_expect_tx(full, part == kKeys12 ? 2 * kChunk : kChunk);
+                        const uint32_t to = su32(ring) + slot * kChunk;
+                        if (c < kHeadDim / 64) tma_load_4d(to, &maps.k, 0, key, c, it.h, full);
+                        else if (c < kKChunks) tma_load_2d(to, &maps.r, 0, key, full);
+                        else tma_load_4d(to, &maps.v, 0, key + 64 * (c - kKChunks), 0, it.h, full);
+                    }
+                    __syncwarp();
+                    if (++c == kTileChunks) c = 0, ++i;
                 }
                 t0 += nt;
                 if (!ok) break;
@@ -402,42 +393,30 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
                 const Item it = next_item(k);
                 if (!ok || it.lq == 0) break;
                 const int n = key_tiles(it, w, A.causal), nt = max(n, key_tiles(it, 1 - w, A.causal));
-                if (n > 0) {
-                    wait(&sm->q_full[w], k);
-                    landed(t0, kKeys0);
-                    landed(t0, kKeys12);
-                }
-                if (nt > 0) {
-                    take();
-                    fence_after();
-                    if (ok && n > 0 && leader) scores(t0, 0, kKChunks);
-                    __syncwarp();
-                    give();
-                    if (n == 0) skip(t0, kKeys0), skip(t0, kKeys12);
-                }
-                if (leader && ok) {
-                    if (n == 0) bar_arrive(&sm->q_free[w]), bar_arrive(&sm->o_full[w]);
-                    if (n == 1) mma_commit(&sm->q_free[w]);
-                }
-                __syncwarp();
-                for (int i = 0; ok && i < nt; ++i) {
-                    const bool next = i + 1 < n;
+                // Of every item, or this warp could give the queries' place back twice before the copies
+                // take it once: a wait for the first time would then see the phase after it.
+                wait(&sm->q_full[w], k);
+                if (n == 0 && ok && leader) bar_arrive(&sm->q_free[w]);
+                // turn i: key tile i's values, the next one's scores; before the first, its scores alone
+                for (int i = nt > 0 ? -1 : 0; ok && i < nt; ++i) {
+                    const bool mine = i < n && n > 0, next = i + 1 < n;
                     const int t = t0 + i;
-                    if (i < n) {  // what has had the time to land is waited for before the turn
-                        landed(t, kValues0);
-                        landed(t, kValues1);
+                    if (mine) {  // what has had the time to land is waited for before the turn
+                        if (i >= 0) landed(t, kValues0), landed(t, kValues1);
                         if (next) landed(t + 1, kKeys0);
-                        wait(&sm->p_full[w][0], c0 + i);
+                        if (i >= 0) wait(&sm->p_full[w][0], c0 + i);
                     }
                     take();
-                    if (ok && i < n) {
+                    if (ok && mine) {
                         fence_after();
-                        if (leader) values(t, 0, i);
-                        __syncwarp();
-                        wait(&sm->p_full[w][1], c0 + i);
-                        fence_after();
+                        if (i >= 0) {
+                            if (leader) values(t, 0, i);
+                            __syncwarp();
+                            wait(&sm->p_full[w][1], c0 + i);
+                            fence_after();
+                        }
                         if (ok && leader) {
-                            values(t, 1, i);
+                            if (i >= 0) values(t, 1, i);
                             if (next) scores(t + 1, 0, 1);
                             else mma_commit(&sm->o_full[w]);
                         }
@@ -453,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
                         }
                     }
                     give();
-                    if (i >= n) skip(t, kValues0), skip(t, kValues1);
+                    if (i >= 0 && !mine) skip(t, kValues0), skip(t, kValues1);
                     if (!next && i + 1 < nt) skip(t + 1, kKeys0), skip(t + 1, kKeys12);
                 }
                 t0 += nt;
@@ -472,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16, s_at = tmem + lanes + kColS + 128 * w, o_at = tmem + lanes + kColO + 128 * w;
         const float scale = A.scale * 1.4426950408889634f;
         bool ok = true;
-        int t0 = 0, c0 = 0;
+        int t0 = 0, c0 = 0, items = 0;
         for (int k = 0;; ++k) {
             ok = __all_sync(0xffffffffu, bar_wait(&sm->item_full[k % kItems], (k / kItems) & 1, &sm->abort));
             if (!ok) break;
@@ -560,7 +539,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
                 }
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             }
-            ok = __all_sync(0xffffffffu, ok && bar_wait(&sm->o_full[w], k & 1, &sm->abort));
+            // o_full counts the items that have values: for each of them the products wait for these warps
+            if (n > 0) ok = __all_sync(0xffffffffu, ok && bar_wait(&sm->o_full[w], items++ & 1, &sm->abort));
             fence_after();
             const float inv = l != 0.f ? 1.f / l : 0.f, none = __uint_as_float(0x7FC00000u);
             const int64_t to = it.q0 + row;
@@ -569,33 +549,28 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
             __syncwarp();
             if (lane == 0) bar_arrive(&sm->item_free[k % kItems]);
             uint16_t* const out = A.o + to * A.o_token + h * A.o_head;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {  // 32 columns at a time: code that runs once for an item is kept short
+                uint32_t o[32], r[16];
+                if (n > 0) {
+                    tmem_load32(o, o_at + 32 * c);
+                    tmem_wait_ld();
+                }
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                uint32_t r[32];
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t o[32];
-                    if (n > 0) {
-                        tmem_load32(o, o_at + 64 * half + 32 * c);
-                        tmem_wait_ld();
-                    }
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const uint32_t both = pack<BF16>(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
-                        r[16 * c + j] = !ok ? 0x7FFF7FFFu : l == 0.f ? 0u : both;
-                    }
+                for (int j = 0; j < 16; ++j) {
+                    const uint32_t both = pack<BF16>(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
+                    r[j] = !ok ? 0x7FFF7FFFu : l == 0.f ? 0u : both;
                 }
                 if (!there) continue;
+                uint16_t* const at = out + 32 * c;
+                if (order.wide) {
 #pragma unroll
-                for (int c = 0; c < 32; c += 8) {
-                    uint16_t* const at = out + 64 * half + 2 * c;
-                    if (order.wide) {
-                        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(r[c]), "r"(r[c + 1]),
-                                     "r"(r[c + 2]), "r"(r[c + 3]), "r"(r[c + 4]), "r"(r[c + 5]), "r"(r[c + 6]), "r"(r[c + 7]) : "memory");
-                    } else {
-                        reinterpret_cast<uint4*>(at)[0] = make_uint4(r[c], r[c + 1], r[c + 2], r[c + 3]);
-                        reinterpret_cast<uint4*>(at)[1] = make_uint4(r[c + 4], r[c + 5], r[c + 6], r[c + 7]);
-                    }
+                    for (int j = 0; j < 16; j += 8)
+                        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at + 2 * j), "r"(r[j]), "r"(r[j + 1]),
+                                     "r"(r[j + 2]), "r"(r[j + 3]), "r"(r[j + 4]), "r"(r[j + 5]), "r"(r[j + 6]), "r"(r[j + 7]) : "memory");
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) reinterpret_cast<uint4*>(at)[j] = make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
                 }
             }
             if (there)

@@ -40,14 +40,17 @@ __device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t parity) {
     return ok != 0;
 }
 // Waits for the phase of `parity` to complete. False, with *abort set, once this wait has lasted
-// kWaitNs, or when another role has set *abort: a lost hand-off then ends the CTA, not the GPU.
+// kWaitNs, or when another role has set *abort: a lost hand-off then ends the CTA, not the GPU. The time
+// is looked at once in 256 tries (each sleeps for a while unless the phase is complete).
 constexpr uint64_t kWaitNs = 1000000000ull;
 __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, volatile int* abort) {
-    if (bar_try(b, parity)) return true;
-    const uint64_t by = global_ns() + kWaitNs;
-    while (!bar_try(b, parity)) {
-        if (*abort) return false;
-        if (global_ns() > by) {
+    uint64_t by = 0;
+#pragma unroll 1
+    for (int i = 1; !bar_try(b, parity); ++i) {
+        if (i & 255) continue;
+        const uint64_t now = global_ns();
+        if (by == 0) by = now + kWaitNs;
+        if (*abort || now > by) {
             *abort = 1;
             return false;
         }

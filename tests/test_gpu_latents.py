@@ -229,6 +229,17 @@ def test_prompts(lens, H, dtype, causal):
     check_prompts(lens, H, dtype, causal, prompts(lens, H, dtype, len(lens) + H, first=(3, 2), behind=(9, 150)))
 
 
+@pytest.mark.parametrize("most,H", [(100, 16), (300, 8), (700, 5)])
+def test_many_prompts(most, H):
+    """More tiles than run at once, whose second half, keys or all rows may be missing."""
+    g = torch.Generator().manual_seed(most)
+    n = 160
+    lens = [(most, most)] * n if most == 100 else [
+        tuple((torch.rand(2, generator=g) * most).int().tolist()) if i % 3 else (int(most * float(torch.rand(1, generator=g))), 0 if i % 2 else 129)
+        for i in range(n)]
+    check_prompts(lens, H, BF16, True, prompts(lens, H, BF16, most))
+
+
 def test_prompts_whose_tensors_end_with_them():
     lens = [(100, 140), (129, 257)]
     check_prompts(lens, 3, BF16, True, prompts(lens, 3, BF16, 5))
