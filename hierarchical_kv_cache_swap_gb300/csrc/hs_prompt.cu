@@ -397,26 +397,38 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
                 // take it once: a wait for the first time would then see the phase after it.
                 wait(&sm->q_full[w], k);
                 if (n == 0 && ok && leader) bar_arrive(&sm->q_free[w]);
-                // turn i: key tile i's values, the next one's scores; before the first, its scores alone
-                for (int i = nt > 0 ? -1 : 0; ok && i < nt; ++i) {
-                    const bool mine = i < n && n > 0, next = i + 1 < n;
+                if (n > 0) {
+                    landed(t0, kKeys0);
+                    landed(t0, kKeys12);
+                }
+                if (nt > 0) {
+                    take();
+                    fence_after();
+                    if (ok && n > 0 && leader) scores(t0, 0, kKChunks);
+                    __syncwarp();
+                    give();
+                    if (n == 0) skip(t0, kKeys0), skip(t0, kKeys12);
+                }
+                if (leader && ok && n == 1) mma_commit(&sm->q_free[w]);
+                __syncwarp();
+                for (int i = 0; ok && i < nt; ++i) {
+                    const bool next = i + 1 < n;
                     const int t = t0 + i;
-                    if (mine) {  // what has had the time to land is waited for before the turn
-                        if (i >= 0) landed(t, kValues0), landed(t, kValues1);
+                    if (i < n) {  // what has had the time to land is waited for before the turn
+                        landed(t, kValues0);
+                        landed(t, kValues1);
                         if (next) landed(t + 1, kKeys0);
-                        if (i >= 0) wait(&sm->p_full[w][0], c0 + i);
+                        wait(&sm->p_full[w][0], c0 + i);
                     }
                     take();
-                    if (ok && mine) {
+                    if (ok && i < n) {
                         fence_after();
-                        if (i >= 0) {
-                            if (leader) values(t, 0, i);
-                            __syncwarp();
-                            wait(&sm->p_full[w][1], c0 + i);
-                            fence_after();
-                        }
+                        if (leader) values(t, 0, i);
+                        __syncwarp();
+                        wait(&sm->p_full[w][1], c0 + i);
+                        fence_after();
                         if (ok && leader) {
-                            if (i >= 0) values(t, 1, i);
+                            values(t, 1, i);
                             if (next) scores(t + 1, 0, 1);
                             else mma_commit(&sm->o_full[w]);
                         }
@@ -432,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
                         }
                     }
                     give();
-                    if (i >= 0 && !mine) skip(t, kValues0), skip(t, kValues1);
+                    if (i >= n) skip(t, kValues0), skip(t, kValues1);
                     if (!next && i + 1 < nt) skip(t + 1, kKeys0), skip(t + 1, kKeys12);
                 }
                 t0 += nt;

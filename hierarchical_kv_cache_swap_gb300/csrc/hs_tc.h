@@ -44,13 +44,11 @@ __device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t parity) {
 // is looked at once in 256 tries (each sleeps for a while unless the phase is complete).
 constexpr uint64_t kWaitNs = 1000000000ull;
 __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, volatile int* abort) {
-    uint64_t by = 0;
-#pragma unroll 1
-    for (int i = 1; !bar_try(b, parity); ++i) {
-        if (i & 255) continue;
-        const uint64_t now = global_ns();
-        if (by == 0) by = now + kWaitNs;
-        if (*abort || now > by) {
+    if (bar_try(b, parity)) return true;
+    const uint64_t by = global_ns() + kWaitNs;
+    while (!bar_try(b, parity)) {
+        if (*abort) return false;
+        if (global_ns() > by) {
             *abort = 1;
             return false;
         }
