@@ -10,9 +10,12 @@
 // its scale and reads back as NaN. The rotary key's pairs (a, b) become (a c - b s, a s + b c) in
 // f32, rounded once to bf16.
 //
-// A warp takes a token: a lane has 16 latent values, 8 lanes a block (its maximum by three
-// shuffles), and one pair of the rotary key, so that each of a row's stretches moves in one
-// access of the warp. Both kernels are bound by memory traffic: 1152 bytes of rows against 656.
+// A warp takes a token at a time: a lane has 16 latent values, 8 lanes a block (its maximum by three
+// shuffles), and one pair of the rotary key, so that each of a row's stretches moves in one access of
+// the warp. Both kernels are bound by memory traffic, 1152 bytes of rows against 656 of an entry:
+// 131072 tokens (237 MB) are written in 41.6 us (5.7 TB/s, 84 % of a copy's rate) and read in 38.1
+// (6.2 TB/s, 92 %; a copy of as many bytes took 38.3). A decode step's 64 tokens take 1.8 and 1.5 us, the
+// launches' own pace.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -95,50 +98,60 @@ struct ToHistory {
     }
 };
 
-struct Entry {  // a lane's part
-    uint4 codes;
-    float scale;
-    uint32_t pair;  // interleaved: dimensions 2 lane, 2 lane + 1; halves: lane, lane + 32
-};
-template <bool HALVES>
-__device__ __forceinline__ void store_entry(uint8_t* at, int lane, const Entry& e) {
-    reinterpret_cast<uint4*>(at)[lane] = e.codes;
-    if ((lane & 7) == 0) reinterpret_cast<float*>(at + kLatent)[lane >> 3] = e.scale;
-    uint8_t* rope = at + kLatent + 16;
-    if (HALVES) {
-        reinterpret_cast<uint16_t*>(rope)[lane] = (uint16_t)e.pair;
-        reinterpret_cast<uint16_t*>(rope)[lane + 32] = (uint16_t)(e.pair >> 16);
-    } else {
-        reinterpret_cast<uint32_t*>(rope)[lane] = e.pair;
+// A warp's entry is 41 units of 16 bytes: lane l's codes are unit l, and lanes 0 to 8 bring the scales
+// (one in each eighth lane) and the 32 words of rotary values (a lane a word) into units 32 to 40. In two
+// stores instead of four, an entry's sectors are written whole but at its ends: 131072 tokens 41.6 us
+// instead of 49.4.
+__device__ __forceinline__ uint4 tail_unit(int lane, float scale, uint32_t word) {
+    uint32_t r[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t s = __shfl_sync(0xffffffffu, __float_as_uint(scale), 8 * j);
+        const uint32_t w = __shfl_sync(0xffffffffu, word, (4 * lane - 4 + j) & 31);
+        r[j] = lane == 0 ? s : w;
     }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+}
+__device__ __forceinline__ void store_entry(uint8_t* at, int lane, const uint4& codes, const uint4& tail) {
+    reinterpret_cast<uint4*>(at)[lane] = codes;
+    if (lane < 9) reinterpret_cast<uint4*>(at)[32 + lane] = tail;
 }
 
+// A warp takes `per` (at most 32) consecutive tokens: its lanes look up where each goes and its position
+// in one load, so that the loop over them waits for nothing but the rows and the table's.
 template <bool BF16, bool HALVES, class Dest>
-__global__ void __launch_bounds__(kThreads) write_kernel(const LatentRows in, int64_t n, const Rotation rot, const Dest dest) {
+__global__ void __launch_bounds__(kThreads) write_kernel(const LatentRows in, int64_t n, int per, const Rotation rot, const Dest dest) {
     const int lane = threadIdx.x & 31;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    for (int64_t i = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); i < n; i += (int64_t)gridDim.x * kWarps) {
+    const int64_t first = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * per;
+    const int count = (int)(n - first < per ? n - first : per);  // may be negative
+    Place mine{nullptr, nullptr, false};
+    int32_t row_of = 0;
+    if (lane < count) {
+        mine = dest(first + lane);
+        if (rot.table) {
+            row_of = load(rot.positions + first + lane);
+            if (mine.a && (row_of < 0 || row_of >= rot.rows)) mine = Place{nullptr, nullptr, true};
+        }
+        if (mine.bad && dest.status) atomicOr(dest.status, 1u /* HS_STATUS_RANGE */);
+    }
+#pragma unroll 2
+    for (int k = 0; k < count; ++k) {
+        uint8_t* const a_at = (uint8_t*)__shfl_sync(0xffffffffu, (unsigned long long)mine.a, k);
+        uint8_t* const b_at = (uint8_t*)__shfl_sync(0xffffffffu, (unsigned long long)mine.b, k);
+        const int32_t at = __shfl_sync(0xffffffffu, row_of, k);
+        if (!a_at) continue;
+        const int64_t i = first + k;
         const uint4* row = reinterpret_cast<const uint4*>(in.latent + i * in.latent_stride) + 2 * lane;
         const uint16_t* rope = in.rope + i * in.rope_stride;
         const uint4 w0 = load(row), w1 = load(row + 1);
         uint32_t pair;
         if (HALVES) pair = (uint32_t)load(rope + lane) | (uint32_t)load(rope + lane + 32) << 16;
         else pair = load(reinterpret_cast<const uint32_t*>(rope) + lane);
-        Place p = dest(i);
         float c = 1.f, s = 0.f;
-        if (rot.table && p.a) {
-            const int32_t at = load(rot.positions + i);
-            if (at < 0 || at >= rot.rows) {
-                p.a = nullptr;
-                p.bad = true;
-            } else {
-                c = load(rot.table + (int64_t)at * kRope + lane);
-                s = load(rot.table + (int64_t)at * kRope + 32 + lane);
-            }
-        }
-        if (!p.a) {
-            if (p.bad && lane == 0 && dest.status) atomicOr(dest.status, 1u /* HS_STATUS_RANGE */);
-            continue;
+        if (rot.table) {
+            c = load(rot.table + (int64_t)at * kRope + lane);
+            s = load(rot.table + (int64_t)at * kRope + 32 + lane);
         }
         const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
         // the magnitudes' bits order like the magnitudes, infinities and NaNs above every number
@@ -153,37 +166,50 @@ __global__ void __launch_bounds__(kThreads) write_kernel(const LatentRows in, in
         const uint32_t a = __float_as_uint(to_float<BF16>((uint16_t)m));
         const int power = max((int)((a + 0x1FFFFFu) >> 23) - 8, 1);
         const float inv = bad ? 0.f : __uint_as_float((uint32_t)(254 - power) << 23);
-        Entry e;
-        e.scale = bad ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)power << 23);
+        const float scale = bad ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)power << 23);
         uint32_t codes[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             codes[j] = codes4(to_float<BF16>((uint16_t)w[2 * j]) * inv, to_float<BF16>((uint16_t)(w[2 * j] >> 16)) * inv,
                               to_float<BF16>((uint16_t)w[2 * j + 1]) * inv, to_float<BF16>((uint16_t)(w[2 * j + 1] >> 16)) * inv);
-        e.codes = make_uint4(codes[0], codes[1], codes[2], codes[3]);
+        const uint4 unit = make_uint4(codes[0], codes[1], codes[2], codes[3]);
         float2 r = make_float2(to_float<BF16>((uint16_t)pair), to_float<BF16>((uint16_t)(pair >> 16)));
         if (rot.table) r = turn(r.x, r.y, c, s);
-        e.pair = pack<true>(r.x, r.y);
-        store_entry<HALVES>(p.a, lane, e);
-        if (p.b) store_entry<HALVES>(p.b, lane, e);
+        uint32_t word = pack<true>(r.x, r.y);
+        if (HALVES) {  // dimensions lane and lane + 32 become 2 lane and 2 lane + 1
+            const uint32_t x = __shfl_sync(0xffffffffu, word, 2 * lane & 31), y = __shfl_sync(0xffffffffu, word, (2 * lane + 1) & 31);
+            word = lane < 16 ? (x & 0xFFFFu) | y << 16 : x >> 16 | (y & 0xFFFF0000u);
+        }
+        const uint4 tail = tail_unit(lane, scale, word);
+        store_entry(a_at, lane, unit, tail);
+        if (b_at) store_entry(b_at, lane, unit, tail);
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 template <bool BF16, bool WIDE>
-__global__ void __launch_bounds__(kThreads) read_kernel(const uint8_t* entries, int64_t S, const int32_t* slots, int64_t n, int64_t total,
+__global__ void __launch_bounds__(kThreads) read_kernel(const uint8_t* entries, int64_t S, const int32_t* slots, int64_t n, int64_t total, int per,
                                                         uint16_t* latent, uint16_t* rope, uint32_t* status) {
     const int lane = threadIdx.x & 31;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    for (int64_t j = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); j < total; j += (int64_t)gridDim.x * kWarps) {
-        const int32_t s = load(slots + j);
+    const int64_t first = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * per;
+    const int count = (int)(total - first < per ? total - first : per);  // may be negative
+    int32_t slot = -1;
+    int64_t of = 0;  // the entry's number
+    if (lane < count) {
+        slot = load(slots + first + lane);
+        of = (first + lane) / n * S + slot;
+        if (slot >= S && status) atomicOr(status, 1u /* HS_STATUS_RANGE */);
+    }
+#pragma unroll 2
+    for (int k = 0; k < count; ++k) {
+        const int64_t j = first + k, entry = __shfl_sync(0xffffffffu, of, k);
+        const int32_t s = __shfl_sync(0xffffffffu, slot, k);
         uint4 c = make_uint4(0, 0, 0, 0);
         float scale = 0.f;
         uint32_t pair = 0;
-        if (s >= S) {
-            if (lane == 0 && status) atomicOr(status, 1u /* HS_STATUS_RANGE */);
-        } else if (s >= 0) {
-            const uint8_t* at = entries + (j / n * S + s) * kLatentEntry;
+        if (s >= 0 && s < S) {
+            const uint8_t* at = entries + entry * kLatentEntry;
             c = load(reinterpret_cast<const uint4*>(at) + lane);
             scale = load(reinterpret_cast<const float*>(at + kLatent) + (lane >> 3));
             pair = load(reinterpret_cast<const uint32_t*>(at + kLatent + 16) + lane);
@@ -210,20 +236,24 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const uint8_t* entries, 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// A warp for each of `items`, but at most kWave CTAs an SM, which then take further ones.
-dim3 grid_of(int64_t items, int num_sms) {
-    constexpr int kWave = 32;
-    const int64_t ctas = (items + kWarps - 1) / kWarps, most = (int64_t)num_sms * kWave;
-    return dim3((unsigned)(ctas < most ? ctas : most));
+// CTAs an SM that the items are shared over. 131072 tokens written: 45 us with 2, 41.6 with 4 (what is
+// resident at 64 registers), 43 with 8, 48 with an item a warp; read: 40.5 with 12, 38.1 with 48.
+constexpr int kWriteWave = 4, kReadWave = 48;
+// Items of a warp: as many as `wave` CTAs an SM leave to each, at most one a lane.
+int share(int64_t items, int num_sms, int wave) {
+    const int64_t warps = (int64_t)num_sms * wave * kWarps, per = (items + warps - 1) / warps;
+    return (int)(per < 32 ? per : 32);
 }
+dim3 grid_of(int64_t items, int per) { return dim3((unsigned)((items + (int64_t)per * kWarps - 1) / ((int64_t)per * kWarps))); }
 
 template <class Dest>
 cudaError_t write_any(cudaStream_t stream, bool bf16, const LatentRows& rows, int64_t n, const Rotation& rot, const Dest& dest, int num_sms) {
     if (n == 0) return cudaSuccess;
-    return launch_dependent(stream, grid_of(n, num_sms), kThreads, 0,
+    const int per = share(n, num_sms, kWriteWave);
+    return launch_dependent(stream, grid_of(n, per), kThreads, 0,
                   bf16 ? (rot.halves ? write_kernel<true, true, Dest> : write_kernel<true, false, Dest>)
                        : (rot.halves ? write_kernel<false, true, Dest> : write_kernel<false, false, Dest>),
-                  rows, n, rot, dest);
+                  rows, n, per, rot, dest);
 }
 
 }  // namespace
@@ -242,9 +272,10 @@ cudaError_t launch_read_latents(cudaStream_t stream, bool bf16, const uint8_t* e
                                 int64_t total, void* latent, void* rope, uint32_t* status, int num_sms) {
     if (total == 0) return cudaSuccess;
     const bool wide = ((uintptr_t)latent & 31) == 0;
-    return launch_dependent(stream, grid_of(total, num_sms), kThreads, 0,
+    const int per = share(total, num_sms, kReadWave);
+    return launch_dependent(stream, grid_of(total, per), kThreads, 0,
                   bf16 ? (wide ? read_kernel<true, true> : read_kernel<true, false>) : (wide ? read_kernel<false, true> : read_kernel<false, false>),
-                  entries, S, slots, n, total, (uint16_t*)latent, (uint16_t*)rope, status);
+                  entries, S, slots, n, total, per, (uint16_t*)latent, (uint16_t*)rope, status);
 }
 
 }  // namespace hs
