@@ -15,6 +15,7 @@
 
 #include <algorithm>
 #include <array>
+#include <initializer_list>
 #include <new>
 
 #include "hs.h"
@@ -757,6 +758,19 @@ int hs_read_latents(hs_stream_t stream, int dtype, const uint8_t* entries, int B
     return HS_OK;
 }
 
+// Strides as copies through tensor maps take them: positive, below 2^40 bytes (2^39 elements of two),
+// where there is more than one row.
+struct Step {
+    const char* name;
+    int64_t n, stride;
+};
+static int steps_check(std::initializer_list<Step> steps) {
+    for (const Step& s : steps)
+        if (s.n > 1 && (s.stride <= 0 || s.stride >= (int64_t)1 << 39))
+            return fail(HS_ERR_INVALID, "%s_stride=%lld must be positive, below 2^39", s.name, (long long)s.stride);
+    return HS_OK;
+}
+
 // `align`: elements of x in 16 bytes.
 static int product_check(const hs_head_product* p, int align, hs::HeadProduct* out) {
     if (!p) return fail(HS_ERR_INVALID, "null product");
@@ -766,6 +780,8 @@ static int product_check(const hs_head_product* p, int align, hs::HeadProduct* o
     if (!aligned16(p->x) || !aligned16(p->w) || !aligned16(p->out) || ((p->x_token_stride | p->x_head_stride) & (align - 1)) ||
         ((p->w_head_stride | p->w_row_stride) & 7))
         return fail(HS_ERR_INVALID, "rows of x, w and out must be 16-byte aligned");
+    const int rc = steps_check({Step{"w_head", p->heads, p->w_head_stride}, Step{"w_row", 2, p->w_row_stride}});
+    if (rc != HS_OK) return rc;
     *out = hs::HeadProduct{p->x, p->x_token_stride, p->x_head_stride, (const uint16_t*)p->w, p->w_head_stride, p->w_row_stride,
                            (uint16_t*)p->out, p->n, p->heads};
     return HS_OK;
@@ -775,7 +791,11 @@ int hs_absorb_queries(hs_stream_t stream, const hs_head_product* product, const 
     hs::HeadProduct p;
     hs::Rotation rot;
     int rc = product_check(product, 8, &p), sms = 0;
-    if (rc != HS_OK || (rc = rotation_check(rotation, p.n, nullptr, &rot)) != HS_OK || (rc = sm_count(&sms)) != HS_OK) return rc;
+    if (rc != HS_OK || (rc = rotation_check(rotation, p.n, nullptr, &rot)) != HS_OK ||
+        (rc = steps_check({Step{"x_token", p.n, p.x_token}, Step{"x_head", p.heads, p.x_head}})) != HS_OK)
+        return rc;
+    if (p.n > 1 << 22) return fail(HS_ERR_LIMIT, "n=%lld exceeds 2^22 tokens", (long long)p.n);
+    if ((rc = sm_count(&sms)) != HS_OK) return rc;
     cudaError_t e = hs::launch_absorb_queries((cudaStream_t)stream, p, rot, status, sms);
     if (e != cudaSuccess) return cuda_fail(e, "query absorption kernel launch");
     g_err[0] = 0;
@@ -807,16 +827,12 @@ int hs_attend_prompts(hs_stream_t stream, const hs_prompt_attention* a) {
         ((a->q_token_stride | a->q_head_stride | a->k_token_stride | a->k_head_stride | a->k_rope_stride | a->v_token_stride |
           a->v_head_stride | a->o_token_stride | a->o_head_stride) & 7))
         return fail(HS_ERR_INVALID, "rows of q, k, k_rope, v and o must be 16-byte aligned");
-    // the copies' strides: positive, below 2^40 bytes
-    const struct {
-        const char* name;
-        int64_t n, stride;
-    } steps[] = {{"q_token", a->q_rows, a->q_token_stride}, {"q_head", a->heads, a->q_head_stride}, {"k_token", a->k_rows, a->k_token_stride},
-                 {"k_head", a->heads, a->k_head_stride}, {"k_rope", a->k_rows, a->k_rope_stride}, {"v_token", a->k_rows, a->v_token_stride},
-                 {"v_head", a->heads, a->v_head_stride}};
-    for (const auto& s : steps)
-        if (s.n > 1 && (s.stride <= 0 || s.stride >= (int64_t)1 << 39))
-            return fail(HS_ERR_INVALID, "%s_stride=%lld must be positive, below 2^39", s.name, (long long)s.stride);
+    const int rc = steps_check({Step{"q_token", a->q_rows, a->q_token_stride}, Step{"q_head", a->heads, a->q_head_stride},
+                                Step{"k_token", a->k_rows, a->k_token_stride}, Step{"k_head", a->heads, a->k_head_stride},
+                                Step{"k_rope", a->k_rows, a->k_rope_stride}, Step{"v_token", a->k_rows, a->v_token_stride},
+                                Step{"v_head", a->heads, a->v_head_stride}});
+    if (rc != HS_OK) return rc;
+    if ((a->q_rows / 256 + a->B) * a->heads > 0x7fffffff) return fail(HS_ERR_LIMIT, "more than 2^31 tiles of 256 rows and a head");
     if (rows_overlap(hs::kHeadDim, {Axis{a->q_rows, a->o_token_stride}, Axis{a->heads, a->o_head_stride}, Axis{1, 0}}))
         return fail(HS_ERR_INVALID, "rows of o overlap");
     hs::PromptAttention p;

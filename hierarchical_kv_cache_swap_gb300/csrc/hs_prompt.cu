@@ -131,12 +131,12 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
 // Finds the prompt and the tile of it that the `at`-th of the prompts' tiles is, by one warp: 32
 // prompts at a time, their tiles counted and added up over the lanes. A prompt whose bounds are not in
 // order, or not within the rows there are, has no tiles. False: there are not so many; else *found is
-// true for the lane whose *item is filled in.
-__device__ bool find_tile(const PromptAttention& A, int at, Item* item, bool* found) {
+// true for the lane whose *item is filled in. The search goes on from where the last one ended: `from` is
+// a number of prompts, a multiple of 32, that have `before` <= at tiles.
+__device__ bool find_tile(const PromptAttention& A, int at, int& from, int64_t& before, Item* item, bool* found) {
     const int lane = threadIdx.x & 31;
-    int64_t before = 0;
-    for (int b0 = 0; b0 < A.B; b0 += 32) {
-        const int b = b0 + lane;
+    for (; from < A.B; from += 32) {
+        const int b = from + lane;
         int64_t q0 = 0, q1 = 0, k0 = 0, k1 = 0;
         if (b < A.B) {
             q0 = A.q_starts[b], q1 = A.q_starts[b + 1];
@@ -245,13 +245,20 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
         };
         if (warp == kItemWarp) {
             // ------------------------------------------------------------ items
-            uint32_t index = blockIdx.x;
+            uint32_t index = blockIdx.x, last = 0;
+            int from = 0;
+            int64_t before = 0;
             for (int k = 0, asked = 0;;) {
                 const uint32_t group = index / order.per_group, in = index - group * order.per_group;
                 const uint32_t heads = min(order.heads, A.H - group * order.heads);
                 Item it;
                 bool found;
-                if (find_tile(A, (int)(in / heads), &it, &found)) {
+                if (group != last || (int64_t)(in / heads) < before) {  // the prompts from the first again
+                    from = 0;
+                    before = 0;
+                }
+                last = group;
+                if (find_tile(A, (int)(in / heads), from, before, &it, &found)) {
                     if (k >= kItems) wait(&sm->item_free[k % kItems], k / kItems - 1);
                     if (!ok) break;
                     if (found) {
@@ -271,7 +278,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
                 }
                 __syncwarp();
                 wait(&sm->answered, asked++);
-                if (!ok) break;
+                if (!ok) {
+                    bar_drain(&sm->answered, (asked - 1) & 1);  // the answer lands before the CTA's end
+                    break;
+                }
                 const bool more = block_given(sm->answer, &index);
                 __syncwarp();
                 if (!more) {
@@ -668,7 +678,6 @@ cudaError_t launch_attend_prompts(cudaStream_t stream, bool bf16, const PromptAt
     const int64_t fit = kShared / ((a.k_rows > 0 ? a.k_rows : 1) * 4 * kHeadDim), heads = fit < 1 ? 1 : fit < 16 ? fit : 16;
     Order order;
     order.heads = (uint32_t)(heads < a.H ? heads : a.H);
-    if (tiles * a.H > 0x7fffffff) return cudaErrorInvalidConfiguration;
     order.per_group = (uint32_t)(order.heads * tiles);
     order.wide = (((uintptr_t)a.o | (uintptr_t)(a.o_token * 2) | (uintptr_t)(a.o_head * 2)) & 31) == 0;
     return launch_dependent(stream, dim3((unsigned)(tiles * a.H)), kThreads, kSmemBytes, bf16 ? prompt_kernel<true> : prompt_kernel<false>, a, order,

@@ -560,7 +560,8 @@ int hs_read_latents(hs_stream_t stream, int dtype, const uint8_t* entries, int B
 /* Rows of n tokens and `heads` heads, each times its head's matrix: row (token, head) of x starts
  * token * x_token_stride + head * x_head_stride elements in; w, bf16, holds a matrix of 128 rows of
  * 512 for each head, w_head_stride apart, its rows w_row_stride apart (a part of one projection's
- * weights, say). Rows are contiguous and 16-byte aligned; out is contiguous and 16-byte aligned. */
+ * weights, say; positive strides). Rows are contiguous and 16-byte aligned; out is contiguous and
+ * 16-byte aligned. */
 typedef struct {
     const void* x;
     int64_t x_token_stride, x_head_stride;
@@ -575,7 +576,7 @@ typedef struct {
  * hs_absorb_queries -- the queries of the absorbed form, as hs_attend takes them: of x (bf16
  * [n][heads][128 + 64]) the first 128 values become out[..][c] = sum_d x[..][d] w[head][d][c], c <
  * 512, and the last 64, rotated (rotation: NULL if they are already), out[..][512 ..] (out: bf16
- * [n][heads][576], not x). bf16 products, f32 sums, one rounding. A token whose position is
+ * [n][heads][576], not x; x's strides positive, n at most 2^22). bf16 products, f32 sums, one rounding. A token whose position is
  * negative gets zeros for its rotary values; so does one that the table has no row for, which
  * sets HS_STATUS_RANGE in *status (or NULL). Returns HS_OK, HS_ERR_INVALID or HS_ERR_CUDA.
  */
@@ -595,12 +596,15 @@ int hs_expand_outputs(hs_stream_t stream, const hs_head_product* product);
  * row i of Lq and key j of Lk, s_j = sm_scale (<q[:128], k_j> + <q[128:], k_rope_j>), over j < Lk,
  * or with `causal` j <= i + Lk - Lq: o = sum_j softmax_j(s) v_j, lse = ln sum_j exp(s_j). A row
  * that sees no key gets o = 0 and lse = -inf. Keys behind a prompt's last are not read into its
- * result, whatever they hold, and rows of q outside every prompt leave o and lse as they were. A prompt whose starts descend, or lie outside the rows there are, is left out and sets
- * HS_STATUS_RANGE. The products run on the tensor cores in `dtype` with f32 sums; the softmax
- * weights are rounded to it, relative to a maximum that is at most 2^8 times too small. Rows of every tensor
- * are contiguous and 16-byte aligned (strides multiples of 8, positive where there is more than
- * one row); rows of o that overlap are refused. HS_STATUS_TIMEOUT: a lost hand-off within the
- * kernel (a defect); its rows are then NaN.
+ * result, whatever they hold, and rows of q outside every prompt leave o and lse as they were. (With
+ * `causal`, an infinity or a NaN among a key's values reaches the 128 rows of which some see the
+ * key, the earlier ones with a weight of 0, so as NaN.) A prompt whose starts descend, or lie
+ * outside the rows there are, is left out and sets HS_STATUS_RANGE. The products run on the tensor
+ * cores in `dtype` with f32 sums; the softmax weights are rounded to it, relative to a maximum that
+ * is at most 2^8 times too small. Rows of every tensor are contiguous and 16-byte aligned (strides
+ * multiples of 8, positive where there is more than one row); rows of o that overlap are refused.
+ * HS_STATUS_TIMEOUT: a hand-off within the kernel was lost (a defect); rows may then be NaN, or
+ * missing. Returns HS_OK, HS_ERR_INVALID, HS_ERR_LIMIT or HS_ERR_CUDA.
  */
 typedef struct {
     int dtype;                 /* of q, k, k_rope, v and o: HS_BF16 or HS_F16 */

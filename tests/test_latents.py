@@ -77,8 +77,13 @@ def test_products_are_checked(lib):
         for bad in ("x", "w", "out"):
             invalid(call(product(**{bad: None})), "null")
             invalid(call(product(**{bad: A + 8})), "aligned")
+        for bad in (dict(w_head_stride=0), dict(w_row_stride=-512), dict(w_row_stride=0), dict(w_head_stride=2**39)):
+            invalid(call(product(**bad)), "must be positive")
         for bad in (dict(x_token_stride=770), dict(x_head_stride=2), dict(w_head_stride=4), dict(w_row_stride=516)):
             invalid(call(product(**bad)), "aligned")
+    for bad in (dict(x_token_stride=0), dict(x_head_stride=-192)):
+        invalid(lib.hs_absorb_queries(None, ctypes.byref(product(**bad)), None, None), "must be positive")
+    assert lib.hs_absorb_queries(None, ctypes.byref(product(n=2**22 + 1)), None, None) == hs.HS_ERR_LIMIT
     invalid(lib.hs_absorb_queries(None, ctypes.byref(product()), ctypes.byref(rotation(positions=None)), None), "without positions")
     invalid(lib.hs_absorb_queries(None, ctypes.byref(product(x_token_stride=772)), None, None), "aligned")
 
@@ -114,6 +119,7 @@ def test_prompts_are_checked(lib):
         invalid(call(**{name + "_stride": 12}), "aligned")
         invalid(call(**{name + "_stride": 0}), "overlap")
     invalid(call(o_token_stride=512, o_head_stride=120), "overlap")
+    assert call(q_rows=2**31 - 256, heads=256, q_token_stride=2**20, o_token_stride=2**20) == hs.HS_ERR_LIMIT
 
 
 def test_the_binding_checks_its_tensors():
