@@ -236,13 +236,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
         bool ok = true;
         auto wait = [&](uint64_t* b, int parity) { ok = __all_sync(0xffffffffu, ok && bar_wait(b, parity & 1, &sm->abort)); };
-        auto next_item = [&](int k) {  // the k-th item
-            wait(&sm->item_full[k % kItems], k / kItems);
-            const Item it = sm->item[k % kItems];
-            __syncwarp();
-            if (lane == 0) bar_arrive(&sm->item_free[k % kItems]);
-            return it;
-        };
         if (warp == kItemWarp) {
             // ------------------------------------------------------------ items
             uint32_t index = blockIdx.x, last = 0;
@@ -297,51 +290,44 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
             // ------------------------------------------------------------ copies (issued by one lane)
             const bool leader = elect_one();
             int t0 = 0, issued = 0, asked = -1;  // chunks; the last item whose queries are on their way
-            for (int k = 0;; ++k) {
-                const Item it = next_item(k);
+            for (int k = 0; leader; ++k) {
+                auto until = [&](uint64_t* bar, int parity) { ok = ok && bar_wait(bar, parity & 1, &sm->abort); };
+                until(&sm->item_full[k % kItems], k / kItems);
+                const Item it = sm->item[k % kItems];
+                bar_arrive(&sm->item_free[k % kItems]);
                 if (!ok || it.lq == 0) break;
                 const int n0 = key_tiles(it, 0, A.causal), n1 = key_tiles(it, 1, A.causal), nt = max(n0, n1);
                 const int q_row = (int)it.q0 + it.row0;
-                auto queries = [&](int w, int n) {
-                    if (k > 0) wait(&sm->q_free[w], k - 1);
-                    if (!ok) return;
-                    if (w == 1) asked = k;
-                    if (leader) {
-                        if (n > 0) {
-                            bar_expect_tx(&sm->q_full[w], kKChunks * kChunk);
-                            tma_load_4d(su32(base) + w * kKChunks * kChunk, &maps.q, 0, q_row + w * kRows, 0, it.h, &sm->q_full[w]);
-                        } else {
-                            bar_arrive(&sm->q_full[w]);
-                        }
-                    }
-                    __syncwarp();
-                };
                 const int first = t0 * kTileChunks, end = first + nt * kTileChunks;
                 for (int g = first, i = 0, c = 0;; ++g) {
                     // the first keys have room before the queries do, whose place the item before still reads
                     if (g == first + (nt > 0 ? kKChunks : 0)) {
 #pragma unroll 1
-                        for (int w = 0; w < 2; ++w) queries(w, w ? n1 : n0);
+                        for (int w = 0; w < 2; ++w) {
+                            if (k > 0) until(&sm->q_free[w], k - 1);
+                            if (!ok) break;
+                            if (w == 1) asked = k;
+                            if ((w ? n1 : n0) > 0) {
+                                bar_expect_tx(&sm->q_full[w], kKChunks * kChunk);
+                                tma_load_4d(su32(base) + w * kKChunks * kChunk, &maps.q, 0, q_row + w * kRows, 0, it.h, &sm->q_full[w]);
+                            } else {
+                                bar_arrive(&sm->q_full[w]);
+                            }
+                        }
                     }
                     // the next item is wanted: what is left of this one covers the search for it
-                    if (g == max(end - 2 * kTileChunks, first)) {
-                        if (leader) bar_arrive(&sm->wanted);
-                        __syncwarp();
-                    }
+                    if (g == max(end - 2 * kTileChunks, first)) bar_arrive(&sm->wanted);
                     if (!ok || g == end) break;
                     const int slot = g % kSlots, part = c < 2 ? c : c - 1, key = (int)it.k0 + i * kKeys;
-                    if (g >= kSlots) wait(&sm->free[slot], g / kSlots - 1);
+                    if (g >= kSlots) until(&sm->free[slot], g / kSlots - 1);
                     if (!ok) break;
                     issued = g + 1;
-                    if (leader) {
-                        uint64_t* const full = &sm->full[(t0 + i) & 1][part];
-                        if (c != 2) bar_expect_tx(full, part == kKeys12 ? 2 * kChunk : kChunk);
-                        const uint32_t to = su32(ring) + slot * kChunk;
-                        if (c < kHeadDim / 64) tma_load_4d(to, &maps.k, 0, key, c, it.h, full);
-                        else if (c < kKChunks) tma_load_2d(to, &maps.r, 0, key, full);
-                        else tma_load_4d(to, &maps.v, 0, key + 64 * (c - kKChunks), 0, it.h, full);
-                    }
-                    __syncwarp();
+                    uint64_t* const full = &sm->full[(t0 + i) & 1][part];
+                    if (c != 2) bar_expect_tx(full, part == kKeys12 ? 2 * kChunk : kChunk);
+                    const uint32_t to = su32(ring) + slot * kChunk;
+                    if (c < kHeadDim / 64) tma_load_4d(to, &maps.k, 0, key, c, it.h, full);
+                    else if (c < kKChunks) tma_load_2d(to, &maps.r, 0, key, full);
+                    else tma_load_4d(to, &maps.v, 0, key + 64 * (c - kKChunks), 0, it.h, full);
                     if (++c == kTileChunks) c = 0, ++i;
                 }
                 t0 += nt;
@@ -362,7 +348,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
             const uint32_t q_at = smem_desc(su32(base), 16) + w * kKChunks * (kChunk / 16), k_at = smem_desc(su32(ring), 16),
                            v_at = smem_desc(su32(ring), kChunk / 2), s_col = tmem + kColS + 128 * w, o_col = tmem + kColO + 128 * w;
             const bool leader = elect_one();
-            auto landed = [&](int t, int part) { wait(&sm->full[t & 1][part], t >> 1); };
+            auto until = [&](uint64_t* bar, int parity) { ok = ok && bar_wait(bar, parity & 1, &sm->abort); };
+            auto landed = [&](int t, int part) { until(&sm->full[t & 1][part], t >> 1); };
             // The products of one lane; a chunk's slot is free once both tiles' that read it are done.
             auto scores = [&](int t, int from, int to) {
 #pragma unroll
@@ -384,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
             };
             auto skip = [&](int t, int part) {  // a part that only the other tile reads
                 landed(t, part);
-                if (!ok || !leader) return;
+                if (!ok) return;
                 const int g = t * kTileChunks + (part < 2 ? part : part + 1);
                 bar_arrive(&sm->free[g % kSlots]);
                 if (part == kKeys12) bar_arrive(&sm->free[(g + 1) % kSlots]);
@@ -394,19 +381,21 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
             // both softmaxes run (4050 cycles a key tile instead of 3500).
             int turns = 0;
             auto take = [&] {
-                if (w == 1 || turns > 0) wait(&sm->turn[w], turns - (w == 0));
+                if (w == 1 || turns > 0) until(&sm->turn[w], turns - (w == 0));
                 ++turns;
             };
-            auto give = [&] { if (ok && leader) bar_arrive(&sm->turn[1 - w]); };
+            auto give = [&] { if (ok) bar_arrive(&sm->turn[1 - w]); };
             int t0 = 0, c0 = 0;
-            for (int k = 0;; ++k) {
-                const Item it = next_item(k);
+            for (int k = 0; leader; ++k) {  // one lane alone: a vote after each wait costs more than the wait
+                until(&sm->item_full[k % kItems], k / kItems);
+                const Item it = sm->item[k % kItems];
+                bar_arrive(&sm->item_free[k % kItems]);
                 if (!ok || it.lq == 0) break;
                 const int n = key_tiles(it, w, A.causal), nt = max(n, key_tiles(it, 1 - w, A.causal));
                 // Of every item, or this warp could give the queries' place back twice before the copies
                 // take it once: a wait for the first time would then see the phase after it.
-                wait(&sm->q_full[w], k);
-                if (n == 0 && ok && leader) bar_arrive(&sm->q_free[w]);
+                until(&sm->q_full[w], k);
+                if (n == 0 && ok) bar_arrive(&sm->q_free[w]);
                 if (n > 0) {
                     landed(t0, kKeys0);
                     landed(t0, kKeys12);
@@ -414,13 +403,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
                 if (nt > 0) {
                     take();
                     fence_after();
-                    if (ok && n > 0 && leader) scores(t0, 0, kKChunks);
-                    __syncwarp();
+                    if (ok && n > 0) scores(t0, 0, kKChunks);
                     give();
                     if (n == 0) skip(t0, kKeys0), skip(t0, kKeys12);
                 }
-                if (leader && ok && n == 1) mma_commit(&sm->q_free[w]);
-                __syncwarp();
+                if (ok && n == 1) mma_commit(&sm->q_free[w]);
                 for (int i = 0; ok && i < nt; ++i) {
                     const bool next = i + 1 < n;
                     const int t = t0 + i;
@@ -428,29 +415,23 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
                         landed(t, kValues0);
                         landed(t, kValues1);
                         if (next) landed(t + 1, kKeys0);
-                        wait(&sm->p_full[w][0], c0 + i);
+                        until(&sm->p_full[w][0], c0 + i);
                     }
                     take();
                     if (ok && i < n) {
                         fence_after();
-                        if (leader) values(t, 0, i);
-                        __syncwarp();
-                        wait(&sm->p_full[w][1], c0 + i);
+                        values(t, 0, i);
+                        until(&sm->p_full[w][1], c0 + i);
                         fence_after();
-                        if (ok && leader) {
-                            values(t, 1, i);
-                            if (next) scores(t + 1, 0, 1);
-                            else mma_commit(&sm->o_full[w]);
-                        }
-                        __syncwarp();
-                        if (next) {
+                        if (ok) values(t, 1, i);
+                        if (ok && next) {
+                            scores(t + 1, 0, 1);
                             landed(t + 1, kKeys12);
                             fence_after();
-                            if (ok && leader) {
-                                scores(t + 1, 1, kKChunks);
-                                if (i + 2 == n) mma_commit(&sm->q_free[w]);
-                            }
-                            __syncwarp();
+                            if (ok) scores(t + 1, 1, kKChunks);
+                            if (i + 2 == n) mma_commit(&sm->q_free[w]);
+                        } else if (ok) {
+                            mma_commit(&sm->o_full[w]);
                         }
                     }
                     give();
@@ -461,6 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
                 c0 += n;
                 if (!ok) break;
             }
+            __syncwarp();
             // whatever happened, every product issued here is done before the columns are freed. (O is free for
             // an item's first values as soon as its first P is there: the same threads had read O before.)
             if (leader) mma_commit(&sm->drain[w]);
