@@ -5,10 +5,18 @@
 // (hs_expand_outputs).
 //
 // Both are a batch of products over the heads, [tokens x 128][128 x 512] and [tokens x 512][512 x 128],
-// with the few tokens of a decode step: memory traffic bounds them, the matrices (128 KB a head each)
-// at few tokens, the rows at many. So a CTA keeps a piece of a head's matrix in shared memory and takes
-// tiles of tokens in turn; the products are mma.sync m16n8k16 in bf16 with f32 sums, at well under
-// what the tensor cores give even in this form.
+// with the few tokens of a decode step: memory traffic bounds them, the matrices (128 KB a head each) at
+// few tokens, the rows at many, and at the smallest calls the chain from launch to store. The matrices
+// are the products' rows, so that an instruction of 128 rows wastes nothing on the few tokens, which are
+// its columns (tcgen05, bf16 operands, f32 sums). Measured on one GB300 (us, in a graph, with L2 cold
+// where "cold"; in brackets the bytes at a copy's rate):
+//   tokens x heads   1 x 128     64 x 128   256 x 128   256 x 128 cold   512 x 128 cold   37 x 20
+//   queries          3.9 (2.5)   5.3 (4.3)  13.8 (9.9)  18.4 (9.9)       30.9 (17.3)      2.9
+//   outputs          3.8 (2.5)   5.9 (5.3)  15.6 (13.6) 20.5 (13.6)      33.2 (24.8)      3.3
+// Cold, DRAM is at 20 % (queries) and 49 % (outputs) of its peak: what is left is the time of a CTA's
+// chain of copy, product and store, of which an SM has four (one) at once. CTAs of the queries that
+// loop over tiles of tokens with two under way were slower (21.6 us for 256 tokens, cold), and so were
+// tiles of 128 tokens (20.1 warm).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -21,7 +29,7 @@
 namespace hs {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 256;  // of the kernel for few tokens
 
 __device__ __forceinline__ void copy16(uint32_t to, const void* from, bool there) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16u : 0u) : "memory");
@@ -40,10 +48,8 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&r);
 }
-// Byte offset of 16-byte unit u of row r in rows of UNITS units (a multiple of 8): eight rows' units
-// lie in different banks.
-template <int UNITS>
-__device__ __forceinline__ uint32_t at(int r, int u) { return (uint32_t)(r * UNITS + (u ^ (r & 7))) * 16; }
+// Byte offset of 16-byte unit u of row r in rows of 128 bytes: eight rows' units lie in different banks.
+__device__ __forceinline__ uint32_t at(int r, int u) { return (uint32_t)(r * 8 + (u ^ (r & 7))) * 16; }
 
 // ---------------------------------------------------------------- queries
 // A CTA takes 128 latent dimensions (the product's rows, lanes of tensor memory) of a head and NT tokens
@@ -125,6 +131,7 @@ __global__ void __launch_bounds__(kAbsorbThreads) absorb_kernel(const HeadProduc
     const uint32_t tmem = sm->tmem;
     if (warp == 4) {
         const bool ok = __all_sync(0xffffffffu, bar_wait(&sm->landed, 0, &sm->abort));
+        fence_after();
         if (ok && elect_one()) {
             constexpr uint32_t id = mma_idesc(true, 128, NT, 0) | 1u << 15;  // A across its rows
             const uint32_t a = smem_desc(su32(base), 16384), b = smem_desc(su32(base) + 32768, 16);
@@ -133,6 +140,7 @@ __global__ void __launch_bounds__(kAbsorbThreads) absorb_kernel(const HeadProduc
             mma_commit(&sm->done);
         }
         __syncwarp();
+        bar_drain(&sm->landed, 0);  // no copy lands after the CTA's end, whatever happened
     }
     if (warp < 4) {  // the rotations: a warp a token, a lane a pair
 #pragma unroll
@@ -184,115 +192,78 @@ __global__ void __launch_bounds__(kAbsorbThreads) absorb_kernel(const HeadProduc
 }
 
 // ---------------------------------------------------------------- outputs
-// Grid: pieces of TE output dimensions, the heads, tiles of TM tokens. Steps of 64 latent dimensions of
-// both operands pass through kStages places of shared memory. The f32 rows are rounded to bf16 for the
-// product, as the sums behind them have been: a relative 2^-8 of each at most, about the result's own
-// rounding once 512 of them are summed.
-template <int TM, int TE, int STAGES>
-__global__ void __launch_bounds__(kThreads) expand_kernel(const HeadProduct p) {
-    constexpr int kM = TM >= 32 ? 2 : 1, kWarpRows = TM / (16 * kM), kN = TE / 8 / (kWarps / kWarpRows) >= 2 ? TE / 8 / (kWarps / kWarpRows) : 2;
-    constexpr int kWarpCols = TE / (8 * kN), kShares = kWarps / (kWarpRows * kWarpCols);  // of a step's dimensions
-    static_assert(kShares >= 1 && kShares <= 4, "a share has at least 16 dimensions of a step");
-    constexpr int kSteps = kLatent / 64;
-    constexpr uint32_t kW = TE * 128, kX = TM * 256, kStage = kW + kX;  // W rows of 64 bf16, x rows of 64 f32
+// The f32 rows are rounded to bf16 for the products, as the sums behind them have been: 2^-8 of each at
+// most, of the size of the result's own rounding once 512 of them are summed.
+//
+// Few tokens of few heads: a CTA takes 32 output dimensions and 16 tokens, all copies under way at once,
+// eight steps of 64 latent dimensions. Its eight warps are two over the dimensions by four shares of a
+// step, whose sums are added up in their order (mma.sync m16n8k16, which has no set-up to wait for).
+constexpr int kFewTokens = 16, kFewDims = 32, kSteps = kLatent / 64, kShares = 4;
+constexpr uint32_t kStepW = kFewDims * 128, kStepX = kFewTokens * 256, kStep = kStepW + kStepX;  // rows of 64 bf16, of 64 f32
+constexpr uint32_t kFewSmem = kSteps * kStep;
+
+template <int S>
+__device__ __forceinline__ void steps_landed(int s) {  // steps up to s, of which each is a group of copies
+    if constexpr (S < kSteps) {
+        if (s == S) copies_landed<kSteps - 1 - S>();
+        else steps_landed<S + 1>(s);
+    }
+}
+
+__global__ void __launch_bounds__(kThreads) expand_few_kernel(const HeadProduct p) {
     extern __shared__ __align__(128) uint8_t smem[];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, e0 = blockIdx.x * TE, h = blockIdx.y;
-    const int64_t t0 = (int64_t)blockIdx.z * TM;
-    const float* in = (const float*)p.x + h * p.x_head;
-    const uint16_t* mat = p.w + h * p.w_head + e0 * p.w_row;
-    const int64_t pitch = (int64_t)p.heads * kHeadDim;
-    uint16_t* out = p.out + (int64_t)h * kHeadDim + e0 + t0 * pitch;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, e0 = blockIdx.x * kFewDims, h = blockIdx.y;
+    const int64_t t0 = (int64_t)blockIdx.z * kFewTokens, pitch = (int64_t)p.heads * kHeadDim;
+    const float* const in = (const float*)p.x + h * p.x_head;
+    const uint16_t* const mat = p.w + h * p.w_head + e0 * p.w_row;
+    uint16_t* const out = p.out + (int64_t)h * kHeadDim + e0 + t0 * pitch;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // 16-byte unit u of row t of x lies at u ^ 2 (t % 8): the eight rows of a fragment in different banks
-    auto fetch = [&](int s) {
-        if (s < kSteps) {
-            const uint32_t wa = su32(smem) + s % STAGES * kStage, xa = wa + kW;
-            for (int i = tid; i < TE * 8; i += kThreads) copy16(wa + at<8>(i >> 3, i & 7), mat + (i >> 3) * p.w_row + 64 * s + 8 * (i & 7), true);
-            for (int i = tid; i < TM * 16; i += kThreads) {
-                const int t = i >> 4, u = i & 15;
-                const bool there = t0 + t < p.n;
-                copy16(xa + t * 256 + ((u ^ (t & 7) << 1) << 4), in + (there ? t0 + t : 0) * p.x_token + 64 * s + 4 * u, there);
-            }
-        }
-        copies_end();
-    };
-    const int share = warp / (kWarpRows * kWarpCols), wr = warp / kWarpCols % kWarpRows, wc = warp % kWarpCols;
-    float acc[kM][kN][4] = {};
-#pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) fetch(s);
     for (int s = 0; s < kSteps; ++s) {
-        copies_landed<STAGES - 2>();
+        const uint32_t wa = su32(smem) + s * kStep, xa = wa + kStepW;
+        copy16(wa + at(tid >> 3, tid & 7), mat + (tid >> 3) * p.w_row + 64 * s + 8 * (tid & 7), true);
+        const int t = tid >> 4, u = tid & 15;
+        const bool there = t0 + t < p.n;
+        copy16(xa + t * 256 + ((u ^ (t & 7) << 1) << 4), in + (there ? t0 + t : 0) * p.x_token + 64 * s + 4 * u, there);
+        copies_end();
+    }
+    const int share = warp >> 1, col = (warp & 1) * 16;
+    float acc[2][4] = {};
+    for (int s = 0; s < kSteps; ++s) {
+        steps_landed<0>(s);
         __syncthreads();
-        fetch(s + STAGES - 1);
-        const uint8_t* const w = smem + s % STAGES * kStage;
-        const uint8_t* const x = w + kW;
+        const uint8_t* const w = smem + s * kStep;
+        const uint8_t* const x = w + kStepW;
+        uint32_t a[4], b[4];
 #pragma unroll
-        for (int k = share; k < 4; k += kShares) {
-            uint32_t a[kM][4];
-#pragma unroll
-            for (int m = 0; m < kM; ++m)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {  // rows g and g + 8, columns 2 c and 2 c + 8
-                    const int t = (wr * kM + m) * 16 + (lane >> 2) + 8 * (r & 1), u = 4 * k + 2 * (r >> 1) + ((lane & 3) >> 1);
-                    const float2 v = *reinterpret_cast<const float2*>(x + t * 256 + ((u ^ (t & 7) << 1) << 4) + 8 * (lane & 1));
-                    a[m][r] = pack(v.x, v.y);
-                }
-#pragma unroll
-            for (int n = 0; n < kN; n += 2) {
-                uint32_t c[4];  // 16 output dimensions by 16 latent ones
-                ldsm(c, su32(w) + at<8>((wc * kN + n) * 8 + (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)));
-#pragma unroll
-                for (int m = 0; m < kM; ++m) {
-                    mma(acc[m][n], a[m], c[0], c[1]);
-                    mma(acc[m][n + 1], a[m], c[2], c[3]);
-                }
-            }
+        for (int r = 0; r < 4; ++r) {  // rows g and g + 8, columns 2 c and 2 c + 8 of the share's 16
+            const int t = (lane >> 2) + 8 * (r & 1), u = 4 * share + 2 * (r >> 1) + ((lane & 3) >> 1);
+            const float2 v = *reinterpret_cast<const float2*>(x + t * 256 + ((u ^ (t & 7) << 1) << 4) + 8 * (lane & 1));
+            a[r] = pack(v.x, v.y);
         }
+        ldsm(b, su32(w) + at(col + (lane & 7) + ((lane >> 4) << 3), 2 * share + ((lane >> 3) & 1)));
+        mma(acc[0], a, b[0], b[1]);
+        mma(acc[1], a, b[2], b[3]);
     }
-    copies_landed<0>();
+    __syncthreads();  // the operands' place becomes the shares'
+    float* const sums = reinterpret_cast<float*>(smem);  // [kShares][kFewTokens][kFewDims]
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+            *reinterpret_cast<float2*>(sums + (share * kFewTokens + 8 * r + (lane >> 2)) * kFewDims + col + 8 * n + 2 * (lane & 3)) =
+                make_float2(acc[n][2 * r], acc[n][2 * r + 1]);
     __syncthreads();
-    // the shares are added up in their order, in what held the operands
-    auto place = [&](int m, int n, int r) { return ((wr * kM + m) * 16 + 8 * r + (lane >> 2)) * TE + (wc * kN + n) * 8 + 2 * (lane & 3); };
-    float* const sums = reinterpret_cast<float*>(smem + TM * TE * 2);  // [kShares - 1][TM][TE], behind the staged result
-    static_assert(TM * TE * 2 + (kShares - 1) * TM * TE * 4 <= STAGES * kStage, "room for the shares");
-    if (kShares > 1) {
-        if (share > 0)
+    const int t = tid >> 4, e = 2 * (tid & 15);  // a thread two dimensions of a token
+    float2 v = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int m = 0; m < kM; ++m)
-#pragma unroll
-                for (int n = 0; n < kN; ++n)
-#pragma unroll
-                    for (int r = 0; r < 2; ++r)
-                        *reinterpret_cast<float2*>(sums + (share - 1) * TM * TE + place(m, n, r)) = make_float2(acc[m][n][2 * r], acc[m][n][2 * r + 1]);
-        __syncthreads();
+    for (int s = 0; s < kShares; ++s) {
+        const float2 y = *reinterpret_cast<const float2*>(sums + (s * kFewTokens + t) * kFewDims + e);
+        v = make_float2(v.x + y.x, v.y + y.y);
     }
-    if (share == 0) {
-#pragma unroll
-        for (int m = 0; m < kM; ++m)
-#pragma unroll
-            for (int n = 0; n < kN; ++n)
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    float2 v = make_float2(acc[m][n][2 * r], acc[m][n][2 * r + 1]);
-#pragma unroll
-                    for (int s = 0; s < kShares - 1; ++s) {
-                        const float2 y = *reinterpret_cast<const float2*>(sums + s * TM * TE + place(m, n, r));
-                        v = make_float2(v.x + y.x, v.y + y.y);
-                    }
-                    const int t = (wr * kM + m) * 16 + 8 * r + (lane >> 2), e = wc * kN + n;
-                    *reinterpret_cast<uint32_t*>(smem + (t * (TE / 8) + (e ^ (t & (TE / 8 - 1) & 7))) * 16 + 4 * (lane & 3)) = pack(v.x, v.y);
-                }
-    }
-    __syncthreads();
-    constexpr int kOut = TE / 8;
-    for (int i = tid; i < TM * kOut; i += kThreads) {
-        const int t = i / kOut, u = i % kOut;
-        if (t0 + t < p.n) reinterpret_cast<uint4*>(out + t * pitch)[u] = *reinterpret_cast<const uint4*>(smem + (t * kOut + (u ^ (t & (kOut - 1) & 7))) * 16);
-    }
+    if (t0 + t < p.n) *reinterpret_cast<uint32_t*>(out + t * pitch + e) = pack(v.x, v.y);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
-template <int TM, int TE, int STAGES>
-constexpr uint32_t expand_smem() { return STAGES * (TE * 128 + TM * 256); }
 
 // Many tokens: a CTA keeps its head's whole matrix (128 output dimensions: the product's rows) and takes
 // tiles of 32 tokens (its columns), each by one of two groups of eight warps: they load a tile's f32 rows
@@ -422,7 +393,7 @@ cudaError_t set_up() {
     return (cudaError_t)devices.get(device, [](Ready*) {
         cudaError_t x = allow(absorb_kernel<16>, absorb_smem<16>());
         if (x == cudaSuccess) x = allow(absorb_kernel<64>, absorb_smem<64>());
-        if (x == cudaSuccess) x = allow(expand_kernel<16, 32, 8>, expand_smem<16, 32, 8>());
+        if (x == cudaSuccess) x = allow(expand_few_kernel, kFewSmem);
         if (x == cudaSuccess) x = allow(expand_many_kernel, kManySmem);
         return (int)x;
     }, &ready);
@@ -467,9 +438,8 @@ cudaError_t launch_expand_outputs(cudaStream_t stream, const HeadProduct& p, int
     if (e != cudaSuccess) return e;
     // few tokens of few heads: pieces of 32 output dimensions, while all CTAs run at once, two an SM (64
     // tokens of 16 heads: 3.0 us against 5.4; 16 of 128 heads: 4.7 against 4.1)
-    const int64_t small = kHeadDim / 32 * p.heads * tiles(p.n, 16);
-    if (small <= 2 * (int64_t)num_sms)
-        return launch_dependent(stream, dim3(kHeadDim / 32, p.heads, (unsigned)tiles(p.n, 16)), kThreads, expand_smem<16, 32, 8>(), expand_kernel<16, 32, 8>, p);
+    const dim3 few(kHeadDim / kFewDims, p.heads, (unsigned)tiles(p.n, kFewTokens));
+    if ((int64_t)few.x * few.y * few.z <= 2 * (int64_t)num_sms) return launch_dependent(stream, few, kThreads, kFewSmem, expand_few_kernel, p);
     CUtensorMap map;
     if (!encode(&map, p.w, kHeadDim, kLatent / 64, p.heads, p.w_row, p.heads > 1 ? p.w_head : kHeadDim * kLatent, kHeadDim, 2)) return cudaErrorInvalidValue;
     // all CTAs at once: a second round would read the matrices again (256 tokens of 128 heads: 20.5 us, 22.9 in two)

@@ -143,6 +143,61 @@ def test_entries_in_pinned_memory():
     check_entries(entries.cuda(), latent, rope, rope.double())
 
 
+@pytest.mark.parametrize("pooled", [False, True])
+def test_appended_latents(pooled):
+    """Tokens into histories: padding, requests and positions out of range, a resident one rewritten."""
+    R, C, S, n = 3, 20, 8, 26
+    word = hs.HS_STATUS_RANGE
+    if pooled:
+        store = torch.zeros((64, 656), dtype=torch.uint8).pin_memory()
+        ctx = hs.Context(R, C, S, 656, pool=(store.data_ptr(), 64, 656))
+        base, length = [40, 0, 21], [20, 13, 0]
+        ctx.set_extents(base, length)
+    else:
+        ctx = hs.Context(R, C, S, 656)
+        base, length = [0, C, 2 * C], [C] * 3
+    host = ctx.host_kv().reshape(-1, ctx.host_stride)
+    host[:] = 3
+    latent, rope = tokens(n, BF16, 4)
+    tab = lm.table(C + 3, 2).cuda()
+    req = torch.arange(n, dtype=torch.int32) % 3
+    pos = torch.arange(n, dtype=torch.int32) // 3
+    req[5], req[6], pos[7], pos[8], pos[9] = -1, R, -4, C, C - 1
+    turn = pos.clamp(min=0, max=C + 2) * 0 + torch.arange(n, dtype=torch.int32) % (C + 3)
+    turn[10] = C + 3  # no row
+    ctx.append_latents(latent, rope, pos.cuda(), requests=req.cuda(), rotation=tab, rotation_positions=turn.cuda())
+    assert ctx.status() == word
+    want = lm.rotate(rope, tab, turn.cuda().clamp(max=C + 2), False)
+    seen = set()
+    got = torch.from_numpy(host).cuda()
+    for i in range(n):
+        r, p = int(req[i]), int(pos[i])
+        if r < 0 or r >= R or p < 0 or p >= length[r] or i == 10:
+            continue
+        seen.add(base[r] + p)
+        check_entries(got[base[r] + p][None, :656], latent[i:i + 1], rope[i:i + 1], want[i:i + 1])
+    rest = [i for i in range(host.shape[0]) if i not in seen]
+    assert len(seen) >= 12 and (host[rest][:, :656] == 3).all()
+    ctx.clear_status()
+    # resident entries are rewritten in their slots, in fp16 and with halves this time
+    sel = torch.tensor([[0, 1, 2], [3, 2, 0], [-1, -1, -1]], dtype=torch.int32, device="cuda")
+    slots, miss = torch.empty_like(sel), torch.empty(R, dtype=torch.int32, device="cuda")
+    ctx.resolve(sel, slots, miss)
+    latent, rope = tokens(R, F16, 5)
+    ctx.append_latents(latent, rope, torch.tensor([1, 3, -1], dtype=torch.int32, device="cuda"), rotation=tab, halves=True)
+    lo, ro = torch.empty((R, 3, 512), dtype=BF16, device="cuda"), torch.empty((R, 3, 64), dtype=BF16, device="cuda")
+    ctx.read_latents(slots, lo, ro)
+    assert ctx.status() == 0
+    got = torch.from_numpy(host).cuda()
+    want = lm.rotate(rope, tab, torch.tensor([1, 3, 0], device="cuda"), True)
+    for r, p, j in ((0, 1, 1), (1, 3, 0)):
+        check_entries(got[base[r] + p][None, :656], latent[r:r + 1], rope[r:r + 1], want[r:r + 1])
+        a, b = lm.values(got[base[r] + p][:656])
+        assert torch.equal(lo[r, j], a.to(BF16)) and torch.equal(ro[r, j].double(), b)
+    assert not lo[2].any()
+    ctx.close()
+
+
 # ------------------------------------------------------------------------ the absorbed form
 @pytest.mark.parametrize("n,H,halves,turned", [(1, 128, False, True), (1, 1, True, True), (16, 3, True, True), (17, 5, False, True),
                                                (37, 20, True, True), (64, 16, False, True), (65, 2, False, False), (256, 8, False, True),
@@ -322,6 +377,39 @@ def test_a_captured_and_replayed_layer():
         layer()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, outs))
+
+
+def test_calls_on_two_streams_at_once():
+    """Nothing is shared between calls: each stream's results are those of its call alone."""
+    H, lens = 8, [(700, 900), (33, 33), (129, 400)]
+    sets = [prompts(lens, H, BF16, seed) for seed in (1, 2)]
+    n = 300
+    more = [(normal(gen(s), n, H, 192).to(BF16), normal(gen(s + 5), H, 256, 512).to(BF16), normal(gen(s + 9), n, H, 512)) for s in (3, 4)]
+    rows = sets[0][0].shape[0]
+
+    def outs():
+        return (torch.zeros((rows, H, 128), dtype=BF16, device="cuda"), torch.zeros((rows, H), device="cuda"),
+                torch.zeros((n, H, 576), dtype=BF16, device="cuda"), torch.zeros((n, H, 128), dtype=BF16, device="cuda"))
+
+    def calls(i, to, stream=None):
+        q, k, r, v, qs, ks = sets[i]
+        x, both, o = more[i]
+        hs.attend_prompts(q, k, r, v, qs, ks, to[0], to[1], 0.1, stream=stream)
+        hs.absorb_queries(x, both[:, :128], to[2], stream=stream)
+        hs.expand_outputs(o, both[:, 128:], to[3], stream=stream)
+
+    want = [outs(), outs()]
+    for i in (0, 1):
+        calls(i, want[i])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [outs(), outs()]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i in (0, 1):
+            calls(i, got[i], streams[i])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for i in (0, 1) for a, b in zip(got[i], want[i]))
 
 
 # ------------------------------------------------------------------------ a layer of a model

@@ -179,4 +179,4 @@ def test_every_kernel_waits_before_it_reads_and_none_leaves_before():
             depth = before.count("{") - before.count("}")
             assert depth == 0 and not re.search(r"\breturn\b|\bif\b|\bload\(|ld\.global|cp\.async", before), m.group(1)
             found.append(m.group(1))
-    assert sorted(found) == ["absorb_kernel", "expand_kernel", "expand_many_kernel", "prompt_kernel", "read_kernel", "write_kernel"]
+    assert sorted(found) == ["absorb_kernel", "expand_few_kernel", "expand_many_kernel", "prompt_kernel", "read_kernel", "write_kernel"]
