@@ -101,7 +101,7 @@ struct Order {
 };
 
 struct Maps {
-    CUtensorMap q, k, r, v;
+    CUtensorMap q, k, r, v;  // as an array of four, too
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -214,6 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
     uint8_t* ring = base + kQBytes;
     Smem* sm = reinterpret_cast<Smem*>(ring + kSlots * kChunk);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    tma_prefetch_map(&maps.q + (tid & 3));
 
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (tid == 0) {
