@@ -1,6 +1,9 @@
 """Latent entries, the absorbed form's products and prompts' attention on the GPU, against the 64-bit
 models of tests/latent_models.py: written codes and read values are equal, sums within derived bounds."""
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -300,6 +303,11 @@ def test_prompts_whose_tensors_end_with_them():
     check_prompts(lens, 3, BF16, True, prompts(lens, 3, BF16, 5))
 
 
+def test_prompts_without_any_key():
+    lens = [(3, 0), (140, 0)]
+    check_prompts(lens, 2, BF16, True, prompts(lens, 2, BF16, 5))
+
+
 @pytest.mark.parametrize("scale", [1e-6, 0.5, 30.0])
 def test_prompts_of_small_and_large_scores(scale):
     lens = [(150, 400), (33, 33)]
@@ -377,6 +385,36 @@ def test_a_captured_and_replayed_layer():
         layer()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, outs))
+
+
+FIRST = """
+import torch, hierarchical_kv_cache_swap_gb300 as hs
+z = lambda *s, t=torch.bfloat16: torch.zeros(s, dtype=t, device="cuda")
+lat, rope, ent, dest = z(3, 512), z(3, 64), z(4, 656, t=torch.uint8), torch.arange(3, device="cuda")
+slots, q, up, qo, o, oo = dest.int().view(1, 3), z(40, 2, 192) + 1, z(2, 128, 512) + 1, z(40, 2, 576), z(40, 2, 512, t=torch.float32) + 1, z(40, 2, 128)
+many = z(200, 128, 512, t=torch.float32) + 1, z(128, 128, 512) + 1, z(200, 128, 128)
+starts, po, pl = torch.tensor([0, 40], dtype=torch.int32, device="cuda"), z(40, 2, 128), z(40, 2, t=torch.float32)
+k = z(40, 2, 128) + 1
+torch.cuda.synchronize()
+graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+with torch.cuda.stream(side):
+    graph.capture_begin()
+    hs.write_latents(lat + 1, rope, dest, ent)
+    hs.read_latents(ent[None], slots, lat[None], rope[None])
+    hs.absorb_queries(q, up, qo)
+    hs.expand_outputs(o, up, oo)
+    hs.expand_outputs(*many)
+    hs.attend_prompts(q, k, z(40, 64), k, starts, starts, po, pl, 0.1)
+    graph.capture_end()
+graph.replay()
+torch.cuda.synchronize()
+assert (lat == 1).all() and (qo[..., :512] == 128).all() and (oo == 512).all() and (many[2] == 512).all() and (po == 1).all()
+"""
+
+
+def test_first_calls_of_a_process_are_captured():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run([sys.executable, "-c", FIRST], cwd=root, check=True, timeout=200)
 
 
 def test_calls_on_two_streams_at_once():
