@@ -90,6 +90,7 @@ struct Smem {  // beyond Q and the ring
     volatile int abort;
 };
 constexpr uint32_t kSmemBytes = 1024 + kQBytes + kSlots * kChunk + sizeof(Smem);
+static_assert(kSmemBytes <= 227 * 1024, "what a CTA may have");
 
 // The CTAs' order: groups of `heads` heads; within one the prompts' tiles, those with the most keys
 // first, and for each tile the heads. The long tiles of all heads of a group so start before its short
