@@ -794,7 +794,7 @@ int hs_absorb_queries(hs_stream_t stream, const hs_head_product* product, const 
     if (rc != HS_OK || (rc = rotation_check(rotation, p.n, nullptr, &rot)) != HS_OK ||
         (rc = steps_check({Step{"x_token", p.n, p.x_token}, Step{"x_head", p.heads, p.x_head}})) != HS_OK)
         return rc;
-    if (p.n > 1 << 22) return fail(HS_ERR_LIMIT, "n=%lld exceeds 2^22 tokens", (long long)p.n);
+    if (p.n > 65535 * 64) return fail(HS_ERR_LIMIT, "n=%lld exceeds 65535 tiles of 64 tokens", (long long)p.n);
     if ((rc = sm_count(&sms)) != HS_OK) return rc;
     cudaError_t e = hs::launch_absorb_queries((cudaStream_t)stream, p, rot, status, sms);
     if (e != cudaSuccess) return cuda_fail(e, "query absorption kernel launch");

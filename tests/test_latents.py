@@ -180,3 +180,12 @@ def test_every_kernel_waits_before_it_reads_and_none_leaves_before():
             assert depth == 0 and not re.search(r"\breturn\b|\bif\b|\bload\(|ld\.global|cp\.async", before), m.group(1)
             found.append(m.group(1))
     assert sorted(found) == ["absorb_kernel", "expand_few_kernel", "expand_many_kernel", "prompt_kernel", "read_kernel", "write_kernel"]
+
+
+def test_the_most_tokens_absorbed_are_what_a_grid_holds():
+    """65535 tiles of 64 tokens: one more is refused, not left to the launch to fail."""
+    lib = hs.load()
+    most = 65535 * 64
+    for n in (most + 1, 2**22):
+        assert lib.hs_absorb_queries(None, ctypes.byref(product(n=n)), None, None) == hs.HS_ERR_LIMIT
+    assert lib.hs_absorb_queries(None, ctypes.byref(product(n=most, heads=0)), None, None) == hs.HS_ERR_INVALID
