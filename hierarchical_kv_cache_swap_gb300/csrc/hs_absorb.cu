@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) expand_many_kernel(const Head
             const int64_t t = t0 + 16 * half + j + odd;
             if (t < p.n) *reinterpret_cast<uint32_t*>(to + t * pitch) = ok ? pack(lo, hi) : 0x7FFF7FFFu;
         }
-        if (!ok) break;
+        // after an abort, too: warps may differ in whether a wait ran out, and the others come here
         asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(kGroupThreads) : "memory");  // all have read the columns
     }
     // after an abort: no copy and no product may be under way at the CTA's end

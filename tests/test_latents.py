@@ -189,3 +189,24 @@ def test_the_most_tokens_absorbed_are_what_a_grid_holds():
     for n in (most + 1, 2**22):
         assert lib.hs_absorb_queries(None, ctypes.byref(product(n=n)), None, None) == hs.HS_ERR_LIMIT
     assert lib.hs_absorb_queries(None, ctypes.byref(product(n=most, heads=0)), None, None) == hs.HS_ERR_INVALID
+
+
+def body(name, kernel):
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "hierarchical_kv_cache_swap_gb300", "csrc")
+    with open(os.path.join(csrc, name)) as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    i = start = text.index("{", re.search(r"__global__ void __launch_bounds__\([^)]*\)\s*" + kernel + r"\b", text).end())
+    depth = 0
+    while True:
+        depth += {"{": 1, "}": -1}.get(text[i], 0)
+        i += 1
+        if depth == 0:
+            return text[start:i]
+
+
+def test_no_warp_leaves_a_loop_whose_barriers_the_others_wait_at():
+    """Warps may differ in whether a wait ran out: none of them leaves the output expansion's loop, which
+    holds barriers of the group."""
+    loop = body("hs_absorb.cu", "expand_many_kernel").split("for (int k = 0; t0 < p.n;")[1]
+    assert loop.count("bar.sync") == 2
+    assert not re.search(r"\b(break|return|continue|goto)\b", loop)
