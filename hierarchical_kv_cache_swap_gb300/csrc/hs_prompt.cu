@@ -552,6 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
                         for (int u = tid & (kRows - 1); ok && u < (64 - first) * 16; u += kRows)
                             at[(u & 8 ? 512 : 0) + (first + (u >> 4)) * 8 + (u & 7)] = make_uint4(0, 0, 0, 0);
                         fence_async_smem();
+                        __syncwarp();  // what follows is the whole warp's
                     }
                     tmem_wait_st();
                     fence_before();

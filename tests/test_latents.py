@@ -210,3 +210,10 @@ def test_no_warp_leaves_a_loop_whose_barriers_the_others_wait_at():
     loop = body("hs_absorb.cu", "expand_many_kernel").split("for (int k = 0; t0 < p.n;")[1]
     assert loop.count("bar.sync") == 2
     assert not re.search(r"\b(break|return|continue|goto)\b", loop)
+
+
+def test_the_softmax_warps_meet_again_before_their_stores_are_waited_for():
+    """Threads differ in how many values behind a prompt's end they make zeros, and the wait for a
+    warp's stores to tensor memory is the whole warp's."""
+    zeroes = body("hs_prompt.cu", "prompt_kernel").split("if (live < 64)")[1]
+    assert zeroes.index("fence_async_smem();") < zeroes.index("__syncwarp();") < zeroes.index("tmem_wait_st();")
