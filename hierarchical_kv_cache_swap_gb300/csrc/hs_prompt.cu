@@ -145,21 +145,35 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
 
 // Finds the prompt and the tile of it that the `at`-th of the prompts' tiles is, by one warp: 32
 // prompts at a time, their tiles counted and added up over the lanes. A prompt whose bounds are not in
-// order, or not within the rows there are, has no tiles. False: there are not so many; else *found is
-// true for the lane whose *item is filled in. The search goes on from where the last one ended: `from` is
-// a number of prompts, a multiple of 32, that have `before` <= at tiles.
-__device__ bool find_tile(const PromptAttention& A, int at, int& from, int64_t& before, Item* item, bool* found) {
+// order, or not within the rows there are, has no tiles, nor has one whose rows begin before the end of an
+// earlier one's (behind starts that descend): no row has two writers, and the tiles are never more than
+// the grid's. False: there are not so many; else *found is true for the lane whose *item is filled in.
+// The search goes on from where the last one ended.
+struct Search {
+    int from;        // a number of prompts, a multiple of 32, that have
+    int64_t before;  // so many tiles, no more than the last one looked for,
+    int end;         // and this as the largest end of those whose bounds are in order
+};
+__device__ bool find_tile(const PromptAttention& A, int at, Search& done, Item* item, bool* found) {
     const int lane = threadIdx.x & 31;
-    for (; from < A.B; from += 32) {
-        const int b = from + lane;
+    for (; done.from < A.B; done.from += 32) {
+        const int b = done.from + lane;
         int64_t q0 = 0, q1 = 0, k0 = 0, k1 = 0;
+        bool bad = false;
         if (b < A.B) {
             q0 = A.q_starts[b], q1 = A.q_starts[b + 1];
             k0 = A.k_starts[b], k1 = A.k_starts[b + 1];
-            if (q0 < 0 || q1 < q0 || q1 > A.q_rows || k0 < 0 || k1 < k0 || k1 > A.k_rows) {
-                if (A.status) atomicOr(A.status, 1u /* HS_STATUS_RANGE */);
-                q1 = q0 = k1 = k0 = 0;
-            }
+            bad = q0 < 0 || q1 < q0 || q1 > A.q_rows || k0 < 0 || k1 < k0 || k1 > A.k_rows;
+        }
+        int end = bad ? 0 : (int)q1;  // the largest of the lanes' so far
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) end = max(end, __shfl_up_sync(0xffffffffu, end, d));  // (a lane's own where there is none)
+        int ahead = __shfl_up_sync(0xffffffffu, end, 1);
+        ahead = lane > 0 ? max(ahead, done.end) : done.end;
+        bad = bad || (b < A.B && q0 < ahead);
+        if (bad) {
+            if (A.status) atomicOr(A.status, 1u /* HS_STATUS_RANGE */);
+            q1 = q0 = k1 = k0 = 0;
         }
         const int tiles = (int)((q1 - q0 + kTileRows - 1) / kTileRows);
         int upto = tiles;
@@ -168,17 +182,18 @@ __device__ bool find_tile(const PromptAttention& A, int at, int& from, int64_t& 
             const int x = __shfl_up_sync(0xffffffffu, upto, d);
             if (lane >= d) upto += x;
         }
-        const bool mine = at >= before + upto - tiles && at < before + upto;
+        const bool mine = at >= done.before + upto - tiles && at < done.before + upto;
         *found = mine;
         if (mine) {
             item->q0 = q0;
             item->k0 = k0;
             item->lq = (int)(q1 - q0);
             item->lk = (int)(k1 - k0);
-            item->row0 = (int)(before + upto - 1 - at) * kTileRows;  // the last rows, which see the most keys, first
+            item->row0 = (int)(done.before + upto - 1 - at) * kTileRows;  // the last rows, which see the most keys, first
         }
         if (__any_sync(0xffffffffu, mine)) return true;
-        before += __shfl_sync(0xffffffffu, upto, 31);
+        done.before += __shfl_sync(0xffffffffu, upto, 31);
+        done.end = max(done.end, __shfl_sync(0xffffffffu, end, 31));
     }
     return false;
 }
@@ -255,19 +270,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
         if (warp == kItemWarp) {
             // ------------------------------------------------------------ items
             uint32_t index = blockIdx.x, last = 0;
-            int from = 0;
-            int64_t before = 0;
+            Search done{0, 0, 0};
             for (int k = 0, asked = 0;;) {
                 const uint32_t group = index / order.per_group, in = index - group * order.per_group;
                 const uint32_t heads = min(order.heads, A.H - group * order.heads);
                 Item it;
                 bool found;
-                if (group != last || (int64_t)(in / heads) < before) {  // the prompts from the first again
-                    from = 0;
-                    before = 0;
-                }
+                if (group != last || (int64_t)(in / heads) < done.before) done = Search{0, 0, 0};  // the prompts from the first again
                 last = group;
-                if (find_tile(A, (int)(in / heads), from, before, &it, &found)) {
+                if (find_tile(A, (int)(in / heads), done, &it, &found)) {
                     if (k >= kItems) wait(&sm->item_free[k % kItems], k / kItems - 1);
                     if (!ok) break;
                     if (found) {

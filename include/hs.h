@@ -600,7 +600,8 @@ int hs_expand_outputs(hs_stream_t stream, const hs_head_product* product);
  * result, whatever they hold, and rows of q outside every prompt leave o and lse as they were. (With
  * `causal`, an infinity or a NaN among a key's values reaches the 128 rows of which some see the
  * key, the earlier ones with a weight of 0, so as NaN.) A prompt whose starts descend, or lie
- * outside the rows there are, is left out and sets HS_STATUS_RANGE. The products run on the tensor
+ * outside the rows there are, or whose rows begin before those of an earlier prompt end (behind
+ * starts that descend), is left out and sets HS_STATUS_RANGE. The products run on the tensor
  * cores in `dtype` with f32 sums; the softmax weights are rounded to it, relative to a maximum that
  * is at most 2^8 times too small. Rows of every tensor are contiguous and 16-byte aligned (strides
  * multiples of 8, positive where there is more than one row); rows of o that overlap are refused.
