@@ -651,7 +651,7 @@ struct Ready {};
 }  // namespace
 
 cudaError_t launch_attend_prompts(cudaStream_t stream, bool bf16, const PromptAttention& a) {
-    if (a.q_rows == 0 || a.B == 0) return cudaSuccess;
+    if (a.B == 0 || (a.q_rows == 0 && !a.status)) return cudaSuccess;
     static PerDevice<Ready> devices;
     int device = 0;
     cudaError_t e = cudaGetDevice(&device);
@@ -670,19 +670,22 @@ cudaError_t launch_attend_prompts(cudaStream_t stream, bool bf16, const PromptAt
     }, &ready);
     if (e != cudaSuccess) return e;
     Maps maps;
-    // without keys no copy is made of them: the maps then stand on the queries
-    const bool keys = a.k_rows > 0;
-    const int64_t n = keys ? a.k_rows : a.q_rows, q_head = a.H > 1 ? a.q_head : kQDims, q_token = a.q_rows > 1 ? a.q_token : kQDims;
+    // Without keys, or rows, no copy is made of them: their maps then are of one row at some aligned address.
+    const bool rows = a.q_rows > 0, keys = rows && a.k_rows > 0;
+    const uint16_t* const nothing = (const uint16_t*)((uintptr_t)a.q_starts & ~uintptr_t(15));
+    const int64_t m = rows ? a.q_rows : 1, n = keys ? a.k_rows : 1;
+    const int64_t q_head = rows && a.H > 1 ? a.q_head : kQDims, q_token = m > 1 ? a.q_token : kQDims;
     const int64_t k_head = keys && a.H > 1 ? a.k_head : kHeadDim, v_head = keys && a.H > 1 ? a.v_head : kHeadDim;
-    const int64_t k_token = keys && n > 1 ? a.k_token : kHeadDim, v_token = keys && n > 1 ? a.v_token : kHeadDim;
-    const int64_t r_token = keys && n > 1 ? a.r_token : kRope;
-    if (!encode(&maps.q, bf16, a.q, kQDims, a.H, a.q_rows, q_head, q_token, kRows, kKChunks) ||
-        !encode(&maps.k, bf16, keys ? a.k : a.q, kHeadDim, a.H, n, k_head, k_token, kKeys, 1) ||
-        !encode(&maps.v, bf16, keys ? a.v : a.q, kHeadDim, a.H, n, v_head, v_token, 64, kHeadDim / 64) ||
-        !encode_rope(&maps.r, bf16, keys ? a.k_rope : a.q, n, r_token))
+    const int64_t k_token = n > 1 ? a.k_token : kHeadDim, v_token = n > 1 ? a.v_token : kHeadDim;
+    const int64_t r_token = n > 1 ? a.r_token : kRope;
+    if (!encode(&maps.q, bf16, rows ? a.q : nothing, kQDims, a.H, m, q_head, q_token, kRows, kKChunks) ||
+        !encode(&maps.k, bf16, keys ? a.k : nothing, kHeadDim, a.H, n, k_head, k_token, kKeys, 1) ||
+        !encode(&maps.v, bf16, keys ? a.v : nothing, kHeadDim, a.H, n, v_head, v_token, 64, kHeadDim / 64) ||
+        !encode_rope(&maps.r, bf16, keys ? a.k_rope : nothing, n, r_token))
         return cudaErrorInvalidValue;
-    // a CTA for every 256 rows of a prompt, at most one more than full ones for each prompt
-    const int64_t tiles = a.q_rows / kTileRows + a.B;
+    // a CTA for every 256 rows of a prompt, at most one more than full ones for each prompt; without rows one,
+    // which only looks the starts over
+    const int64_t tiles = rows ? a.q_rows / kTileRows + a.B : 1;
     // as many heads to a group as keep their keys and values in 64 MB, half of L2, and at most 16
     constexpr int64_t kShared = 64 << 20;
     const int64_t fit = kShared / ((a.k_rows > 0 ? a.k_rows : 1) * 4 * kHeadDim), heads = fit < 1 ? 1 : fit < 16 ? fit : 16;
@@ -690,7 +693,7 @@ cudaError_t launch_attend_prompts(cudaStream_t stream, bool bf16, const PromptAt
     order.heads = (uint32_t)(heads < a.H ? heads : a.H);
     order.per_group = (uint32_t)(order.heads * tiles);
     order.wide = (((uintptr_t)a.o | (uintptr_t)(a.o_token * 2) | (uintptr_t)(a.o_head * 2)) & 31) == 0;
-    return launch_dependent(stream, dim3((unsigned)(tiles * a.H)), kThreads, kSmemBytes, bf16 ? prompt_kernel<true> : prompt_kernel<false>, a, order,
+    return launch_dependent(stream, dim3((unsigned)(rows ? tiles * a.H : 1)), kThreads, kSmemBytes, bf16 ? prompt_kernel<true> : prompt_kernel<false>, a, order,
                             maps);
 }
 

@@ -37,3 +37,17 @@ def test_a_prompt_behind_descending_starts_does_not_cost_another_its_rows(before
     for a, b, c, d in ((0, 1000, 0, 900), (1000, 1256, 1205, 1605)):
         wo, wl, bo, bl = lm.attend(q[a:b], k[c:d], r[c:d], v[c:d], 0.1, True, BF16)
         assert lm.near(o[a:b], wo, bo) and lm.near(lse[a:b], wl, bl), (a, b)
+
+
+@pytest.mark.parametrize("rows,keys", [(0, 20), (0, 0), (5, 0)])
+def test_starts_outside_tensors_without_rows_or_keys_are_reported(rows, keys):
+    H = 3
+    q, k, r, v, *_ = prompts([(rows, keys)], H, BF16, 3)
+    o, lse = torch.full((rows, H, 128), 7.0, dtype=BF16, device="cuda"), torch.full((rows, H), 7.0, device="cuda")
+    for qs, ks, bad in ((starts(0, rows), starts(0, keys), False), (starts(0, rows + 1), starts(0, keys), True),
+                        (starts(0, 0, rows, rows), starts(0, 0, keys, keys + 1), True), (starts(*[0] * 50, -1), starts(*[0] * 51), True)):
+        word = status_word()
+        hs.attend_prompts(q, k, r, v, qs, ks, o, lse, 0.1, status=word)
+        assert int(word) == (hs.HS_STATUS_RANGE if bad else 0)
+        hs.attend_prompts(q, k, r, v, qs, ks, o, lse, 0.1)
+        torch.cuda.synchronize()
