@@ -19,8 +19,9 @@
 //   * four warps a row tile hold a row a thread: no value crosses lanes. The maximum m of a row moves
 //     only when a tile's exceeds it by more than 8 (log2), and O is then rescaled in tensor memory; P =
 //     2^(x - m) stays below 2^8 and is rounded to the operands' type for the product (2^-8 or 2^-11 of
-//     each weight at most, as the queries and keys have been), the sum is of the unrounded f32 values.
-//     P goes to the products by halves of its keys.
+//     each weight at most, as the queries and keys have been; fp16, held at 2^7 times P, has no better than
+//     2^-32 of the kept maximum for weights below 2^-21 of it), the sum is of the unrounded f32 values. P
+//     goes to the products by halves of its keys.
 // Keys past a prompt's end that a tile reads (the next prompt's, or zeros behind the tensor) are masked
 // in S, and their values zeroed in shared memory, whatever they hold.
 //
@@ -69,6 +70,10 @@ static_assert(2 * kSoftRegs + kIssueRegs <= 3 * kLaunchRegs, "the split stays wi
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;      // row tile w: scores (P over their first half) at + 128 w
 constexpr float kRescaleLog2 = 8.f;
+// P is held at 2^lift times the weights: fp16 has its smallest numbers at 2^-24, so that it would lose what
+// weights below that add up to (16383 of 2^-25.5 are 2^-11.5); 2^(7 + 8) is still half of its largest.
+template <bool BF16>
+constexpr float kLiftLog2 = BF16 ? 0.f : 7.f;
 
 constexpr int kItems = 4;  // that may be known ahead
 
@@ -541,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
                     l *= f;
                 }
                 if (move) m = best;
-                const float from = m == -INFINITY ? 0.f : -m;
+                const float from = m == -INFINITY ? 0.f : kLiftLog2<BF16> - m;
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
@@ -606,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
                 }
             }
             if (there)
-                A.lse[to * A.H + h] = !ok ? none : l == 0.f ? -INFINITY : (m + lg2(l)) * 0.69314718055994531f;
+                A.lse[to * A.H + h] = !ok ? none : l == 0.f ? -INFINITY : (m + (lg2(l) - kLiftLog2<BF16>)) * 0.69314718055994531f;
             t0 += nt;
             c0 += n;
             if (!ok) break;

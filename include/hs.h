@@ -602,8 +602,8 @@ int hs_expand_outputs(hs_stream_t stream, const hs_head_product* product);
  * key, the earlier ones with a weight of 0, so as NaN.) A prompt whose starts descend, or lie
  * outside the rows there are, or whose rows begin before those of an earlier prompt end (behind
  * starts that descend), is left out and sets HS_STATUS_RANGE. The products run on the tensor
- * cores in `dtype` with f32 sums; the softmax weights are rounded to it, relative to a maximum that
- * is at most 2^8 times too small. Rows of every tensor are contiguous and 16-byte aligned (strides
+ * cores in `dtype` with f32 sums; the softmax weights are rounded to it, in fp16 to within 2^-32 of
+ * the row's largest at the least. Rows of every tensor are contiguous and 16-byte aligned (strides
  * multiples of 8, positive where there is more than one row); rows of o that overlap are refused.
  * HS_STATUS_TIMEOUT: a hand-off within the kernel was lost (a defect); rows may then be NaN, or
  * missing. Returns HS_OK, HS_ERR_INVALID, HS_ERR_LIMIT or HS_ERR_CUDA.

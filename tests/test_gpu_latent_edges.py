@@ -51,3 +51,56 @@ def test_starts_outside_tensors_without_rows_or_keys_are_reported(rows, keys):
         assert int(word) == (hs.HS_STATUS_RANGE if bad else 0)
         hs.attend_prompts(q, k, r, v, qs, ks, o, lse, 0.1)
         torch.cuda.synchronize()
+
+
+# ------------------------------------------------------------------------ weights
+def small_weights(n, less, dtype):
+    """A prompt of one row: key n weighs 1, and each of the n before it 2^-less; dimension 0 of the
+    values is theirs alone, dimension 1 the dominant key's, dimension 2 everyone's."""
+    q, k, r, v, qs, ks = prompts([(1, n + 1)], 1, dtype, 12)
+    for t in (q, k, r, v):
+        t.zero_()
+    q[0, 0, 0], k[n, 0, 0] = 1, less * 0.6931471805599453
+    v[:n, 0, 0], v[n, 0, 1], v[:, 0, 2] = 1, 1, 1
+    return q, k, r, v, qs, ks
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("n,less,first", [(16383, 25.5, True), (16383, 25.5, False), (4000, 23.3, True), (100000, 27.0, True), (100000, 27.0, False)])
+def test_weights_far_below_the_largest_are_not_lost(n, less, first, dtype):
+    """Many keys of weights that half precision holds poorly or not at all, behind a dominant key (whose
+    maximum is then there from the first tile) or ahead of it.
+
+    A weight w is rounded to the operands' type: by half a step u of itself, and in half precision by 2^-25
+    at the least; weights being held at 2^7 times their size or more, that is 2^-32 of the largest. exp2,
+    the score's and the exponent's f32 roundings, 2^-24 of at most 18 each, change it by 2^-18 of itself at
+    most; sums of n terms by n 2^-23; the result is rounded, by 2^-25 at the least."""
+    q, k, r, v, qs, ks = small_weights(n, less, dtype)
+    if first:
+        for t in (k, v):
+            t.copy_(t.flip(0))
+    o, lse = torch.full((1, 1, 128), 7.0, dtype=dtype, device="cuda"), torch.full((1, 1), 7.0, device="cuda")
+    word = status_word()
+    hs.attend_prompts(q, k, r, v, qs, ks, o, lse, 1.0, causal=False, status=word)
+    assert int(word) == 0
+    w = torch.softmax(k[:, 0, 0].double(), 0)
+    want, u = torch.einsum("k,kd->d", w, v[:, 0].double()), lm.half_step(dtype)
+    least = 2.0 ** -25 if dtype == F16 else 2.0 ** -134
+    bound = (2 * u + 2.0 ** -18 + (n + 16) * 2.0 ** -23) * want + 2.0 ** -32 * v[:, 0].double().sum(0) + least
+    assert (want[0] > 2.0 ** -13) and ((o[0, 0].double() - want).abs() <= bound).all(), (o[0, 0, :3], want[:3], bound[:3])
+    ref = torch.logsumexp(k[:, 0, 0].double(), 0)
+    assert abs(float(lse) - float(ref)) <= 2.0 ** -18 + (n + 16) * 2.0 ** -23 + 2.0 ** -22 * float(ref)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("scale", [0.5, 5.0])
+def test_maxima_that_grow_in_small_steps(scale, dtype):
+    """The kept maximum lags behind by up to 2^8: weights above 1, which half precision has to hold too."""
+    n = 2000
+    q, k, r, v, qs, ks = prompts([(130, n)], 2, dtype, 14)
+    q.abs_()
+    k.copy_((torch.arange(n, device="cuda")[:, None, None] / 2048.0 * torch.ones_like(k)).to(dtype))
+    o, lse = torch.empty((130, 2, 128), dtype=dtype, device="cuda"), torch.empty((130, 2), device="cuda")
+    hs.attend_prompts(q, k, r, v, qs, ks, o, lse, scale, causal=False)
+    wo, wl, bo, bl = lm.attend(q, k, r, v, scale, False, dtype)
+    assert lm.near(o, wo, bo) and lm.near(lse, wl, bl)
