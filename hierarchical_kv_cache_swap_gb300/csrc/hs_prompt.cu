@@ -203,14 +203,15 @@ __device__ bool find_tile(const PromptAttention& A, int at, Search& done, Item* 
     return false;
 }
 
-// The key tiles that row tile w of an item sees: row i sees the keys below i + 1 + lk - lq (causal), or all.
-__device__ __forceinline__ int key_tiles(const Item& it, int w, int causal) {
+// The keys that some row of an item's row tile w sees, of which its last row sees all: row i sees the keys
+// below i + 1 + lk - lq (causal), or all. And the key tiles they are in.
+__device__ __forceinline__ int keys_seen(const Item& it, int w, int causal) {
     const int first = it.row0 + w * kRows;
     if (first >= it.lq) return 0;
     const int last = min(first + kRows, it.lq);
-    const int seen = causal ? min(max(last + it.lk - it.lq, 0), it.lk) : it.lk;
-    return (seen + kKeys - 1) / kKeys;
+    return causal ? min(max(last - it.lq + it.lk, 0), it.lk) : it.lk;
 }
+__device__ __forceinline__ int key_tiles(const Item& it, int w, int causal) { return (keys_seen(it, w, causal) + kKeys - 1) / kKeys; }
 
 // Asks for the index of a CTA of this grid that has not begun, which then never will: its work is this
 // CTA's. The answer lands at `to`, counted on `bar`.
@@ -394,11 +395,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
                 }
                 if (to == kKChunks) mma_commit(&sm->s_full[w]);
             };
-            auto values = [&](int t, int c, int add) {
+            // `keys` of the tile's are seen: the products end with the 16 that the last of them is in, and no
+            // later key's value comes near the tile's rows, whatever it is.
+            auto values = [&](int t, int c, int add, int keys) {
                 const int slot = (t * kTileChunks + kKChunks + c) % kSlots;
                 const uint32_t b = v_at + slot * (kChunk / 16);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) mma_ts(o_col, s_col + 32 * c + 8 * k, b + 128 * k, id_o, (c | k) ? 1u : add);
+                for (int k = 0; k < 4; ++k)
+                    if (64 * c + 16 * k < keys) mma_ts(o_col, s_col + 32 * c + 8 * k, b + 128 * k, id_o, (c | k) ? 1u : add);
                 mma_commit(&sm->free[slot]);
             };
             auto skip = [&](int t, int part) {  // a part that only the other tile reads
@@ -423,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
                 const Item it = sm->item[k % kItems];
                 bar_arrive(&sm->item_free[k % kItems]);
                 if (!ok || it.lq == 0) break;
-                const int n = key_tiles(it, w, A.causal), nt = max(n, key_tiles(it, 1 - w, A.causal));
+                const int n = key_tiles(it, w, A.causal), nt = max(n, key_tiles(it, 1 - w, A.causal)), seen = keys_seen(it, w, A.causal);
                 // Of every item, or this warp could give the queries' place back twice before the copies
                 // take it once: a wait for the first time would then see the phase after it.
                 until(&sm->q_full[w], k);
@@ -452,10 +456,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
                     take();
                     if (ok && i < n) {
                         fence_after();
-                        values(t, 0, i);
+                        values(t, 0, i, seen - i * kKeys);
                         until(&sm->p_full[w][1], c0 + i);
                         fence_after();
-                        if (ok) values(t, 1, i);
+                        if (ok) values(t, 1, i, seen - i * kKeys);
                         if (ok && next) {
                             scores(t + 1, 0, 1);
                             landed(t + 1, kKeys12);
@@ -495,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
             if (it.lq == 0) break;
             const int n = key_tiles(it, w, A.causal), nt = max(n, key_tiles(it, 1 - w, A.causal)), lk = it.lk;
             const int row = it.row0 + w * kRows + (tid & (kRows - 1));  // of the prompt
-            const int seen = row < it.lq ? (A.causal ? min(max(row + 1 + lk - it.lq, 0), lk) : lk) : 0;
+            const int seen = row < it.lq ? (A.causal ? min(max(row + 1 - it.lq + lk, 0), lk) : lk) : 0;
             float m = -INFINITY, l = 0.f;
             for (int i = 0; i < n; ++i) {
                 const int here = seen - i * kKeys;  // keys of this tile that the row sees

@@ -598,8 +598,9 @@ int hs_expand_outputs(hs_stream_t stream, const hs_head_product* product);
  * or with `causal` j <= i + Lk - Lq: o = sum_j softmax_j(s) v_j, lse = ln sum_j exp(s_j). A row
  * that sees no key gets o = 0 and lse = -inf. Keys behind a prompt's last are not read into its
  * result, whatever they hold, and rows of q outside every prompt leave o and lse as they were. (With
- * `causal`, an infinity or a NaN among a key's values reaches the 128 rows of which some see the
- * key, the earlier ones with a weight of 0, so as NaN.) A prompt whose starts descend, or lie
+ * `causal`, an infinity or a NaN among a key's values reaches rows that do not see the key, with a weight
+ * of 0, so as NaN: those of the same 128, from the prompt's first row on, of which the last one sees
+ * the key or one of the 15 before it.) A prompt whose starts descend, or lie
  * outside the rows there are, or whose rows begin before those of an earlier prompt end (behind
  * starts that descend), is left out and sets HS_STATUS_RANGE. The products run on the tensor
  * cores in `dtype` with f32 sums; the softmax weights are rounded to it, in fp16 to within 2^-32 of

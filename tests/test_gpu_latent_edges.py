@@ -104,3 +104,32 @@ def test_maxima_that_grow_in_small_steps(scale, dtype):
     hs.attend_prompts(q, k, r, v, qs, ks, o, lse, scale, causal=False)
     wo, wl, bo, bl = lm.attend(q, k, r, v, scale, False, dtype)
     assert lm.near(o, wo, bo) and lm.near(lse, wl, bl)
+
+
+# ------------------------------------------------------------------------ values that are not finite
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("lq,lk", [(256, 306), (256, 256), (300, 300), (130, 1000), (256, 100), (40, 41), (600, 615)])
+def test_what_an_infinite_value_reaches_under_a_causal_mask(lq, lk, dtype):
+    """Rows that see the key: what the definition gives. Rows that do not: nothing, unless one of the same
+    128 rows sees the key or one of the 15 before it (then the row may be NaN)."""
+    H, scale = 2, 0.1
+    q, k, r, v, qs, ks = prompts([(lq, lk)], H, dtype, 13)
+    tiles = [(a, min(a + 128, lq)) for a in range(0, lq, 128)]
+    seen = [max(0, min(lk, b + lk - lq)) for _, b in tiles]  # by a tile's last row, which sees the most
+    keys = {x for s in seen for x in (s - 1, s, -(-s // 16) * 16 - 1, -(-s // 16) * 16, s + 40) if 0 <= x < lk}
+    for key in sorted(keys):
+        vv = v.clone()
+        vv[key, 0, 5], vv[key, 1, 6] = float("inf"), float("nan")
+        o, lse = torch.full((lq, H, 128), 7.0, dtype=dtype, device="cuda"), torch.full((lq, H), 7.0, device="cuda")
+        word = status_word()
+        hs.attend_prompts(q, k, r, vv, qs, ks, o, lse, scale, status=word)
+        assert int(word) == 0
+        wo, wl, bo, bl = lm.attend(q, k, r, vv, scale, True, dtype)
+        assert lm.near(lse, wl, bl)
+        for (a, b), s in zip(tiles, seen):
+            row = torch.arange(a, b, device="cuda")
+            free = (key > row + lk - lq) & (key < -(-s // 16) * 16)  # not seen, but within the products
+            for h, d in ((0, 5), (1, 6)):
+                assert (torch.isnan(o[a:b, h, d]) | ~free | (wo[a:b, h, d] == 0)).all()
+                o[a:b, h, d] = torch.where(free, wo[a:b, h, d].to(dtype), o[a:b, h, d])
+        assert lm.near(o, wo, bo), (key, seen)
