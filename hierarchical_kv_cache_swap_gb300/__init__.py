@@ -135,6 +135,7 @@ SIGNATURES = {
     "hs_absorb_queries": (_I, [_VP, _VP, _VP, _VP]),
     "hs_expand_outputs": (_I, [_VP, _VP]),
     "hs_attend_prompts": (_I, [_VP, _VP]),
+    "hs_set_latent_waits": (_I, [ctypes.c_uint64, ctypes.c_uint]),
     "hs_status_word": (_VP, [_VP]),
     "hs_device": (_I, [_VP]),
     "hs_kernels_per_call": (_I, [_VP]),
@@ -331,6 +332,14 @@ def attend_prompts(q, k, k_rope, v, q_starts, k_starts, o, lse, sm_scale: float,
     k_starts int32 [B + 1] bound in k and v [keys, heads, 128] and k_rope [keys, 64] (rotated);
     bf16 or fp16, rows contiguous. status: a device int32 word [1], or None."""
     (_torch_binding or _native()).attend_prompts(q, k, k_rope, v, q_starts, k_starts, o, lse, sm_scale, causal, status, stream)
+
+
+def set_latent_waits(ns: int = 1_000_000_000, stall: bool = False) -> None:
+    """hs_set_latent_waits: the limit of a wait within the kernels of the latent calls that this
+    thread makes from now on; `stall` (tests) makes their first wait run out."""
+    lib = load_library()
+    if lib.hs_set_latent_waits(int(ns), HS_FLAG_TEST_STALL if stall else 0) != HS_OK:
+        raise HsError(f"hs_set_latent_waits failed: {last_error()}")
 
 
 class Pool:

@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kAbsorbThreads) absorb_kernel(const HeadProduc
     }
     const uint32_t tmem = sm->tmem;
     if (warp == 4) {
-        const bool ok = __all_sync(0xffffffffu, bar_wait(&sm->landed, 0, &sm->abort));
+        const bool ok = __all_sync(0xffffffffu, bar_wait(&sm->landed, 0, &sm->abort, p.waits.ns));
         fence_after();
         if (ok && elect_one()) {
             constexpr uint32_t id = mma_idesc(true, 128, NT, 0) | 1u << 15;  // A across its rows
@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kAbsorbThreads) absorb_kernel(const HeadProduc
             mma_commit(&sm->done);
         }
         __syncwarp();
-        bar_drain(&sm->landed, 0);  // no copy lands after the CTA's end, whatever happened
+        bar_drain(&sm->landed, 0, p.waits.ns);  // no copy lands after the CTA's end, whatever happened
     }
     if (warp < 4) {  // the rotations: a warp a token, a lane a pair
 #pragma unroll
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kAbsorbThreads) absorb_kernel(const HeadProduc
         }
     }
     if (warp < 4) {
-        const bool ok = __all_sync(0xffffffffu, bar_wait(&sm->done, 0, &sm->abort));
+        const bool ok = __all_sync(0xffffffffu, bar_wait(&sm->done, 0, &sm->abort, p.waits.ns));
         fence_after();
         if (!ok && lane == 0 && status) atomicOr(status, 8u /* HS_STATUS_TIMEOUT */);
         const int odd = lane & 1, unit = (warp & 1) * 4 + (lane >> 3), byte = (lane & 6) * 2;  // of the 128-byte row of 64 dimensions
@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) expand_many_kernel(const Head
         asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(kGroupThreads) : "memory");
         if (t0 + step < p.n) fetch(t0 + step);
         if ((warp & 7) == 0) {
-            ok = __all_sync(0xffffffffu, ok && bar_wait(&sm->landed, 0, &sm->abort));
+            ok = __all_sync(0xffffffffu, ok && bar_wait(&sm->landed, 0, &sm->abort, p.waits.ns));
             fence_after();
             if (ok && elect_one()) {
                 constexpr uint32_t id = mma_idesc(true, kHeadDim, kTokens, 0);
@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) expand_many_kernel(const Head
             }
             __syncwarp();
         }
-        ok = __all_sync(0xffffffffu, ok && bar_wait(&sm->done[group], k & 1, &sm->abort));
+        ok = __all_sync(0xffffffffu, ok && bar_wait(&sm->done[group], k & 1, &sm->abort, p.waits.ns));
         fence_after();
         // warps w and w + 4 share 32 output dimensions: half of the columns each
         uint32_t d[16];
@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) expand_many_kernel(const Head
         asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(kGroupThreads) : "memory");  // all have read the columns
     }
     // after an abort: no copy and no product may be under way at the CTA's end
-    if (threadIdx.x == 0) bar_drain(&sm->landed, 0);
+    if (threadIdx.x == 0) bar_drain(&sm->landed, 0, p.waits.ns);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     fence_before();
     __syncthreads();

@@ -678,6 +678,18 @@ int hs_attend_pages(hs_stream_t stream, const hs_page_attention* a) {
     return HS_OK;
 }
 
+// The calling thread's (hs_set_latent_waits).
+static thread_local hs::Waits g_latent_waits{hs::kLatentWaitNs, 0};
+
+int hs_set_latent_waits(uint64_t ns, unsigned flags) {
+    if (flags & ~(unsigned)HS_FLAG_TEST_STALL) return fail(HS_ERR_INVALID, "unknown flags 0x%x", flags);
+    if (ns < hs::kMinWaitNs || ns > hs::kMaxWaitNs)
+        return fail(HS_ERR_INVALID, "wait limit %llu ns outside [%llu, %llu]", (unsigned long long)ns,
+                    (unsigned long long)hs::kMinWaitNs, (unsigned long long)hs::kMaxWaitNs);
+    g_latent_waits = hs::Waits{ns, (flags & HS_FLAG_TEST_STALL) ? 1 : 0};
+    return HS_OK;
+}
+
 static int latent_rows_check(int dtype, const hs_latent_rows* r, int64_t n, hs::LatentRows* out) {
     if (dtype != HS_BF16 && dtype != HS_F16) return fail(HS_ERR_INVALID, "unknown dtype %d", dtype);
     if (!r) return fail(HS_ERR_INVALID, "null latent rows");
@@ -783,7 +795,7 @@ static int product_check(const hs_head_product* p, int align, hs::HeadProduct* o
     const int rc = steps_check({Step{"w_head", p->heads, p->w_head_stride}, Step{"w_row", 2, p->w_row_stride}});
     if (rc != HS_OK) return rc;
     *out = hs::HeadProduct{p->x, p->x_token_stride, p->x_head_stride, (const uint16_t*)p->w, p->w_head_stride, p->w_row_stride,
-                           (uint16_t*)p->out, p->n, p->heads};
+                           (uint16_t*)p->out, p->n, p->heads, g_latent_waits};
     return HS_OK;
 }
 
@@ -860,6 +872,7 @@ int hs_attend_prompts(hs_stream_t stream, const hs_prompt_attention* a) {
     p.H = a->heads;
     p.causal = a->causal != 0;
     p.scale = a->sm_scale;
+    p.waits = g_latent_waits;
     cudaError_t e = hs::launch_attend_prompts((cudaStream_t)stream, a->dtype == HS_BF16, p);
     if (e != cudaSuccess) return cuda_fail(e, "prompt attention kernel launch");
     g_err[0] = 0;

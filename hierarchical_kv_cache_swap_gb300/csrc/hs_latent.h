@@ -32,6 +32,14 @@ __device__ __forceinline__ float2 turn(float x, float y, float c, float s) {
 }
 #endif
 
+// The waits of a call's kernel: the limit of each, in nanoseconds, and (tests) whether the first copy is
+// withheld, so that they run out (hs_set_latent_waits).
+constexpr uint64_t kLatentWaitNs = 1000000000ull;
+struct Waits {
+    uint64_t ns;
+    int stall;
+};
+
 // Rows of n tokens, 16-bit floats, 16-byte aligned, `latent_stride` and `rope_stride` elements apart.
 struct LatentRows {
     const uint16_t* latent;
@@ -59,6 +67,7 @@ struct HeadProduct {
     uint16_t* out;            // contiguous
     int64_t n;
     int heads;
+    Waits waits;
 };
 // bf16 x [n][heads][128 + 64] -> out [n][heads][512 + 64]: x[:128] w[h], then x[128:] rotated.
 cudaError_t launch_absorb_queries(cudaStream_t stream, const HeadProduct& p, const Rotation& rot, uint32_t* status, int num_sms);
@@ -79,6 +88,7 @@ struct PromptAttention {
     int B, H;
     int causal;
     float scale;
+    Waits waits;
 };
 cudaError_t launch_attend_prompts(cudaStream_t stream, bool bf16, const PromptAttention& a);
 

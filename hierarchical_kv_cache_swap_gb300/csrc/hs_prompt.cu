@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
     if (warp >= kSoftWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
         bool ok = true;
-        auto wait = [&](uint64_t* b, int parity) { ok = __all_sync(0xffffffffu, ok && bar_wait(b, parity & 1, &sm->abort)); };
+        auto wait = [&](uint64_t* b, int parity) { ok = __all_sync(0xffffffffu, ok && bar_wait(b, parity & 1, &sm->abort, A.waits.ns)); };
         if (warp == kItemWarp) {
             // ------------------------------------------------------------ items
             uint32_t index = blockIdx.x, last = 0;
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
                 __syncwarp();
                 wait(&sm->answered, asked++);
                 if (!ok) {
-                    bar_drain(&sm->answered, (asked - 1) & 1);  // the answer lands before the CTA's end
+                    bar_drain(&sm->answered, (asked - 1) & 1, A.waits.ns);  // the answer lands before the CTA's end
                     break;
                 }
                 const bool more = block_given(sm->answer, &index);
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
             const bool leader = elect_one();
             int t0 = 0, issued = 0, asked = -1;  // chunks; the last item whose queries are on their way
             for (int k = 0; leader; ++k) {
-                auto until = [&](uint64_t* bar, int parity) { ok = ok && bar_wait(bar, parity & 1, &sm->abort); };
+                auto until = [&](uint64_t* bar, int parity) { ok = ok && bar_wait(bar, parity & 1, &sm->abort, A.waits.ns); };
                 until(&sm->item_full[k % kItems], k / kItems);
                 const Item it = sm->item[k % kItems];
                 bar_arrive(&sm->item_free[k % kItems]);
@@ -358,7 +358,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
                     uint64_t* const full = &sm->full[(t0 + i) & 1][part];
                     if (c != 2) bar_expect_tx(full, part == kKeys12 ? 2 * kChunk : kChunk);
                     const uint32_t to = su32(ring) + slot * kChunk;
-                    if (c < kHeadDim / 64) tma_load_4d(to, &maps.k, 0, key, c, it.h, full);
+                    if (A.waits.stall && g == 0) {}  // (tests) announced, and never made
+                    else if (c < kHeadDim / 64) tma_load_4d(to, &maps.k, 0, key, c, it.h, full);
                     else if (c < kKChunks) tma_load_2d(to, &maps.r, 0, key, full);
                     else tma_load_4d(to, &maps.v, 0, key + 64 * (c - kKChunks), 0, it.h, full);
                     if (++c == kTileChunks) c = 0, ++i;
@@ -370,8 +371,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
             if (leader) {
                 for (int t = max(issued / kTileChunks - 2, 0); t * kTileChunks < issued; ++t)
                     for (int part = 0; part < kParts; ++part)
-                        if (issued > t * kTileChunks + (part < 2 ? part : part + 1)) bar_drain(&sm->full[t & 1][part], (t >> 1) & 1);
-                for (int w = 0; w < 2 && asked >= 0; ++w) bar_drain(&sm->q_full[w], asked & 1);
+                        if (issued > t * kTileChunks + (part < 2 ? part : part + 1)) bar_drain(&sm->full[t & 1][part], (t >> 1) & 1, A.waits.ns);
+                for (int w = 0; w < 2 && asked >= 0; ++w) bar_drain(&sm->q_full[w], asked & 1, A.waits.ns);
             }
             __syncwarp();
         } else {
@@ -381,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
             const uint32_t q_at = smem_desc(su32(base), 16) + w * kKChunks * (kChunk / 16), k_at = smem_desc(su32(ring), 16),
                            v_at = smem_desc(su32(ring), kChunk / 2), s_col = tmem + kColS + 128 * w, o_col = tmem + kColO + 128 * w;
             const bool leader = elect_one();
-            auto until = [&](uint64_t* bar, int parity) { ok = ok && bar_wait(bar, parity & 1, &sm->abort); };
+            auto until = [&](uint64_t* bar, int parity) { ok = ok && bar_wait(bar, parity & 1, &sm->abort, A.waits.ns); };
             auto landed = [&](int t, int part) { until(&sm->full[t & 1][part], t >> 1); };
             // The products of one lane; a chunk's slot is free once both tiles' that read it are done.
             auto scores = [&](int t, int from, int to) {
@@ -482,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
             // whatever happened, every product issued here is done before the columns are freed. (O is free for
             // an item's first values as soon as its first P is there: the same threads had read O before.)
             if (leader) mma_commit(&sm->drain[w]);
-            bar_drain(&sm->drain[w], 0);
+            bar_drain(&sm->drain[w], 0, A.waits.ns);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
@@ -493,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
         bool ok = true;
         int t0 = 0, c0 = 0, items = 0;
         for (int k = 0;; ++k) {
-            ok = __all_sync(0xffffffffu, bar_wait(&sm->item_full[k % kItems], (k / kItems) & 1, &sm->abort));
+            ok = __all_sync(0xffffffffu, bar_wait(&sm->item_full[k % kItems], (k / kItems) & 1, &sm->abort, A.waits.ns));
             if (!ok) break;
             const Item& it = sm->item[k % kItems];  // until it is given back
             if (it.lq == 0) break;
@@ -503,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
             float m = -INFINITY, l = 0.f;
             for (int i = 0; i < n; ++i) {
                 const int here = seen - i * kKeys;  // keys of this tile that the row sees
-                ok = ok && bar_wait(&sm->s_full[w], (c0 + i) & 1, &sm->abort);
+                ok = ok && bar_wait(&sm->s_full[w], (c0 + i) & 1, &sm->abort, A.waits.ns);
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                 fence_after();
                 uint32_t s[128];
@@ -567,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
                     if (live < 64) {  // values behind the prompt's end become zeros
                         // (the scores are there, so the fill before this one of the barrier is over)
                         const int t = t0 + i, first = max(live, 0);
-                        ok = ok && bar_wait(&sm->full[t & 1][kValues0 + c], (t >> 1) & 1, &sm->abort);
+                        ok = ok && bar_wait(&sm->full[t & 1][kValues0 + c], (t >> 1) & 1, &sm->abort, A.waits.ns);
                         uint4* at = reinterpret_cast<uint4*>(ring + (t * kTileChunks + kKChunks + c) % kSlots * kChunk);
                         for (int u = tid & (kRows - 1); ok && u < (64 - first) * 16; u += kRows)
                             at[(u & 8 ? 512 : 0) + (first + (u >> 4)) * 8 + (u & 7)] = make_uint4(0, 0, 0, 0);
@@ -581,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             }
             // o_full counts the items that have values: for each of them the products wait for these warps
-            if (n > 0) ok = __all_sync(0xffffffffu, ok && bar_wait(&sm->o_full[w], items++ & 1, &sm->abort));
+            if (n > 0) ok = __all_sync(0xffffffffu, ok && bar_wait(&sm->o_full[w], items++ & 1, &sm->abort, A.waits.ns));
             fence_after();
             const float inv = l != 0.f ? 1.f / l : 0.f, none = __uint_as_float(0x7FC00000u);
             const int64_t to = it.q0 + row;

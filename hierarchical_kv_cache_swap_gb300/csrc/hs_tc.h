@@ -39,13 +39,12 @@ __device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t parity) {
                  : "=r"(ok) : "r"(su32(b)), "r"(parity) : "memory");
     return ok != 0;
 }
-// Waits for the phase of `parity` to complete. False, with *abort set, once this wait has lasted
-// kWaitNs, or when another role has set *abort: a lost hand-off then ends the CTA, not the GPU. The time
-// is looked at once in 256 tries (each sleeps for a while unless the phase is complete).
-constexpr uint64_t kWaitNs = 1000000000ull;
-__device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, volatile int* abort) {
+// Waits for the phase of `parity` to complete. False, with *abort set, once this wait has lasted `ns`
+// nanoseconds, or when another role has set *abort: a lost hand-off then ends the CTA, not the GPU. The
+// time and *abort are looked at after each try (which sleeps for a while unless the phase is complete).
+__device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, volatile int* abort, uint64_t ns) {
     if (bar_try(b, parity)) return true;
-    const uint64_t by = global_ns() + kWaitNs;
+    const uint64_t by = global_ns() + ns;
     while (!bar_try(b, parity)) {
         if (*abort) return false;
         if (global_ns() > by) {
@@ -56,9 +55,9 @@ __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, volatile 
     return true;
 }
 // The same wait whatever *abort says: for what must land before the CTA ends.
-__device__ __forceinline__ void bar_drain(uint64_t* b, uint32_t parity) {
+__device__ __forceinline__ void bar_drain(uint64_t* b, uint32_t parity, uint64_t ns) {
     int ignored = 0;
-    bar_wait(b, parity, &ignored);
+    bar_wait(b, parity, &ignored, ns);
 }
 
 // ---------------------------------------------------------------- copies by tensor maps
