@@ -93,6 +93,8 @@ struct Smem {  // beyond Q and the ring
     Item item[kItems];
     uint32_t tmem;
     volatile int abort;
+    volatile uint32_t beat[2];                           // counts the look-up's steps, and the copies': the waits for
+                                                         // an item, and for one to be wanted, may be long
 };
 constexpr uint32_t kSmemBytes = 1024 + kQBytes + kSlots * kChunk + sizeof(Smem);
 static_assert(kSmemBytes <= 227 * 1024, "what a CTA may have");
@@ -159,9 +161,10 @@ struct Search {
     int64_t before;  // so many tiles, no more than the last one looked for,
     int end;         // and this as the largest end of those whose bounds are in order
 };
-__device__ bool find_tile(const PromptAttention& A, int at, Search& done, Item* item, bool* found) {
+__device__ bool find_tile(const PromptAttention& A, int at, Search& done, Item* item, bool* found, volatile uint32_t* beat) {
     const int lane = threadIdx.x & 31;
     for (; done.from < A.B; done.from += 32) {
+        if (lane == 0) beat[0] = beat[0] + 1;
         const int b = done.from + lane;
         int64_t q0 = 0, q1 = 0, k0 = 0, k1 = 0;
         bool bad = false;
@@ -259,6 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
             bar_init(&sm->drain[w], 1);
         }
         sm->abort = 0;
+        sm->beat[0] = sm->beat[1] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kMmaWarp) tmem_alloc<kTmemCols>(&sm->tmem);
@@ -284,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
                 bool found;
                 if (group != last || (int64_t)(in / heads) < done.before) done = Search{0, 0, 0};  // the prompts from the first again
                 last = group;
-                if (find_tile(A, (int)(in / heads), done, &it, &found)) {
+                if (find_tile(A, (int)(in / heads), done, &it, &found, sm->beat)) {
                     if (k >= kItems) wait(&sm->item_free[k % kItems], k / kItems - 1);
                     if (!ok) break;
                     if (found) {
@@ -293,11 +297,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
                         bar_arrive(&sm->item_full[k % kItems]);
                     }
                     __syncwarp();
-                    wait(&sm->wanted, k);
+                    ok = __all_sync(0xffffffffu, ok && bar_wait_moving(&sm->wanted, k & 1, &sm->abort, A.waits.ns, sm->beat));
                     ++k;
                 }
                 if (!ok) break;
                 if (lane == 0) {
+                    sm->beat[0] = sm->beat[0] + 1;
                     fence_async_smem();
                     bar_expect_tx(&sm->answered, sizeof sm->answer);
                     ask_for_block(sm->answer, &sm->answered);
@@ -325,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
             int t0 = 0, issued = 0, asked = -1;  // chunks; the last item whose queries are on their way
             for (int k = 0; leader; ++k) {
                 auto until = [&](uint64_t* bar, int parity) { ok = ok && bar_wait(bar, parity & 1, &sm->abort, A.waits.ns); };
-                until(&sm->item_full[k % kItems], k / kItems);
+                ok = ok && bar_wait_moving(&sm->item_full[k % kItems], (k / kItems) & 1, &sm->abort, A.waits.ns, sm->beat);
                 const Item it = sm->item[k % kItems];
                 bar_arrive(&sm->item_free[k % kItems]);
                 if (!ok || it.lq == 0) break;
@@ -355,6 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
                     if (g >= kSlots) until(&sm->free[slot], g / kSlots - 1);
                     if (!ok) break;
                     issued = g + 1;
+                    sm->beat[1] = issued;
                     uint64_t* const full = &sm->full[(t0 + i) & 1][part];
                     if (c != 2) bar_expect_tx(full, part == kKeys12 ? 2 * kChunk : kChunk);
                     const uint32_t to = su32(ring) + slot * kChunk;
@@ -424,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
             auto give = [&] { if (ok) bar_arrive(&sm->turn[1 - w]); };
             int t0 = 0, c0 = 0;
             for (int k = 0; leader; ++k) {  // one lane alone: a vote after each wait costs more than the wait
-                until(&sm->item_full[k % kItems], k / kItems);
+                ok = ok && bar_wait_moving(&sm->item_full[k % kItems], (k / kItems) & 1, &sm->abort, A.waits.ns, sm->beat);
                 const Item it = sm->item[k % kItems];
                 bar_arrive(&sm->item_free[k % kItems]);
                 if (!ok || it.lq == 0) break;
@@ -494,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
         bool ok = true;
         int t0 = 0, c0 = 0, items = 0;
         for (int k = 0;; ++k) {
-            ok = __all_sync(0xffffffffu, bar_wait(&sm->item_full[k % kItems], (k / kItems) & 1, &sm->abort, A.waits.ns));
+            ok = __all_sync(0xffffffffu, bar_wait_moving(&sm->item_full[k % kItems], (k / kItems) & 1, &sm->abort, A.waits.ns, sm->beat));
             if (!ok) break;
             const Item& it = sm->item[k % kItems];  // until it is given back
             if (it.lq == 0) break;

@@ -54,6 +54,24 @@ __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, volatile 
     }
     return true;
 }
+// The same wait where others may take long before they hand over: it is given up once neither of the two
+// counts at `beat` has moved within `ns`.
+__device__ __forceinline__ bool bar_wait_moving(uint64_t* b, uint32_t parity, volatile int* abort, uint64_t ns, volatile uint32_t* beat) {
+    if (bar_try(b, parity)) return true;
+    for (uint32_t seen = beat[0] + beat[1];;) {
+        const uint64_t by = global_ns() + ns;
+        do {
+            if (bar_try(b, parity)) return true;
+            if (*abort) return false;
+        } while (global_ns() <= by);
+        const uint32_t now = beat[0] + beat[1];
+        if (now == seen) {
+            *abort = 1;
+            return false;
+        }
+        seen = now;
+    }
+}
 // The same wait whatever *abort says: for what must land before the CTA ends.
 __device__ __forceinline__ void bar_drain(uint64_t* b, uint32_t parity, uint64_t ns) {
     int ignored = 0;

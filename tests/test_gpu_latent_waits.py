@@ -56,3 +56,46 @@ def test_prompts(stalled):
         wo, wl, bo, bl = lm.attend(q[a:a + lq], k[c:c + lk], r[c:c + lk], v[c:c + lk], 0.1, True, BF16)
         assert lm.near(o[a:a + lq], wo, bo) and lm.near(lse[a:a + lq], wl, bl)
         a, c = a + lq, c + lk
+
+
+@pytest.fixture
+def short():
+    hs.set_latent_waits(10 * LIMIT_NS)
+    yield
+    hs.set_latent_waits()
+
+
+def test_a_prompt_that_takes_longer_than_the_limit_of_a_wait(short):
+    """The look-up waits for as long as an item's keys take: that is not a hand-off lost.
+
+    Values of 1 give 1: the f32 sums of 2^23 keys, 16 at a time (the products, each addition truncated)
+    and 128 at a time (the weights), are off by 2^19 2^-23 and 2^16 2^-24 at most, the result by 2^-8."""
+    n = 1 << 23
+    q, k, r = normal(gen(1), 3, 1, 192).to(BF16), torch.empty((n, 1, 128), dtype=BF16, device="cuda"), torch.zeros((n, 64), dtype=BF16, device="cuda")
+    for i in range(0, n, n // 8):
+        k[i:i + n // 8] = normal(gen(i + 2), n // 8, 1, 128).to(BF16)
+    v = torch.ones_like(k)
+    qs, ks = torch.tensor([0, 1, 3], dtype=torch.int32, device="cuda"), torch.tensor([0, n, n], dtype=torch.int32, device="cuda")
+    o, lse, word = torch.empty((3, 1, 128), dtype=BF16, device="cuda"), torch.empty((3, 1), device="cuda"), status_word()
+    ms = gpu_ms(lambda: hs.attend_prompts(q, k, r, v, qs, ks, o, lse, 0.1, causal=False, status=word))
+    assert ms > 25, "the item has to last for some limits"
+    assert int(word) == 0
+    assert ((o[0].double() - 1).abs() <= 2.0 ** -4 + 2.0 ** -7).all() and not o[1:].any()
+    x = torch.cat([(c[:, 0].double() @ q[0, 0, :128].double()) * 0.1 for c in k.split(n // 8)])
+    assert abs(float(lse[0]) - float(torch.logsumexp(x, 0))) <= 2.0 ** -8 + 2.0 ** -12
+    assert torch.isinf(lse[1:]).all()
+
+
+@pytest.mark.parametrize("B,H", [(1 << 21, 1), (1 << 17, 64)])
+def test_a_search_that_takes_longer_than_the_limit_of_a_wait(short, B, H):
+    """Two prompts with rows, the first and the last of very many: the others have none."""
+    q, k, r, v, *_ = prompts([(40, 40), (30, 50)], H, BF16, 8)
+    qs, ks = (torch.full((B + 1,), a, dtype=torch.int32, device="cuda") for a in (40, 40))
+    qs[0], ks[0], qs[-1], ks[-1] = 0, 0, 70, 90
+    o, lse, word = torch.empty((70, H, 128), dtype=BF16, device="cuda"), torch.empty((70, H), device="cuda"), status_word()
+    ms = gpu_ms(lambda: hs.attend_prompts(q, k, r, v, qs, ks, o, lse, 0.1, status=word))
+    assert ms > 25, "the search has to last for some limits"
+    assert int(word) == 0
+    for a, b, c, d in ((0, 40, 0, 40), (40, 70, 40, 90)):
+        wo, wl, bo, bl = lm.attend(q[a:b], k[c:d], r[c:d], v[c:d], 0.1, True, BF16)
+        assert lm.near(o[a:b], wo, bo) and lm.near(lse[a:b], wl, bl)
