@@ -61,7 +61,7 @@ __device__ __forceinline__ uint32_t at(int r, int u) { return (uint32_t)(r * 8 +
 constexpr int kPieces = kLatent / 128, kAbsorbThreads = 160;
 
 struct AbsorbSmem {  // beyond the operands
-    uint64_t landed, done;
+    uint64_t landed, done, over;  // over: nothing is under way any more, whatever happened
     uint32_t tmem;
     volatile int abort;
 };
@@ -87,11 +87,12 @@ __global__ void __launch_bounds__(kAbsorbThreads) absorb_kernel(const HeadProduc
         if (lane == 0) {
             bar_init(&sm->landed, 1);
             bar_init(&sm->done, 1);
+            bar_init(&sm->over, 1);
             sm->abort = 0;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
             bar_expect_tx(&sm->landed, 32768 + NT * 256);
             tma_load_4d(su32(base), &maps.w, 0, 0, 2 * piece, h, &sm->landed);
-            tma_load_4d(su32(base) + 32768, &maps.x, 0, (int)t0, 0, h, &sm->landed);
+            if (!p.waits.stall) tma_load_4d(su32(base) + 32768, &maps.x, 0, (int)t0, 0, h, &sm->landed);
         }
         __syncwarp();
         tmem_alloc<kCols>(&sm->tmem);
@@ -138,9 +139,13 @@ __global__ void __launch_bounds__(kAbsorbThreads) absorb_kernel(const HeadProduc
 #pragma unroll
             for (int k = 0; k < 8; ++k) mma_ss(tmem, a + 128 * k, b + NT * 8 * (k >> 2) + 2 * (k & 3), id, k ? 1u : 0u);
             mma_commit(&sm->done);
+            mma_commit(&sm->over);
         }
         __syncwarp();
-        bar_drain(&sm->landed, 0, p.waits.ns);  // no copy lands after the CTA's end, whatever happened
+        if (__builtin_expect(!ok, 0)) {  // no copy lands after the CTA's end
+            bar_drain(&sm->landed, 0, p.waits.ns);
+            if (lane == 0) bar_arrive(&sm->over);
+        }
     }
     if (warp < 4) {  // the rotations: a warp a token, a lane a pair
 #pragma unroll
@@ -161,7 +166,11 @@ __global__ void __launch_bounds__(kAbsorbThreads) absorb_kernel(const HeadProduc
     if (warp < 4) {
         const bool ok = __all_sync(0xffffffffu, bar_wait(&sm->done, 0, &sm->abort, p.waits.ns));
         fence_after();
-        if (!ok && lane == 0 && status) atomicOr(status, 8u /* HS_STATUS_TIMEOUT */);
+        if (__builtin_expect(!ok, 0)) {  // the operands' place is written below: not while copies or products use it
+            bar_drain(&sm->over, 0, 4 * p.waits.ns);  // (after the issuing warp's wait and its drain)
+            if (lane == 0 && status) atomicOr(status, 8u /* HS_STATUS_TIMEOUT */);
+            __syncwarp();
+        }
         const int odd = lane & 1, unit = (warp & 1) * 4 + (lane >> 3), byte = (lane & 6) * 2;  // of the 128-byte row of 64 dimensions
         uint8_t* const to = base + (warp >> 1) * NT * 128 + byte;
 #pragma unroll

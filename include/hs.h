@@ -578,8 +578,9 @@ typedef struct {
  * 512, and the last 64, rotated (rotation: NULL if they are already), out[..][512 ..] (out: bf16
  * [n][heads][576], not x; x's strides positive, n at most 65535 * 64). bf16 products, f32 sums, one rounding. A token
  * whose position is negative gets zeros for its rotary values; so does one that the table has no row
- * for, which sets HS_STATUS_RANGE in *status (or NULL). Returns HS_OK, HS_ERR_INVALID, HS_ERR_LIMIT or
- * HS_ERR_CUDA.
+ * for, which sets HS_STATUS_RANGE in *status (or NULL). HS_STATUS_TIMEOUT: a hand-off within the kernel
+ * was lost (a defect); rows are then NaN in out[..][.. 512]. Returns HS_OK, HS_ERR_INVALID, HS_ERR_LIMIT
+ * or HS_ERR_CUDA.
  */
 int hs_absorb_queries(hs_stream_t stream, const hs_head_product* product, const hs_rotation* rotation, uint32_t* status);
 

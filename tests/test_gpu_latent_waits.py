@@ -99,3 +99,20 @@ def test_a_search_that_takes_longer_than_the_limit_of_a_wait(short, B, H):
     for a, b, c, d in ((0, 40, 0, 40), (40, 70, 40, 90)):
         wo, wl, bo, bl = lm.attend(q[a:b], k[c:d], r[c:d], v[c:d], 0.1, True, BF16)
         assert lm.near(o[a:b], wo, bo) and lm.near(lse[a:b], wl, bl)
+
+
+@pytest.mark.parametrize("n,H", [(5, 2), (100, 40)])
+def test_absorbed_queries(stalled, n, H):
+    """Rows are NaN but for their rotary values, and nothing behind them is written."""
+    q, up = normal(gen(1), n, H, 192).to(BF16), normal(gen(2), H, 128, 512).to(BF16)
+    out = torch.full((n + 70, H, 576), 7.0, dtype=BF16, device="cuda")
+    word = status_word()
+    in_time(stalled(lambda: hs.absorb_queries(q, up, out[:n], status=word)))
+    assert int(word) == hs.HS_STATUS_TIMEOUT
+    assert torch.isnan(out[:n, :, :512]).all() and torch.equal(out[:n, :, 512:], q[..., 128:]) and (out[n:] == 7).all()
+    word.zero_()
+    hs.absorb_queries(q, up, out[:n], status=word)
+    ref = torch.einsum("nhd,hdc->nhc", q[..., :128].double(), up.double())
+    size = torch.einsum("nhd,hdc->nhc", q[..., :128].double().abs(), up.double().abs())
+    assert ((out[:n, :, :512].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 130 * 2.0 ** -23 * size).all()
+    assert int(word) == 0 and (out[n:] == 7).all()

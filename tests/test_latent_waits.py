@@ -1,4 +1,6 @@
 """The limit of the latent kernels' waits, without a GPU."""
+import os
+import re
 import threading
 
 import pytest
@@ -32,3 +34,20 @@ def test_threads_set_their_own():
     t.start()
     t.join()
     assert got == [hs.HS_OK]
+
+
+def kernel(name):
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "hierarchical_kv_cache_swap_gb300", "csrc")
+    with open(os.path.join(csrc, "hs_absorb.cu")) as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    return re.split(r"__global__ void", text.split(name + "(const HeadProduct p")[1])[0]
+
+
+def test_absorbed_queries_leave_what_is_in_flight_alone():
+    """After a wait that ran out, a copy or the products may still be at work on the operands' place: their
+    end is told by `over`, which the other warps wait for before they write there."""
+    body = kernel("absorb_kernel")
+    steps = ["mma_commit(&sm->done);", "mma_commit(&sm->over);", "bar_drain(&sm->landed", "bar_arrive(&sm->over)", "bar_wait(&sm->done",
+             "bar_drain(&sm->over", "*reinterpret_cast<uint32_t*>(to", "__syncthreads();\n    if (warp == 4)", "tmem_free"]
+    assert [body.count(x) for x in steps] == [1] * len(steps)
+    assert [body.index(x) for x in steps] == sorted(body.index(x) for x in steps)
