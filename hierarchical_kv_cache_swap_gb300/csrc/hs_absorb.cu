@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kThreads) expand_few_kernel(const HeadProduct 
 // loads under way, which is what it takes to draw an SM's share of the memory's rate.
 constexpr int kTokens = 32, kGroupThreads = 256, kManyThreads = 2 * kGroupThreads;
 struct ExpandSmem {  // beyond the operands
-    uint64_t landed, done[2];
+    uint64_t landed, done[2], over[2];  // over: a tile's products have ended, or there are none, whatever happened
     uint32_t tmem;
     volatile int abort;
 };
@@ -297,12 +297,11 @@ __global__ void __launch_bounds__(kManyThreads, 1) expand_many_kernel(const Head
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (threadIdx.x == 0) {
         bar_init(&sm->landed, 1);
-        bar_init(&sm->done[0], 1);
-        bar_init(&sm->done[1], 1);
+        for (int i = 0; i < 2; ++i) bar_init(&sm->done[i], 1), bar_init(&sm->over[i], 1);
         sm->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         bar_expect_tx(&sm->landed, kMatrix);
-        for (int c = 0; c < 4; ++c) tma_load_4d(su32(base) + c * (kMatrix / 4), &map, 0, 0, 2 * c, h, &sm->landed);
+        for (int c = p.waits.stall; c < 4; ++c) tma_load_4d(su32(base) + c * (kMatrix / 4), &map, 0, 0, 2 * c, h, &sm->landed);
     }
     if (warp == 0) tmem_alloc<2 * kTokens>(&sm->tmem);
     // unit u (8 values) of the group's tile: of token u / 64, dimensions 8 (u % 64) on
@@ -354,10 +353,16 @@ __global__ void __launch_bounds__(kManyThreads, 1) expand_many_kernel(const Head
                 for (int s = 0; s < kLatent / 16; ++s)
                     mma_ss(cols, a + (s >> 2) * (kHeadDim * 8) + 2 * (s & 3), b + (s >> 2) * (kTokens * 8) + 2 * (s & 3), id, s ? 1u : 0u);
                 mma_commit(&sm->done[group]);
+                mma_commit(&sm->over[group]);
             }
+            if (__builtin_expect(!ok, 0) && lane == 0) bar_arrive(&sm->over[group]);
             __syncwarp();
         }
         ok = __all_sync(0xffffffffu, ok && bar_wait(&sm->done[group], k & 1, &sm->abort, p.waits.ns));
+        if (__builtin_expect(!ok, 0)) {  // the tile's place is not written again, nor the columns freed, under its products
+            bar_drain(&sm->over[group], k & 1, 4 * p.waits.ns);
+            __syncwarp();
+        }
         fence_after();
         // warps w and w + 4 share 32 output dimensions: half of the columns each
         uint32_t d[16];
@@ -376,7 +381,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) expand_many_kernel(const Head
         // after an abort, too: warps may differ in whether a wait ran out, and the others come here
         asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(kGroupThreads) : "memory");  // all have read the columns
     }
-    // after an abort: no copy and no product may be under way at the CTA's end
+    // after an abort: no copy may be under way at the CTA's end
     if (threadIdx.x == 0) bar_drain(&sm->landed, 0, p.waits.ns);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     fence_before();

@@ -116,3 +116,16 @@ def test_absorbed_queries(stalled, n, H):
     size = torch.einsum("nhd,hdc->nhc", q[..., :128].double().abs(), up.double().abs())
     assert ((out[:n, :, :512].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 130 * 2.0 ** -23 * size).all()
     assert int(word) == 0 and (out[n:] == 7).all()
+
+
+@pytest.mark.parametrize("n,H", [(200, 40), (900, 152)])
+def test_expanded_outputs(stalled, n, H):
+    o, up = normal(gen(1), n, H, 512), normal(gen(2), H, 128, 512).to(BF16)
+    out = torch.full((n + 70, H, 128), 7.0, dtype=BF16, device="cuda")
+    in_time(stalled(lambda: hs.expand_outputs(o, up, out[:n])))
+    assert torch.isnan(out[:n]).all() and (out[n:] == 7).all()
+    hs.expand_outputs(o, up, out[:n])
+    ref = torch.einsum("nhc,hec->nhe", o.double(), up.double())
+    size = torch.einsum("nhc,hec->nhe", o.double().abs(), up.double().abs())
+    assert ((out[:n].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 514 * 2.0 ** -23) * size).all()
+    assert (out[n:] == 7).all()

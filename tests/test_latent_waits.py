@@ -51,3 +51,13 @@ def test_absorbed_queries_leave_what_is_in_flight_alone():
              "bar_drain(&sm->over", "*reinterpret_cast<uint32_t*>(to", "__syncthreads();\n    if (warp == 4)", "tmem_free"]
     assert [body.count(x) for x in steps] == [1] * len(steps)
     assert [body.index(x) for x in steps] == sorted(body.index(x) for x in steps)
+
+
+def test_expanded_outputs_leave_what_is_in_flight_alone():
+    """After a wait that ran out no warp writes a next tile, and none frees the columns, before the products of
+    this one have ended: `over` tells, once a tile in any case."""
+    loop = kernel("expand_many_kernel").split("for (int k = 0; t0 < p.n;")[1]
+    steps = ["mma_commit(&sm->done[group]);", "mma_commit(&sm->over[group]);", "if (__builtin_expect(!ok, 0) && lane == 0) bar_arrive(&sm->over[group]);",
+             "bar_wait(&sm->done[group], k & 1", "bar_drain(&sm->over[group], k & 1", "tmem_load16", "tmem_free"]
+    assert [loop.count(x) for x in steps] == [1] * len(steps)
+    assert [loop.index(x) for x in steps] == sorted(loop.index(x) for x in steps)
