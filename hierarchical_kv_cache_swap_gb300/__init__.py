@@ -88,7 +88,7 @@ class _LatentRows(ctypes.Structure):
 class _HeadProduct(ctypes.Structure):
     """hs_head_product (include/hs.h)."""
     _fields_ = [("x", _VP), ("x_token_stride", _I64), ("x_head_stride", _I64), ("w", _VP), ("w_head_stride", _I64),
-                ("w_row_stride", _I64), ("out", _VP), ("n", _I64), ("heads", _I)]
+                ("w_row_stride", _I64), ("out", _VP), ("n", _I64), ("heads", _I), ("status", _VP)]
 
 
 class _PromptAttention(ctypes.Structure):
@@ -319,10 +319,11 @@ def absorb_queries(q, up_k, out, rotation=None, positions=None, halves: bool = F
     (_torch_binding or _native()).absorb_queries(q, up_k, out, rotation, positions, halves, status, stream)
 
 
-def expand_outputs(o, up_v, out, stream=None) -> None:
+def expand_outputs(o, up_v, out, stream=None, status=None) -> None:
     """hs_expand_outputs: o float32 [n, heads, 512], as Context.attend gives it, through the heads'
-    value matrices up_v bf16 [heads, 128, 512] into out bf16 [n, heads, 128]."""
-    (_torch_binding or _native()).expand_outputs(o, up_v, out, stream)
+    value matrices up_v bf16 [heads, 128, 512] into out bf16 [n, heads, 128]. status: a device int32
+    word [1], or None."""
+    (_torch_binding or _native()).expand_outputs(o, up_v, out, status, stream)
 
 
 def attend_prompts(q, k, k_rope, v, q_starts, k_starts, o, lse, sm_scale: float, causal: bool = True, status=None,

@@ -73,7 +73,7 @@ struct AbsorbMaps {
 };
 
 template <int NT>
-__global__ void __launch_bounds__(kAbsorbThreads) absorb_kernel(const HeadProduct p, const Rotation rot, uint32_t* status,
+__global__ void __launch_bounds__(kAbsorbThreads) absorb_kernel(const HeadProduct p, const Rotation rot,
                                                                 const __grid_constant__ AbsorbMaps maps) {
     constexpr uint32_t kCols = NT < 32 ? 32 : NT;  // of tensor memory
     extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(kAbsorbThreads) absorb_kernel(const HeadProduc
             s[i] = rot.table[(int64_t)pos[i] * kRope + 32 + lane];
         } else {
             x[i] = y[i] = 0;
-            if (pos[i] >= 0 && lane == 0 && h == 0 && status) atomicOr(status, 1u /* HS_STATUS_RANGE */);
+            if (pos[i] >= 0 && lane == 0 && h == 0 && p.status) atomicOr(p.status, 1u /* HS_STATUS_RANGE */);
         }
     }
     const uint32_t tmem = sm->tmem;
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kAbsorbThreads) absorb_kernel(const HeadProduc
         fence_after();
         if (__builtin_expect(!ok, 0)) {  // the operands' place is written below: not while copies or products use it
             bar_drain(&sm->over, 0, 4 * p.waits.ns);  // (after the issuing warp's wait and its drain)
-            if (lane == 0 && status) atomicOr(status, 8u /* HS_STATUS_TIMEOUT */);
+            if (lane == 0 && p.status) atomicOr(p.status, 8u /* HS_STATUS_TIMEOUT */);
             __syncwarp();
         }
         const int odd = lane & 1, unit = (warp & 1) * 4 + (lane >> 3), byte = (lane & 6) * 2;  // of the 128-byte row of 64 dimensions
@@ -361,6 +361,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) expand_many_kernel(const Head
         ok = __all_sync(0xffffffffu, ok && bar_wait(&sm->done[group], k & 1, &sm->abort, p.waits.ns));
         if (__builtin_expect(!ok, 0)) {  // the tile's place is not written again, nor the columns freed, under its products
             bar_drain(&sm->over[group], k & 1, 4 * p.waits.ns);
+            if (lane == 0 && p.status) atomicOr(p.status, 8u /* HS_STATUS_TIMEOUT */);
             __syncwarp();
         }
         fence_after();
@@ -429,7 +430,7 @@ static bool encode(CUtensorMap* map, const uint16_t* x, int64_t rows, int column
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-cudaError_t launch_absorb_queries(cudaStream_t stream, const HeadProduct& p, const Rotation& rot, uint32_t* status, int num_sms) {
+cudaError_t launch_absorb_queries(cudaStream_t stream, const HeadProduct& p, const Rotation& rot, int num_sms) {
     if (p.n == 0 || p.heads == 0) return cudaSuccess;
     cudaError_t e = set_up();
     if (e != cudaSuccess) return e;
@@ -442,8 +443,8 @@ cudaError_t launch_absorb_queries(cudaStream_t stream, const HeadProduct& p, con
         !encode(&maps.out, p.out, p.n, (kLatent + kRope) / 64, p.heads, (int64_t)p.heads * (kLatent + kRope), kLatent + kRope, nt, 2))
         return cudaErrorInvalidValue;
     const dim3 grid(kPieces, p.heads, (unsigned)tiles(p.n, nt));
-    if (nt == 16) return launch_dependent(stream, grid, kAbsorbThreads, absorb_smem<16>(), absorb_kernel<16>, p, rot, status, maps);
-    return launch_dependent(stream, grid, kAbsorbThreads, absorb_smem<64>(), absorb_kernel<64>, p, rot, status, maps);
+    if (nt == 16) return launch_dependent(stream, grid, kAbsorbThreads, absorb_smem<16>(), absorb_kernel<16>, p, rot, maps);
+    return launch_dependent(stream, grid, kAbsorbThreads, absorb_smem<64>(), absorb_kernel<64>, p, rot, maps);
 }
 
 cudaError_t launch_expand_outputs(cudaStream_t stream, const HeadProduct& p, int num_sms) {

@@ -795,7 +795,7 @@ static int product_check(const hs_head_product* p, int align, hs::HeadProduct* o
     const int rc = steps_check({Step{"w_head", p->heads, p->w_head_stride}, Step{"w_row", 2, p->w_row_stride}});
     if (rc != HS_OK) return rc;
     *out = hs::HeadProduct{p->x, p->x_token_stride, p->x_head_stride, (const uint16_t*)p->w, p->w_head_stride, p->w_row_stride,
-                           (uint16_t*)p->out, p->n, p->heads, g_latent_waits};
+                           (uint16_t*)p->out, p->n, p->heads, g_latent_waits, p->status};
     return HS_OK;
 }
 
@@ -806,9 +806,10 @@ int hs_absorb_queries(hs_stream_t stream, const hs_head_product* product, const 
     if (rc != HS_OK || (rc = rotation_check(rotation, p.n, nullptr, &rot)) != HS_OK ||
         (rc = steps_check({Step{"x_token", p.n, p.x_token}, Step{"x_head", p.heads, p.x_head}})) != HS_OK)
         return rc;
+    p.status = status;
     if (p.n > 65535 * 64) return fail(HS_ERR_LIMIT, "n=%lld exceeds 65535 tiles of 64 tokens", (long long)p.n);
     if ((rc = sm_count(&sms)) != HS_OK) return rc;
-    cudaError_t e = hs::launch_absorb_queries((cudaStream_t)stream, p, rot, status, sms);
+    cudaError_t e = hs::launch_absorb_queries((cudaStream_t)stream, p, rot, sms);
     if (e != cudaSuccess) return cuda_fail(e, "query absorption kernel launch");
     g_err[0] = 0;
     return HS_OK;

@@ -68,9 +68,10 @@ struct HeadProduct {
     int64_t n;
     int heads;
     Waits waits;
+    uint32_t* status;         // or nullptr
 };
 // bf16 x [n][heads][128 + 64] -> out [n][heads][512 + 64]: x[:128] w[h], then x[128:] rotated.
-cudaError_t launch_absorb_queries(cudaStream_t stream, const HeadProduct& p, const Rotation& rot, uint32_t* status, int num_sms);
+cudaError_t launch_absorb_queries(cudaStream_t stream, const HeadProduct& p, const Rotation& rot, int num_sms);
 // f32 x [n][heads][512] -> bf16 out [n][heads][128]: x w[h]^T.
 cudaError_t launch_expand_outputs(cudaStream_t stream, const HeadProduct& p, int num_sms);
 

@@ -441,7 +441,7 @@ hs_head_product product_of(const at::Tensor& x, const char* name, at::ScalarType
     vector(out, "out", at::kBFloat16, {n, H, out_width});
     on_device({{name, &x}, {"the matrices", &w}, {"out", &out}});
     return hs_head_product{x.data_ptr(), stride(x, 0), stride(x, 1), w.data_ptr(), stride(w, 0), stride(w, 1), out.data_ptr(), n,
-                           int_of(H, "heads")};
+                           int_of(H, "heads"), nullptr};
 }
 
 // absorb_queries(q, up_k, out, rotation, positions, halves, status, stream)
@@ -458,12 +458,13 @@ PyObject* absorb_queries(PyObject*, PyObject* const* a, Py_ssize_t na) {
     });
 }
 
-// expand_outputs(o, up_v, out, stream)
+// expand_outputs(o, up_v, out, status, stream)
 PyObject* expand_outputs(PyObject*, PyObject* const* a, Py_ssize_t na) {
-    if (!arity(na, 4)) return nullptr;
+    if (!arity(na, 5)) return nullptr;
     return guarded([&] {
-        const hs_head_product p = product_of(tensor(a[0], "o"), "o", at::kFloat, 512, tensor(a[1], "up_v"), tensor(a[2], "out"), 128);
-        const hs_stream_t stream = stream_of(a[3]);
+        hs_head_product p = product_of(tensor(a[0], "o"), "o", at::kFloat, 512, tensor(a[1], "up_v"), tensor(a[2], "out"), 128);
+        p.status = status_of(a[3]);
+        const hs_stream_t stream = stream_of(a[4]);
         return done("hs_expand_outputs", [&] { return hs_expand_outputs(stream, &p); });
     });
 }

@@ -570,6 +570,7 @@ typedef struct {
     void* out;
     int64_t n;
     int heads; /* 1 .. 65535 */
+    uint32_t* status; /* hs_expand_outputs: device word, or NULL (hs_absorb_queries takes its own) */
 } hs_head_product;
 
 /*
@@ -587,7 +588,8 @@ int hs_absorb_queries(hs_stream_t stream, const hs_head_product* product, const 
 /*
  * hs_expand_outputs -- what hs_attend gives (x: f32 [n][heads][512], strides multiples of 4)
  * through the heads' value matrices: out[..][e] = sum_c x[..][c] w[head][e][c], e < 128 (out: bf16
- * [n][heads][128]). x is rounded to bf16 for the products, the sums are f32.
+ * [n][heads][128]). x is rounded to bf16 for the products, the sums are f32. HS_STATUS_TIMEOUT in
+ * *product->status (or NULL): a hand-off within the kernel was lost (a defect); rows are then NaN.
  */
 int hs_expand_outputs(hs_stream_t stream, const hs_head_product* product);
 

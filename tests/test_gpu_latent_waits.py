@@ -122,10 +122,18 @@ def test_absorbed_queries(stalled, n, H):
 def test_expanded_outputs(stalled, n, H):
     o, up = normal(gen(1), n, H, 512), normal(gen(2), H, 128, 512).to(BF16)
     out = torch.full((n + 70, H, 128), 7.0, dtype=BF16, device="cuda")
-    in_time(stalled(lambda: hs.expand_outputs(o, up, out[:n])))
+    word = status_word()
+    in_time(stalled(lambda: hs.expand_outputs(o, up, out[:n], status=word)))
+    assert int(word) == hs.HS_STATUS_TIMEOUT
     assert torch.isnan(out[:n]).all() and (out[n:] == 7).all()
-    hs.expand_outputs(o, up, out[:n])
+    in_time(stalled(lambda: hs.expand_outputs(o, up, out[:n])))
+    word.zero_()
+    hs.expand_outputs(o, up, out[:n], status=word)
+    assert int(word) == 0
     ref = torch.einsum("nhc,hec->nhe", o.double(), up.double())
     size = torch.einsum("nhc,hec->nhe", o.double().abs(), up.double().abs())
     assert ((out[:n].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 514 * 2.0 ** -23) * size).all()
     assert (out[n:] == 7).all()
+    for bad in (word.cpu(), status_word().long(), torch.zeros(2, dtype=torch.int32, device="cuda")):
+        with pytest.raises(ValueError, match="status must be"):
+            hs.expand_outputs(o, up, out[:n], status=bad)

@@ -4,6 +4,7 @@ import re
 import threading
 
 import pytest
+import torch
 
 import hierarchical_kv_cache_swap_gb300 as hs
 
@@ -61,3 +62,12 @@ def test_expanded_outputs_leave_what_is_in_flight_alone():
              "bar_wait(&sm->done[group], k & 1", "bar_drain(&sm->over[group], k & 1", "tmem_load16", "tmem_free"]
     assert [loop.count(x) for x in steps] == [1] * len(steps)
     assert [loop.index(x) for x in steps] == sorted(loop.index(x) for x in steps)
+
+
+def test_the_outputs_call_takes_a_status_word():
+    o, up, out = torch.zeros(2, 4, 512), torch.zeros(4, 128, 512, dtype=torch.bfloat16), torch.zeros(2, 4, 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="on the CPU"):
+        hs.expand_outputs(o, up, out, status=torch.zeros(1, dtype=torch.int32))
+    with pytest.raises(TypeError, match="5 arguments"):
+        hs._native().expand_outputs(o, up, out, None)
+    assert hs._HeadProduct().status is None and hs._HeadProduct._fields_[-1][0] == "status"
