@@ -552,7 +552,8 @@ int hs_append_latents(hs_ctx* ctx, hs_stream_t stream, int dtype, const hs_laten
  * becomes latent[b][j] and rope[b][j] (device [B][n][512] and [B][n][64] of `dtype`, contiguous,
  * 16-byte aligned, overwritten). A negative slot reads as zeros, one >= S too, setting
  * HS_STATUS_RANGE in *status (or NULL). A value is code * scale rounded to `dtype`, which is exact
- * in bf16 but below 2^-126; what is too large for fp16 becomes infinite.
+ * in bf16 but below 2^-126 and at 2^128, the code nearest to a latent of 248 * 2^120 or more, which
+ * becomes infinite; so does what is too large for fp16.
  */
 int hs_read_latents(hs_stream_t stream, int dtype, const uint8_t* entries, int B, int S, const int32_t* slots, int n,
                     void* latent, void* rope, uint32_t* status);

@@ -133,3 +133,31 @@ def test_what_an_infinite_value_reaches_under_a_causal_mask(lq, lk, dtype):
                 assert (torch.isnan(o[a:b, h, d]) | ~free | (wo[a:b, h, d] == 0)).all()
                 o[a:b, h, d] = torch.where(free, wo[a:b, h, d].to(dtype), o[a:b, h, d])
         assert lm.near(o, wo, bo), (key, seen)
+
+
+# ------------------------------------------------------------------------ entries
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_every_magnitude_reads_back_as_its_code_times_the_scale(dtype):
+    """Each number of the type as the largest of a block, beside fractions of it, in both output types:
+    the 64-bit product rounded once, infinite where that is too large (2^128 in bf16)."""
+    a = torch.arange(0, 32768, dtype=torch.int16).view(dtype).cuda()
+    a = a[torch.isfinite(a)]
+    a = a[:a.numel() // 4 * 4]
+    x = (a.double()[:, None] * torch.linspace(1, -1, 128, device="cuda", dtype=torch.float64)).to(dtype)
+    latent = x.view(-1, 512)
+    n = latent.shape[0]
+    entries, rope = torch.zeros((n, 656), dtype=torch.uint8, device="cuda"), torch.zeros((n, 64), dtype=dtype, device="cuda")
+    hs.write_latents(latent, rope, torch.arange(n, device="cuda"), entries)
+    want, _ = lm.values(entries)
+    # half a step of an E4M3 code, or of its smallest ones
+    assert ((want - latent.double()).abs() <= torch.maximum(2.0 ** -4 * latent.double().abs(), 2.0 ** -10 * lm.scales(latent).repeat_interleave(128, 1))).all()
+    assert (want.abs().amax() == 2.0 ** 128) == (dtype == BF16)
+    for out in (BF16, F16):
+        lo, ro = torch.empty((1, n, 512), dtype=out, device="cuda"), torch.empty((1, n, 64), dtype=out, device="cuda")
+        hs.read_latents(entries.view(1, n, 656), torch.arange(n, dtype=torch.int32, device="cuda").view(1, n), lo, ro)
+        got, most = lo[0].double(), torch.finfo(out).max
+        step = 2.0 ** -133 if out == BF16 else 2.0 ** -24  # the smallest number
+        large = want.abs() >= most * (1 + lm.half_step(out) / 2)
+        assert torch.isinf(got[large]).all() and torch.equal(torch.sign(got[large]), torch.sign(want[large]))
+        exact = want[~large] if out == BF16 else want[~large].to(torch.float32).to(out).double()
+        assert ((got[~large] - exact).abs() <= (step / 2 if out == BF16 else 0)).all()
