@@ -202,7 +202,9 @@ __global__ void __launch_bounds__(kAbsorbThreads) absorb_kernel(const HeadProduc
 
 // ---------------------------------------------------------------- outputs
 // The f32 rows are rounded to bf16 for the products, as the sums behind them have been: 2^-8 of each at
-// most, of the size of the result's own rounding once 512 of them are summed.
+// most, of the size of the result's own rounding once 512 of them are summed (0.0024 of the result against
+// 64 bits, 0.0017 by its own rounding alone). Each as two bf16, its upper half and the rest, gave those
+// 0.0017 at 18.4 us instead of 15.6 for 256 tokens of 128 heads and 3.6 instead of 3.0 for 37 of 20.
 //
 // Few tokens of few heads: a CTA takes 32 output dimensions and 16 tokens, all copies under way at once,
 // eight steps of 64 latent dimensions. Its eight warps are two over the dimensions by four shares of a
@@ -451,13 +453,17 @@ cudaError_t launch_expand_outputs(cudaStream_t stream, const HeadProduct& p, int
     if (p.n == 0 || p.heads == 0) return cudaSuccess;
     cudaError_t e = set_up();
     if (e != cudaSuccess) return e;
-    // few tokens of few heads: pieces of 32 output dimensions, while all CTAs run at once, two an SM (64
-    // tokens of 16 heads: 3.0 us against 5.4; 16 of 128 heads: 4.7 against 4.1)
+    // few tokens of few heads: pieces of 32 output dimensions of 16 tokens, while all CTAs run at once, three an
+    // SM. us of this kernel and of the other, in a graph, by CTAs (152 SMs): 320 (80 tokens of 16 heads) 3.6 and
+    // 5.6, 384 (16 of 96) 3.6 and 4.3, 512 (128 of 16) 4.3 and 5.6, 512 (16 of 128) 4.3 and 4.3, 512 (1 of 128)
+    // 4.5 and 4.0, 768 (48 of 64) 5.9 and 5.4, 1024 (256 of 16) 6.8 and 5.6, 1536 (48 of 128) 9.8 and 5.6
     const dim3 few(kHeadDim / kFewDims, p.heads, (unsigned)tiles(p.n, kFewTokens));
-    if ((int64_t)few.x * few.y * few.z <= 2 * (int64_t)num_sms) return launch_dependent(stream, few, kThreads, kFewSmem, expand_few_kernel, p);
+    if ((int64_t)few.x * few.y * few.z <= 3 * (int64_t)num_sms) return launch_dependent(stream, few, kThreads, kFewSmem, expand_few_kernel, p);
     CUtensorMap map;
     if (!encode(&map, p.w, kHeadDim, kLatent / 64, p.heads, p.w_row, p.heads > 1 ? p.w_head : kHeadDim * kLatent, kHeadDim, 2)) return cudaErrorInvalidValue;
-    // all CTAs at once: a second round would read the matrices again (256 tokens of 128 heads: 20.5 us, 22.9 in two)
+    // a head's CTAs are as many as run at once with the other heads': a second round of them would read the
+    // matrices again (256 tokens of 128 heads, cold: 20.5 us, 22.9 in two). More heads than SMs take two
+    // all the same (64 tokens of 160 heads 10.7 us, of 128 heads 6.1), 80 heads leave half of the SMs idle
     const int64_t most = p.heads < num_sms ? num_sms / p.heads : 1, t = tiles(p.n, 2 * kTokens);
     return launch_dependent(stream, dim3(p.heads, (unsigned)(t < most ? t : most)), kManyThreads, kManySmem, expand_many_kernel, p, map);
 }

@@ -161,3 +161,19 @@ def test_every_magnitude_reads_back_as_its_code_times_the_scale(dtype):
         assert torch.isinf(got[large]).all() and torch.equal(torch.sign(got[large]), torch.sign(want[large]))
         exact = want[~large] if out == BF16 else want[~large].to(torch.float32).to(out).double()
         assert ((got[~large] - exact).abs() <= (step / 2 if out == BF16 else 0)).all()
+
+
+# ------------------------------------------------------------------------ outputs
+@pytest.mark.parametrize("n,H", [(1, 114), (1, 115), (16, 114), (17, 57), (17, 58), (1, 153), (33, 160), (65, 100), (95, 101), (300, 31), (1100, 3)])
+def test_outputs_at_sizes_about_the_kernels_limits(n, H):
+    g = gen(n + H)
+    x = (normal(g, n, H, 520) * torch.exp(2 * normal(g, n, H, 1)))[..., 4:516]
+    up = (normal(g, H, 130, 512) * 512 ** -0.5).to(BF16)[:, 1:129]
+    back = torch.full((n + 33, H, 128), 7.0, dtype=BF16, device="cuda")
+    word = status_word()
+    hs.expand_outputs(x, up, back[:n], status=word)
+    ref = torch.einsum("nhc,hec->nhe", x.double(), up.double())
+    size = torch.einsum("nhc,hec->nhe", x.double().abs(), up.double().abs())
+    # x's rounding and the result's, and f32 sums of 512
+    assert ((back[:n].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 514 * 2.0 ** -23) * size).all()
+    assert int(word) == 0 and (back[n:] == 7).all()
