@@ -44,10 +44,6 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t pack(float lo, float hi) {
-    const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&r);
-}
 // Byte offset of 16-byte unit u of row r in rows of 128 bytes: eight rows' units lie in different banks.
 __device__ __forceinline__ uint32_t at(int r, int u) { return (uint32_t)(r * 8 + (u ^ (r & 7))) * 16; }
 
@@ -154,7 +150,7 @@ __global__ void __launch_bounds__(kAbsorbThreads) absorb_kernel(const HeadProduc
             float2 v = make_float2(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16));
             if (rot.table) v = turn(v.x, v.y, c[i], s[i]);
             uint16_t* const o = out + token(i) * pitch + kLatent;
-            const uint32_t both = pack(v.x, v.y);
+            const uint32_t both = pack<true>(v.x, v.y);
             if (rot.halves) {
                 o[first] = (uint16_t)both;
                 o[second] = (uint16_t)(both >> 16);
@@ -183,7 +179,7 @@ __global__ void __launch_bounds__(kAbsorbThreads) absorb_kernel(const HeadProduc
                 const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
                 const float x = __uint_as_float(odd ? other : v[j]), y = __uint_as_float(odd ? v[j + 1] : other);
                 const int t = c + j + odd;
-                *reinterpret_cast<uint32_t*>(to + t * 128 + ((unit ^ (t & 7)) << 4)) = ok ? pack(x, y) : 0x7FFF7FFFu;
+                *reinterpret_cast<uint32_t*>(to + t * 128 + ((unit ^ (t & 7)) << 4)) = ok ? pack<true>(x, y) : 0x7FFF7FFFu;
             }
         }
         fence_async_smem();
@@ -250,7 +246,7 @@ __global__ void __launch_bounds__(kThreads) expand_few_kernel(const HeadProduct 
         for (int r = 0; r < 4; ++r) {  // rows g and g + 8, columns 2 c and 2 c + 8 of the share's 16
             const int t = (lane >> 2) + 8 * (r & 1), u = 4 * share + 2 * (r >> 1) + ((lane & 3) >> 1);
             const float2 v = *reinterpret_cast<const float2*>(x + t * 256 + ((u ^ (t & 7) << 1) << 4) + 8 * (lane & 1));
-            a[r] = pack(v.x, v.y);
+            a[r] = pack<true>(v.x, v.y);
         }
         ldsm(b, su32(w) + at(col + (lane & 7) + ((lane >> 4) << 3), 2 * share + ((lane >> 3) & 1)));
         mma(acc[0], a, b[0], b[1]);
@@ -272,7 +268,7 @@ __global__ void __launch_bounds__(kThreads) expand_few_kernel(const HeadProduct 
         const float2 y = *reinterpret_cast<const float2*>(sums + (s * kFewTokens + t) * kFewDims + e);
         v = make_float2(v.x + y.x, v.y + y.y);
     }
-    if (t0 + t < p.n) *reinterpret_cast<uint32_t*>(out + t * pitch + e) = pack(v.x, v.y);
+    if (t0 + t < p.n) *reinterpret_cast<uint32_t*>(out + t * pitch + e) = pack<true>(v.x, v.y);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
@@ -338,8 +334,8 @@ __global__ void __launch_bounds__(kManyThreads, 1) expand_many_kernel(const Head
         for (int i = 0; i < kUnits; ++i) {
             const int u = i * kGroupThreads + tid, t = u >> 6, c = u & 63;  // a column of 64 dimensions after the other
             *reinterpret_cast<uint4*>(x + (c >> 3) * (kTokens * 128) + t * 128 + (((c & 7) ^ (t & 7)) << 4)) =
-                make_uint4(pack(v[2 * i].x, v[2 * i].y), pack(v[2 * i].z, v[2 * i].w), pack(v[2 * i + 1].x, v[2 * i + 1].y),
-                           pack(v[2 * i + 1].z, v[2 * i + 1].w));
+                make_uint4(pack<true>(v[2 * i].x, v[2 * i].y), pack<true>(v[2 * i].z, v[2 * i].w), pack<true>(v[2 * i + 1].x, v[2 * i + 1].y),
+                           pack<true>(v[2 * i + 1].z, v[2 * i + 1].w));
         }
         fence_async_smem();
         fence_before();
@@ -379,7 +375,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) expand_many_kernel(const Head
             const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? d[j] : d[j + 1], 1);
             const float lo = __uint_as_float(odd ? other : d[j]), hi = __uint_as_float(odd ? d[j + 1] : other);
             const int64_t t = t0 + 16 * half + j + odd;
-            if (t < p.n) *reinterpret_cast<uint32_t*>(to + t * pitch) = ok ? pack(lo, hi) : 0x7FFF7FFFu;
+            if (t < p.n) *reinterpret_cast<uint32_t*>(to + t * pitch) = ok ? pack<true>(lo, hi) : 0x7FFF7FFFu;
         }
         // after an abort, too: warps may differ in whether a wait ran out, and the others come here
         asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(kGroupThreads) : "memory");  // all have read the columns
@@ -420,18 +416,6 @@ int64_t tiles(int64_t n, int of) { return (n + of - 1) / of; }
 
 }  // namespace
 
-// A tensor [heads][rows][columns of 64] of bf16, its strides in elements, in boxes of `box_rows` rows of
-// `box_columns` columns of one head: a column after the other, rows of 128 swizzled bytes.
-static bool encode(CUtensorMap* map, const uint16_t* x, int64_t rows, int columns, int heads, int64_t row, int64_t head, int box_rows, int box_columns) {
-    const EncodeTiled enc = tensor_map_encoder();
-    if (!enc) return false;
-    const cuuint64_t size[4] = {64, (cuuint64_t)rows, (cuuint64_t)columns, (cuuint64_t)heads};
-    const cuuint64_t stride[3] = {(cuuint64_t)row * 2, 128, (cuuint64_t)head * 2};
-    const cuuint32_t box[4] = {64, (cuuint32_t)box_rows, (cuuint32_t)box_columns, 1}, step[4] = {1, 1, 1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t*>(x), size, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 cudaError_t launch_absorb_queries(cudaStream_t stream, const HeadProduct& p, const Rotation& rot, int num_sms) {
     if (p.n == 0 || p.heads == 0) return cudaSuccess;
     cudaError_t e = set_up();
@@ -440,9 +424,9 @@ cudaError_t launch_absorb_queries(cudaStream_t stream, const HeadProduct& p, con
     // 3.6; 64 of 128 heads: 10.6 against 6.2)
     const int nt = 4 * tiles(p.n, 16) * p.heads <= 4 * (int64_t)num_sms ? 16 : 64;
     AbsorbMaps maps;
-    if (!encode(&maps.w, p.w, kHeadDim, kLatent / 64, p.heads, p.w_row, p.heads > 1 ? p.w_head : kHeadDim * kLatent, kHeadDim, 2) ||
-        !encode(&maps.x, (const uint16_t*)p.x, p.n, kHeadDim / 64, p.heads, p.n > 1 ? p.x_token : kHeadDim, p.heads > 1 ? p.x_head : kHeadDim, nt, 2) ||
-        !encode(&maps.out, p.out, p.n, (kLatent + kRope) / 64, p.heads, (int64_t)p.heads * (kLatent + kRope), kLatent + kRope, nt, 2))
+    if (!encode_columns(&maps.w, true, p.w, kHeadDim, kLatent / 64, p.heads, p.w_row, p.heads > 1 ? p.w_head : kHeadDim * kLatent, kHeadDim, 2) ||
+        !encode_columns(&maps.x, true, (const uint16_t*)p.x, p.n, kHeadDim / 64, p.heads, p.n > 1 ? p.x_token : kHeadDim, p.heads > 1 ? p.x_head : kHeadDim, nt, 2) ||
+        !encode_columns(&maps.out, true, p.out, p.n, (kLatent + kRope) / 64, p.heads, (int64_t)p.heads * (kLatent + kRope), kLatent + kRope, nt, 2))
         return cudaErrorInvalidValue;
     const dim3 grid(kPieces, p.heads, (unsigned)tiles(p.n, nt));
     if (nt == 16) return launch_dependent(stream, grid, kAbsorbThreads, absorb_smem<16>(), absorb_kernel<16>, p, rot, maps);
@@ -460,7 +444,7 @@ cudaError_t launch_expand_outputs(cudaStream_t stream, const HeadProduct& p, int
     const dim3 few(kHeadDim / kFewDims, p.heads, (unsigned)tiles(p.n, kFewTokens));
     if ((int64_t)few.x * few.y * few.z <= 3 * (int64_t)num_sms) return launch_dependent(stream, few, kThreads, kFewSmem, expand_few_kernel, p);
     CUtensorMap map;
-    if (!encode(&map, p.w, kHeadDim, kLatent / 64, p.heads, p.w_row, p.heads > 1 ? p.w_head : kHeadDim * kLatent, kHeadDim, 2)) return cudaErrorInvalidValue;
+    if (!encode_columns(&map, true, p.w, kHeadDim, kLatent / 64, p.heads, p.w_row, p.heads > 1 ? p.w_head : kHeadDim * kLatent, kHeadDim, 2)) return cudaErrorInvalidValue;
     // a head's CTAs are as many as run at once with the other heads': a second round of them would read the
     // matrices again (256 tokens of 128 heads, cold: 20.5 us, 22.9 in two). More heads than SMs take two
     // all the same (64 tokens of 160 heads 10.7 us, of 128 heads 6.1), 80 heads leave half of the SMs idle

@@ -39,15 +39,6 @@ __device__ __forceinline__ float to_float(uint16_t bits) {
     if (BF16) return __uint_as_float((uint32_t)bits << 16);
     return __half2float(__ushort_as_half(bits));
 }
-template <bool BF16>
-__device__ __forceinline__ uint32_t pack(float lo, float hi) {
-    if (BF16) {
-        const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t*>(&r);
-    }
-    const __half2 r = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&r);
-}
 
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
     uint32_t r;

@@ -3,6 +3,8 @@
 // hs_prompt.cu).
 #pragma once
 
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -13,7 +15,6 @@ namespace hs {
 constexpr int kLatent = 512;      // values of a latent
 constexpr int kRope = 64;         // values of a rotary key
 constexpr int kHeadDim = 128;     // of a head's expanded keys and values
-constexpr int kLatentBlock = 128; // codes to a scale
 constexpr int kLatentEntry = 656; // 512 codes, 4 scales, 64 bf16
 
 // Positions as angles: row p of `table` holds 32 cosines, then 32 sines. table == nullptr:
@@ -26,6 +27,16 @@ struct Rotation {
 };
 
 #ifdef __CUDACC__
+// Two values rounded to 16-bit floats, in a word.
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    if (BF16) {
+        const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&r);
+    }
+    const __half2 r = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
 // The pair (x, y) turned by the angle whose cosine and sine are c and s.
 __device__ __forceinline__ float2 turn(float x, float y, float c, float s) {
     return make_float2(fmaf(x, c, -(y * s)), fmaf(x, s, y * c));

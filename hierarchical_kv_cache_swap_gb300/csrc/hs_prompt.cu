@@ -140,15 +140,6 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
         : "=f"(r.x), "=f"(r.y) : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
     return r;
 }
-template <bool BF16>
-__device__ __forceinline__ uint32_t pack(float lo, float hi) {
-    if (BF16) {
-        const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t*>(&r);
-    }
-    const __half2 r = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&r);
-}
 
 // Finds the prompt and the tile of it that the `at`-th of the prompts' tiles is, by one warp: 32
 // prompts at a time, their tiles counted and added up over the lanes. A prompt whose bounds are not in
@@ -638,20 +629,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
     }
 }
 
-// A tensor [tokens][heads][dims] of 16-bit floats (token and head strides in elements) read in boxes of
-// all dimensions, or the first `columns` times 64, of `rows` tokens of one head: a column of 64 after
-// the other, rows of 128 swizzled bytes.
-bool encode(CUtensorMap* map, bool bf16, const uint16_t* x, int dims, int64_t heads, int64_t tokens, int64_t head, int64_t token, int rows,
-            int columns) {
-    const EncodeTiled enc = tensor_map_encoder();
-    if (!enc) return false;
-    const cuuint64_t size[4] = {64, (cuuint64_t)tokens, (cuuint64_t)dims / 64, (cuuint64_t)heads};
-    const cuuint64_t stride[3] = {(cuuint64_t)token * 2, 128, (cuuint64_t)head * 2};
-    const cuuint32_t box[4] = {64, (cuuint32_t)rows, (cuuint32_t)columns, 1}, step[4] = {1, 1, 1, 1};
-    return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<uint16_t*>(x), size, stride, box,
-               step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 bool encode_rope(CUtensorMap* map, bool bf16, const uint16_t* x, int64_t tokens, int64_t token) {
     const EncodeTiled enc = tensor_map_encoder();
     if (!enc) return false;
@@ -694,9 +671,9 @@ cudaError_t launch_attend_prompts(cudaStream_t stream, bool bf16, const PromptAt
     const int64_t k_head = keys && a.H > 1 ? a.k_head : kHeadDim, v_head = keys && a.H > 1 ? a.v_head : kHeadDim;
     const int64_t k_token = n > 1 ? a.k_token : kHeadDim, v_token = n > 1 ? a.v_token : kHeadDim;
     const int64_t r_token = n > 1 ? a.r_token : kRope;
-    if (!encode(&maps.q, bf16, rows ? a.q : nothing, kQDims, a.H, m, q_head, q_token, kRows, kKChunks) ||
-        !encode(&maps.k, bf16, keys ? a.k : nothing, kHeadDim, a.H, n, k_head, k_token, kKeys, 1) ||
-        !encode(&maps.v, bf16, keys ? a.v : nothing, kHeadDim, a.H, n, v_head, v_token, 64, kHeadDim / 64) ||
+    if (!encode_columns(&maps.q, bf16, rows ? a.q : nothing, m, kQDims / 64, a.H, q_token, q_head, kRows, kKChunks) ||
+        !encode_columns(&maps.k, bf16, keys ? a.k : nothing, n, kHeadDim / 64, a.H, k_token, k_head, kKeys, 1) ||
+        !encode_columns(&maps.v, bf16, keys ? a.v : nothing, n, kHeadDim / 64, a.H, v_token, v_head, 64, kHeadDim / 64) ||
         !encode_rope(&maps.r, bf16, keys ? a.k_rope : nothing, n, r_token))
         return cudaErrorInvalidValue;
     // a CTA for every 256 rows of a prompt, at most one more than full ones for each prompt; without rows one,

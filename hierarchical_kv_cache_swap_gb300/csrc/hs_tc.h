@@ -184,4 +184,18 @@ inline EncodeTiled tensor_map_encoder() {
     return fn;
 }
 
+// A tensor [rows][heads][columns of 64] of 16-bit floats, its strides in elements, in boxes of `box_rows`
+// rows of `box_columns` columns of one head: a column after the other, rows of 128 swizzled bytes.
+inline bool encode_columns(CUtensorMap* map, bool bf16, const uint16_t* x, int64_t rows, int columns, int64_t heads, int64_t row, int64_t head,
+                           int box_rows, int box_columns) {
+    const EncodeTiled enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t size[4] = {64, (cuuint64_t)rows, (cuuint64_t)columns, (cuuint64_t)heads};
+    const cuuint64_t stride[3] = {(cuuint64_t)row * 2, 128, (cuuint64_t)head * 2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)box_rows, (cuuint32_t)box_columns, 1}, step[4] = {1, 1, 1, 1};
+    return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<uint16_t*>(x), size, stride, box,
+               step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace hs
