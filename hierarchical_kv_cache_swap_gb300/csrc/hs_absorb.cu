@@ -197,15 +197,22 @@ __global__ void __launch_bounds__(kAbsorbThreads) absorb_kernel(const HeadProduc
 }
 
 // ---------------------------------------------------------------- outputs
-// The f32 rows are rounded to bf16 for the products, as the sums behind them have been: 2^-8 of each at
-// most, of the size of the result's own rounding once 512 of them are summed (0.0024 of the result against
-// 64 bits, 0.0017 by its own rounding alone). Each as two bf16, its upper half and the rest, gave those
-// 0.0017 at 18.4 us instead of 15.6 for 256 tokens of 128 heads and 3.6 instead of 3.0 for 37 of 20.
-//
+// The f32 rows are sums that nothing has been rounded of yet, and the products take each value as two bf16,
+// its upper half and the rest, rounded: to within 2^-15 of it. (One bf16 each, 2^-8 of them at most, made the
+// results' error against 64 bits 0.0024 of them, where their own rounding alone makes it 0.0017; it took 15.8
+// us instead of 18.0 for 256 tokens of 128 heads, 3.0 instead of 3.2 for 37 of 20.)
+__device__ __forceinline__ void split(float x, float y, uint32_t& upper, uint32_t& rest) {
+    const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
+    upper = __byte_perm(a, b, 0x7632);
+    // (an infinity has no rest; a NaN's is one)
+    rest = pack<true>(fabsf(x) == INFINITY ? 0.f : x - __uint_as_float(a & 0xFFFF0000u), fabsf(y) == INFINITY ? 0.f : y - __uint_as_float(b & 0xFFFF0000u));
+}
+
 // Few tokens of few heads: a CTA takes 32 output dimensions and 16 tokens, all copies under way at once,
-// eight steps of 64 latent dimensions. Its eight warps are two over the dimensions by four shares of a
-// step, whose sums are added up in their order (mma.sync m16n8k16, which has no set-up to wait for).
-constexpr int kFewTokens = 16, kFewDims = 32, kSteps = kLatent / 64, kShares = 4;
+// eight steps of 64 latent dimensions. Its eight warps take a share of 16 latent dimensions each of two
+// steps, so that a value is split once, and their sums are added up in the warps' order (mma.sync
+// m16n8k16, which has no set-up to wait for).
+constexpr int kFewTokens = 16, kFewDims = 32, kSteps = kLatent / 64, kShares = 8;
 constexpr uint32_t kStepW = kFewDims * 128, kStepX = kFewTokens * 256, kStep = kStepW + kStepX;  // rows of 64 bf16, of 64 f32
 constexpr uint32_t kFewSmem = kSteps * kStep;
 
@@ -234,32 +241,35 @@ __global__ void __launch_bounds__(kThreads) expand_few_kernel(const HeadProduct 
         copy16(xa + t * 256 + ((u ^ (t & 7) << 1) << 4), in + (there ? t0 + t : 0) * p.x_token + 64 * s + 4 * u, there);
         copies_end();
     }
-    const int share = warp >> 1, col = (warp & 1) * 16;
-    float acc[2][4] = {};
-    for (int s = 0; s < kSteps; ++s) {
-        steps_landed<0>(s);
+    float acc[2][4][4] = {};  // of the upper halves and of the rests, eight output dimensions each
+    for (int i = 0; i < kSteps / 2; ++i) {
+        steps_landed<0>(2 * i + 1);
         __syncthreads();
-        const uint8_t* const w = smem + s * kStep;
+        const uint8_t* const w = smem + (2 * i + (warp >> 2)) * kStep;
         const uint8_t* const x = w + kStepW;
-        uint32_t a[4], b[4];
+        const int share = warp & 3;  // of the step's
+        uint32_t a[2][4], b[2][4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {  // rows g and g + 8, columns 2 c and 2 c + 8 of the share's 16
             const int t = (lane >> 2) + 8 * (r & 1), u = 4 * share + 2 * (r >> 1) + ((lane & 3) >> 1);
             const float2 v = *reinterpret_cast<const float2*>(x + t * 256 + ((u ^ (t & 7) << 1) << 4) + 8 * (lane & 1));
-            a[r] = pack<true>(v.x, v.y);
+            split(v.x, v.y, a[0][r], a[1][r]);
         }
-        ldsm(b, su32(w) + at(col + (lane & 7) + ((lane >> 4) << 3), 2 * share + ((lane >> 3) & 1)));
-        mma(acc[0], a, b[0], b[1]);
-        mma(acc[1], a, b[2], b[3]);
+#pragma unroll
+        for (int n = 0; n < 2; ++n) ldsm(b[n], su32(w) + at(16 * n + (lane & 7) + ((lane >> 4) << 3), 2 * share + ((lane >> 3) & 1)));
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int n = 0; n < 4; ++n) mma(acc[part][n], a[part], b[n >> 1][2 * (n & 1)], b[n >> 1][2 * (n & 1) + 1]);
     }
     __syncthreads();  // the operands' place becomes the shares'
     float* const sums = reinterpret_cast<float*>(smem);  // [kShares][kFewTokens][kFewDims]
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+    for (int n = 0; n < 4; ++n)
 #pragma unroll
         for (int r = 0; r < 2; ++r)
-            *reinterpret_cast<float2*>(sums + (share * kFewTokens + 8 * r + (lane >> 2)) * kFewDims + col + 8 * n + 2 * (lane & 3)) =
-                make_float2(acc[n][2 * r], acc[n][2 * r + 1]);
+            *reinterpret_cast<float2*>(sums + (warp * kFewTokens + 8 * r + (lane >> 2)) * kFewDims + 8 * n + 2 * (lane & 3)) =
+                make_float2(acc[0][n][2 * r] + acc[1][n][2 * r], acc[0][n][2 * r + 1] + acc[1][n][2 * r + 1]);
     __syncthreads();
     const int t = tid >> 4, e = 2 * (tid & 15);  // a thread two dimensions of a token
     float2 v = make_float2(0.f, 0.f);
@@ -272,42 +282,50 @@ __global__ void __launch_bounds__(kThreads) expand_few_kernel(const HeadProduct 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// Many tokens: a CTA keeps its head's whole matrix (128 output dimensions: the product's rows) and takes
-// tiles of 32 tokens (its columns), each by one of two groups of eight warps: they load a tile's f32 rows
-// straight into registers, round them into shared memory, and load the next ones while one thread
-// multiplies and all write the columns, two at a time as above. The two groups' tiles keep 128 KB of
-// loads under way, which is what it takes to draw an SM's share of the memory's rate.
-constexpr int kTokens = 32, kGroupThreads = 256, kManyThreads = 2 * kGroupThreads;
+// Many tokens: a CTA brings its head's whole matrix (128 output dimensions: the product's rows) into tensor
+// memory, 256 columns, and takes tiles of 32 tokens, each by one of two groups of eight warps: they load a
+// tile's f32 rows straight into registers, split them into shared memory (64 rows: the tokens' upper halves,
+// then their rests: the product's columns), and load the next ones while one thread multiplies and all write
+// the sums of the two halves' columns, two tokens at a time as above. The two groups' tiles keep 128 KB of
+// loads under way, which is what it takes to draw an SM's share of the memory's rate. The matrix comes by way
+// of the tiles' place, before the first ones: 1.1 us a CTA, but then both halves of the rows have room there
+// (with the matrix in shared memory and tiles in four stages 512 tokens of 128 heads took 46 us instead of 36).
+constexpr int kTokens = 32, kGroupThreads = 256, kManyThreads = 2 * kGroupThreads, kCols = 2 * kTokens;
 struct ExpandSmem {  // beyond the operands
-    uint64_t landed, done[2], over[2];  // over: a tile's products have ended, or there are none, whatever happened
+    uint64_t landed[4], done[2], over[2];  // landed: a quarter of the matrix; over: a tile's products have ended, or there are none, whatever happened
     uint32_t tmem;
     volatile int abort;
 };
-constexpr uint32_t kMatrix = kHeadDim * kLatent * 2, kTokenTile = kTokens * kLatent * 2;
-constexpr uint32_t kManySmem = 1024 + kMatrix + 2 * kTokenTile + sizeof(ExpandSmem);
+constexpr uint32_t kMatrix = kHeadDim * kLatent * 2, kTile64 = kCols * 128, kTokenTile = kLatent / 64 * kTile64;
+constexpr uint32_t kManyTmem = 512, kMatrixCols = kLatent / 2;
+constexpr uint32_t kManySmem = 1024 + 2 * kTokenTile + sizeof(ExpandSmem);
+static_assert(kMatrix <= 2 * kTokenTile, "the matrix comes by way of the tiles' place");
 
 __global__ void __launch_bounds__(kManyThreads, 1) expand_many_kernel(const HeadProduct p, const __grid_constant__ CUtensorMap map) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     uint8_t* const base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    ExpandSmem* const sm = reinterpret_cast<ExpandSmem*>(base + kMatrix + 2 * kTokenTile);
+    ExpandSmem* const sm = reinterpret_cast<ExpandSmem*>(base + 2 * kTokenTile);
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31, h = blockIdx.x;
     const int group = warp >> 3, tid = threadIdx.x & (kGroupThreads - 1);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (threadIdx.x == 0) {
-        bar_init(&sm->landed, 1);
+        for (int i = 0; i < 4; ++i) bar_init(&sm->landed[i], 1);
         for (int i = 0; i < 2; ++i) bar_init(&sm->done[i], 1), bar_init(&sm->over[i], 1);
         sm->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        bar_expect_tx(&sm->landed, kMatrix);
-        for (int c = p.waits.stall; c < 4; ++c) tma_load_4d(su32(base) + c * (kMatrix / 4), &map, 0, 0, 2 * c, h, &sm->landed);
+        for (int c = 0; c < 4; ++c) {
+            bar_expect_tx(&sm->landed[c], kMatrix / 4);
+            if (!p.waits.stall || c > 0) tma_load_4d(su32(base) + c * (kMatrix / 4), &map, 0, 0, 2 * c, h, &sm->landed[c]);
+        }
     }
-    if (warp == 0) tmem_alloc<2 * kTokens>(&sm->tmem);
+    if (warp == 0) tmem_alloc<kManyTmem>(&sm->tmem);
     // unit u (8 values) of the group's tile: of token u / 64, dimensions 8 (u % 64) on
     const float* const in = (const float*)p.x + h * p.x_head;
     const int64_t step = (int64_t)gridDim.y * 2 * kTokens, pitch = (int64_t)p.heads * kHeadDim;
     constexpr int kUnits = kTokens * kLatent / 8 / kGroupThreads;  // of a thread
-    uint8_t* const x = base + kMatrix + group * kTokenTile;
+    uint8_t* const x = base + group * kTokenTile;
     float4 v[2 * kUnits];
+    uint4 upper[kUnits], rest[kUnits];
     auto fetch = [&](int64_t t0) {
 #pragma unroll
         for (int i = 0; i < kUnits; ++i) {
@@ -322,34 +340,61 @@ __global__ void __launch_bounds__(kManyThreads, 1) expand_many_kernel(const Head
             }
         }
     };
+    auto halve = [&] {
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i) {
+            split(v[2 * i].x, v[2 * i].y, upper[i].x, rest[i].x);
+            split(v[2 * i].z, v[2 * i].w, upper[i].y, rest[i].y);
+            split(v[2 * i + 1].x, v[2 * i + 1].y, upper[i].z, rest[i].z);
+            split(v[2 * i + 1].z, v[2 * i + 1].w, upper[i].w, rest[i].w);
+        }
+    };
     int64_t t0 = ((int64_t)blockIdx.y * 2 + group) * kTokens;
     fetch(t0);
     fence_before();
     __syncthreads();
     fence_after();
-    const uint32_t cols = sm->tmem + group * kTokens;
-    bool ok = true;
+    // The matrix, from rows of 128 swizzled bytes: a lane a row, warps w, w + 4, w + 8 and w + 12 a quarter each.
+    const uint32_t matrix = sm->tmem, lanes = (uint32_t)((warp & 3) * 32) << 16, cols = matrix + kMatrixCols + group * kCols;
+    const bool landed = __all_sync(0xffffffffu, bar_wait(&sm->landed[warp >> 2], 0, &sm->abort, p.waits.ns));
+    if (__builtin_expect(!landed, 0)) bar_drain(&sm->landed[warp >> 2], 0, 4 * p.waits.ns);  // the tiles' place is written below
+#pragma unroll 1
+    for (int c = 2 * (warp >> 2); c < 2 * (warp >> 2) + 2; ++c) {
+        const int row = (warp & 3) * 32 + lane;
+        const uint4* const from = reinterpret_cast<const uint4*>(base + c * (kHeadDim * 128) + row * 128);
+        uint32_t r[32];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const uint4 w = from[u ^ (row & 7)];
+            r[4 * u] = w.x, r[4 * u + 1] = w.y, r[4 * u + 2] = w.z, r[4 * u + 3] = w.w;
+        }
+        tmem_store32(matrix + lanes + 32 * c, r);
+    }
+    tmem_wait_st();
+    fence_before();
+    __syncthreads();
+    fence_after();
+    bool ok = !sm->abort;  // one for all warps: who set it did before they met
     for (int k = 0; t0 < p.n; t0 += step, ++k) {
+        halve();
 #pragma unroll
         for (int i = 0; i < kUnits; ++i) {
             const int u = i * kGroupThreads + tid, t = u >> 6, c = u & 63;  // a column of 64 dimensions after the other
-            *reinterpret_cast<uint4*>(x + (c >> 3) * (kTokens * 128) + t * 128 + (((c & 7) ^ (t & 7)) << 4)) =
-                make_uint4(pack<true>(v[2 * i].x, v[2 * i].y), pack<true>(v[2 * i].z, v[2 * i].w), pack<true>(v[2 * i + 1].x, v[2 * i + 1].y),
-                           pack<true>(v[2 * i + 1].z, v[2 * i + 1].w));
+            uint8_t* const to = x + (c >> 3) * kTile64 + t * 128 + (((c & 7) ^ (t & 7)) << 4);
+            *reinterpret_cast<uint4*>(to) = upper[i];
+            *reinterpret_cast<uint4*>(to + kTokens * 128) = rest[i];
         }
         fence_async_smem();
         fence_before();
         asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(kGroupThreads) : "memory");
         if (t0 + step < p.n) fetch(t0 + step);
         if ((warp & 7) == 0) {
-            ok = __all_sync(0xffffffffu, ok && bar_wait(&sm->landed, 0, &sm->abort, p.waits.ns));
             fence_after();
             if (ok && elect_one()) {
-                constexpr uint32_t id = mma_idesc(true, kHeadDim, kTokens, 0);
-                const uint32_t a = smem_desc(su32(base), 16), b = smem_desc(su32(x), 16);
+                constexpr uint32_t id = mma_idesc(true, kHeadDim, kCols, 0);
+                const uint32_t b = smem_desc(su32(x), 16);
 #pragma unroll
-                for (int s = 0; s < kLatent / 16; ++s)
-                    mma_ss(cols, a + (s >> 2) * (kHeadDim * 8) + 2 * (s & 3), b + (s >> 2) * (kTokens * 8) + 2 * (s & 3), id, s ? 1u : 0u);
+                for (int s = 0; s < kLatent / 16; ++s) mma_ts(cols, matrix + 8 * s, b + (s >> 2) * (kTile64 / 16) + 2 * (s & 3), id, s ? 1u : 0u);
                 mma_commit(&sm->done[group]);
                 mma_commit(&sm->over[group]);
             }
@@ -363,12 +408,15 @@ __global__ void __launch_bounds__(kManyThreads, 1) expand_many_kernel(const Head
             __syncwarp();
         }
         fence_after();
-        // warps w and w + 4 share 32 output dimensions: half of the columns each
-        uint32_t d[16];
+        // warps w and w + 4 share 32 output dimensions: half of the tokens each
+        uint32_t both[2][16], d[16];
         const int half = (warp >> 2) & 1, odd = lane & 1;
-        tmem_load16(d, cols + ((uint32_t)((warp & 3) * 32) << 16) + 16 * half);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) tmem_load16(both[i], cols + lanes + i * kTokens + 16 * half);
         tmem_wait_ld();
         fence_before();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) d[j] = __float_as_uint(__uint_as_float(both[0][j]) + __uint_as_float(both[1][j]));
         uint16_t* const to = p.out + h * kHeadDim + (warp & 3) * 32 + (lane & ~1);
 #pragma unroll
         for (int j = 0; j < 16; j += 2) {
@@ -380,14 +428,12 @@ __global__ void __launch_bounds__(kManyThreads, 1) expand_many_kernel(const Head
         // after an abort, too: warps may differ in whether a wait ran out, and the others come here
         asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(kGroupThreads) : "memory");  // all have read the columns
     }
-    // after an abort: no copy may be under way at the CTA's end
-    if (threadIdx.x == 0) bar_drain(&sm->landed, 0, p.waits.ns);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     fence_before();
     __syncthreads();
     if (warp == 0) {
         fence_after();
-        tmem_free<2 * kTokens>(sm->tmem);
+        tmem_free<kManyTmem>(sm->tmem);
     }
 }
 
@@ -438,16 +484,16 @@ cudaError_t launch_expand_outputs(cudaStream_t stream, const HeadProduct& p, int
     cudaError_t e = set_up();
     if (e != cudaSuccess) return e;
     // few tokens of few heads: pieces of 32 output dimensions of 16 tokens, while all CTAs run at once, three an
-    // SM. us of this kernel and of the other, in a graph, by CTAs (152 SMs): 320 (80 tokens of 16 heads) 3.6 and
-    // 5.6, 384 (16 of 96) 3.6 and 4.3, 512 (128 of 16) 4.3 and 5.6, 512 (16 of 128) 4.3 and 4.3, 512 (1 of 128)
-    // 4.5 and 4.0, 768 (48 of 64) 5.9 and 5.4, 1024 (256 of 16) 6.8 and 5.6, 1536 (48 of 128) 9.8 and 5.6
+    // SM. us of this kernel and of the other, in a graph, by CTAs (152 SMs): 320 (80 tokens of 16 heads) 3.9 and
+    // 6.7, 384 (16 of 96) 4.0 and 5.0, 512 (128 of 16) 4.9 and 6.8, 512 (16 of 128) 4.9 and 5.0, 512 (1 of 128)
+    // 5.0 and 4.6, 768 (48 of 64) 6.6 and 6.6, 1024 (256 of 16) 7.8 and 6.9, 1536 (48 of 128) 11.2 and 6.9
     const dim3 few(kHeadDim / kFewDims, p.heads, (unsigned)tiles(p.n, kFewTokens));
     if ((int64_t)few.x * few.y * few.z <= 3 * (int64_t)num_sms) return launch_dependent(stream, few, kThreads, kFewSmem, expand_few_kernel, p);
     CUtensorMap map;
     if (!encode_columns(&map, true, p.w, kHeadDim, kLatent / 64, p.heads, p.w_row, p.heads > 1 ? p.w_head : kHeadDim * kLatent, kHeadDim, 2)) return cudaErrorInvalidValue;
     // a head's CTAs are as many as run at once with the other heads': a second round of them would read the
     // matrices again (256 tokens of 128 heads, cold: 20.5 us, 22.9 in two). More heads than SMs take two
-    // all the same (64 tokens of 160 heads 10.7 us, of 128 heads 6.1), 80 heads leave half of the SMs idle
+    // all the same (64 tokens of 160 heads 13.2 us, of 128 heads 7.2), 80 heads leave half of the SMs idle
     const int64_t most = p.heads < num_sms ? num_sms / p.heads : 1, t = tiles(p.n, 2 * kTokens);
     return launch_dependent(stream, dim3(p.heads, (unsigned)(t < most ? t : most)), kManyThreads, kManySmem, expand_many_kernel, p, map);
 }

@@ -589,7 +589,7 @@ int hs_absorb_queries(hs_stream_t stream, const hs_head_product* product, const 
 /*
  * hs_expand_outputs -- what hs_attend gives (x: f32 [n][heads][512], strides multiples of 4)
  * through the heads' value matrices: out[..][e] = sum_c x[..][c] w[head][e][c], e < 128 (out: bf16
- * [n][heads][128]). x is rounded to bf16 for the products, the sums are f32. HS_STATUS_TIMEOUT in
+ * [n][heads][128]). x is taken to within 2^-15 of itself (as two bf16), the sums are f32. HS_STATUS_TIMEOUT in
  * *product->status (or NULL): a hand-off within the kernel was lost (a defect); rows are then NaN.
  */
 int hs_expand_outputs(hs_stream_t stream, const hs_head_product* product);

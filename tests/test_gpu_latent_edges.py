@@ -177,3 +177,35 @@ def test_outputs_at_sizes_about_the_kernels_limits(n, H):
     # x's rounding and the result's, and f32 sums of 512
     assert ((back[:n].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 514 * 2.0 ** -23) * size).all()
     assert int(word) == 0 and (back[n:] == 7).all()
+
+
+@pytest.mark.parametrize("n,H", [(1, 2), (1, 128), (16, 5), (40, 20), (65, 2), (70, 128), (300, 9), (1000, 30)])
+def test_outputs_take_sums_of_latents_as_they_are(n, H):
+    """Sums that differ by less than a step of bf16, which the matrices make all of the result: f32 rows are taken
+    to within 2^-15, with f32 sums of 1024 products, and the result is rounded."""
+    x = 1 + torch.randint(-5, 6, (n, H, 512), generator=gen(n), device="cuda") * 2.0 ** -10
+    up = torch.randint(0, 2, (H, 128, 512), generator=gen(H), device="cuda").to(BF16) * 2 - 1
+    up[..., 1::2] = -up[..., ::2]  # pairs of opposite signs
+    out = torch.empty((n, H, 128), dtype=BF16, device="cuda")
+    hs.expand_outputs(x, up, out)
+    want = torch.einsum("nhc,hec->nhe", x.double(), up.double())
+    size = torch.einsum("nhc,hec->nhe", x.double().abs(), up.double().abs())
+    assert ((out.double() - want).abs() <= 2.0 ** -8 * want.abs() + (2.0 ** -15 + 1026 * 2.0 ** -23) * size).all()
+
+
+@pytest.mark.parametrize("n,H", [(3, 2), (200, 40)])
+def test_outputs_of_rows_that_are_not_finite(n, H):
+    """Infinities stay infinite, through the largest numbers too, and NaNs NaNs, whatever their bits."""
+    x, up = normal(gen(1), n, H, 512), normal(gen(2), H, 128, 512).to(BF16).abs() + 1
+    x[0, 0, 5], x[1, 0, 6], x[2, 0, 7] = float("inf"), float("-inf"), float("nan")
+    x[1, 1] = 0
+    x[1, 1, 9] = torch.finfo(torch.float32).max
+    x.view(torch.int32)[2, 1, 511] = 0x7F800001
+    out = torch.empty((n, H, 128), dtype=BF16, device="cuda")
+    hs.expand_outputs(x, up, out)
+    assert (out[0, 0] == float("inf")).all() and (out[1, 0] == float("-inf")).all()
+    assert torch.isnan(out[2, 0]).all() and torch.isnan(out[2, 1]).all()
+    assert (out[1, 1] == float("inf")).all()  # times 1 or more: too large, but for 1 itself, which rounds up in bf16
+    assert torch.isfinite(out[0, 1]).all()
+    if n > 3:
+        assert torch.isfinite(out[3:]).all()
