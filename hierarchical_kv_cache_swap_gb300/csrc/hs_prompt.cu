@@ -613,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
                 }
             }
             if (there)
-                A.lse[to * A.H + h] = !ok ? none : l == 0.f ? -INFINITY : (m + (lg2(l) - kLiftLog2<BF16>)) * 0.69314718055994531f;
+                A.lse[to * A.H + h] = !ok ? none : l == 0.f ? -INFINITY : (m + lg2(BF16 ? l : l * 0x1p-7f)) * 0.69314718055994531f;
             t0 += nt;
             c0 += n;
             if (!ok) break;

@@ -209,3 +209,21 @@ def test_outputs_of_rows_that_are_not_finite(n, H):
     assert torch.isfinite(out[0, 1]).all()
     if n > 3:
         assert torch.isfinite(out[3:]).all()
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_the_lse_of_a_single_key_is_its_score(dtype):
+    """Whole numbers, whose products and sums are exact: the score's factor (of two roundings, 2^-24 each), its
+    product, the sum with the weights' logarithm and the way back are off by 5 2^-24, the logarithm of a sum
+    of about 1 by 2^-22."""
+    n, H = 300, 3
+    q, k, r, v, *_ = prompts([(n, n)], H, dtype, 17)
+    for t in (q, k, r):
+        t.copy_(torch.randint(-4, 5, t.shape, generator=gen(t.numel()), device="cuda"))
+    at = torch.arange(n + 1, dtype=torch.int32, device="cuda")  # n prompts of a row and a key
+    o, lse = torch.empty((n, H, 128), dtype=dtype, device="cuda"), torch.empty((n, H), device="cuda")
+    hs.attend_prompts(q, k, r, v, at, at, o, lse, 0.0625)
+    kk = torch.cat((k, r[:, None].expand(-1, H, -1)), -1)
+    want = (q.double() * kk.double()).sum(-1) * 0.0625
+    assert torch.equal(o, v)
+    assert ((lse.double() - want).abs() <= 5 * 2.0 ** -24 * want.abs() + 2.0 ** -22).all()
