@@ -11,9 +11,9 @@
 // its columns (tcgen05, bf16 operands, f32 sums). Measured on one GB300 (us, in a graph, with L2 cold
 // where "cold"; in brackets the bytes at a copy's rate):
 //   tokens x heads   1 x 128     64 x 128   256 x 128   256 x 128 cold   512 x 128 cold   37 x 20
-//   queries          3.9 (2.5)   5.3 (4.3)  13.8 (9.9)  18.4 (9.9)       30.9 (17.3)      2.9
-//   outputs          3.8 (2.5)   5.9 (5.3)  15.6 (13.6) 20.5 (13.6)      33.2 (24.8)      3.3
-// Cold, DRAM is at 20 % (queries) and 49 % (outputs) of its peak: what is left is the time of a CTA's
+//   queries          4.0 (2.5)   5.4 (4.3)  13.9 (9.9)  18.5 (9.9)       31.6 (17.3)      2.9
+//   outputs          4.6 (2.5)   7.3 (5.3)  17.9 (13.6) 22.8 (13.6)      36.0 (24.8)      3.2
+// Cold, DRAM is at 20 % (queries) and 44 % (outputs) of its peak: what is left is the time of a CTA's
 // chain of copy, product and store, of which an SM has four (one) at once. CTAs of the queries that
 // loop over tiles of tokens with two under way were slower (21.6 us for 256 tokens, cold), and so were
 // tiles of 128 tokens (20.1 warm).

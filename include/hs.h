@@ -578,8 +578,8 @@ typedef struct {
  * hs_absorb_queries -- the queries of the absorbed form, as hs_attend takes them: of x (bf16
  * [n][heads][128 + 64]) the first 128 values become out[..][c] = sum_d x[..][d] w[head][d][c], c <
  * 512, and the last 64, rotated (rotation: NULL if they are already), out[..][512 ..] (out: bf16
- * [n][heads][576], not x; x's strides positive, n at most 65535 * 64). bf16 products, f32 sums, one rounding. A token
- * whose position is negative gets zeros for its rotary values; so does one that the table has no row
+ * [n][heads][576], not x; x's strides positive, n at most 65535 * 64). bf16 products, f32 sums, one
+ * rounding. A token whose position is negative gets zeros for its rotary values; so does one that the table has no row
  * for, which sets HS_STATUS_RANGE in *status (or NULL). HS_STATUS_TIMEOUT: a hand-off within the kernel
  * was lost (a defect); rows are then NaN in out[..][.. 512]. Returns HS_OK, HS_ERR_INVALID, HS_ERR_LIMIT
  * or HS_ERR_CUDA.
@@ -589,8 +589,9 @@ int hs_absorb_queries(hs_stream_t stream, const hs_head_product* product, const 
 /*
  * hs_expand_outputs -- what hs_attend gives (x: f32 [n][heads][512], strides multiples of 4)
  * through the heads' value matrices: out[..][e] = sum_c x[..][c] w[head][e][c], e < 128 (out: bf16
- * [n][heads][128]). x is taken to within 2^-15 of itself (as two bf16), the sums are f32. HS_STATUS_TIMEOUT in
- * *product->status (or NULL): a hand-off within the kernel was lost (a defect); rows are then NaN.
+ * [n][heads][128]). x is taken to within 2^-15 of itself (as two bf16), the sums are f32.
+ * HS_STATUS_TIMEOUT in *product->status (or NULL): a hand-off within the kernel was lost (a defect);
+ * rows are then NaN.
  */
 int hs_expand_outputs(hs_stream_t stream, const hs_head_product* product);
 
