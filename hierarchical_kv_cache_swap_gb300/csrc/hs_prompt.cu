@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
         } else if (warp == kCopyWarp) {
             // ------------------------------------------------------------ copies (issued by one lane)
             const bool leader = elect_one();
-            int t0 = 0, issued = 0, asked = -1;  // chunks; the last item whose queries are on their way
+            int t0 = 0, issued = 0, asked0 = -1, asked1 = -1;  // chunks; the last item whose queries, by row tile, are on their way
             for (int k = 0; leader; ++k) {
                 auto until = [&](uint64_t* bar, int parity) { ok = ok && bar_wait(bar, parity & 1, &sm->abort, A.waits.ns); };
                 ok = ok && bar_wait_moving(&sm->item_full[k % kItems], (k / kItems) & 1, &sm->abort, A.waits.ns, sm->beat);
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
                         for (int w = 0; w < 2; ++w) {
                             if (k > 0) until(&sm->q_free[w], k - 1);
                             if (!ok) break;
-                            if (w == 1) asked = k;
+                            (w ? asked1 : asked0) = k;
                             if ((w ? n1 : n0) > 0) {
                                 bar_expect_tx(&sm->q_full[w], kKChunks * kChunk);
                                 tma_load_4d(su32(base) + w * kKChunks * kChunk, &maps.q, 0, q_row + w * kRows, 0, it.h, &sm->q_full[w]);
@@ -369,7 +369,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
                 for (int t = max(issued / kTileChunks - 2, 0); t * kTileChunks < issued; ++t)
                     for (int part = 0; part < kParts; ++part)
                         if (issued > t * kTileChunks + (part < 2 ? part : part + 1)) bar_drain(&sm->full[t & 1][part], (t >> 1) & 1, A.waits.ns);
-                for (int w = 0; w < 2 && asked >= 0; ++w) bar_drain(&sm->q_full[w], asked & 1, A.waits.ns);
+                for (int w = 0; w < 2; ++w) {
+                    const int asked = w ? asked1 : asked0;
+                    if (asked >= 0) bar_drain(&sm->q_full[w], asked & 1, A.waits.ns);
+                }
             }
             __syncwarp();
         } else {

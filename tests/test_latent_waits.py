@@ -37,11 +37,11 @@ def test_threads_set_their_own():
     assert got == [hs.HS_OK]
 
 
-def kernel(name):
+def kernel(name, source="hs_absorb.cu", first="const HeadProduct p"):
     csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "hierarchical_kv_cache_swap_gb300", "csrc")
-    with open(os.path.join(csrc, "hs_absorb.cu")) as f:
+    with open(os.path.join(csrc, source)) as f:
         text = re.sub(r"//[^\n]*", "", f.read())
-    return re.split(r"__global__ void", text.split(name + "(const HeadProduct p")[1])[0]
+    return re.split(r"__global__ void", text.split(name + "(" + first)[1])[0]
 
 
 def test_absorbed_queries_leave_what_is_in_flight_alone():
@@ -71,3 +71,12 @@ def test_the_outputs_call_takes_a_status_word():
     with pytest.raises(TypeError, match="5 arguments"):
         hs._native().expand_outputs(o, up, out, None)
     assert hs._HeadProduct().status is None and hs._HeadProduct._fields_[-1][0] == "status"
+
+
+def test_each_row_tiles_queries_are_waited_for_at_the_end():
+    """The copies of an item's queries are issued a row tile at a time, with a wait between them that may run out:
+    what is on its way is noted for each, before it is."""
+    body = kernel("prompt_kernel", "hs_prompt.cu", "const PromptAttention A")
+    turn = body[body.index("until(&sm->q_free[w], k - 1)"):body.index("&maps.q, 0, q_row")]
+    assert turn.count("(w ? asked1 : asked0) = k;") == 1
+    assert re.search(r"asked = w \? asked1 : asked0;\s*if \(asked >= 0\) bar_drain\(&sm->q_full\[w\], asked & 1", body)
