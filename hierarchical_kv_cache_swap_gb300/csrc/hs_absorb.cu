@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kAbsorbThreads) absorb_kernel(const HeadProduc
         }
         __syncwarp();
         if (__builtin_expect(!ok, 0)) {  // no copy lands after the CTA's end
-            bar_drain(&sm->landed, 0, p.waits.ns);
+            bar_drain(&sm->landed, 0, p.waits.drain);
             if (lane == 0) bar_arrive(&sm->over);
         }
     }
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kAbsorbThreads) absorb_kernel(const HeadProduc
         const bool ok = __all_sync(0xffffffffu, bar_wait(&sm->done, 0, &sm->abort, p.waits.ns));
         fence_after();
         if (__builtin_expect(!ok, 0)) {  // the operands' place is written below: not while copies or products use it
-            bar_drain(&sm->over, 0, 4 * p.waits.ns);  // (after the issuing warp's wait and its drain)
+            bar_drain(&sm->over, 0, 4 * p.waits.drain);  // (after the issuing warp's wait and its drain)
             if (lane == 0 && p.status) atomicOr(p.status, 8u /* HS_STATUS_TIMEOUT */);
             __syncwarp();
         }
@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) expand_many_kernel(const Head
     // The matrix, from rows of 128 swizzled bytes: a lane a row, warps w, w + 4, w + 8 and w + 12 a quarter each.
     const uint32_t matrix = sm->tmem, lanes = (uint32_t)((warp & 3) * 32) << 16, cols = matrix + kMatrixCols + group * kCols;
     const bool landed = __all_sync(0xffffffffu, bar_wait(&sm->landed[warp >> 2], 0, &sm->abort, p.waits.ns));
-    if (__builtin_expect(!landed, 0)) bar_drain(&sm->landed[warp >> 2], 0, 4 * p.waits.ns);  // the tiles' place is written below
+    if (__builtin_expect(!landed, 0)) bar_drain(&sm->landed[warp >> 2], 0, p.waits.drain);  // the tiles' place is written below
 #pragma unroll 1
     for (int c = 2 * (warp >> 2); c < 2 * (warp >> 2) + 2; ++c) {
         const int row = (warp & 3) * 32 + lane;
@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) expand_many_kernel(const Head
         }
         ok = __all_sync(0xffffffffu, ok && bar_wait(&sm->done[group], k & 1, &sm->abort, p.waits.ns));
         if (__builtin_expect(!ok, 0)) {  // the tile's place is not written again, nor the columns freed, under its products
-            bar_drain(&sm->over[group], k & 1, 4 * p.waits.ns);
+            bar_drain(&sm->over[group], k & 1, 4 * p.waits.drain);
             if (lane == 0 && p.status) atomicOr(p.status, 8u /* HS_STATUS_TIMEOUT */);
             __syncwarp();
         }

@@ -679,14 +679,14 @@ int hs_attend_pages(hs_stream_t stream, const hs_page_attention* a) {
 }
 
 // The calling thread's (hs_set_latent_waits).
-static thread_local hs::Waits g_latent_waits{hs::kLatentWaitNs, 0};
+static thread_local hs::Waits g_latent_waits = hs::waits_of(hs::kLatentWaitNs, false);
 
 int hs_set_latent_waits(uint64_t ns, unsigned flags) {
     if (flags & ~(unsigned)HS_FLAG_TEST_STALL) return fail(HS_ERR_INVALID, "unknown flags 0x%x", flags);
     if (ns < hs::kMinWaitNs || ns > hs::kMaxWaitNs)
         return fail(HS_ERR_INVALID, "wait limit %llu ns outside [%llu, %llu]", (unsigned long long)ns,
                     (unsigned long long)hs::kMinWaitNs, (unsigned long long)hs::kMaxWaitNs);
-    g_latent_waits = hs::Waits{ns, (flags & HS_FLAG_TEST_STALL) ? 1 : 0};
+    g_latent_waits = hs::waits_of(ns, (flags & HS_FLAG_TEST_STALL) != 0);
     return HS_OK;
 }
 

@@ -43,13 +43,16 @@ __device__ __forceinline__ float2 turn(float x, float y, float c, float s) {
 }
 #endif
 
-// The waits of a call's kernel: the limit of each, in nanoseconds, and (tests) whether the first copy is
-// withheld, so that they run out (hs_set_latent_waits).
-constexpr uint64_t kLatentWaitNs = 1000000000ull;
+// The waits of a call's kernel (hs_set_latent_waits): the limit of each, in nanoseconds, that of a wait for
+// what is still in flight after one of them ran out, and (tests) whether the first copy is withheld, so that
+// they run out. A copy that landed after its CTA's end would land in another's memory: the second limit is
+// never short of what a copy or a product can take.
+constexpr uint64_t kLatentWaitNs = 1000000000ull, kLeastDrainNs = 10000000ull;
 struct Waits {
-    uint64_t ns;
+    uint64_t ns, drain;
     int stall;
 };
+inline Waits waits_of(uint64_t ns, bool stall) { return Waits{ns, ns > kLeastDrainNs ? ns : kLeastDrainNs, stall ? 1 : 0}; }
 
 // Rows of n tokens, 16-bit floats, 16-byte aligned, `latent_stride` and `rope_stride` elements apart.
 struct LatentRows {

@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
                 __syncwarp();
                 wait(&sm->answered, asked++);
                 if (!ok) {
-                    bar_drain(&sm->answered, (asked - 1) & 1, A.waits.ns);  // the answer lands before the CTA's end
+                    bar_drain(&sm->answered, (asked - 1) & 1, A.waits.drain);  // the answer lands before the CTA's end
                     break;
                 }
                 const bool more = block_given(sm->answer, &index);
@@ -368,10 +368,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
             if (leader) {
                 for (int t = max(issued / kTileChunks - 2, 0); t * kTileChunks < issued; ++t)
                     for (int part = 0; part < kParts; ++part)
-                        if (issued > t * kTileChunks + (part < 2 ? part : part + 1)) bar_drain(&sm->full[t & 1][part], (t >> 1) & 1, A.waits.ns);
+                        if (issued > t * kTileChunks + (part < 2 ? part : part + 1)) bar_drain(&sm->full[t & 1][part], (t >> 1) & 1, A.waits.drain);
                 for (int w = 0; w < 2; ++w) {
                     const int asked = w ? asked1 : asked0;
-                    if (asked >= 0) bar_drain(&sm->q_full[w], asked & 1, A.waits.ns);
+                    if (asked >= 0) bar_drain(&sm->q_full[w], asked & 1, A.waits.drain);
                 }
             }
             __syncwarp();
@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const PromptAttenti
             // whatever happened, every product issued here is done before the columns are freed. (O is free for
             // an item's first values as soon as its first P is there: the same threads had read O before.)
             if (leader) mma_commit(&sm->drain[w]);
-            bar_drain(&sm->drain[w], 0, A.waits.ns);
+            bar_drain(&sm->drain[w], 0, A.waits.drain);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));

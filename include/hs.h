@@ -640,8 +640,8 @@ int hs_attend_prompts(hs_stream_t stream, const hs_prompt_attention* args);
 /*
  * hs_set_latent_waits -- for the latent calls that the calling thread makes after it returns: the
  * time limit, in nanoseconds of the GPU's global timer, of each wait within their kernels, whose
- * roles hand tiles to one another, and of each drain of what is still in flight once a wait has run
- * out; default 1 s, range [1 us, 10 s]. (hs_set_wait_limit's is for a CTA as a whole; one of
+ * roles hand tiles to one another, and (10 ms where that is more) of each drain of what is still in
+ * flight once a wait has run out; default 1 s, range [1 us, 10 s]. (hs_set_wait_limit's is for a CTA as a whole; one of
  * hs_attend_prompts may work for seconds, on one tile after another; while it does, or searches the
  * prompts for its next, those that wait for it do not run out.) flags: 0, or
  * HS_FLAG_TEST_STALL (tests): the kernel's first copy is announced and never made, so that the waits

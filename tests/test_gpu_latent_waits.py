@@ -137,3 +137,37 @@ def test_expanded_outputs(stalled, n, H):
     for bad in (word.cpu(), status_word().long(), torch.zeros(2, dtype=torch.int32, device="cuda")):
         with pytest.raises(ValueError, match="status must be"):
             hs.expand_outputs(o, up, out[:n], status=bad)
+
+
+def test_a_limit_that_ordinary_waits_do_not_keep():
+    """1 us: waits run out anywhere, with copies and products under way; each row is then right or NaN or, of a
+    prompt, as it was, what is not right is reported, and the next calls are as ever."""
+    H, lens = 24, [(300, 700), (33, 33), (129, 1400)] * 4
+    q, k, r, v, qs, ks = prompts(lens, H, BF16, 6)
+    m, n = q.shape[0], 300
+    x, w, s = normal(gen(1), n, H, 192).to(BF16), normal(gen(2), H, 256, 512).to(BF16), normal(gen(3), n, H, 512)
+
+    def calls():
+        words = [status_word() for _ in range(3)]
+        o, lse = torch.full((m, H, 128), 7.0, dtype=BF16, device="cuda"), torch.full((m, H), 7.0, device="cuda")
+        qo, oo = torch.zeros((n, H, 576), dtype=BF16, device="cuda"), torch.zeros((n, H, 128), dtype=BF16, device="cuda")
+        hs.attend_prompts(q, k, r, v, qs, ks, o, lse, 0.1, status=words[0])
+        hs.absorb_queries(x, w[:, :128], qo, status=words[1])
+        hs.expand_outputs(s, w[:, 128:], oo, status=words[2])
+        torch.cuda.synchronize()
+        return (o, lse, qo, oo), [int(a) for a in words]
+
+    want, words = calls()
+    assert words == [0, 0, 0]
+    hs.set_latent_waits(1000)
+    try:
+        for _ in range(4):
+            got, words = calls()
+            assert all(a in (0, hs.HS_STATUS_TIMEOUT) for a in words)
+            for i, word in ((0, words[0]), (1, words[0]), (2, words[1]), (3, words[2])):
+                same = (got[i] == want[i]) | torch.isnan(got[i]) | ((got[i] == 7) if i < 2 else False)
+                assert same.all() and (word or torch.equal(got[i], want[i]))
+    finally:
+        hs.set_latent_waits()
+    got, words = calls()
+    assert words == [0, 0, 0] and all(torch.equal(a, b) for a, b in zip(got, want))

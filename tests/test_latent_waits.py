@@ -80,3 +80,15 @@ def test_each_row_tiles_queries_are_waited_for_at_the_end():
     turn = body[body.index("until(&sm->q_free[w], k - 1)"):body.index("&maps.q, 0, q_row")]
     assert turn.count("(w ? asked1 : asked0) = k;") == 1
     assert re.search(r"asked = w \? asked1 : asked0;\s*if \(asked >= 0\) bar_drain\(&sm->q_full\[w\], asked & 1", body)
+
+
+@pytest.mark.parametrize("name,source,first", [("absorb_kernel", "hs_absorb.cu", "const HeadProduct p"), ("expand_many_kernel", "hs_absorb.cu", "const HeadProduct p"),
+                                               ("prompt_kernel", "hs_prompt.cu", "const PromptAttention A")])
+def test_what_is_in_flight_is_waited_for_longer_than_it_can_take(name, source, first):
+    """However short the limit of a wait: a copy landing behind its CTA's end would land in another's memory."""
+    drains = re.findall(r"bar_drain\(([^;]*)\);", kernel(name, source, first))
+    assert drains and all(x.endswith("waits.drain") for x in drains)
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "hierarchical_kv_cache_swap_gb300", "csrc")
+    with open(os.path.join(csrc, "hs_latent.h")) as f:
+        text = f.read()
+    assert "kLeastDrainNs = 10000000ull" in text and "ns > kLeastDrainNs ? ns : kLeastDrainNs" in text
