@@ -27,7 +27,7 @@
 //
 // A key tile costs the tensor core 2560 cycles (64 an instruction). Measured on one GB300: 16384 rows of
 // 16 heads, causal, 743 us = 1.85 PFLOP/s, 96 % of what a library product reaches in a burst (in a run of
-// seconds the card's power limit holds both lower); 512 rows over 16384 keys of 64 heads 217 us, on the 128
+// seconds the card's power limit holds both lower); 512 rows over 16384 keys of 64 heads 219 us, on the 128
 // SMs that its items fill; a lone item 3500 cycles a key tile: the two turns, each 1280 cycles of products
 // and about 450 of waits. Short items (64 prompts of 100 tokens, 16 heads: 32 us) cost about 7500
 // cycles each, of which code that has left the instruction cache is a good part. What brought it

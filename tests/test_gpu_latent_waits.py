@@ -78,7 +78,7 @@ def test_a_prompt_that_takes_longer_than_the_limit_of_a_wait(short):
     qs, ks = torch.tensor([0, 1, 3], dtype=torch.int32, device="cuda"), torch.tensor([0, n, n], dtype=torch.int32, device="cuda")
     o, lse, word = torch.empty((3, 1, 128), dtype=BF16, device="cuda"), torch.empty((3, 1), device="cuda"), status_word()
     ms = gpu_ms(lambda: hs.attend_prompts(q, k, r, v, qs, ks, o, lse, 0.1, causal=False, status=word))
-    assert ms > 25, "the item has to last for some limits"
+    assert ms > 12, "the item has to last for longer than the limit"
     assert int(word) == 0
     assert ((o[0].double() - 1).abs() <= 2.0 ** -4 + 2.0 ** -7).all() and not o[1:].any()
     x = torch.cat([(c[:, 0].double() @ q[0, 0, :128].double()) * 0.1 for c in k.split(n // 8)])
@@ -94,7 +94,7 @@ def test_a_search_that_takes_longer_than_the_limit_of_a_wait(short, B, H):
     qs[0], ks[0], qs[-1], ks[-1] = 0, 0, 70, 90
     o, lse, word = torch.empty((70, H, 128), dtype=BF16, device="cuda"), torch.empty((70, H), device="cuda"), status_word()
     ms = gpu_ms(lambda: hs.attend_prompts(q, k, r, v, qs, ks, o, lse, 0.1, status=word))
-    assert ms > 25, "the search has to last for some limits"
+    assert ms > 12, "the search has to last for longer than the limit"
     assert int(word) == 0
     for a, b, c, d in ((0, 40, 0, 40), (40, 70, 40, 90)):
         wo, wl, bo, bl = lm.attend(q[a:b], k[c:d], r[c:d], v[c:d], 0.1, True, BF16)
