@@ -197,8 +197,8 @@ __global__ void __launch_bounds__(kAbsorbThreads) absorb_kernel(const HeadProduc
 }
 
 // ---------------------------------------------------------------- outputs
-// The f32 rows are sums that nothing has been rounded of yet, and the products take each value as two bf16,
-// its upper half and the rest, rounded: to within 2^-15 of it. (One bf16 each, 2^-8 of them at most, made the
+// The f32 rows are sums that have not been rounded yet, and the products take each value as two bf16, its upper
+// half and the rest, rounded: to within 2^-15 of it. (One bf16 each, 2^-8 of them at most, made the
 // results' error against 64 bits 0.0024 of them, where their own rounding alone makes it 0.0017; it took 15.8
 // us instead of 18.0 for 256 tokens of 128 heads, 3.0 instead of 3.2 for 37 of 20.)
 __device__ __forceinline__ void split(float x, float y, uint32_t& upper, uint32_t& rest) {
